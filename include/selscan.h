@@ -23,6 +23,13 @@
  *            (projections on cuBLAS, conv, scan, gate, output projection).
  *   ss_ssd_fwd  the multi-head scan with a scalar decay per head (Mamba-2's
  *            SSD model) on the tensor cores.
+ *   ss_gdr_fwd / ss_gdr_step / ss_gdr_bwd  the gated delta rule: a multi-head
+ *            scan whose d_v x d_k state is decayed by one scalar per head and
+ *            step and corrected along the key -- over a sequence, for one
+ *            token, and its gradients.
+ *   ss_norm_fwd / ss_norm_bwd  layer norm over the last dimension and its
+ *            gradients; ss_block_fwd_prenorm puts it in front of the Mamba
+ *            block, with the residual around both.
  *   ss_fwd_with_state  ss_fwd from a given entering state (continuation).
  *   ss_fwd_host  ss_fwd on activations in host memory, with uploads, scans
  *            and downloads of batch slices overlapped.
@@ -114,6 +121,8 @@ enum {
     SS_BF16            = 1u << 0,  /* u, delta, z, B, C, y are bf16 (else fp32) */
     SS_DELTA_SOFTPLUS  = 1u << 1,  /* Δ = softplus(delta + delta_bias); else Δ = delta + delta_bias */
     SS_SYNC_CHECK      = 1u << 2,  /* synchronize the stream and return the device status */
+    SS_BETA_SIGMOID    = 1u << 4,  /* ss_gdr_*: β = sigmoid(beta); else β = beta */
+    SS_QK_L2NORM       = 1u << 5,  /* ss_gdr_*: scale every row of q and k to unit length */
     SS_FORCE_GENERAL_A = 1u << 3,  /* skip the A[d,n] = a_d (n+1) fast path even when A has that form */
     SS_TEST_DROP_CARRY = 1u << 30  /* TEST ONLY: the first chunk of batch 0, channel block 0 never
                                       publishes its carry, so its successor's bounded wait runs out
@@ -226,6 +235,19 @@ typedef struct ss_block_weights {
 SS_API int ss_block_fwd(const void* hidden, void* out, const ss_block_weights* w, int64_t batch, int64_t seqlen,
                         void* scratch, size_t scratch_bytes, void* stream);
 
+/* ss_block_fwd_prenorm -- one residual layer around the block:
+ *   out = hidden + block(layer_norm(hidden))
+ *   norm_weight, norm_bias  [d_model] fp32 or NULL, eps: as in ss_norm_fwd
+ *   scratch                 at least ss_block_prenorm_scratch_bytes() bytes
+ * out must not overlap hidden.  The residual is added by the output projection,
+ * before its one rounding to bf16.  Other arguments and errors: as ss_block_fwd. */
+SS_API int ss_block_fwd_prenorm(const void* hidden, const float* norm_weight, const float* norm_bias, float eps,
+                                void* out, const ss_block_weights* w, int64_t batch, int64_t seqlen, void* scratch,
+                                size_t scratch_bytes, void* stream);
+
+/* Scratch bytes ss_block_fwd_prenorm needs (0 for invalid sizes). */
+SS_API size_t ss_block_prenorm_scratch_bytes(const ss_block_weights* w, int64_t batch, int64_t seqlen);
+
 /* Scratch bytes ss_block_fwd needs (0 for invalid sizes). */
 SS_API size_t ss_block_scratch_bytes(const ss_block_weights* w, int64_t batch, int64_t seqlen);
 
@@ -282,6 +304,102 @@ SS_API int ss_ssd_fwd(const void* x, const void* dt, const float* dt_bias, const
 /* Workspace bytes that let ss_ssd_fwd split sequences into segments
  * (records for up to 8 segments); 0 for sizes it would reject. */
 SS_API size_t ss_ssd_fwd_workspace_bytes(const ss_ssd_dims* dims, uint32_t flags);
+
+/* Sizes of a gated delta rule (ss_gdr_*).  seqlen is ignored by ss_gdr_step. */
+typedef struct ss_gdr_dims {
+    int64_t batch;
+    int64_t seqlen;
+    int64_t nheads;     /* heads of v, dt, beta and y */
+    int64_t nheads_k;   /* heads of q and k; divides nheads: value head h reads key head h / (nheads / nheads_k) */
+    int64_t d_k;        /* 64 or 128 */
+    int64_t d_v;        /* 64 or 128 */
+} ss_gdr_dims;
+
+/* ss_gdr_fwd -- the gated delta rule over a sequence (an engineering addition:
+ * the pages have no counterpart).  For each (b, head h), from S = h_init:
+ *   Δ_t = softplus(dt_t,h + dt_bias_h)  (dt + bias without SS_DELTA_SOFTPLUS),  α_t = exp(Δ_t A_h)
+ *   β_t = σ(beta_t,h)                   (beta without SS_BETA_SIGMOID)
+ *   q_t, k_t divided by sqrt(|.|² + 1e-6) with SS_QK_L2NORM
+ *   e_t = v_t - α_t S_t-1 k_t
+ *   S_t = α_t S_t-1 + β_t e_t k_tᵀ
+ *   y_t = scale · S_t q_t
+ *   q, k         [batch, seqlen, nheads_k, d_k]  element type
+ *   v, y         [batch, seqlen, nheads, d_v]    element type
+ *   dt, beta     [batch, seqlen, nheads]         element type
+ *   A            [nheads] fp32 (negative, so that α < 1); dt_bias [nheads] fp32 or NULL
+ *   h_init       [batch, nheads, d_v, d_k] fp32, or NULL: S_-1 = 0
+ *   seqlens      [batch] int32, or NULL: sequence b has the tokens t < seqlens[b]
+ *                (clamped to 0 .. seqlen).  Tokens behind its end are not used, whatever
+ *                they hold, and their rows of y are left as they were.
+ *   final_state  [batch, nheads, d_v, d_k] fp32, or NULL: S after a sequence's last
+ *                token (h_init or zero for an empty one); may be h_init itself
+ *   flags        SS_BF16, SS_DELTA_SOFTPLUS, SS_BETA_SIGMOID, SS_QK_L2NORM, SS_SYNC_CHECK,
+ *                SS_TEST_DROP_CARRY for tests
+ *   launch       stream; workspace of at least ss_gdr_fwd_workspace_bytes() bytes,
+ *                16-byte aligned (its first word is a status word that the call clears;
+ *                see ss_ssd_fwd); timeout_iters bounds one wait in microseconds (0: two
+ *                seconds); chunk_len > 0 fixes the length of the time segments that a
+ *                bf16 sequence is cut into, 0 lets the library choose.
+ * The state is fp32 throughout.  bf16 runs chunk by chunk (64 steps) as dense products
+ * on the tensor cores, in which the fp32 operands (the state, the chunk's inverse and
+ * its corrections) enter as two bf16 terms each; fp32, and short bf16 sequences, run
+ * token by token in fp32.  Errors: SS_ERR_INVALID_ARG for NULL or misaligned pointers
+ * or sizes, SS_ERR_UNSUPPORTED for d_k or d_v other than 64 and 128, SS_ERR_WORKSPACE,
+ * SS_ERR_CUDA.  batch or nheads 0 is a no-op; seqlen 0 copies h_init (or zero) to
+ * final_state. */
+SS_API int ss_gdr_fwd(const void* q, const void* k, const void* v, const void* dt, const float* dt_bias,
+                      const float* A, const void* beta, const float* h_init, const int32_t* seqlens, void* y,
+                      float* final_state, float scale, uint32_t flags, const ss_gdr_dims* dims,
+                      const ss_launch* launch);
+
+/* Workspace bytes ss_gdr_fwd needs (0 for sizes it would reject). */
+SS_API size_t ss_gdr_fwd_workspace_bytes(const ss_gdr_dims* dims, uint32_t flags);
+
+/* ss_gdr_step -- one token of the gated delta rule on a carried state.
+ *   state        [batch, nheads, d_v, d_k] fp32, read and overwritten in place
+ *   q, k [batch, nheads_k, d_k], v, y [batch, nheads, d_v], dt, beta [batch, nheads]
+ * Everything else as in ss_gdr_fwd; dims->seqlen is ignored and launch->workspace is
+ * not used.  Token by token, ss_gdr_step gives ss_gdr_fwd up to rounding. */
+SS_API int ss_gdr_step(float* state, const void* q, const void* k, const void* v, const void* dt,
+                       const float* dt_bias, const float* A, const void* beta, void* y, float scale,
+                       uint32_t flags, const ss_gdr_dims* dims, const ss_launch* launch);
+
+/* Sizes of a layer norm: `rows` rows of `cols` consecutive values. */
+typedef struct ss_norm_dims {
+    int64_t rows;
+    int64_t cols;
+} ss_norm_dims;
+
+/* ss_norm_fwd -- layer norm of every row (an engineering addition):
+ *   μ = Σ x / cols,  r = 1 / sqrt(Σ (x - μ)² / cols + eps),  y = (x - μ) r · weight + bias
+ *   x, y         [rows, cols] element type (bf16 with SS_BF16, else fp32); y may be x
+ *   weight, bias [cols] fp32 or NULL (1 and 0)
+ *   mean, rstd   [rows] fp32 or NULL: μ and r, which ss_norm_bwd reads
+ *   flags        SS_BF16, SS_SYNC_CHECK
+ * Any rows and cols (rows that do not start on 16 bytes take narrower accesses);
+ * statistics in fp32, over the row held in registers.  launch->workspace is not used.
+ * Errors: SS_ERR_INVALID_ARG for NULL or misaligned pointers, negative sizes, cols = 0
+ * with rows > 0 or a negative eps; rows = 0 is a no-op. */
+SS_API int ss_norm_fwd(const void* x, const float* weight, const float* bias, void* y, float* mean, float* rstd,
+                       float eps, uint32_t flags, const ss_norm_dims* dims, const ss_launch* launch);
+
+/* ss_norm_bwd -- gradients of ss_norm_fwd's inputs from dy = dJ/dy.  With
+ * x̂ = (x - μ) r and w = dy · weight, per row:
+ *   dx = r (w - mean(w) - x̂ mean(w x̂)),  dweight = Σ_rows dy x̂,  dbias = Σ_rows dy
+ *   dy, x, dx       [rows, cols] element type; dx may be dy
+ *   mean, rstd      [rows] fp32, as ss_norm_fwd wrote them
+ *   weight          [cols] fp32 or NULL
+ *   dweight, dbias  [cols] fp32, or NULL to skip
+ *   launch          workspace of at least ss_norm_bwd_workspace_bytes() bytes, 16-byte
+ *                   aligned (column sums of the blocks; added in a fixed order, so the
+ *                   results do not change from run to run)
+ * rows = 0 writes zeros to dweight and dbias.  Errors: as ss_norm_fwd, SS_ERR_WORKSPACE. */
+SS_API int ss_norm_bwd(const void* dy, const void* x, const float* mean, const float* rstd, const float* weight,
+                       void* dx, float* dweight, float* dbias, uint32_t flags, const ss_norm_dims* dims,
+                       const ss_launch* launch);
+
+/* Workspace bytes ss_norm_bwd needs (0 for sizes it would reject). */
+SS_API size_t ss_norm_bwd_workspace_bytes(const ss_norm_dims* dims, uint32_t flags);
 
 /* ss_bwd -- backward of ss_fwd: given dy = dJ/dy and optionally
  * dlast_state = dJ/dlast_state for a scalar J, writes dJ/d(input) for every

@@ -10,6 +10,10 @@ sm_100a in csrc/).  Three operations:
            prologue fused in;
   ss_block_fwd  the Mamba block's inner forward path around the scan;
   ss_ssd_fwd    the multi-head scalar-decay scan (Mamba-2's SSD model);
+  ss_gdr_fwd / ss_gdr_step / ss_gdr_bwd  the gated delta rule: over a
+                sequence, for one token, and its gradients;
+  ss_norm_fwd / ss_norm_bwd  layer norm and its gradients;
+  ss_block_fwd_prenorm  the block behind a layer norm, with its residual;
   ss_fwd_host   ss_fwd on activations in host memory, batch slices'
                 uploads, scans and downloads overlapped.
 
@@ -23,7 +27,9 @@ from ._binding import (D_STATE, EXPORTED, LIB_PATH, SS_BF16, SS_DELTA_SOFTPLUS,
                        fwd_chunk_len, ss_block_fwd, ss_block_weights, ss_ssd_dims, ss_ssd_fwd,
                        fwd_workspace_bytes, lib, ss_bwd, ss_check, ss_dims, ss_fwd, ss_fwd_conv,
                        ss_launch, ss_step, ss_step_conv, status_string, workspace_for,
-                       ss_fwd_host, fwd_host_workspace_bytes, clear_workspaces)
+                       ss_fwd_host, fwd_host_workspace_bytes, clear_workspaces, SS_BETA_SIGMOID, SS_QK_L2NORM,
+                       ss_gdr_dims, ss_gdr_fwd, ss_gdr_step, ss_norm_dims, ss_norm_fwd, ss_norm_bwd,
+                       ss_block_fwd_prenorm)
 
 __all__ = ["ss_fwd", "ss_fwd_host", "fwd_host_workspace_bytes", "ss_step", "ss_bwd", "ss_fwd_conv", "ss_step_conv", "ss_block_fwd", "ss_ssd_fwd",
            "block_scratch_bytes", "ss_block_weights", "ss_ssd_dims", "ss_check", "fwd_workspace_bytes", "fwd_chunk_len",
@@ -32,4 +38,5 @@ __all__ = ["ss_fwd", "ss_fwd_host", "fwd_host_workspace_bytes", "ss_step", "ss_b
            "D_STATE", "EXPORTED", "LIB_PATH", "SS_OK", "SS_ERR_INVALID_ARG",
            "SS_ERR_UNSUPPORTED", "SS_ERR_CUDA", "SS_ERR_TIMEOUT", "SS_ERR_WORKSPACE",
            "SS_BF16", "SS_DELTA_SOFTPLUS", "SS_SYNC_CHECK", "SS_FORCE_GENERAL_A",
-           "SS_TEST_DROP_CARRY"]
+           "SS_TEST_DROP_CARRY", "SS_BETA_SIGMOID", "SS_QK_L2NORM", "ss_gdr_dims", "ss_gdr_fwd", "ss_gdr_step",
+           "ss_norm_dims", "ss_norm_fwd", "ss_norm_bwd", "ss_block_fwd_prenorm"]

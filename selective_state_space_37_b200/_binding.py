@@ -6,6 +6,7 @@ the current stream.  There is no CPU fallback: if the library is missing or a
 call fails, an exception is raised.
 """
 import ctypes
+import functools
 import os
 import threading
 
@@ -27,6 +28,8 @@ SS_BF16 = 1 << 0
 SS_DELTA_SOFTPLUS = 1 << 1
 SS_SYNC_CHECK = 1 << 2
 SS_FORCE_GENERAL_A = 1 << 3
+SS_BETA_SIGMOID = 1 << 4
+SS_QK_L2NORM = 1 << 5
 SS_TEST_DROP_CARRY = 1 << 30
 
 D_STATE = 16
@@ -35,7 +38,9 @@ D_STATE = 16
 EXPORTED = ("ss_fwd", "ss_step", "ss_fwd_workspace_bytes", "ss_fwd_chunk_len", "ss_check",
             "ss_status_string", "ss_version", "ss_fwd_noalloc", "ss_bwd", "ss_bwd_workspace_bytes",
             "ss_fwd_conv", "ss_step_conv", "ss_block_fwd", "ss_block_scratch_bytes", "ss_ssd_fwd",
-            "ss_fwd_host", "ss_fwd_host_workspace_bytes", "ss_ssd_fwd_workspace_bytes", "ss_fwd_with_state")
+            "ss_fwd_host", "ss_fwd_host_workspace_bytes", "ss_ssd_fwd_workspace_bytes", "ss_fwd_with_state",
+            "ss_gdr_fwd", "ss_gdr_fwd_workspace_bytes", "ss_gdr_step", "ss_norm_fwd", "ss_norm_bwd",
+            "ss_norm_bwd_workspace_bytes", "ss_block_fwd_prenorm", "ss_block_prenorm_scratch_bytes")
 
 
 class ss_dims(ctypes.Structure):
@@ -69,6 +74,15 @@ BLOCK_WEIGHT_SHAPES = {   # name: (shape as a function of (d_model, d_inner, dt_
 class ss_ssd_dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
                 ("headdim", ctypes.c_int64), ("d_state", ctypes.c_int64)]
+
+
+class ss_gdr_dims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
+                ("nheads_k", ctypes.c_int64), ("d_k", ctypes.c_int64), ("d_v", ctypes.c_int64)]
+
+
+class ss_norm_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
 
 
 class SelscanError(RuntimeError):
@@ -144,6 +158,22 @@ def lib():
         L.ss_ssd_fwd.restype = ctypes.c_int
         L.ss_ssd_fwd_workspace_bytes.argtypes = [ctypes.POINTER(ss_ssd_dims), ctypes.c_uint32]
         L.ss_ssd_fwd_workspace_bytes.restype = ctypes.c_size_t
+        gp, np_ = ctypes.POINTER(ss_gdr_dims), ctypes.POINTER(ss_norm_dims)
+        u32, f32, lp = ctypes.c_uint32, ctypes.c_float, ctypes.POINTER(ss_launch)
+        L.ss_gdr_fwd.argtypes = [vp, vp, vp, vp, f32p, f32p, vp, f32p, vp, vp, f32p, f32, u32, gp, lp]
+        L.ss_gdr_step.argtypes = [f32p, vp, vp, vp, vp, f32p, f32p, vp, vp, f32, u32, gp, lp]
+        L.ss_norm_fwd.argtypes = [vp, f32p, f32p, vp, f32p, f32p, f32, u32, np_, lp]
+        L.ss_norm_bwd.argtypes = [vp, vp, f32p, f32p, f32p, vp, f32p, f32p, u32, np_, lp]
+        L.ss_block_fwd_prenorm.argtypes = [vp, f32p, f32p, f32, vp, ctypes.POINTER(ss_block_weights),
+                                           ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_size_t, vp]
+        for f in (L.ss_gdr_fwd, L.ss_gdr_step, L.ss_norm_fwd, L.ss_norm_bwd, L.ss_block_fwd_prenorm):
+            f.restype = ctypes.c_int
+        L.ss_gdr_fwd_workspace_bytes.argtypes = [gp, u32]
+        L.ss_norm_bwd_workspace_bytes.argtypes = [np_, u32]
+        L.ss_block_prenorm_scratch_bytes.argtypes = [ctypes.POINTER(ss_block_weights), ctypes.c_int64,
+                                                     ctypes.c_int64]
+        for f in (L.ss_gdr_fwd_workspace_bytes, L.ss_norm_bwd_workspace_bytes, L.ss_block_prenorm_scratch_bytes):
+            f.restype = ctypes.c_size_t
         _lib = L
     return _lib
 
@@ -207,6 +237,34 @@ def _stream_handle(stream, device):
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream
+
+
+def _on_device(fn):
+    """Runs a function with its first tensor's device current (the library launches on the current device)."""
+    @functools.wraps(fn)
+    def call(first, *args, **kw):
+        dev = getattr(first, "device", None)
+        if dev is None or dev.type != "cuda":
+            raise ValueError(f"{fn.__name__} runs on CUDA tensors only")
+        if dev.index == torch.cuda.current_device():
+            return fn(first, *args, **kw)
+        with torch.cuda.device(dev):
+            return fn(first, *args, **kw)
+    return call
+
+
+def _launch_for(need, dev, stream, workspace, timeout_iters=0, chunk_len=0):
+    sh = _stream_handle(stream, dev)
+    if workspace is None:
+        # a captured graph gets a workspace of its own, from its memory pool: graphs may be replayed at once,
+        # and the cached buffer may have been replaced by a larger one by then
+        capturing = torch.cuda.is_current_stream_capturing()
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev) if capturing else \
+            workspace_for(need, dev, sh)
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(timeout_iters),
+                     int(chunk_len))
 
 
 def fwd_workspace_bytes(batch, seqlen, d_inner, bf16=True, chunk_len=0, d_state=D_STATE):
@@ -556,6 +614,182 @@ def ss_ssd_fwd(x, dt, A, B, C, D=None, dt_bias=None, *, softplus=True, y=None, f
     if rc != SS_OK:
         raise SelscanError(rc, "ss_ssd_fwd")
     return y, final_state
+
+
+def _gdr_setup(q, k, v, dt, A, beta, dt_bias, io, softplus, beta_sigmoid, qk_l2norm, tok):
+    """Checks the inputs that the ss_gdr_* calls share (`tok`: the token dimensions, [batch] or
+    [batch, L]) and returns (dims, flags)."""
+    n = len(tok)
+    for t, name in ((q, "q"), (v, "v")):
+        if t.dim() != n + 2:
+            raise ValueError(f"{name} must have {n + 2} dimensions")
+    hk, d_k = q.shape[n:]
+    h, d_v = v.shape[n:]
+    dev = q.device
+    for t, name, shape in ((q, "q", (*tok, hk, d_k)), (k, "k", (*tok, hk, d_k)), (v, "v", (*tok, h, d_v)),
+                           (dt, "dt", (*tok, h)), (beta, "beta", (*tok, h))):
+        _check(t, name, shape, io, dev)
+    _check(A, "A", (h,), torch.float32, dev)
+    _check(dt_bias, "dt_bias", (h,), torch.float32, dev)
+    flags = _io_flag(q) | (SS_DELTA_SOFTPLUS if softplus else 0) | (SS_BETA_SIGMOID if beta_sigmoid else 0) | \
+        (SS_QK_L2NORM if qk_l2norm else 0)
+    return ss_gdr_dims(tok[0], tok[1] if n > 1 else 1, h, hk, d_k, d_v), flags
+
+
+@_on_device
+def ss_gdr_fwd(q, k, v, dt, A, beta, dt_bias=None, initial_state=None, seqlens=None, *, scale=None, softplus=True,
+               beta_sigmoid=True, qk_l2norm=True, y=None, final_state=None, return_final_state=True, chunk_len=0,
+               workspace=None, stream=None, sync_check=False, timeout_iters=0, extra_flags=0):
+    """Gated delta rule over a sequence through libselscan's ss_gdr_fwd.
+    q, k [batch, L, nheads_k, d_k]; v [batch, L, nheads, d_v]; dt, beta [batch, L, nheads] (bf16 or fp32,
+    all the same; d_k, d_v 64 or 128; nheads a multiple of nheads_k); A, dt_bias [nheads] fp32;
+    initial_state [batch, nheads, d_v, d_k] fp32 or None; seqlens [batch] int32 on the device or None:
+    the tokens of each sequence, the rows of y behind them staying as they were (zero when y is made
+    here).  scale defaults to d_k ** -0.5.  Returns (y, final_state or None); final_state may be
+    initial_state."""
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, L, nheads_k, d_k]")
+    batch, L = q.shape[:2]
+    dims, flags = _gdr_setup(q, k, v, dt, A, beta, dt_bias, q.dtype, softplus, beta_sigmoid, qk_l2norm, (batch, L))
+    dev = q.device
+    states = (batch, dims.nheads, dims.d_v, dims.d_k)
+    _check(initial_state, "initial_state", states, torch.float32, dev)
+    _check(seqlens, "seqlens", (batch,), torch.int32, dev)
+    if y is None:
+        y = torch.empty_like(v) if seqlens is None else torch.zeros_like(v)
+    _check(y, "y", v.shape, v.dtype, dev)
+    if final_state is None and return_final_state:
+        final_state = torch.empty(states, dtype=torch.float32, device=dev)
+    _check(final_state, "final_state", states, torch.float32, dev)
+    flags |= (SS_SYNC_CHECK if sync_check else 0) | int(extra_flags)
+    need = int(lib().ss_gdr_fwd_workspace_bytes(ctypes.byref(dims), flags))
+    launch = _launch_for(need, dev, stream, workspace, timeout_iters, chunk_len)
+    rc = lib().ss_gdr_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(beta),
+                          _ptr(initial_state), _ptr(seqlens), _ptr(y), _ptr(final_state),
+                          dims.d_k ** -0.5 if scale is None else float(scale), flags, ctypes.byref(dims),
+                          ctypes.byref(launch))
+    if rc != SS_OK:
+        raise SelscanError(rc, "ss_gdr_fwd")
+    return y, final_state
+
+
+@_on_device
+def ss_gdr_step(state, q, k, v, dt, A, beta, dt_bias=None, *, scale=None, softplus=True, beta_sigmoid=True,
+                qk_l2norm=True, y=None, stream=None, sync_check=False):
+    """One token of the gated delta rule through libselscan's ss_gdr_step; `state`
+    [batch, nheads, d_v, d_k] fp32 is updated in place.  q, k [batch, nheads_k, d_k]; v [batch, nheads, d_v];
+    dt, beta [batch, nheads]; the rest as in ss_gdr_fwd.  Returns y [batch, nheads, d_v]."""
+    if state.dim() != 4:
+        raise ValueError("state must be [batch, nheads, d_v, d_k]")
+    dev = state.device
+    if q.device != dev:
+        raise ValueError(f"q is on {q.device}, expected {dev}")
+    dims, flags = _gdr_setup(q, k, v, dt, A, beta, dt_bias, q.dtype, softplus, beta_sigmoid, qk_l2norm,
+                             (state.shape[0],))
+    _check(state, "state", (dims.batch, dims.nheads, dims.d_v, dims.d_k), torch.float32, dev)
+    if y is None:
+        y = torch.empty_like(v)
+    _check(y, "y", v.shape, v.dtype, dev)
+    flags |= SS_SYNC_CHECK if sync_check else 0
+    launch = ss_launch(_stream_handle(stream, dev), None, 0, 0, 0)
+    rc = lib().ss_gdr_step(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(beta),
+                           _ptr(y), dims.d_k ** -0.5 if scale is None else float(scale), flags, ctypes.byref(dims),
+                           ctypes.byref(launch))
+    if rc != SS_OK:
+        raise SelscanError(rc, "ss_gdr_step")
+    return y
+
+
+@_on_device
+def ss_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, y=None, stats=True, stream=None, sync_check=False):
+    """Layer norm over the last dimension of x (bf16 or fp32, contiguous) through libselscan's
+    ss_norm_fwd; weight, bias [cols] fp32 or None; y may be x.  Returns (y, mean, rstd), the statistics
+    [rows] in fp32 for ss_norm_bwd (None with stats=False)."""
+    if x.dim() == 0:
+        raise ValueError("x needs at least one dimension")
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    dev = x.device
+    _check(x, "x", x.shape, x.dtype, dev)
+    _check(weight, "weight", (cols,), torch.float32, dev)
+    _check(bias, "bias", (cols,), torch.float32, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    _check(y, "y", x.shape, x.dtype, dev)
+    mean = torch.empty(rows, dtype=torch.float32, device=dev) if stats else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if stats else None
+    flags = _io_flag(x) | (SS_SYNC_CHECK if sync_check else 0)
+    dims = ss_norm_dims(rows, cols)
+    launch = ss_launch(_stream_handle(stream, dev), None, 0, 0, 0)
+    rc = lib().ss_norm_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), float(eps), flags,
+                           ctypes.byref(dims), ctypes.byref(launch))
+    if rc != SS_OK:
+        raise SelscanError(rc, "ss_norm_fwd")
+    return y, mean, rstd
+
+
+@_on_device
+def ss_norm_bwd(dy, x, mean, rstd, weight=None, *, dx=None, dweight=None, dbias=None, sums=True, workspace=None,
+                stream=None, sync_check=False):
+    """Backward of ss_norm_fwd through libselscan's ss_norm_bwd: dy and x of one shape and type, mean and
+    rstd [rows] fp32 from the forward, weight [cols] fp32 or None; dx may be dy.  Returns a dict with
+    dx, dweight and dbias (fp32 [cols]; without them for sums=False)."""
+    if x.dim() == 0:
+        raise ValueError("x needs at least one dimension")
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    dev = dy.device
+    _check(x, "x", x.shape, x.dtype, dev)
+    _check(dy, "dy", x.shape, x.dtype, dev)
+    _check(mean, "mean", (rows,), torch.float32, dev)
+    _check(rstd, "rstd", (rows,), torch.float32, dev)
+    _check(weight, "weight", (cols,), torch.float32, dev)
+    g = {"dx": torch.empty_like(x) if dx is None else dx}
+    _check(g["dx"], "dx", x.shape, x.dtype, dev)
+    if sums:
+        for name, t in (("dweight", dweight), ("dbias", dbias)):
+            g[name] = torch.empty(cols, dtype=torch.float32, device=dev) if t is None else t
+            _check(g[name], name, (cols,), torch.float32, dev)
+    flags = _io_flag(x) | (SS_SYNC_CHECK if sync_check else 0)
+    dims = ss_norm_dims(rows, cols)
+    need = int(lib().ss_norm_bwd_workspace_bytes(ctypes.byref(dims), flags))
+    launch = _launch_for(need, dev, stream, workspace)
+    rc = lib().ss_norm_bwd(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(g["dx"]),
+                           _ptr(g.get("dweight")), _ptr(g.get("dbias")), flags, ctypes.byref(dims),
+                           ctypes.byref(launch))
+    if rc != SS_OK:
+        raise SelscanError(rc, "ss_norm_bwd")
+    return g
+
+
+@_on_device
+def ss_block_fwd_prenorm(hidden, weights, norm_weight=None, norm_bias=None, *, eps=1e-5, out=None, scratch=None,
+                         stream=None):
+    """hidden + block(layer_norm(hidden)) through libselscan's ss_block_fwd_prenorm: ss_block_fwd's arguments,
+    norm_weight and norm_bias [d_model] fp32 or None.  out must not be hidden."""
+    if hidden.dim() != 3:
+        raise ValueError("hidden must be [batch, L, d_model]")
+    batch, L, d_model = hidden.shape
+    dev = hidden.device
+    st = _block_struct(weights, dev)
+    if st.d_model != d_model:
+        raise ValueError("hidden's last dimension must equal d_model")
+    _check(hidden, "hidden", (batch, L, d_model), torch.bfloat16, dev)
+    _check(norm_weight, "norm_weight", (d_model,), torch.float32, dev)
+    _check(norm_bias, "norm_bias", (d_model,), torch.float32, dev)
+    if out is None:
+        out = torch.empty_like(hidden)
+    _check(out, "out", (batch, L, d_model), torch.bfloat16, dev)
+    need = int(lib().ss_block_prenorm_scratch_bytes(ctypes.byref(st), batch, L))
+    if need == 0:
+        raise SelscanError(SS_ERR_INVALID_ARG, "ss_block_fwd_prenorm")
+    launch = _launch_for(need, dev, stream, scratch)
+    rc = lib().ss_block_fwd_prenorm(_ptr(hidden), _ptr(norm_weight), _ptr(norm_bias), float(eps), _ptr(out),
+                                    ctypes.byref(st), batch, L, launch.workspace, launch.workspace_bytes,
+                                    launch.stream)
+    if rc != SS_OK:
+        raise SelscanError(rc, "ss_block_fwd_prenorm")
+    return out
 
 
 def ss_check(workspace, stream=None, device=None):

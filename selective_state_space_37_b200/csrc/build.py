@@ -8,12 +8,15 @@ The CUDA runtime is linked statically so the library loads in any process
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(os.path.dirname(HERE))
 LIB = os.path.join(HERE, "libselscan.so")
-SOURCES = ["selscan.cu"]
-HEADERS = ["common.cuh", "cp_async.cuh", "fwd.cuh", "ssd_tc.cuh", "bwd.cuh", "step.cuh", "block.cuh", "ssd.cuh"]
+SOURCES = ["selscan.cu", "gdr.cu", "norm.cu"]
+HEADERS = ["common.cuh", "cp_async.cuh", "fwd.cuh", "ssd_tc.cuh", "bwd.cuh", "step.cuh", "block.cuh", "ssd.cuh",
+           "host.cuh", "gdr_rec.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 NVCC_FLAGS = [
@@ -43,14 +46,23 @@ def up_to_date() -> bool:
 def build(force: bool = False, verbose: bool = False, out: str = LIB, defines=()) -> str:
     """Compile the library to `out`; `defines` are extra -D preprocessor
     definitions passed to nvcc (e.g. for a differently configured copy built
-    next to the in-tree one and loaded through SELSCAN_LIB)."""
+    next to the in-tree one and loaded through SELSCAN_LIB).  The sources
+    compile in parallel, one object file each."""
     if not force and out == LIB and not defines and up_to_date():
         return out
-    cmd = [NVCC, *NVCC_FLAGS] + [f"-D{d}" for d in defines]
+    flags = [*NVCC_FLAGS] + [f"-D{d}" for d in defines]
     if verbose:
-        cmd += ["-Xptxas", "-v"]
-    cmd += ["-shared", "-o", out + ".tmp"] + [os.path.join(HERE, s) for s in SOURCES]
-    subprocess.run(cmd, check=True)
+        flags += ["-Xptxas", "-v"]
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = [os.path.join(tmp, s + ".o") for s in SOURCES]
+
+        def compile_one(pair):
+            src, obj = pair
+            subprocess.run([NVCC, *flags, "-c", "-o", obj, os.path.join(HERE, src)], check=True)
+
+        with ThreadPoolExecutor(len(SOURCES)) as pool:
+            list(pool.map(compile_one, zip(SOURCES, objs)))
+        subprocess.run([NVCC, *flags, "-shared", "-o", out + ".tmp", *objs], check=True)
     os.replace(out + ".tmp", out)
     return out
 

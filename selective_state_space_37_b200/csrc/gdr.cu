@@ -1,0 +1,115 @@
+// gdr.cu -- the gated delta rule's entry points (ss_gdr_fwd, ss_gdr_step, ss_gdr_bwd): argument checks,
+// workspace layout, choice of kernel and launches.
+#include "common.cuh"
+#include "gdr_rec.cuh"
+#include "host.cuh"
+
+using namespace selscan;
+
+namespace {
+
+constexpr uint32_t kGdrFlags = SS_BF16 | SS_DELTA_SOFTPLUS | SS_BETA_SIGMOID | SS_QK_L2NORM | SS_SYNC_CHECK |
+                               SS_TEST_DROP_CARRY;
+
+int check_gdr(const ss_gdr_dims* d, uint32_t flags) {
+    if (!d || (flags & ~kGdrFlags)) return SS_ERR_INVALID_ARG;
+    if (d->batch < 0 || d->seqlen < 0 || d->nheads < 0 || d->nheads_k < 0) return SS_ERR_INVALID_ARG;
+    if ((d->d_k != 64 && d->d_k != 128) || (d->d_v != 64 && d->d_v != 128)) return SS_ERR_UNSUPPORTED;
+    if (d->nheads > 0 && (d->nheads_k == 0 || d->nheads % d->nheads_k)) return SS_ERR_INVALID_ARG;
+    const int64_t lim = int64_t(1) << 27;   // (b, head) items times the blocks that share one stay below 2^31
+    if (d->batch >= lim || d->nheads >= lim || d->batch * d->nheads >= lim || d->seqlen >= (int64_t(1) << 31) - 256 ||
+        double(d->batch) * double(d->seqlen) * double(d->nheads) * 128.0 > 2.0e18)
+        return SS_ERR_INVALID_ARG;
+    return SS_OK;
+}
+
+GdrParams gdr_params(const void* q, const void* k, const void* v, const void* dt, const float* dt_bias,
+                     const float* A, const void* beta, float scale, uint32_t flags, const ss_gdr_dims* d, int64_t L) {
+    GdrParams p{};
+    p.q = q; p.k = k; p.v = v; p.dt = dt; p.beta = beta; p.dt_bias = dt_bias; p.A = A;
+    p.L = L; p.batch = static_cast<int>(d->batch); p.H = static_cast<int>(d->nheads);
+    p.Hk = static_cast<int>(d->nheads_k); p.scale = scale;
+    p.softplus = (flags & SS_DELTA_SOFTPLUS) ? 1 : 0;
+    p.sigmoid = (flags & SS_BETA_SIGMOID) ? 1 : 0;
+    p.l2norm = (flags & SS_QK_L2NORM) ? 1 : 0;
+    return p;
+}
+
+template <typename IO, int DK>
+void launch_rec(const GdrParams& p, int dv, cudaStream_t stream) {
+    // four rows of the state per thread where the blocks still fill the GPU twice, else one
+    const int64_t items = static_cast<int64_t>(p.batch) * p.H;
+    const int big = dv / (kGdrRecRows * 4);
+    if (items * big >= 2 * sm_count_of_current_device())
+        ss_gdr_rec_kernel<IO, DK, 4><<<static_cast<unsigned>(items * big), kGdrRecThreads, 0, stream>>>(p, dv, big);
+    else
+        ss_gdr_rec_kernel<IO, DK, 1><<<static_cast<unsigned>(items * big * 4), kGdrRecThreads, 0, stream>>>(p, dv, big * 4);
+}
+
+int run_rec(const GdrParams& p, const ss_gdr_dims* d, uint32_t flags, cudaStream_t stream) {
+    const int dv = static_cast<int>(d->d_v);
+    if (flags & SS_BF16) {
+        if (d->d_k == 128) launch_rec<__nv_bfloat16, 128>(p, dv, stream);
+        else launch_rec<__nv_bfloat16, 64>(p, dv, stream);
+    } else {
+        if (d->d_k == 128) launch_rec<float, 128>(p, dv, stream);
+        else launch_rec<float, 64>(p, dv, stream);
+    }
+    return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ss_gdr_fwd_workspace_bytes(const ss_gdr_dims* dims, uint32_t flags) {
+    return check_gdr(dims, flags) == SS_OK ? kHeaderBytes : 0;
+}
+
+int ss_gdr_fwd(const void* q, const void* k, const void* v, const void* dt, const float* dt_bias, const float* A,
+               const void* beta, const float* h_init, const int32_t* seqlens, void* y, float* final_state,
+               float scale, uint32_t flags, const ss_gdr_dims* dims, const ss_launch* launch) {
+    if (!launch) return SS_ERR_INVALID_ARG;
+    int rc = check_gdr(dims, flags);
+    if (rc != SS_OK) return rc;
+    const int64_t L = dims->seqlen;
+    if (dims->batch == 0 || dims->nheads == 0) return SS_OK;
+    if (!A || (L > 0 && (!q || !k || !v || !dt || !beta || !y))) return SS_ERR_INVALID_ARG;
+    const void* ptrs[] = {q, k, v, dt, dt_bias, A, beta, h_init, seqlens, y, final_state};
+    for (const void* x : ptrs)
+        if (!aligned16(x)) return SS_ERR_INVALID_ARG;
+    if (!launch->workspace || launch->workspace_bytes < ss_gdr_fwd_workspace_bytes(dims, flags) ||
+        !aligned16(launch->workspace))
+        return SS_ERR_WORKSPACE;
+    cudaStream_t stream = static_cast<cudaStream_t>(launch->stream);
+    if (cudaMemsetAsync(launch->workspace, 0, sizeof(uint32_t), stream) != cudaSuccess) return SS_ERR_CUDA;
+    GdrParams p = gdr_params(q, k, v, dt, dt_bias, A, beta, scale, flags, dims, L);
+    p.h_init = h_init; p.seqlens = seqlens; p.y = y; p.final_state = final_state;
+    rc = run_rec(p, dims, flags, stream);
+    if (rc != SS_OK) return rc;
+    return (flags & SS_SYNC_CHECK) ? ss_check(launch) : SS_OK;
+}
+
+int ss_gdr_step(float* state, const void* q, const void* k, const void* v, const void* dt, const float* dt_bias,
+                const float* A, const void* beta, void* y, float scale, uint32_t flags, const ss_gdr_dims* dims,
+                const ss_launch* launch) {
+    if (!launch || !dims) return SS_ERR_INVALID_ARG;
+    ss_gdr_dims d = *dims;
+    d.seqlen = 1;
+    int rc = check_gdr(&d, flags);
+    if (rc != SS_OK) return rc;
+    if (d.batch == 0 || d.nheads == 0) return SS_OK;
+    if (!state || !q || !k || !v || !dt || !A || !beta || !y) return SS_ERR_INVALID_ARG;
+    const void* ptrs[] = {state, q, k, v, dt, dt_bias, A, beta, y};
+    for (const void* x : ptrs)
+        if (!aligned16(x)) return SS_ERR_INVALID_ARG;
+    cudaStream_t stream = static_cast<cudaStream_t>(launch->stream);
+    GdrParams p = gdr_params(q, k, v, dt, dt_bias, A, beta, scale, flags, &d, 1);
+    p.h_init = state; p.final_state = state; p.y = y;
+    rc = run_rec(p, &d, flags, stream);
+    if (rc != SS_OK) return rc;
+    if ((flags & SS_SYNC_CHECK) && cudaStreamSynchronize(stream) != cudaSuccess) return SS_ERR_CUDA;
+    return SS_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,532 @@
+// norm.cu -- layer norm over rows, forward and backward (sm_100a).
+//
+//   μ = Σ x / C,  r = 1 / sqrt(Σ (x - μ)² / C + eps),  x̂ = (x - μ) r,  y = x̂ w + b
+//   dx = r (g - mean(g) - x̂ mean(g x̂)),  g = dy w;   dw = Σ_rows dy x̂,  db = Σ_rows dy
+//
+// Both are bound by HBM: x (and dy) read once, y (or dx) written once.  A row is
+// therefore held in registers between its statistics and its output, by the
+// threads of one block (or of one warp where a row is short): thread i holds the
+// 16-byte vectors i, i + T, ... of the row, T chosen so that every thread has
+// work.  The variance is Σ (x - μ)² over the held values, so a large mean costs
+// no precision.  The backward pass keeps each thread's columns of dw and db in
+// registers over all the rows that its block takes, writes one partial row per
+// block, and a second small kernel adds the partials in a fixed order.
+// Rows whose length is not a multiple of 16 bytes take single-element accesses in
+// the same scheme; rows too long for the registers are read again from L2.
+#include <type_traits>
+
+#include "common.cuh"
+#include "host.cuh"
+
+using namespace selscan;
+
+namespace {
+
+constexpr int kWarpRows = 4;     // rows per block where one warp takes a row
+constexpr int kHeld = 16;        // values of a row that a thread holds
+constexpr int kMaxThreads = 512;
+
+struct NormParams {
+    const void* x;
+    const void* dy;
+    const float* weight;
+    const float* bias;
+    void* out;               // y, or dx
+    float* mean;             // written by the forward, read by the backward
+    float* rstd;
+    float* part;             // [blocks][2][cols]: partial dw, db
+    int64_t rows, cols;
+    float eps;
+};
+
+template <typename IO>
+struct VecOf {
+    static constexpr int kN = 16 / sizeof(IO);
+    static constexpr int kSlots = kHeld / kN;   // vectors that a thread holds
+};
+
+// Element e of this thread's vector s: in a row of 16-byte vectors, or (VEC false)
+// element by element with neighbouring threads on neighbouring elements.
+template <typename IO, bool VEC>
+__device__ __forceinline__ int64_t col_of(int s, int e, int t, int T) {
+    constexpr int N = VecOf<IO>::kN;
+    return VEC ? (static_cast<int64_t>(s) * T + t) * N + e : (static_cast<int64_t>(s) * N + e) * T + t;
+}
+
+// This thread's vector s of a row as fp32 (zero behind the row's end).
+template <typename IO, bool VEC>
+__device__ __forceinline__ void load_vec(const IO* row, int64_t cols, int s, int t, int T,
+                                         float (&v)[VecOf<IO>::kN]) {
+    constexpr int N = VecOf<IO>::kN;
+    if (VEC) {
+        const int64_t c = col_of<IO, true>(s, 0, t, T);
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (c < cols) w = *reinterpret_cast<const uint4*>(row + c);
+        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (sizeof(IO) == 2) {
+                v[2 * e] = __uint_as_float(a[e] << 16);
+                v[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
+            } else {
+                v[e] = __uint_as_float(a[e]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int64_t c = col_of<IO, false>(s, e, t, T);
+            v[e] = c < cols ? to_f32(row[c]) : 0.0f;
+        }
+    }
+}
+
+template <typename IO, bool VEC>
+__device__ __forceinline__ void store_vec(IO* row, int64_t cols, int s, int t, int T,
+                                          const float (&v)[VecOf<IO>::kN]) {
+    constexpr int N = VecOf<IO>::kN;
+    if (VEC) {
+        const int64_t c = col_of<IO, true>(s, 0, t, T);
+        if (c >= cols) return;
+        uint32_t a[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (sizeof(IO) == 2) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+                a[e] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                a[e] = __float_as_uint(v[e]);
+            }
+        }
+        *reinterpret_cast<uint4*>(row + c) = make_uint4(a[0], a[1], a[2], a[3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int64_t c = col_of<IO, false>(s, e, t, T);
+            if (c < cols) row[c] = from_f32<IO>(v[e]);
+        }
+    }
+}
+
+// fp32 parameters at a vector's columns (`other` behind the row's end or without a parameter).
+template <typename IO, bool VEC>
+__device__ __forceinline__ void load_par(const float* par, float other, int64_t cols, int s, int t, int T,
+                                         float (&v)[VecOf<IO>::kN]) {
+    constexpr int N = VecOf<IO>::kN;
+    const int64_t c0 = col_of<IO, true>(s, 0, t, T);
+    if (VEC && par && c0 < cols) {
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(par + c0 + e);
+            v[e] = q.x;
+            v[e + 1] = q.y;
+            v[e + 2] = q.z;
+            v[e + 3] = q.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const int64_t c = col_of<IO, VEC>(s, e, t, T);
+        v[e] = (par && c < cols) ? par[c] : other;
+    }
+}
+
+// Sums of a and b over the threads of a row (a warp, or the whole block), in every thread, in a fixed order.
+template <bool WARP>
+__device__ __forceinline__ void row_sum2(float& a, float& b, float (&red)[2][2][32], int& flip) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (WARP) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
+    float (&buf)[2][32] = red[flip];   // two buffers: the next sum may start before every warp has read this one
+    flip ^= 1;
+    if (lane == 0) {
+        buf[0][warp] = a;
+        buf[1][warp] = b;
+    }
+    __syncthreads();
+    a = lane < nw ? buf[0][lane] : 0.0f;
+    b = lane < nw ? buf[1][lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+}
+
+// HELD: the row fits the block's registers (kHeld values per thread); otherwise `slots` vectors are read
+// again for each use.  WARP: one warp per row.
+template <typename IO, bool VEC, bool WARP, bool HELD>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads) ss_norm_fwd_kernel(const NormParams p, int slots) {
+    constexpr int N = VecOf<IO>::kN, kSlots = VecOf<IO>::kSlots;
+    __shared__ float red[2][2][32];
+    int flip = 0;
+    const int T = WARP ? 32 : blockDim.x, t = WARP ? (threadIdx.x & 31) : threadIdx.x;
+    const int64_t first = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * kWarpRows : gridDim.x;
+    const int64_t C = p.cols;
+    const float inv = 1.0f / static_cast<float>(C);
+    float w[HELD ? kSlots : 1][N], b[HELD ? kSlots : 1][N];
+    if (HELD) {
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s) {
+            load_par<IO, VEC>(p.weight, 1.0f, C, s, t, T, w[s]);
+            load_par<IO, VEC>(p.bias, 0.0f, C, s, t, T, b[s]);
+        }
+    }
+    for (int64_t r = first; r < p.rows; r += step) {
+        const IO* row = static_cast<const IO*>(p.x) + r * C;
+        IO* out = static_cast<IO*>(p.out) + r * C;
+        float v[HELD ? kSlots : 1][N];
+        float sum = 0.0f, none = 0.0f;
+        if (HELD) {
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) load_vec<IO, VEC>(row, C, s, t, T, v[s]);
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s)
+#pragma unroll
+                for (int e = 0; e < N; ++e) sum += v[s][e];
+        } else {
+            for (int s = 0; s < slots; ++s) {
+                load_vec<IO, VEC>(row, C, s, t, T, v[0]);
+#pragma unroll
+                for (int e = 0; e < N; ++e) sum += v[0][e];
+            }
+        }
+        row_sum2<WARP>(sum, none, red, flip);
+        const float mu = sum * inv;
+        float sq = 0.0f;
+        if (HELD) {
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s)
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float d = col_of<IO, VEC>(s, e, t, T) < C ? v[s][e] - mu : 0.0f;
+                    v[s][e] = d;
+                    sq = fmaf(d, d, sq);
+                }
+        } else {
+            for (int s = 0; s < slots; ++s) {
+                load_vec<IO, VEC>(row, C, s, t, T, v[0]);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float d = col_of<IO, VEC>(s, e, t, T) < C ? v[0][e] - mu : 0.0f;
+                    sq = fmaf(d, d, sq);
+                }
+            }
+        }
+        row_sum2<WARP>(sq, none, red, flip);
+        const float rs = 1.0f / sqrtf(fmaf(sq, inv, p.eps));
+        if (HELD) {
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) {
+#pragma unroll
+                for (int e = 0; e < N; ++e) v[s][e] = fmaf(v[s][e] * rs, w[s][e], b[s][e]);
+                store_vec<IO, VEC>(out, C, s, t, T, v[s]);
+            }
+        } else {
+            for (int s = 0; s < slots; ++s) {
+                load_vec<IO, VEC>(row, C, s, t, T, v[0]);
+                load_par<IO, VEC>(p.weight, 1.0f, C, s, t, T, w[0]);
+                load_par<IO, VEC>(p.bias, 0.0f, C, s, t, T, b[0]);
+#pragma unroll
+                for (int e = 0; e < N; ++e) v[0][e] = fmaf((v[0][e] - mu) * rs, w[0][e], b[0][e]);
+                store_vec<IO, VEC>(out, C, s, t, T, v[0]);
+            }
+        }
+        if (t == 0) {
+            if (p.mean) p.mean[r] = mu;
+            if (p.rstd) p.rstd[r] = rs;
+        }
+    }
+}
+
+// dx, and (HELD) this block's partial sums of dw and db.  Without HELD the column sums are a kernel of their own.
+template <typename IO, bool VEC, bool WARP, bool HELD>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads)
+ss_norm_bwd_kernel(const NormParams p, int slots, int sums) {
+    constexpr int N = VecOf<IO>::kN, kSlots = VecOf<IO>::kSlots;
+    __shared__ float red[2][2][32];
+    int flip = 0;
+    const int T = WARP ? 32 : blockDim.x, t = WARP ? (threadIdx.x & 31) : threadIdx.x;
+    const int64_t first = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * kWarpRows : gridDim.x;
+    const int64_t C = p.cols;
+    const float inv = 1.0f / static_cast<float>(C);
+    float w[HELD ? kSlots : 1][N], dw[HELD ? kSlots : 1][N] = {}, db[HELD ? kSlots : 1][N] = {};
+    if (HELD) {
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s) load_par<IO, VEC>(p.weight, 1.0f, C, s, t, T, w[s]);
+    }
+    for (int64_t r = first; r < p.rows; r += step) {
+        const IO* xrow = static_cast<const IO*>(p.x) + r * C;
+        const IO* grow = static_cast<const IO*>(p.dy) + r * C;
+        IO* out = static_cast<IO*>(p.out) + r * C;
+        const float mu = p.mean[r], rs = p.rstd[r];
+        float x[HELD ? kSlots : 1][N], g[HELD ? kSlots : 1][N];
+        float c1 = 0.0f, c2 = 0.0f;
+        if (HELD) {
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) {
+                load_vec<IO, VEC>(xrow, C, s, t, T, x[s]);
+                load_vec<IO, VEC>(grow, C, s, t, T, g[s]);
+            }
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s)
+#pragma unroll
+                for (int e = 0; e < N; ++e) {   // behind the row's end g is zero, and with it every term
+                    const float xh = (x[s][e] - mu) * rs;
+                    dw[s][e] = fmaf(g[s][e], xh, dw[s][e]);
+                    db[s][e] += g[s][e];
+                    x[s][e] = xh;
+                    g[s][e] *= w[s][e];
+                    c1 += g[s][e];
+                    c2 = fmaf(g[s][e], xh, c2);
+                }
+        } else {
+            for (int s = 0; s < slots; ++s) {
+                load_vec<IO, VEC>(xrow, C, s, t, T, x[0]);
+                load_vec<IO, VEC>(grow, C, s, t, T, g[0]);
+                load_par<IO, VEC>(p.weight, 1.0f, C, s, t, T, w[0]);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float gw = g[0][e] * w[0][e];
+                    c1 += gw;
+                    c2 = fmaf(gw, (x[0][e] - mu) * rs, c2);
+                }
+            }
+        }
+        row_sum2<WARP>(c1, c2, red, flip);
+        c1 *= inv;
+        c2 *= inv;
+        if (HELD) {
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) {
+#pragma unroll
+                for (int e = 0; e < N; ++e) x[s][e] = rs * (g[s][e] - c1 - x[s][e] * c2);
+                store_vec<IO, VEC>(out, C, s, t, T, x[s]);
+            }
+        } else {
+            for (int s = 0; s < slots; ++s) {
+                load_vec<IO, VEC>(xrow, C, s, t, T, x[0]);
+                load_vec<IO, VEC>(grow, C, s, t, T, g[0]);
+                load_par<IO, VEC>(p.weight, 1.0f, C, s, t, T, w[0]);
+#pragma unroll
+                for (int e = 0; e < N; ++e) x[0][e] = rs * (g[0][e] * w[0][e] - c1 - (x[0][e] - mu) * rs * c2);
+                store_vec<IO, VEC>(out, C, s, t, T, x[0]);
+            }
+        }
+    }
+    if (!HELD || !sums) return;
+    const int64_t pr = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    float* pw = p.part + pr * 2 * C;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int64_t c = col_of<IO, VEC>(s, e, t, T);
+            if (c < C) {
+                pw[c] = dw[s][e];
+                pw[C + c] = db[s][e];
+            }
+        }
+}
+
+// Partial column sums of rows too long for the kernel above: block (i, j) adds the rows j, j + gridDim.y, ...
+template <typename IO>
+__global__ void __launch_bounds__(256) ss_norm_colsum_kernel(const NormParams p) {
+    const int64_t C = p.cols, c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (c >= C) return;
+    float dw = 0.0f, db = 0.0f;
+    for (int64_t r = blockIdx.y; r < p.rows; r += gridDim.y) {
+        const float g = to_f32(static_cast<const IO*>(p.dy)[r * C + c]);
+        const float xh = (to_f32(static_cast<const IO*>(p.x)[r * C + c]) - p.mean[r]) * p.rstd[r];
+        dw = fmaf(g, xh, dw);
+        db += g;
+    }
+    float* pw = p.part + static_cast<int64_t>(blockIdx.y) * 2 * C;
+    pw[c] = dw;
+    pw[C + c] = db;
+}
+
+// dw, db = the sums of `n` partial rows, 32 columns of the 2 C per block, 8 threads per column.
+__global__ void __launch_bounds__(256)
+ss_norm_fold_kernel(const float* __restrict__ part, int n, int64_t C, float* dw, float* db) {
+    __shared__ float acc[8][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + x;
+    float s = 0.0f;
+    if (c < 2 * C) {
+#pragma unroll 4
+        for (int i = y; i < n; i += 8) s += part[static_cast<int64_t>(i) * 2 * C + c];
+    }
+    acc[y][x] = s;
+    __syncthreads();
+    if (y != 0 || c >= 2 * C) return;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += acc[i][x];
+    if (c < C) {
+        if (dw) dw[c] = s;
+    } else if (db) {
+        db[c - C] = s;
+    }
+}
+
+// How a row is spread: T threads with `slots` vectors each.
+struct NormPlan {
+    bool vec, warp, held;
+    int T, slots;
+    int64_t blocks, parts;   // backward: blocks, and partial rows
+};
+
+NormPlan norm_plan(int64_t rows, int64_t cols, bool bf16, bool bwd) {
+    NormPlan pl{};
+    const int64_t N = bf16 ? 8 : 4;
+    pl.vec = cols % N == 0;
+    const int64_t vecs = ceil_div(cols, N);
+    const int64_t slots = kHeld / N;
+    pl.warp = vecs <= 32 * slots;
+    pl.held = vecs <= kMaxThreads * slots;
+    if (pl.warp) {
+        pl.T = 32;
+    } else if (pl.held) {
+        pl.T = static_cast<int>(ceil_div(ceil_div(vecs, slots), 32) * 32);
+    } else {
+        pl.T = kMaxThreads;
+    }
+    pl.slots = static_cast<int>(std::min<int64_t>(ceil_div(vecs, pl.T), INT32_MAX));
+    const int64_t items = pl.warp ? ceil_div(rows, kWarpRows) : rows;
+    const int threads = pl.warp ? 32 * kWarpRows : pl.T;
+    const int64_t sms = sm_count_of_current_device();
+    // forward: a block per row while there are few, else resident blocks that walk rows with the parameters in
+    // registers; backward: as many blocks as are resident together (their partial rows are written and read once)
+    const int64_t resident = sms * std::max(1, (bwd ? 1024 : 2048) / threads);
+    pl.blocks = std::max<int64_t>(1, std::min(items, resident));
+    if (bwd && !pl.held) {
+        pl.parts = std::max<int64_t>(1, std::min<int64_t>(rows, 64));
+    } else {
+        pl.parts = pl.blocks * (pl.warp ? kWarpRows : 1);
+    }
+    return pl;
+}
+
+int check_norm(const ss_norm_dims* dims, uint32_t flags) {
+    if (!dims || (flags & ~static_cast<uint32_t>(SS_BF16 | SS_SYNC_CHECK))) return SS_ERR_INVALID_ARG;
+    if (dims->rows < 0 || dims->cols < 0 || (dims->cols == 0 && dims->rows > 0)) return SS_ERR_INVALID_ARG;
+    if (dims->cols >= (int64_t(1) << 31) || double(dims->rows) * double(dims->cols) > 4.0e18) return SS_ERR_INVALID_ARG;
+    return SS_OK;
+}
+
+size_t norm_ws(const ss_norm_dims* dims, bool bf16) {
+    if (dims->cols == 0 || dims->rows == 0) return 256;
+    const NormPlan pl = norm_plan(dims->rows, dims->cols, bf16, true);
+    return std::max<size_t>(256, static_cast<size_t>(pl.parts) * 2 * static_cast<size_t>(dims->cols) * sizeof(float));
+}
+
+template <typename IO, bool VEC>
+void launch_norm_fwd(const NormParams& p, const NormPlan& pl, cudaStream_t stream) {
+    const unsigned g = static_cast<unsigned>(pl.blocks), t = static_cast<unsigned>(pl.warp ? 32 * kWarpRows : pl.T);
+    if (pl.warp) ss_norm_fwd_kernel<IO, VEC, true, true><<<g, t, 0, stream>>>(p, pl.slots);
+    else if (pl.held) ss_norm_fwd_kernel<IO, VEC, false, true><<<g, t, 0, stream>>>(p, pl.slots);
+    else ss_norm_fwd_kernel<IO, VEC, false, false><<<g, t, 0, stream>>>(p, pl.slots);
+}
+
+template <typename IO, bool VEC>
+void launch_norm_bwd(const NormParams& p, const NormPlan& pl, int sums, cudaStream_t stream) {
+    const unsigned g = static_cast<unsigned>(pl.blocks), t = static_cast<unsigned>(pl.warp ? 32 * kWarpRows : pl.T);
+    if (!pl.held && sums) {   // before the pass that may overwrite dy
+        const dim3 grid(static_cast<unsigned>(ceil_div(p.cols, 256)), static_cast<unsigned>(pl.parts));
+        ss_norm_colsum_kernel<IO><<<grid, 256, 0, stream>>>(p);
+    }
+    if (pl.warp) ss_norm_bwd_kernel<IO, VEC, true, true><<<g, t, 0, stream>>>(p, pl.slots, sums);
+    else if (pl.held) ss_norm_bwd_kernel<IO, VEC, false, true><<<g, t, 0, stream>>>(p, pl.slots, sums);
+    else ss_norm_bwd_kernel<IO, VEC, false, false><<<g, t, 0, stream>>>(p, pl.slots, sums);
+}
+
+int finish(uint32_t flags, cudaStream_t stream) {
+    if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
+    if ((flags & SS_SYNC_CHECK) && cudaStreamSynchronize(stream) != cudaSuccess) return SS_ERR_CUDA;
+    return SS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ss_norm_fwd(const void* x, const float* weight, const float* bias, void* y, float* mean, float* rstd, float eps,
+                uint32_t flags, const ss_norm_dims* dims, const ss_launch* launch) {
+    if (!launch) return SS_ERR_INVALID_ARG;
+    const int rc = check_norm(dims, flags);
+    if (rc != SS_OK) return rc;
+    if (!(eps >= 0.0f)) return SS_ERR_INVALID_ARG;
+    if (dims->rows == 0) return SS_OK;
+    if (!x || !y) return SS_ERR_INVALID_ARG;
+    const void* ptrs[] = {x, weight, bias, y, mean, rstd};
+    for (const void* q : ptrs)
+        if (!aligned16(q)) return SS_ERR_INVALID_ARG;
+    const bool bf16 = flags & SS_BF16;
+    cudaStream_t stream = static_cast<cudaStream_t>(launch->stream);
+    const NormPlan pl = norm_plan(dims->rows, dims->cols, bf16, false);
+    NormParams p{};
+    p.x = x; p.weight = weight; p.bias = bias; p.out = y; p.mean = mean; p.rstd = rstd;
+    p.rows = dims->rows; p.cols = dims->cols; p.eps = eps;
+    if (bf16) {
+        if (pl.vec) launch_norm_fwd<__nv_bfloat16, true>(p, pl, stream);
+        else launch_norm_fwd<__nv_bfloat16, false>(p, pl, stream);
+    } else {
+        if (pl.vec) launch_norm_fwd<float, true>(p, pl, stream);
+        else launch_norm_fwd<float, false>(p, pl, stream);
+    }
+    return finish(flags, stream);
+}
+
+size_t ss_norm_bwd_workspace_bytes(const ss_norm_dims* dims, uint32_t flags) {
+    return check_norm(dims, flags) == SS_OK ? norm_ws(dims, flags & SS_BF16) : 0;
+}
+
+int ss_norm_bwd(const void* dy, const void* x, const float* mean, const float* rstd, const float* weight, void* dx,
+                float* dweight, float* dbias, uint32_t flags, const ss_norm_dims* dims, const ss_launch* launch) {
+    if (!launch) return SS_ERR_INVALID_ARG;
+    const int rc = check_norm(dims, flags);
+    if (rc != SS_OK) return rc;
+    const void* ptrs[] = {dy, x, mean, rstd, weight, dx, dweight, dbias};
+    for (const void* q : ptrs)
+        if (!aligned16(q)) return SS_ERR_INVALID_ARG;
+    const bool bf16 = flags & SS_BF16;
+    cudaStream_t stream = static_cast<cudaStream_t>(launch->stream);
+    const int64_t C = dims->cols;
+    if (dims->rows == 0) {
+        const size_t n = static_cast<size_t>(C) * sizeof(float);
+        if ((dweight && n && cudaMemsetAsync(dweight, 0, n, stream) != cudaSuccess) ||
+            (dbias && n && cudaMemsetAsync(dbias, 0, n, stream) != cudaSuccess))
+            return SS_ERR_CUDA;
+        return SS_OK;
+    }
+    if (!dy || !x || !mean || !rstd || !dx) return SS_ERR_INVALID_ARG;
+    if (!launch->workspace || launch->workspace_bytes < norm_ws(dims, bf16) || !aligned16(launch->workspace))
+        return SS_ERR_WORKSPACE;
+    const NormPlan pl = norm_plan(dims->rows, C, bf16, true);
+    NormParams p{};
+    p.x = x; p.dy = dy; p.weight = weight; p.out = dx;
+    p.mean = const_cast<float*>(mean); p.rstd = const_cast<float*>(rstd);
+    p.part = static_cast<float*>(launch->workspace);
+    p.rows = dims->rows; p.cols = C;
+    const int sums = (dweight || dbias) ? 1 : 0;
+    if (bf16) {
+        if (pl.vec) launch_norm_bwd<__nv_bfloat16, true>(p, pl, sums, stream);
+        else launch_norm_bwd<__nv_bfloat16, false>(p, pl, sums, stream);
+    } else {
+        if (pl.vec) launch_norm_bwd<float, true>(p, pl, sums, stream);
+        else launch_norm_bwd<float, false>(p, pl, sums, stream);
+    }
+    if (sums)
+        ss_norm_fold_kernel<<<static_cast<unsigned>(ceil_div(2 * C, 32)), 256, 0, stream>>>(
+            p.part, static_cast<int>(pl.parts), C, dweight, dbias);
+    return finish(flags, stream);
+}
+
+}  // extern "C"

@@ -15,6 +15,7 @@
 #include "block.cuh"
 #include "bwd.cuh"
 #include "fwd.cuh"
+#include "host.cuh"
 #include "ssd.cuh"
 #include "ssd_tc.cuh"
 #include "step.cuh"
@@ -24,44 +25,9 @@ using namespace selscan;
 namespace {
 
 constexpr int kVersion = 10000;             // 1.0.0
-constexpr size_t kHeaderBytes = 256;        // error word, ticket counter, provisional-item count
 constexpr uint32_t kDefaultPolls = 1u << 21;
-constexpr uint64_t kTmaWaitNs = 2000000000ull;
-constexpr int kMaxDevices = 64;
 constexpr uint32_t kKnownFlags = SS_BF16 | SS_DELTA_SOFTPLUS | SS_SYNC_CHECK | SS_FORCE_GENERAL_A |
                                  SS_TEST_DROP_CARRY;
-
-// Per-device caches below are atomics: host threads may make their first
-// calls concurrently (they store the same values).
-int sm_count_of_current_device() {
-    static std::atomic<int> cache[kMaxDevices];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 148;
-    if (dev < kMaxDevices) {
-        const int c = cache[dev].load(std::memory_order_relaxed);
-        if (c > 0) return c;
-    }
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-    if (dev < kMaxDevices) cache[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
-
-// Raises a kernel's dynamic shared-memory limit to `smem` once per device.
-template <typename Kern>
-int set_smem_limit(Kern kern, size_t smem, std::atomic<bool> (&done)[kMaxDevices], int dev) {
-    const bool cached = dev >= 0 && dev < kMaxDevices;
-    if (cached && done[dev].load(std::memory_order_acquire)) return SS_OK;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-        cudaSuccess)
-        return SS_ERR_CUDA;
-    if (cached) done[dev].store(true, std::memory_order_release);
-    return SS_OK;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Forward-kernel variants.  Wide: one resident CTA per SM (two warps per
 // scheduler), a 2-stage tile ring, groups of 4 steps with whole tiles
@@ -151,19 +117,6 @@ Plan make_plan(const ss_dims* dims, uint32_t flags, int32_t chunk_req) {
 }
 
 // ------------------------------------------------------------ TMA descriptors
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
 // 3-D map over a [batch, rows, inner] row-major tensor, box [1, box_rows, box_inner].
 bool make_map(CUtensorMap* m, const void* base, bool bf16, uint64_t inner, uint64_t rows, uint64_t batch,
               uint32_t box_inner, uint32_t box_rows) {
@@ -243,19 +196,6 @@ SsdLayout ssd_layout(const ss_ssd_dims* d) {
 #ifndef SELSCAN_SSD_MMA_SYNC
 #define SELSCAN_SSD_MMA_SYNC 0
 #endif
-
-// Tensor map of a row-major tensor of `rank` dimensions (innermost first,
-// byte strides of dimensions 1..rank-1), bf16, 128-byte swizzle, box `box`.
-bool make_map_sw128(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                    const cuuint32_t* box) {
-    auto enc = tensor_map_encoder();
-    if (!enc) return false;
-    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base),
-                           dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
 
 // The tcgen05 scan (d_state 128): segments of whole 128-step chunks chosen
 // like launch_ssd's (one resident CTA per SM; state pass charged half a
@@ -547,8 +487,10 @@ cublasHandle_t cublas_handle() {
 
 // Row-major Y[M, N] = X[M, K] · W[N, K]ᵀ in bf16 with fp32 accumulation (a
 // column-major cuBLAS call computing Yᵀ = W · Xᵀ).
-bool gemm_bf16(cublasHandle_t h, const void* X, const void* W, void* Y, int64_t M, int64_t N, int64_t K) {
-    const float alpha = 1.0f, beta = 0.0f;
+// With `add`, the product is added to what Y holds before the rounding to bf16.
+bool gemm_bf16(cublasHandle_t h, const void* X, const void* W, void* Y, int64_t M, int64_t N, int64_t K,
+               bool add = false) {
+    const float alpha = 1.0f, beta = add ? 1.0f : 0.0f;
     return cublasGemmEx(h, CUBLAS_OP_T, CUBLAS_OP_N, static_cast<int>(N), static_cast<int>(M), static_cast<int>(K),
                         &alpha, W, CUDA_R_16BF, static_cast<int>(K), X, CUDA_R_16BF, static_cast<int>(K), &beta, Y,
                         CUDA_R_16BF, static_cast<int>(N), CUBLAS_COMPUTE_32F, CUBLAS_GEMM_DEFAULT) ==
@@ -1129,8 +1071,9 @@ size_t ss_block_scratch_bytes(const ss_block_weights* w, int64_t batch, int64_t 
     return block_plan(w, batch, seqlen, &pl) ? pl.total : 0;
 }
 
-int ss_block_fwd(const void* hidden, void* out, const ss_block_weights* w, int64_t batch, int64_t seqlen,
-                 void* scratch, size_t scratch_bytes, void* stream_v) {
+// residual: non-null adds these rows to the block's output (ss_block_fwd_prenorm).
+static int block_impl(const void* hidden, const void* residual, void* out, const ss_block_weights* w, int64_t batch,
+                      int64_t seqlen, void* scratch, size_t scratch_bytes, void* stream_v) {
     BlockPlan pl{};
     if (!block_plan(w, batch, seqlen, &pl)) return SS_ERR_INVALID_ARG;
     const int64_t M = batch * seqlen, di = w->d_inner, dm = w->d_model, rk = w->dt_rank;
@@ -1180,8 +1123,52 @@ int ss_block_fwd(const void* hidden, void* out, const ss_block_weights* w, int64
                     &launch);
     if (rc != SS_OK) return rc;
     // out_proj
-    if (!gemm_bf16(h, y, w->out_proj, out, M, dm, di)) return SS_ERR_CUDA;
+    if (residual && cudaMemcpyAsync(out, residual, static_cast<size_t>(M * dm) * 2, cudaMemcpyDeviceToDevice, stream) !=
+                        cudaSuccess)
+        return SS_ERR_CUDA;
+    if (!gemm_bf16(h, y, w->out_proj, out, M, dm, di, residual != nullptr)) return SS_ERR_CUDA;
     return SS_OK;
+}
+
+int ss_block_fwd(const void* hidden, void* out, const ss_block_weights* w, int64_t batch, int64_t seqlen,
+                 void* scratch, size_t scratch_bytes, void* stream) {
+    return block_impl(hidden, nullptr, out, w, batch, seqlen, scratch, scratch_bytes, stream);
+}
+
+// The normed rows lie in front of the block's own scratch.
+static size_t prenorm_bytes(const ss_block_weights* w, int64_t batch, int64_t seqlen) {
+    return (static_cast<size_t>(batch * seqlen) * static_cast<size_t>(w->d_model) * 2 + 255) / 256 * 256;
+}
+
+size_t ss_block_prenorm_scratch_bytes(const ss_block_weights* w, int64_t batch, int64_t seqlen) {
+    const size_t block = ss_block_scratch_bytes(w, batch, seqlen);
+    return block ? block + prenorm_bytes(w, batch, seqlen) : 0;
+}
+
+int ss_block_fwd_prenorm(const void* hidden, const float* norm_weight, const float* norm_bias, float eps, void* out,
+                         const ss_block_weights* w, int64_t batch, int64_t seqlen, void* scratch,
+                         size_t scratch_bytes, void* stream) {
+    const size_t need = ss_block_prenorm_scratch_bytes(w, batch, seqlen);
+    if (!need) return SS_ERR_INVALID_ARG;
+    const int64_t M = batch * seqlen, dm = w->d_model;
+    if (M == 0) return SS_OK;
+    const size_t bytes = static_cast<size_t>(M) * static_cast<size_t>(dm) * 2;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(hidden), b = reinterpret_cast<uintptr_t>(out);
+    if (!hidden || !out || (a < b + bytes && b < a + bytes)) return SS_ERR_INVALID_ARG;
+    if (!scratch || scratch_bytes < need || !aligned16(scratch)) return SS_ERR_WORKSPACE;
+    const void* ptrs[] = {w->in_proj_x, w->in_proj_z, w->conv_w, w->x_proj_dt, w->x_proj_B, w->x_proj_C,
+                          w->dt_proj,   w->dt_bias,   w->A,      w->out_proj};
+    for (const void* q : ptrs)   // before the norm is launched: a refused call launches nothing
+        if (!q || !aligned16(q)) return SS_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(w->conv_b) || !aligned16(w->D)) return SS_ERR_INVALID_ARG;
+    const ss_norm_dims dims{M, dm};
+    ss_launch launch{};
+    launch.stream = stream;
+    int rc = ss_norm_fwd(hidden, norm_weight, norm_bias, scratch, nullptr, nullptr, eps, SS_BF16, &dims, &launch);
+    if (rc != SS_OK) return rc;
+    const size_t off = prenorm_bytes(w, batch, seqlen);
+    return block_impl(scratch, hidden, out, w, batch, seqlen, static_cast<unsigned char*>(scratch) + off,
+                      scratch_bytes - off, stream);
 }
 
 int ss_fwd_noalloc(const void* u, const void* delta, const float* delta_bias, const float* A, const void* B,
