@@ -2,6 +2,7 @@
 // workspace layout, choice of kernel and launches.
 #include "common.cuh"
 #include "gdr_rec.cuh"
+#include "gdr_tc.cuh"
 #include "host.cuh"
 
 using namespace selscan;
@@ -58,6 +59,49 @@ int run_rec(const GdrParams& p, const ss_gdr_dims* d, uint32_t flags, cudaStream
     return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
+// bf16 sequences of at least this many tokens run in chunks.
+constexpr int64_t kChunkedFrom = 16;
+
+// 4-D map of a [batch, L, heads, d] bf16 tensor, boxes of `cols` x 64 tokens of one head.
+bool head_map(CUtensorMap* m, const void* base, int64_t batch, int64_t L, int64_t heads, int64_t d, int64_t cols,
+              CUtensorMapSwizzle swizzle) {
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(L),
+                                static_cast<cuuint64_t>(batch)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d * 2), static_cast<cuuint64_t>(heads * d * 2),
+                                   static_cast<cuuint64_t>(L * heads * d * 2)};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(cols), 1, static_cast<cuuint32_t>(gdr::kC), 1};
+    return make_map_bf16(m, base, 4, dims, strides, box, swizzle);
+}
+
+template <int DK>
+int launch_tc(const gdr::Params& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+              cudaStream_t stream) {
+    auto kern = gdr::ss_gdr_tc_kernel<DK>;
+    static std::atomic<bool> attr[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || set_smem_limit(kern, gdr::kSmemBytes, attr, dev) != SS_OK)
+        return SS_ERR_CUDA;
+    kern<<<static_cast<unsigned>(p.g.batch) * static_cast<unsigned>(p.g.H), gdr::kThreads, gdr::kSmemBytes, stream>>>(
+        p, mq, mk, mv);
+    return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+int run_tc(const GdrParams& g, const ss_gdr_dims* d, uint32_t flags, const ss_launch* launch, cudaStream_t stream) {
+    gdr::Params p{};
+    p.g = g;
+    p.status = static_cast<uint32_t*>(launch->workspace);
+    p.dv = static_cast<int>(d->d_v);
+    p.test_drop = (flags & SS_TEST_DROP_CARRY) ? 1 : 0;
+    p.wait_ns = launch->timeout_iters ? static_cast<uint64_t>(launch->timeout_iters) * 1000ull : kTmaWaitNs;
+    p.drain_ns = kTmaWaitNs;
+    CUtensorMap mq, mk, mv;
+    if (!head_map(&mq, g.q, d->batch, d->seqlen, d->nheads_k, d->d_k, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !head_map(&mk, g.k, d->batch, d->seqlen, d->nheads_k, d->d_k, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !head_map(&mv, g.v, d->batch, d->seqlen, d->nheads, d->d_v, d->d_v, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return SS_ERR_CUDA;
+    return d->d_k == 128 ? launch_tc<128>(p, mq, mk, mv, stream) : launch_tc<64>(p, mq, mk, mv, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -85,7 +129,8 @@ int ss_gdr_fwd(const void* q, const void* k, const void* v, const void* dt, cons
     if (cudaMemsetAsync(launch->workspace, 0, sizeof(uint32_t), stream) != cudaSuccess) return SS_ERR_CUDA;
     GdrParams p = gdr_params(q, k, v, dt, dt_bias, A, beta, scale, flags, dims, L);
     p.h_init = h_init; p.seqlens = seqlens; p.y = y; p.final_state = final_state;
-    rc = run_rec(p, dims, flags, stream);
+    rc = (flags & SS_BF16) && L >= kChunkedFrom ? run_tc(p, dims, flags, launch, stream)
+                                                : run_rec(p, dims, flags, stream);
     if (rc != SS_OK) return rc;
     return (flags & SS_SYNC_CHECK) ? ss_check(launch) : SS_OK;
 }

@@ -279,8 +279,8 @@ int launch_ssd_tc(const tc::Params& base_p, const SsdParams& fold_p, const void*
                                   static_cast<cuuint64_t>(batch)};
         const cuuint64_t sb[2] = {static_cast<cuuint64_t>(N * 2), static_cast<cuuint64_t>(L * N * 2)};
         const cuuint32_t bb[3] = {64, static_cast<cuuint32_t>(tc::kQ), 1};
-        if (!make_map_sw128(&mx, x, 4, dx, sx, bx) || !make_map_sw128(&mb, B, 3, db, sb, bb) ||
-            !make_map_sw128(&mc, C, 3, db, sb, bb) || !make_map_sw128(&my, p.y, 4, dx, sx, bx))
+        if (!make_map_bf16(&mx, x, 4, dx, sx, bx) || !make_map_bf16(&mb, B, 3, db, sb, bb) ||
+            !make_map_bf16(&mc, C, 3, db, sb, bb) || !make_map_bf16(&my, p.y, 4, dx, sx, bx))
             return SS_ERR_CUDA;
     }
     if (n_cut > 0) {

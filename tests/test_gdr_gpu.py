@@ -180,3 +180,15 @@ def test_captured_and_replayed_and_other_stream(L):
                   stream=streams[0])
     streams[0].synchronize()
     assert torch.equal(y, want[0][0]) and torch.equal(S, want[0][1])
+
+
+def test_bounded_wait_reports_timeout_and_context_survives():
+    """A hand-over that is never signalled (SS_TEST_DROP_CARRY: the first block's first product) runs the bounded
+    waits out: the call reports SS_ERR_TIMEOUT, and the next call on the same context is right."""
+    x = gdr_inputs(2, 300, 2, 2, 128, 128, seed=5)
+    ws = torch.zeros(4096, dtype=torch.uint8, device="cuda:0")
+    ss.ss_gdr_fwd(*call_args(x), dt_bias=x["dt_bias"], workspace=ws, timeout_iters=200,
+                  extra_flags=ss.SS_TEST_DROP_CARRY)
+    assert ss.ss_check(ws) == ss.SS_ERR_TIMEOUT
+    check(x, 300, BF, workspace=ws)
+    assert ss.ss_check(ws) == ss.SS_OK
