@@ -75,14 +75,14 @@ bool head_map(CUtensorMap* m, const void* base, int64_t batch, int64_t L, int64_
 
 template <int DK>
 int launch_tc(const gdr::Params& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-              cudaStream_t stream) {
+              const CUtensorMap& my, cudaStream_t stream) {
     auto kern = gdr::ss_gdr_tc_kernel<DK>;
     static std::atomic<bool> attr[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || set_smem_limit(kern, gdr::kSmemBytes, attr, dev) != SS_OK)
         return SS_ERR_CUDA;
     kern<<<static_cast<unsigned>(p.g.batch) * static_cast<unsigned>(p.g.H), gdr::kThreads, gdr::kSmemBytes, stream>>>(
-        p, mq, mk, mv);
+        p, mq, mk, mv, my);
     return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
@@ -94,12 +94,13 @@ int run_tc(const GdrParams& g, const ss_gdr_dims* d, uint32_t flags, const ss_la
     p.test_drop = (flags & SS_TEST_DROP_CARRY) ? 1 : 0;
     p.wait_ns = launch->timeout_iters ? static_cast<uint64_t>(launch->timeout_iters) * 1000ull : kTmaWaitNs;
     p.drain_ns = kTmaWaitNs;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, my;
     if (!head_map(&mq, g.q, d->batch, d->seqlen, d->nheads_k, d->d_k, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !head_map(&mk, g.k, d->batch, d->seqlen, d->nheads_k, d->d_k, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !head_map(&mv, g.v, d->batch, d->seqlen, d->nheads, d->d_v, d->d_v, CU_TENSOR_MAP_SWIZZLE_NONE))
+        !head_map(&mv, g.v, d->batch, d->seqlen, d->nheads, d->d_v, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !head_map(&my, g.y, d->batch, d->seqlen, d->nheads, d->d_v, d->d_v, CU_TENSOR_MAP_SWIZZLE_NONE))
         return SS_ERR_CUDA;
-    return d->d_k == 128 ? launch_tc<128>(p, mq, mk, mv, stream) : launch_tc<64>(p, mq, mk, mv, stream);
+    return d->d_k == 128 ? launch_tc<128>(p, mq, mk, mv, my, stream) : launch_tc<64>(p, mq, mk, mv, my, stream);
 }
 
 }  // namespace

@@ -13,22 +13,26 @@
 // element-wise steps.
 //
 // The products run transposed: the 128 TMEM lanes are the rows v of the state, and the columns are tokens or keys.
-//   KS  [v, i] = S Kᵀ        A: S (TMEM),  B: K tile, K-major
-//   E   [v, i] = X Tᵀ        A: X = (V - diag KS)ᵀ (TMEM),  B: T tile, K-major; T's zero blocks are left out
-//   dS  [v, k] = W K         A: W = scaled E (TMEM),  B: K tile, MN-major
-//   QS  [v, i] = S Qᵀ,  PV [v, i] = (β E) Pᵀ    off the chain, under the element-wise steps
+//   KS, QS [v, i] = S Kᵀ, S Qᵀ      A: S (TMEM),  B: K and Q tiles in one, K-major
+//   E   [v, i] = Vᵀ Tᵀ + X Tᵀ       A: V tile, MN-major; X = -KS diag(e^G / |k|) (TMEM),  B: T tile, K-major
+//   dS  [v, k] = W K                A: W = E diag(β e^{G_end - G} / |k|) (TMEM),  B: K tile, MN-major
+//   Yᵀ  [v, i] = QS diag(scale e^G / |q|) + E (P β)ᵀ    off the chain, under the element-wise steps
 // so that the state, the right hand side and the corrections go from registers to TMEM and never through shared
-// memory, a thread owning one row v (two threads to a row, each with half its columns).
+// memory, a thread owning one row v (four threads to a row, each with a quarter of the columns).  X is written over
+// KS, E's terms over E, S's terms over dS, by the thread that read them, which is what makes it fit in TMEM.
+// An MMA of 128 x N x 16 takes about 64 cycles for every N up to 128 (measured here), so operands are put side by
+// side to N = 128 where they share A: K with Q, and T's two terms, whose two halves of E the reader adds.
 //
 // Precision: q, k, v are bf16 values as given and unit lengths are factors of rows and columns, so they enter
-// exactly.  fp32 operands -- S, X, T, W, P, β E -- enter as two bf16 terms, hi + lo (the product of two such pairs
-// without lo·lo): 16 bits, an error near 2^-18 a product.  One term for P and β E would do for y's own rounding,
-// but not where keys repeat: the corrections are then differences of values, and P (β E) cancels most of them.
+// exactly.  fp32 operands -- S, X, T, W, P, E -- enter as two bf16 terms, hi + lo (the product of two such pairs
+// without lo·lo): 16 bits, an error near 2^-18 a product.  One term for P and E would do for y's own rounding,
+// but not where keys repeat: the corrections are then differences of values, and P E cancels most of them.
 // Accumulation is fp32, the state is kept in fp32 registers.
 //
-// Warps: 0..7 state (above); 8..11 prepare (per-token scalars, K Kᵀ and Q Kᵀ, the inverse T: up to two chunks ahead);
-// 12 issues the chain's MMAs; 13 the TMA loads (three tiles of K, Q, V in flight).  They hand over through
-// mbarriers.  Every wait is bounded: one that runs out records SS_ERR_TIMEOUT and the CTA winds down.
+// Warps: 0..15 state (above); 16..23 two groups that prepare (per-token scalars, K Kᵀ and Q Kᵀ, the inverse T), one
+// the even and one the odd chunks, up to two chunks ahead of the chain; 24 issues the chain's MMAs; 25 the TMA
+// loads (three tiles of K and Q, one of V in flight); 26 stores y.  They hand over through mbarriers.  Every wait
+// is bounded: one that runs out records SS_ERR_TIMEOUT and the CTA winds down.
 #pragma once
 
 #include "../../include/selscan.h"
@@ -56,45 +60,57 @@ using tc::umma_commit;
 
 constexpr int kC = 64;                 // tokens of a chunk
 constexpr int kStages = 3;             // K, Q tiles in flight (they are prepared ahead)
-constexpr int kVStages = 2;            // V tiles in flight
-constexpr int kStateWarps = 8, kPrepWarps = 4;
-constexpr int kMmaWarp = kStateWarps + kPrepWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kLoadWarp + 1);
+constexpr int kVStages = 1;            // V tiles in flight (read at a chunk's start alone)
+constexpr int kParts = 4;              // threads to a row of the state
+constexpr int kStateWarps = 4 * kParts, kGroupWarps = 4;
+constexpr int kPrepWarp = kStateWarps;                       // two groups
+constexpr int kMmaWarp = kPrepWarp + 2 * kGroupWarps, kLoadWarp = kMmaWarp + 1, kStoreWarp = kMmaWarp + 2;
+constexpr int kThreads = 32 * (kStoreWarp + 1);
+constexpr int kTok = kC / kParts;      // tokens of a state thread
 
-// TMEM columns.  S: the state's bf16 terms (hi and lo of each half of the keys, d_k columns in all); dS is
-// accumulated over them once they have been read.
-constexpr uint32_t kColS = 0, kColKS = 128, kColQS = 192, kColPV = 256, kColX = 320, kColVn = 384, kColGram = 448;
+// TMEM columns.  A: KS, then X's terms over it, then W's; B: E in two halves, then its terms over the first; S: the
+// state's terms (of each 16 keys, hi then lo), then dS over them.
+constexpr uint32_t kColS = 0, kColA = 128, kColQS = 192, kColB = 256, kColY = 384, kColGram = 448;
 constexpr uint32_t kTmemCols = 512;
 
 // Shared memory: byte offsets from a 1024-aligned base.
 constexpr uint32_t kTile = 8192;                       // 64 rows of 128 bytes, 128-byte swizzle
 constexpr uint32_t kStageBytes = 4 * kTile;            // [K 0][Q 0][K 1][Q 1]
-constexpr uint32_t kOffV = kStages * kStageBytes;      // V [64][d_v], not swizzled
+constexpr uint32_t kOffV = kStages * kStageBytes;      // [V 0][V 1]
 constexpr uint32_t kVBytes = 2 * kTile;
-constexpr uint32_t kOffPrep = kOffV + kVStages * kVBytes;   // two buffers of [T hi][T lo][P hi][P lo]
-constexpr uint32_t kPrepBytes = 4 * kTile;
-constexpr uint32_t kOffA = kOffPrep + 2 * kPrepBytes;  // A', then T, fp32 [64][68]
-constexpr int kPitchA = 68;
-constexpr uint32_t kOffXs = kOffA + kC * kPitchA * 4;  // block products, fp32 [32][36]
+constexpr uint32_t kOffPrep = kOffV + kVStages * kVBytes;   // two buffers of [T hi][T lo][P hi][P lo]; while T is
+constexpr uint32_t kPrepBytes = 4 * kTile;                  // computed, fp32 [64][64] in the place of its terms
+constexpr uint32_t kOffY = kOffPrep + 2 * kPrepBytes;  // y [64][d_v] for the store
+constexpr uint32_t kOffXs = kOffY + 2 * kTile;         // block products of each group, fp32 [32][36]
 constexpr int kPitchX = 36;
-constexpr uint32_t kOffScal = kOffXs + 32 * kPitchX * 4;
-// two buffers of per-token factors, then what only the prepare warps use
-constexpr uint32_t kScalBytes = (4 * kC + 4) * 4;
-constexpr uint32_t kOffLocal = kOffScal + 2 * kScalBytes;      // G hi, G lo, |k|^-1, β, 64-bit prefix
+constexpr uint32_t kXsBytes = 32 * kPitchX * 4;
+constexpr uint32_t kOffScal = kOffXs + 2 * kXsBytes;
+constexpr int kScals = 4;              // buffers of per-token factors: chunk c's are written once K and Q of chunk c
+                                       // landed, in the place of chunk c - 3's, whose MMAs are done: its successor
+                                       // in the ring, chunk c - 4, was read before those were issued
+constexpr uint32_t kScalBytes = (3 * kC + 4) * 4;
+constexpr uint32_t kOffLocal = kOffScal + kScals * kScalBytes;   // what only a prepare group uses
 constexpr uint32_t kLocalBytes = 4 * kC * 4 + kC * 8;
-constexpr uint32_t kOffBar = kOffLocal + kLocalBytes;
-constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;
+constexpr uint32_t kOffBar = kOffLocal + 2 * kLocalBytes;
+constexpr uint32_t kSmemBytes = kOffBar + 512 + 1024;
 static_assert(kOffScal % 16 == 0 && kOffLocal % 16 == 0 && kOffBar % 16 == 0, "aligned regions");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 struct alignas(16) Scal {   // one chunk's factors, as the state warps read them
-    float ek[kC];      // e^{G_i} / |k_i|
-    float be[kC];      // β_i
-    float wk[kC];      // β_i e^{G_end - G_i} / |k_i|
-    float qe[kC];      // scale e^{G_i} / |q_i|
-    float end[4];      // e^{G_end}
+    float ek[kC];           // -e^{G_i} / |k_i|
+    float wk[kC];           // β_i e^{G_end - G_i} / |k_i|
+    float qe[kC];           // scale e^{G_i} / |q_i|
+    float end[4];           // e^{G_end}
 };
 static_assert(sizeof(Scal) == kScalBytes, "layout");
+
+struct alignas(16) Local {  // one chunk's factors, for its prepare group
+    float gh[kC], gl[kC];   // log2 of the decay from the chunk's start, as a pair
+    float cb[kC];           // β_j / |k_j|
+    float cf[kC];           // β_j / |k_j| e^{G_31 - G_j}, j < 32
+    double G[kC];           // prefix sums over 32 tokens
+};
+static_assert(sizeof(Local) == kLocalBytes, "layout");
 
 struct Params {
     GdrParams g;
@@ -104,9 +120,9 @@ struct Params {
     uint64_t wait_ns, drain_ns;
 };
 
-// kind::f16, bf16 x bf16 -> fp32, M = 128; bmn: B is MN-major.
-__host__ __device__ constexpr uint32_t idesc(uint32_t n, bool bmn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (bmn ? 1u << 16 : 0u) | ((n >> 3) << 17) | (8u << 24);
+// kind::f16, bf16 x bf16 -> fp32, M = 128; bmn, amn: B, A is MN-major.
+__host__ __device__ constexpr uint32_t idesc(uint32_t n, bool bmn, bool amn = false) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (amn ? 1u << 15 : 0u) | (bmn ? 1u << 16 : 0u) | ((n >> 3) << 17) | (8u << 24);
 }
 
 // D[tmem] (+)= A[tmem] · B[smem descriptor]; issued by one thread.
@@ -119,162 +135,233 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint
         ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc), "r"(z), "r"(z), "r"(z), "r"(z)
         : "memory");
 }
-// 16 columns of this thread's lane, written; complete after tmem_wait_st().
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+// 8 columns of this thread's lane, written; complete after tmem_wait_st().
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// 32 values as 16 words of bf16 pairs: hi, and lo = what hi leaves.
-__device__ __forceinline__ void split32(const float (&v)[32], uint32_t (&hi)[16], uint32_t (&lo)[16]) {
+// 16 columns of this thread's lane as pairs.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, f32x2 (&v)[8]) {
+    float t[16];
+    tc::tmem_ld16(taddr, t);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        hi[e] = pk(v[2 * e], v[2 * e + 1]);
-        lo[e] = pk(v[2 * e] - lo_f(hi[e]), v[2 * e + 1] - hi_f(hi[e]));
+    for (int e = 0; e < 8; ++e) v[e] = pk2(t[2 * e], t[2 * e + 1]);
+}
+
+// Two such ranges, one wait.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t a0, uint32_t a1, f32x2 (&v)[8], f32x2 (&w)[8]) {
+    float t[32];
+    tc::tmem_ld16x2(a0, a1, t);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        v[e] = pk2(t[2 * e], t[2 * e + 1]);
+        w[e] = pk2(t[16 + 2 * e], t[17 + 2 * e]);
+    }
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const f32x2 (&v)[8]) {
+    uint32_t r[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            r[2 * e] = __float_as_uint(v[4 * h + e].x);
+            r[2 * e + 1] = __float_as_uint(v[4 * h + e].y);
+        }
+        tmem_st8(taddr + 8 * h, r);
     }
 }
 
-constexpr int kPrepBar = 1;   // named barrier of the 128 prepare threads
-__device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool prep_any(bool pred) {
+// A pair as a word of bf16 values, hi, and a word of what hi leaves, lo.
+__device__ __forceinline__ void split2(f32x2 v, uint32_t& hi, uint32_t& lo) {
+    hi = pk(v.x, v.y);
+    const f32x2 r = fma2(pk2(lo_f(hi), hi_f(hi)), pk2(-1.0f, -1.0f), v);
+    lo = pk(r.x, r.y);
+}
+// 16 values' terms into 16 columns: hi in the first 8, lo in the others.
+__device__ __forceinline__ void store_terms(uint32_t taddr, const f32x2* v) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split2(v[e], hi[e], lo[e]);
+    tmem_st8(taddr, hi);
+    tmem_st8(taddr + 8, lo);
+}
+// v *= f, 16 consecutive factors of shared memory (16-byte aligned).
+__device__ __forceinline__ void scale16(f32x2 (&v)[8], const float* f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float4 q = *reinterpret_cast<const float4*>(f + 4 * e);
+        v[2 * e] = mul2(v[2 * e], pk2(q.x, q.y));
+        v[2 * e + 1] = mul2(v[2 * e + 1], pk2(q.z, q.w));
+    }
+}
+
+// Named barrier of a prepare group (128 threads).
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool group_any(int id, bool pred) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 1, 128, p;\n\t"
+        "bar.red.or.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(pred ? 1u : 0u)
+        : "r"(pred ? 1u : 0u), "r"(id)
         : "memory");
     return r != 0;
 }
 
 struct Bars {
     uint64_t full[kStages];    // K and Q of a stage landed
-    uint64_t v_full[kVStages], v_empty[kVStages];   // V landed; read (8 warps)
     uint64_t empty[kStages];   // the chunk's last MMA is done with the stage
+    uint64_t v_full[kVStages], v_empty[kVStages];   // V landed; its product done
     uint64_t prep_full[2];     // T, P and the factors of a buffer written (4 warps)
-    uint64_t prep_empty[2];    // its last MMA done (1) and its factors read (8 warps)
-    uint64_t gram;             // K Kᵀ and Q Kᵀ done
+    uint64_t t_empty[2], p_empty[2];   // a buffer's T, P read by their last MMA
+    uint64_t gram, gram_free;  // K Kᵀ and Q Kᵀ of a chunk done; read (4 warps)
     uint64_t ks, e, ds, pv;    // the chain's products done
-    uint64_t qs;               // S's terms read by KS and QS
-    uint64_t s_ready;          // S's terms written (8 warps)
-    uint64_t x_ready, w_ready; // X, W written (8 warps)
-    uint64_t o_free;           // QS and PV read (8 warps)
-    uint64_t fin[2];           // wind-down
+    uint64_t s_ready;          // S's terms written (state warps)
+    uint64_t x_ready, w_ready; // X's terms; W's and E's, and Y's first part, written (state warps)
+    uint64_t y_full, y_free;   // y staged (state warps); stored (1)
+    uint64_t fin[3];           // wind-down
     uint32_t tmem;
 };
-static_assert(sizeof(Bars) <= 256, "barrier region");
+static_assert(sizeof(Bars) <= 512, "barrier region");
 
-// Sum over four values' products of a 16-byte word of bf16 pairs with itself.
-__device__ __forceinline__ float sq8(uint4 w, float s) {
-    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s = fmaf(lo_f(a[e]), lo_f(a[e]), fmaf(hi_f(a[e]), hi_f(a[e]), s));
-    return s;
+// Float offset of element (i, j) of the fp32 [64][64] matrix: 16-byte quads permuted within a row, so that the same
+// quad of eight consecutive rows lies in eight different banks.
+__device__ __forceinline__ int at(int i, int j) { return i * kC + ((((j >> 2) ^ (i & 7)) << 2) | (j & 3)); }
+
+// acc += u · row of four (packed), u a scalar.
+__device__ __forceinline__ void axpy4(f32x2 (&acc)[2], float u, float4 w) {
+    acc[0] = fma2(pk2(u, u), pk2(w.x, w.y), acc[0]);
+    acc[1] = fma2(pk2(u, u), pk2(w.z, w.w), acc[1]);
 }
+__device__ __forceinline__ float4 quad(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-// (I + A')^-1 of the strictly lower triangular A' in `a` ([64][kPitchA]), in place, by the 128 prepare threads:
-// the four 16-blocks on the diagonal column by column, then T21 = -T22 A21 T11 of the 32-blocks and of the whole.
-// fp32 throughout; about 75 000 multiply-adds.
-__device__ __forceinline__ void invert64(float* a, float* xs, int pt) {
-    const int pw = pt >> 5, lane = pt & 31;
+// (I + A')^-1 of the strictly lower triangular A' in `a`, in place, by a prepare group: the four 16-blocks on the
+// diagonal row by row (x (I + A') = a unit row, from its last entry back: a subtracted row of A' per step, with no
+// sum to wait for), then T21 = -T22 A21 T11 of the two 32-blocks and of the whole.  fp32 throughout.  The 32 x 32
+// block above the diagonal is neither read nor written.
+__device__ __forceinline__ void invert64(float* a, float* xs, int pt, int id) {
     {
-        float* d = a + 16 * pw * kPitchA + 16 * pw;
-        const int j = lane & 15;
-        float t[16];
+        const int o = 16 * (pt >> 5), i = pt & 15;
+        float x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float s0 = 0.0f, s1 = 0.0f;
+        for (int j = 0; j < 16; ++j) x[j] = i == j ? 1.0f : 0.0f;
 #pragma unroll
-            for (int l = 0; l < i; l += 4) {
-                const float4 r = *reinterpret_cast<const float4*>(d + i * kPitchA + l);
-                s0 = fmaf(r.x, t[l], s0);
-                if (l + 1 < i) s1 = fmaf(r.y, t[l + 1], s1);
-                if (l + 2 < i) s0 = fmaf(r.z, t[l + 2], s0);
-                if (l + 3 < i) s1 = fmaf(r.w, t[l + 3], s1);
+        for (int l = 15; l > 0; --l) {
+#pragma unroll
+            for (int j = 0; j < l; j += 4) {   // (A' is zero from its diagonal on)
+                const float4 r = quad(a + at(o + l, o + j));
+                f32x2 s[2] = {pk2(x[j], x[j + 1]), pk2(x[j + 2], x[j + 3])};
+                axpy4(s, -x[l], r);
+                x[j] = s[0].x;
+                if (j + 1 < l) x[j + 1] = s[0].y;
+                if (j + 2 < l) x[j + 2] = s[1].x;
+                if (j + 3 < l) x[j + 3] = s[1].y;
             }
-            t[i] = (i == j ? 1.0f : 0.0f) - (s0 + s1);
         }
         __syncwarp();
-        if (lane < 16) {
+        if ((pt & 31) < 16) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) d[i * kPitchA + j] = t[i];
+            for (int j = 0; j < 16; j += 4)
+                *reinterpret_cast<float4*>(a + at(o + i, o + j)) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
         }
     }
-    prep_sync();
-    {   // 16-blocks: threads 64 m .. 64 m + 63 on the 32-block m, four neighbouring columns each
-        const int m = pt >> 6, r = (pt & 63) >> 2, c = (pt & 3) * 4;
-        float* d = a + 32 * m * kPitchA + 32 * m;
-        float* x = xs + m * 16 * kPitchX;
-        auto product = [&](const float* p, int pp, const float* q, int pq) {
-            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    group_sync(id);
+    {   // 16-blocks: threads 64 m .. 64 m + 63 on the 32-block m, a quad of a row each
+        const int m = pt >> 6, r = (pt & 63) >> 2, c = (pt & 3) * 4, o = 32 * m;
+        float* x = xs + m * 16 * kPitchX + c;
+        const float* ur = a + (o + 16 + r) * kC;
+        const float* wc = a + o * kC;
+        int oc[8];   // where this thread's quad of columns lies in the rows 0 .. 7 (mod 8)
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-                const float4 u = *reinterpret_cast<const float4*>(p + r * pp + k);
-                const float uu[4] = {u.x, u.y, u.z, u.w};
+        for (int e = 0; e < 8; ++e) oc[e] = (((o + c) >> 2) ^ e) << 2;
+        const int r7 = r & 7;
+        f32x2 s[2] = {pk2(0.0f, 0.0f), pk2(0.0f, 0.0f)};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 w = *reinterpret_cast<const float4*>(q + (k + e) * pq + c);
-                    s.x = fmaf(uu[e], w.x, s.x);
-                    s.y = fmaf(uu[e], w.y, s.y);
-                    s.z = fmaf(uu[e], w.z, s.z);
-                    s.w = fmaf(uu[e], w.w, s.w);
-                }
-            }
-            return s;
-        };
-        const float4 s = product(d + 16 * kPitchA, kPitchA, d, kPitchA);
-        *reinterpret_cast<float4*>(x + r * kPitchX + c) = make_float4(-s.x, -s.y, -s.z, -s.w);
-        prep_sync();
-        const float4 t = product(d + 16 * kPitchA + 16, kPitchA, x, kPitchX);
-        *reinterpret_cast<float4*>(d + (16 + r) * kPitchA + c) = t;
+        for (int k = 0; k < 16; k += 4) {
+            const float4 u = quad(ur + ((((o + k) >> 2) ^ r7) << 2));
+            const float uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) axpy4(s, uu[e], quad(wc + (k + e) * kC + oc[(k + e) & 7]));
+        }
+        *reinterpret_cast<float4*>(x + r * kPitchX) = make_float4(-s[0].x, -s[0].y, -s[1].x, -s[1].y);
+        group_sync(id);
+        s[0] = s[1] = pk2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+            const float4 u = quad(ur + ((((o + 16 + k) >> 2) ^ r7) << 2));
+            const float uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) axpy4(s, uu[e], quad(x + (k + e) * kPitchX));
+        }
+        *reinterpret_cast<float4*>(a + at(o + 16 + r, o + c)) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
     }
-    prep_sync();
-    {   // 32-blocks: two rows of four columns each
-        const int r = (pt >> 3) * 2, c = (pt & 7) * 4;
-        auto product = [&](const float* p, int pp, const float* q, int pq, float4 (&s)[2]) {
-            s[0] = s[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    group_sync(id);
+    {   // 32-blocks: a quad of two rows each
+        const int r = (pt >> 3) * 2, c = (pt & 7) * 4, r7 = r & 7;   // (r even: row r + 1's permutation is r7 ^ 1)
+        const float* ur = a + (32 + r) * kC;
+        float* x = xs + c;
+        int oc[8];
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-                const float4 u = *reinterpret_cast<const float4*>(p + r * pp + k);
-                const float4 v = *reinterpret_cast<const float4*>(p + (r + 1) * pp + k);
-                const float uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+        for (int e = 0; e < 8; ++e) oc[e] = ((c >> 2) ^ e) << 2;
+        f32x2 s[2] = {pk2(0.0f, 0.0f), pk2(0.0f, 0.0f)}, w[2] = {s[0], s[0]};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 w = *reinterpret_cast<const float4*>(q + (k + e) * pq + c);
-                    s[0] = make_float4(fmaf(uu[e], w.x, s[0].x), fmaf(uu[e], w.y, s[0].y), fmaf(uu[e], w.z, s[0].z),
-                                       fmaf(uu[e], w.w, s[0].w));
-                    s[1] = make_float4(fmaf(vv[e], w.x, s[1].x), fmaf(vv[e], w.y, s[1].y), fmaf(vv[e], w.z, s[1].z),
-                                       fmaf(vv[e], w.w, s[1].w));
-                }
+        for (int k = 0; k < 32; k += 4) {
+            const float4 u = quad(ur + (((k >> 2) ^ r7) << 2)), v = quad(ur + kC + (((k >> 2) ^ r7 ^ 1) << 2));
+            const float uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 q = quad(a + (k + e) * kC + oc[(k + e) & 7]);
+                axpy4(s, uu[e], q);
+                axpy4(w, vv[e], q);
             }
-        };
-        float4 s[2];
-        product(a + 32 * kPitchA, kPitchA, a, kPitchA, s);
+        }
+        *reinterpret_cast<float4*>(x + r * kPitchX) = make_float4(-s[0].x, -s[0].y, -s[1].x, -s[1].y);
+        *reinterpret_cast<float4*>(x + (r + 1) * kPitchX) = make_float4(-w[0].x, -w[0].y, -w[1].x, -w[1].y);
+        group_sync(id);
+        s[0] = s[1] = w[0] = w[1] = pk2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<float4*>(xs + (r + i) * kPitchX + c) = make_float4(-s[i].x, -s[i].y, -s[i].z, -s[i].w);
-        prep_sync();
-        product(a + 32 * kPitchA + 32, kPitchA, xs, kPitchX, s);
+        for (int k = 0; k < 32; k += 4) {
+            const float4 u = quad(ur + (((8 + (k >> 2)) ^ r7) << 2)), v = quad(ur + kC + (((8 + (k >> 2)) ^ r7 ^ 1) << 2));
+            const float uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) *reinterpret_cast<float4*>(a + (32 + r + i) * kPitchA + c) = s[i];
+            for (int e = 0; e < 4; ++e) {
+                const float4 q = quad(x + (k + e) * kPitchX);
+                axpy4(s, uu[e], q);
+                axpy4(w, vv[e], q);
+            }
+        }
+        *reinterpret_cast<float4*>(a + at(32 + r, c)) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+        *reinterpret_cast<float4*>(a + at(33 + r, c)) = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
     }
-    prep_sync();
+    group_sync(id);
+}
+
+// v[i] for a runtime i < 32: a tree of selects on the bits of i.
+__device__ __forceinline__ float pick32(const float (&v)[32], int i) {
+    float a[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) a[e] = (i & 16) ? v[e + 16] : v[e];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = (i & 8) ? a[e + 8] : a[e];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] = (i & 4) ? a[e + 4] : a[e];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) a[e] = (i & 2) ? a[e + 2] : a[e];
+    return (i & 1) ? a[1] : a[0];
 }
 
 // Grid: one CTA per (b, h).
 template <int DK>
 __global__ void __launch_bounds__(kThreads, 1)
 ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_q,
-                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 const __grid_constant__ CUtensorMap tm_y) {
     constexpr int KB = DK / 64;       // 64-wide blocks of a K or Q row
-    constexpr int KH = DK / 2;        // keys of a state thread
+    constexpr int KH = DK / kParts;   // keys of a state thread
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -296,17 +383,18 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         }
         for (int i = 0; i < kVStages; ++i) {
             mbar_init(&bar->v_full[i], 1);
-            mbar_init(&bar->v_empty[i], kStateWarps);
+            mbar_init(&bar->v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar->prep_full[i], kPrepWarps);
-            mbar_init(&bar->prep_empty[i], 1 + kStateWarps);
-            mbar_init(&bar->fin[i], 1);
+            mbar_init(&bar->prep_full[i], kGroupWarps);
+            mbar_init(&bar->t_empty[i], 1);
+            mbar_init(&bar->p_empty[i], 1);
         }
-        uint64_t* one[] = {&bar->gram, &bar->ks, &bar->e, &bar->ds, &bar->pv, &bar->qs};
+        uint64_t* one[] = {&bar->ks, &bar->e, &bar->ds, &bar->pv, &bar->gram, &bar->y_free, bar->fin, bar->fin + 1, bar->fin + 2};
         for (uint64_t* x : one) mbar_init(x, 1);
-        uint64_t* all[] = {&bar->s_ready, &bar->x_ready, &bar->w_ready, &bar->o_free};
+        uint64_t* all[] = {&bar->s_ready, &bar->x_ready, &bar->w_ready, &bar->y_full};
         for (uint64_t* x : all) mbar_init(x, kStateWarps);
+        mbar_init(&bar->gram_free, kGroupWarps);
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -336,7 +424,6 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         __syncwarp();
         if (lane == 0) mbar_arrive(x);
     };
-
     int issued = 0, v_issued = 0;   // loads of the load thread
 
     if (warp == kLoadWarp) {
@@ -346,7 +433,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_v);
             for (int c = 0; c < nchunk; ++c) {
-                const int s = c % kStages;
+                const int s = c % kStages, vs = c % kVStages;
                 if (c >= kStages && !wait1(&bar->empty[s], ((c / kStages) - 1) & 1)) break;
                 const uint32_t st = base + s * kStageBytes;
                 mbar_arrive_expect_tx(&bar->full[s], 2 * KB * kTile);
@@ -355,88 +442,111 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                     tma_load_4d(st + (2 * kb + 1) * kTile, &tm_q, 64 * kb, hk, c * kC, b, &bar->full[s]);
                 }
                 issued = c + 1;
-                const int vs = c % kVStages;
                 if (c >= kVStages && !wait1(&bar->v_empty[vs], ((c / kVStages) - 1) & 1)) break;
                 mbar_arrive_expect_tx(&bar->v_full[vs], kC * p.dv * 2);
-                tma_load_4d(base + kOffV + vs * kVBytes, &tm_v, 0, h, c * kC, b, &bar->v_full[vs]);
+                for (int vb = 0; vb < p.dv / 64; ++vb)
+                    tma_load_4d(base + kOffV + vs * kVBytes + vb * kTile, &tm_v, 64 * vb, h, c * kC, b, &bar->v_full[vs]);
                 v_issued = c + 1;
             }
         }
         __syncwarp();
+    } else if (warp == kStoreWarp) {
+        // ============================================================ y
+        for (int c = 0; c < nchunk; ++c) {
+            if (!wait_warp(&bar->y_full, c & 1)) break;
+            const int64_t t0 = static_cast<int64_t>(c) * kC;
+            if (t0 + kC <= len || len == g.L) {   // rows behind the tensor's end are clipped by the copy
+                if (lane == 0) {
+                    tc::tma_store_4d(&tm_y, base + kOffY, 0, h, c * kC, b);
+                    tc::bulk_commit();
+                    tc::bulk_wait_read0();
+                }
+            } else {                              // rows behind the sequence's end stay as they are
+                const int quads = p.dv / 8, n = static_cast<int>(len - t0) * quads;
+                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(g.y);
+                for (int i = lane; i < n; i += 32) {
+                    const int r = i / quads, q = i % quads;
+                    *reinterpret_cast<uint4*>(y + ((static_cast<int64_t>(b) * g.L + t0 + r) * g.H + h) * p.dv + 8 * q) =
+                        lds128(base + kOffY + (r * p.dv + 8 * q) * 2);
+                }
+            }
+            arrive_warp(&bar->y_free);
+        }
+        if (lane == 0) bulk_wait0();
+        __syncwarp();
     } else if (warp == kMmaWarp) {
         // ============================================================ the chain's MMAs (one thread)
         if (lane == 0) {
+            const uint32_t vlbo = p.dv == 128 ? kTile : 0;   // d_v 64: the lanes 64.. repeat the rows 0..63
             for (int c = 0; c < nchunk; ++c) {
-                const int s = c % kStages, pb = c & 1;
-                const uint32_t par = c & 1, st = base + s * kStageBytes;
+                const int s = c % kStages, pb = c & 1, vs = c % kVStages;
+                const uint32_t par = c & 1, st = base + s * kStageBytes, vt = base + kOffV + vs * kVBytes;
                 const uint32_t pr = base + kOffPrep + pb * kPrepBytes;
-                if (!wait1(&bar->full[s], (c / kStages) & 1)) break;
-                if (!wait1(&bar->prep_full[pb], (c >> 1) & 1)) break;   // the tile's rows behind the end are zero
+                if (!wait1(&bar->prep_full[pb], (c >> 1) & 1)) break;   // (K and Q landed, rows behind the end zero)
+                if (!wait1(&bar->v_full[vs], (c / kVStages) & 1)) break;
+                if (c > 0 && !wait1(&bar->pv, (c - 1) & 1)) break;      // the last chunk's E is read
+                tc_fence_after();
+                // E = Vᵀ Tᵀ, T's terms side by side
+#pragma unroll
+                for (int j = 0; j < kC / 16; ++j)
+                    umma(tmem + kColB, sdesc(vt + 2048u * j, vlbo, 1024), sdesc(pr + 32u * j, 16, 1024),
+                         idesc(2 * kC, false, true), j > 0);
+                umma_commit(&bar->v_empty[vs]);
                 if (!wait1(&bar->s_ready, par)) break;
                 tc_fence_after();
-                // S's two terms of the 16 keys of step ks
-                auto s_hi = [&](int ks) { return tmem + kColS + (ks * 16 / KH) * KH + (ks * 16 % KH) / 2; };
+                // KS and QS: S's terms of 16 keys in 16 columns, K and Q of a 64-key block side by side
 #pragma unroll
                 for (int ks = 0; ks < DK / 16; ++ks) {
                     const uint64_t bd = sdesc(st + (ks >> 2) * 2 * kTile + (ks & 3) * 32, 16, 1024);
-                    umma_ts(tmem + kColKS, s_hi(ks), bd, idesc(kC, false), ks > 0);
-                    umma_ts(tmem + kColKS, s_hi(ks) + KH / 2, bd, idesc(kC, false), 1);
+                    umma_ts(tmem + kColA, tmem + kColS + 16 * ks, bd, idesc(2 * kC, false), ks > 0);
+                    umma_ts(tmem + kColA, tmem + kColS + 16 * ks + 8, bd, idesc(2 * kC, false), 1);
                 }
                 if (!(p.test_drop && blockIdx.x == 0 && c == 0)) umma_commit(&bar->ks);
-                if (c > 0 && !wait1(&bar->o_free, (c - 1) & 1)) break;   // QS and PV of the last chunk read
-                tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks) {
-                    const uint64_t bd = sdesc(st + ((ks >> 2) * 2 + 1) * kTile + (ks & 3) * 32, 16, 1024);
-                    umma_ts(tmem + kColQS, s_hi(ks), bd, idesc(kC, false), ks > 0);
-                    umma_ts(tmem + kColQS, s_hi(ks) + KH / 2, bd, idesc(kC, false), 1);
-                }
-                umma_commit(&bar->qs);
                 if (!wait1(&bar->x_ready, par)) break;
                 tc_fence_after();
-                // E = X Tᵀ: tokens 16 j .. 16 j + 15 reach the rows i >= 16 j of T alone
+                // E += X Tᵀ
 #pragma unroll
                 for (int j = 0; j < kC / 16; ++j) {
-                    const uint32_t n = kC - 16 * j, row = 2048u * j + 32u * j;
-                    const uint32_t d = tmem + kColKS + 16 * j, x = tmem + kColX + 8 * j;
-                    umma_ts(d, x, sdesc(pr + row, 16, 1024), idesc(n, false), j > 0);
-                    umma_ts(d, x, sdesc(pr + kTile + row, 16, 1024), idesc(n, false), 1);
-                    umma_ts(d, x + 32, sdesc(pr + row, 16, 1024), idesc(n, false), 1);
+                    umma_ts(tmem + kColB, tmem + kColA + 16 * j, sdesc(pr + 32u * j, 16, 1024), idesc(2 * kC, false), 1);
+                    umma_ts(tmem + kColB, tmem + kColA + 16 * j + 8, sdesc(pr + 32u * j, 16, 1024), idesc(kC, false), 1);
                 }
                 umma_commit(&bar->e);
-                if (!wait1(&bar->w_ready, par) || !wait1(&bar->qs, par)) break;
+                umma_commit(&bar->t_empty[pb]);
+                if (!wait1(&bar->w_ready, par)) break;
                 tc_fence_after();
                 // dS = W K over the columns of S's terms
 #pragma unroll
                 for (int j = 0; j < kC / 16; ++j) {
                     const uint64_t bd = sdesc(st + 2048u * j, 2 * kTile, 1024);
-                    umma_ts(tmem + kColS, tmem + kColX + 8 * j, bd, idesc(DK, true), j > 0);
-                    umma_ts(tmem + kColS, tmem + kColX + 32 + 8 * j, bd, idesc(DK, true), 1);
+                    umma_ts(tmem + kColS, tmem + kColA + 16 * j, bd, idesc(DK, true), j > 0);
+                    umma_ts(tmem + kColS, tmem + kColA + 16 * j + 8, bd, idesc(DK, true), 1);
                 }
                 umma_commit(&bar->ds);
+                // Yᵀ += E (P β)ᵀ: tokens 16 j .. 16 j + 15 reach the rows i >= 16 j of P alone
 #pragma unroll
                 for (int j = 0; j < kC / 16; ++j) {
                     const uint32_t n = kC - 16 * j, row = 2 * kTile + 2048u * j + 32u * j;
-                    const uint32_t d = tmem + kColPV + 16 * j, x = tmem + kColVn + 8 * j;
-                    umma_ts(d, x, sdesc(pr + row, 16, 1024), idesc(n, false), j > 0);
+                    const uint32_t d = tmem + kColY + 16 * j, x = tmem + kColB + 16 * j;
+                    umma_ts(d, x, sdesc(pr + row, 16, 1024), idesc(n, false), 1);
                     umma_ts(d, x, sdesc(pr + kTile + row, 16, 1024), idesc(n, false), 1);
-                    umma_ts(d, x + 32, sdesc(pr + row, 16, 1024), idesc(n, false), 1);
+                    umma_ts(d, x + 8, sdesc(pr + row, 16, 1024), idesc(n, false), 1);
                 }
                 umma_commit(&bar->pv);
                 umma_commit(&bar->empty[s]);
-                umma_commit(&bar->prep_empty[pb]);
+                umma_commit(&bar->p_empty[pb]);
             }
         }
         __syncwarp();
-    } else if (warp >= kStateWarps) {
-        // ============================================================ prepare warps
-        const int pt = tid - 32 * kStateWarps, i = pt & 63;
+    } else if (warp >= kPrepWarp) {
+        // ============================================================ prepare groups
+        const int grp = (warp - kPrepWarp) >> 2, id = 1 + grp;
+        const int pt = tid - 32 * (kPrepWarp + 4 * grp), i = pt & 63, rb = (pt >> 5) & 1;   // row i, its 32-block rb
         const bool is_q = pt >= 64;
-        float* const Gh = reinterpret_cast<float*>(gbase + kOffLocal);
-        float *const Gl = Gh + kC, *const rk = Gl + kC, *const be = rk + kC;
-        double* const Gd = reinterpret_cast<double*>(be + kC);
-        float* const a = reinterpret_cast<float*>(gbase + kOffA);
-        float* const xs = reinterpret_cast<float*>(gbase + kOffXs);
+        Local& lo = reinterpret_cast<Local*>(gbase + kOffLocal)[grp];
+        float* const xs = reinterpret_cast<float*>(gbase + kOffXs + grp * kXsBytes);
+        const uint32_t pr = base + kOffPrep + grp * kPrepBytes;
+        float* const a = reinterpret_cast<float*>(gbase + kOffPrep + grp * kPrepBytes);
+        const uint32_t gram = tmem + kColGram;
         const float Ah = g.A[h], bias = g.dt_bias ? g.dt_bias[h] : 0.0f;
         const __nv_bfloat16* dtp = static_cast<const __nv_bfloat16*>(g.dt);
         const __nv_bfloat16* bep = static_cast<const __nv_bfloat16*>(g.beta);
@@ -449,272 +559,268 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 be_n = to_f32(bep[o]);
             }
         };
-        if (nchunk > 0) fetch(0);
-        for (int c = 0; c < nchunk; ++c) {
-            const int s = c % kStages, pb = c & 1;
-            const uint32_t st = base + s * kStageBytes, pr = base + kOffPrep + pb * kPrepBytes;
-            Scal& sc = scal[pb];
-            const int valid = static_cast<int>(len - static_cast<int64_t>(c) * kC < kC ? len - static_cast<int64_t>(c) * kC : kC);
+        if (grp < nchunk) fetch(grp);
+        for (int c = grp; c < nchunk; c += 2) {
+            const int s = c % kStages;
+            const uint32_t st = base + s * kStageBytes, ph = (c >> 1) & 1;
+            Scal& sc = scal[c % kScals];
+            const int64_t left = len - static_cast<int64_t>(c) * kC;
+            const int valid = left < kC ? static_cast<int>(left) : kC;
             bool got = mbar_wait_bounded(&bar->full[s], (c / kStages) & 1, lim);
             if (got && valid < kC) got = mbar_wait_bounded(&bar->v_full[c % kVStages], (c / kVStages) & 1, lim);
-            if (got && c >= 2) got = mbar_wait_bounded(&bar->prep_empty[pb], ((c >> 1) - 1) & 1, lim);
-            if (prep_any(!got)) {
+            if (got && c >= 1) got = mbar_wait_bounded(&bar->gram_free, (c - 1) & 1, lim);   // the other group's
+            if (valid < kC && i >= valid && got) {   // rows behind the end, whatever they hold, become zero rows
+                for (int w = 0; w < 8 * KB; ++w)
+                    sts128(st + (2 * (w >> 3) + (is_q ? 1 : 0)) * kTile + i * 128 + (w & 7) * 16, make_uint4(0, 0, 0, 0));
+                if (!is_q)
+                    for (int w = 0; w < p.dv / 8; ++w)
+                        sts128(base + kOffV + (c % kVStages) * kVBytes + (w >> 3) * kTile + i * 128 + (w & 7) * 16,
+                               make_uint4(0, 0, 0, 0));
+                fence_proxy_async_smem();
+            }
+            tc_fence_before();
+            if (group_any(id, !got)) {
                 if (pt == 0) record();
                 break;
             }
-            // rows behind the end (another token's values, or anything) become zero rows
-            if (i >= valid) {
-                for (int kb = 0; kb < KB; ++kb)
-                    for (int w = 0; w < 8; ++w)
-                        sts128(st + (2 * kb + (is_q ? 1 : 0)) * kTile + i * 128 + w * 16, make_uint4(0, 0, 0, 0));
-                if (!is_q)
-                    for (int w = 0; w < p.dv / 8; ++w) 
-                        sts128(base + kOffV + (c % kVStages) * kVBytes + i * p.dv * 2 + w * 16, make_uint4(0, 0, 0, 0));
-                fence_proxy_async_smem();
-            }
-            float rn = 1.0f;   // 1 / |row i| of K, or of Q
-            if (g.l2norm) {
-                float q0 = 0.0f, q1 = 0.0f;
+            if (pt == 0) {   // [K; Q] Kᵀ: lanes 0..63 K's rows, 64..127 Q's
+                tc_fence_after();
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                    for (int w = 0; w < 8; w += 2) {
-                        const uint32_t blk = st + (2 * kb + (is_q ? 1 : 0)) * kTile;
-                        q0 = sq8(lds128(chunk_addr(blk, i, w)), q0);
-                        q1 = sq8(lds128(chunk_addr(blk, i, w + 1)), q1);
-                    }
-                rn = 1.0f / sqrtf(q0 + q1 + kGdrL2Eps);
+                for (int ks = 0; ks < DK / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * 2 * kTile + (ks & 3) * 32;
+                    umma(gram, sdesc(st + off, 16, 1024), sdesc(st + off, 16, 1024), idesc(kC, false), ks > 0);
+                }
+                umma_commit(&bar->gram);
             }
             double G = 0.0;
+            float rn = 1.0f, be = 0.0f;   // 1 / |row i| of K, or of Q
             if (!is_q) {
                 const bool in = i < valid;
                 const float delta = in ? gdr_delta(dt_n, bias, g.softplus) : 0.0f;
-                be[i] = in ? gdr_beta(be_n, g.sigmoid) : 0.0f;
-                rk[i] = rn;
-                if (c + 1 < nchunk) fetch(c + 1);
+                be = in ? gdr_beta(be_n, g.sigmoid) : 0.0f;
+                if (c + 2 < nchunk) fetch(c + 2);
                 G = static_cast<double>(delta) * static_cast<double>(Ah) * 1.4426950408889634074;   // log2 α
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const double v = __shfl_up_sync(0xffffffffu, G, o);
                     if (lane >= o) G += v;
                 }
-                Gd[i] = G;
-            }
-            tc_fence_before();
-            prep_sync();
-            if (pt == 0) {   // [K; Q] Kᵀ: lanes 0..63 K's rows, 64..127 Q's
-                tc_fence_after();
+                lo.G[i] = G;
+            } else if (g.l2norm) {
+                f32x2 q0 = pk2(0.0f, 0.0f), q1 = q0;
 #pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * 2 * kTile + (ks & 3) * 32;
-                    umma(tmem + kColGram, sdesc(st + off, 16, 1024), sdesc(st + off, 16, 1024), idesc(kC, false), ks > 0);
+                for (int w = 0; w < 8 * KB; ++w) {
+                    const uint4 x = lds128(chunk_addr(st + (2 * (w >> 3) + 1) * kTile, i, w & 7));
+                    const f32x2 x0 = pk2(lo_f(x.x), hi_f(x.x)), x1 = pk2(lo_f(x.y), hi_f(x.y));
+                    const f32x2 x2 = pk2(lo_f(x.z), hi_f(x.z)), x3 = pk2(lo_f(x.w), hi_f(x.w));
+                    q0 = fma2(x0, x0, fma2(x2, x2, q0));
+                    q1 = fma2(x1, x1, fma2(x3, x3, q1));
                 }
-                umma_commit(&bar->gram);
+                rn = 1.0f / sqrtf((q0.x + q0.y) + (q1.x + q1.y) + kGdrL2Eps);
             }
-            const double first = Gd[31], end = first + Gd[63];
+            group_sync(id);
+            const double first = lo.G[31];
             if (!is_q) {
+                const double end = first + lo.G[63];
                 if (i >= 32) G += first;
                 const float hi = static_cast<float>(G);
-                Gh[i] = hi;
-                Gl[i] = static_cast<float>(G - static_cast<double>(hi));
-                sc.ek[i] = exp2f(hi) * rn;
-                sc.be[i] = be[i];
-                sc.wk[i] = be[i] * exp2f(static_cast<float>(end - G)) * rn;
+                lo.gh[i] = hi;
+                lo.gl[i] = static_cast<float>(G - static_cast<double>(hi));
+                sc.ek[i] = -exp2f(hi);
+                sc.wk[i] = be * exp2f(static_cast<float>(end - G));
                 if (i == 0) sc.end[0] = exp2f(static_cast<float>(end));
             }
-            if (prep_any(!mbar_wait_bounded(&bar->gram, c & 1, lim))) {
+            got = mbar_wait_bounded(&bar->gram, c & 1, lim);
+            if (got && c >= 2) got = mbar_wait_bounded(is_q ? &bar->p_empty[grp] : &bar->t_empty[grp], ph ^ 1, lim);
+            if (group_any(id, !got)) {
                 if (pt == 0) record();
                 break;
             }
             tc_fence_after();
-            {
-                const float gh = Gh[i], gl = Gl[i];
-                const float row = is_q ? rn * g.scale : rn;
-                if (is_q) sc.qe[i] = exp2f(gh) * row;
-                const uint32_t src = tmem + kColGram + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            const uint32_t src = gram + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            float v[32];
+            tmem_ld32(src + 32 * rb, v);   // the block on the diagonal
+            if (!is_q) {                   // |k_i|² is K Kᵀ's own diagonal
+                if (g.l2norm) rn = 1.0f / sqrtf(pick32(v, lane) + kGdrL2Eps);
+                lo.cb[i] = be * rn;
+                if (rb == 0) lo.cf[i] = be * rn * exp2f(static_cast<float>(first - G));
+                sc.ek[i] *= rn;
+                sc.wk[i] *= rn;
+            }
+            group_sync(id);
+            const float gh = lo.gh[i], gl = lo.gl[i];
+            const float row = is_q ? rn * g.scale : rn;
+            if (is_q) sc.qe[i] = exp2f(gh) * row;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float v[32];
-                    tmem_ld32(src + 32 * half, v);
+            for (int blk = 0; blk < 2; ++blk) {
+                // first the block on the diagonal, then (rows 32..63) the block left of it
+                if (blk == 1) {
+                    if (rb == 0) break;
+                    tmem_ld32(src, v);
+                }
+                const int j0 = blk == 0 ? 32 * rb : 0;
+                if (blk == 0) {
 #pragma unroll
-                    for (int j4 = 0; j4 < 32; j4 += 4) {
-                        const int j = 32 * half + j4;
-                        const float4 h4 = *reinterpret_cast<const float4*>(Gh + j), l4 = *reinterpret_cast<const float4*>(Gl + j);
-                        const float4 r4 = *reinterpret_cast<const float4*>(rk + j), b4 = *reinterpret_cast<const float4*>(be + j);
-                        const float hh[4] = {h4.x, h4.y, h4.z, h4.w}, ll[4] = {l4.x, l4.y, l4.z, l4.w};
-                        const float rr[4] = {r4.x, r4.y, r4.z, r4.w}, bb[4] = {b4.x, b4.y, b4.z, b4.w};
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 h4 = quad(lo.gh + j0 + e), l4 = quad(lo.gl + j0 + e), c4 = quad(lo.cb + j0 + e);
+                        const f32x2 hh[2] = {pk2(h4.x, h4.y), pk2(h4.z, h4.w)}, ll[2] = {pk2(l4.x, l4.y), pk2(l4.z, l4.w)};
+                        const f32x2 cc[2] = {pk2(c4.x, c4.y), pk2(c4.z, c4.w)};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float d = ex2_approx((gh - hh[e]) + (gl - ll[e]));
-                            const float f = v[j4 + e] * row * rr[e] * d * (is_q ? 1.0f : bb[e]);
-                            v[j4 + e] = (is_q ? j + e <= i : j + e < i) ? f : 0.0f;
+                        for (int f = 0; f < 2; ++f) {
+                            const f32x2 m1 = pk2(-1.0f, -1.0f);
+                            const f32x2 d = add2(fma2(hh[f], m1, pk2(gh, gh)), fma2(ll[f], m1, pk2(gl, gl)));
+                            const f32x2 w = mul2(mul2(pk2(v[e + 2 * f], v[e + 2 * f + 1]), cc[f]), pk2(row, row));
+                            const f32x2 r = mul2(w, pk2(ex2_approx(d.x), ex2_approx(d.y)));
+                            const int k = e + 2 * f - (is_q ? 1 : 0);   // P keeps its diagonal
+                            v[e + 2 * f] = k < lane ? r.x : 0.0f;
+                            v[e + 2 * f + 1] = k + 1 < lane ? r.y : 0.0f;
                         }
                     }
-                    if (is_q) {
+                } else {   // j < 32 <= i: both factors of e^{G_i - G_31} e^{G_31 - G_j} lie between the product and 1
+                    const float rf = row * exp2f(static_cast<float>((static_cast<double>(gh) + static_cast<double>(gl)) - first));
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            uint32_t hw[4], lw[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float x0 = v[8 * w + 2 * e], x1 = v[8 * w + 2 * e + 1];
-                                hw[e] = pk(x0, x1);
-                                lw[e] = pk(x0 - lo_f(hw[e]), x1 - hi_f(hw[e]));
-                            }
-                            sts128(chunk_addr(pr + 2 * kTile, i, 4 * half + w), make_uint4(hw[0], hw[1], hw[2], hw[3]));
-                            sts128(chunk_addr(pr + 3 * kTile, i, 4 * half + w), make_uint4(lw[0], lw[1], lw[2], lw[3]));
-                        }
-                    } else {
-#pragma unroll
-                        for (int w = 0; w < 8; ++w)
-                            *reinterpret_cast<float4*>(a + i * kPitchA + 32 * half + 4 * w) =
-                                make_float4(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 c4 = quad(lo.cf + e);
+                        const f32x2 r0 = mul2(mul2(pk2(v[e], v[e + 1]), pk2(c4.x, c4.y)), pk2(rf, rf));
+                        const f32x2 r1 = mul2(mul2(pk2(v[e + 2], v[e + 3]), pk2(c4.z, c4.w)), pk2(rf, rf));
+                        v[e] = r0.x;
+                        v[e + 1] = r0.y;
+                        v[e + 2] = r1.x;
+                        v[e + 3] = r1.y;
                     }
                 }
-            }
-            prep_sync();
-            invert64(a, xs, pt);
-            {   // T as two bf16 terms: half a row each
-                const int r = pt >> 1, j0 = (pt & 1) * 32;
+                if (is_q) {
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const float4 u = *reinterpret_cast<const float4*>(a + r * kPitchA + j0 + 8 * w);
-                    const float4 v = *reinterpret_cast<const float4*>(a + r * kPitchA + j0 + 8 * w + 4);
-                    // what lies above the diagonal blocks was A's zero
-                    const uint32_t h0 = pk(u.x, u.y), h1 = pk(u.z, u.w), h2 = pk(v.x, v.y), h3 = pk(v.z, v.w);
-                    sts128(chunk_addr(pr, r, (pt & 1) * 4 + w), make_uint4(h0, h1, h2, h3));
-                    sts128(chunk_addr(pr + kTile, r, (pt & 1) * 4 + w),
-                           make_uint4(pk(u.x - lo_f(h0), u.y - hi_f(h0)), pk(u.z - lo_f(h1), u.w - hi_f(h1)),
-                                      pk(v.x - lo_f(h2), v.y - hi_f(h2)), pk(v.z - lo_f(h3), v.w - hi_f(h3))));
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t hw[4], lw[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) split2(pk2(v[8 * w + 2 * e], v[8 * w + 2 * e + 1]), hw[e], lw[e]);
+                        sts128(chunk_addr(pr + 2 * kTile, i, j0 / 8 + w), make_uint4(hw[0], hw[1], hw[2], hw[3]));
+                        sts128(chunk_addr(pr + 3 * kTile, i, j0 / 8 + w), make_uint4(lw[0], lw[1], lw[2], lw[3]));
+                    }
+                } else {
+#pragma unroll
+                    for (int w = 0; w < 8; ++w)
+                        *reinterpret_cast<float4*>(a + at(i, j0 + 4 * w)) =
+                            make_float4(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->gram_free);
+            group_sync(id);
+            invert64(a, xs, pt, id);
+            {   // T as two bf16 terms in its own place: half a row each (thread pt: row pt & 63), read by all first
+                const int r = pt & 63, hf = pt >> 6;
+                float4 u[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w)   // (the block above the diagonal holds nothing)
+                    u[w] = r >= 32 || hf == 0 ? quad(a + at(r, 32 * hf + 4 * w)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                group_sync(id);
+                {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t hw[4], lw[4];
+                        split2(pk2(u[2 * w].x, u[2 * w].y), hw[0], lw[0]);
+                        split2(pk2(u[2 * w].z, u[2 * w].w), hw[1], lw[1]);
+                        split2(pk2(u[2 * w + 1].x, u[2 * w + 1].y), hw[2], lw[2]);
+                        split2(pk2(u[2 * w + 1].z, u[2 * w + 1].w), hw[3], lw[3]);
+                        sts128(chunk_addr(pr, r, 4 * hf + w), make_uint4(hw[0], hw[1], hw[2], hw[3]));
+                        sts128(chunk_addr(pr + kTile, r, 4 * hf + w), make_uint4(lw[0], lw[1], lw[2], lw[3]));
+                    }
                 }
             }
             fence_proxy_async_smem();
-            arrive_warp(&bar->prep_full[pb]);
+            arrive_warp(&bar->prep_full[grp]);
         }
     } else {
         // ============================================================ state warps
-        const int v = (warp & 3) * 32 + lane, half = warp >> 2;
+        const int v = (warp & 3) * 32 + lane, part = warp >> 2;
         const bool row_in = v < p.dv;
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const int64_t srow = (static_cast<int64_t>(item) * p.dv + v) * DK + half * KH;
-        float S[KH];
+        const int64_t srow = (static_cast<int64_t>(item) * p.dv + v) * DK + part * KH;
+        f32x2 S[KH / 2];
 #pragma unroll
         for (int k = 0; k < KH; k += 4) {
             float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (g.h_init && row_in) q = *reinterpret_cast<const float4*>(g.h_init + srow + k);
-            S[k] = q.x;
-            S[k + 1] = q.y;
-            S[k + 2] = q.z;
-            S[k + 3] = q.w;
+            if (g.h_init && row_in) q = quad(g.h_init + srow + k);
+            S[k / 2] = pk2(q.x, q.y);
+            S[k / 2 + 1] = pk2(q.z, q.w);
         }
-        auto store_s = [&]() {   // S's two terms into this thread's d_k / 2 columns
 #pragma unroll
-            for (int k = 0; k < KH; k += 32) {
-                float t[32];
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) t[e] = S[k + e];
-                split32(t, hi, lo);
-                tmem_st16(tl + kColS + half * KH + k / 2, hi);
-                tmem_st16(tl + kColS + half * KH + KH / 2 + k / 2, lo);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-        };
-        store_s();
+        for (int k = 0; k < KH; k += 16) store_terms(tl + kColS + part * KH + k, S + k / 2);
+        tmem_wait_st();
+        tc_fence_before();
         arrive_warp(&bar->s_ready);
         bool ok = true;
         for (int c = 0; c < nchunk; ++c) {
-            const int vs = c % kVStages, pb = c & 1;
+            const int pb = c & 1;
             const uint32_t par = c & 1;
-            const Scal& sc = scal[pb];
-            const int64_t t0 = static_cast<int64_t>(c) * kC + half * 32;
-            ok = wait_warp(&bar->v_full[vs], (c / kVStages) & 1) && wait_warp(&bar->prep_full[pb], (c >> 1) & 1) &&
-                 wait_warp(&bar->ks, par);
+            const Scal& sc = scal[c % kScals];
+            ok = wait_warp(&bar->prep_full[pb], (c >> 1) & 1) && wait_warp(&bar->ks, par);
             if (!ok) break;
             tc_fence_after();
-            {   // X = V - diag(e^G / |k|) K Sᵀ of this thread's 32 tokens
-                float x[32];
-                tmem_ld32(tl + kColKS + 32 * half, x);
-                const __nv_bfloat16* vt = reinterpret_cast<const __nv_bfloat16*>(gbase + kOffV + vs * kVBytes) +
-                                          half * 32 * p.dv + v;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float vv = row_in ? __bfloat162float(vt[e * p.dv]) : 0.0f;
-                    x[e] = fmaf(-sc.ek[32 * half + e], x[e], vv);
-                }
-                uint32_t hi[16], lo[16];
-                split32(x, hi, lo);
-                tmem_st16(tl + kColX + 16 * half, hi);
-                tmem_st16(tl + kColX + 32 + 16 * half, lo);
-                tmem_wait_st();
-                tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bar->x_ready);
-                mbar_arrive(&bar->v_empty[vs]);
-            }
+            f32x2 x[8];
+            tmem_ld16(tl + kColA + kTok * part, x);   // X, the factors' sign with it
+            scale16(x, sc.ek + kTok * part);
+            store_terms(tl + kColA + kTok * part, x);
+            tmem_wait_st();
+            tc_fence_before();
+            arrive_warp(&bar->x_ready);
+            tmem_ld16(tl + kColQS + kTok * part, x);  // y's part from the entering state, while E is multiplied
+            scale16(x, sc.qe + kTok * part);
+            tmem_st16(tl + kColY + kTok * part, x);
             ok = wait_warp(&bar->e, par);
             if (!ok) break;
             tc_fence_after();
             {
-                float x[32], w[32];
-                tmem_ld32(tl + kColKS + 32 * half, x);
-                uint32_t hi[16], lo[16];
+                f32x2 w[8];
+                tmem_ld16x2(tl + kColB + kTok * part, tl + kColB + kC + kTok * part, x, w);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) w[e] = x[e] * sc.wk[32 * half + e];
-                split32(w, hi, lo);
-                tmem_st16(tl + kColX + 16 * half, hi);
-                tmem_st16(tl + kColX + 32 + 16 * half, lo);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] *= sc.be[32 * half + e];
-                split32(x, hi, lo);
-                tmem_st16(tl + kColVn + 16 * half, hi);
-                tmem_st16(tl + kColVn + 32 + 16 * half, lo);
-                tmem_wait_st();
-                tc_fence_before();
+                for (int e = 0; e < 8; ++e) x[e] = add2(x[e], w[e]);
             }
+            store_terms(tl + kColB + kTok * part, x);
+            scale16(x, sc.wk + kTok * part);
+            store_terms(tl + kColA + kTok * part, x);
+            tmem_wait_st();
+            tc_fence_before();
             arrive_warp(&bar->w_ready);
+            const float end = sc.end[0];
             ok = wait_warp(&bar->ds, par);
             if (!ok) break;
             tc_fence_after();
-            const float end = sc.end[0];
 #pragma unroll
-            for (int k = 0; k < KH; k += 32) {
-                float d[32];
-                tmem_ld32(tl + kColS + half * KH + k, d);
+            for (int k = 0; k < KH; k += 16) {
+                tmem_ld16(tl + kColS + part * KH + k, x);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) S[k + e] = fmaf(end, S[k + e], d[e]);
+                for (int e = 0; e < 8; ++e) S[k / 2 + e] = fma2(pk2(end, end), S[k / 2 + e], x[e]);
+                store_terms(tl + kColS + part * KH + k, S + k / 2);
             }
-            store_s();
+            tmem_wait_st();
+            tc_fence_before();
             arrive_warp(&bar->s_ready);
             // y, while the next chunk's K Sᵀ runs
-            ok = wait_warp(&bar->pv, par);
+            ok = (c == 0 || wait_warp(&bar->y_free, (c - 1) & 1)) && wait_warp(&bar->pv, par);
             if (!ok) break;
             tc_fence_after();
-            {
-                float qs[32], pv[32];
-                tmem_ld32(tl + kColQS + 32 * half, qs);
-                tmem_ld32(tl + kColPV + 32 * half, pv);
-                tc_fence_before();
-                __nv_bfloat16* yp = static_cast<__nv_bfloat16*>(g.y) +
-                                    ((static_cast<int64_t>(b) * g.L + t0) * g.H + h) * p.dv + v;
-                const int64_t pitch = static_cast<int64_t>(g.H) * p.dv;
-                const int n = row_in ? static_cast<int>(len - t0 < 32 ? len - t0 : 32) : 0;
+            tmem_ld16(tl + kColY + kTok * part, x);
+            tc_fence_before();
+            if (row_in) {
+                __nv_bfloat16* ys = reinterpret_cast<__nv_bfloat16*>(gbase + kOffY) + kTok * part * p.dv + v;
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (e < n) yp[e * pitch] = __float2bfloat16_rn(fmaf(sc.qe[32 * half + e], qs[e], pv[e]));
+                for (int e = 0; e < 8; ++e) {
+                    ys[2 * e * p.dv] = __float2bfloat16_rn(x[e].x);
+                    ys[(2 * e + 1) * p.dv] = __float2bfloat16_rn(x[e].y);
+                }
             }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bar->o_free);
-                mbar_arrive(&bar->prep_empty[pb]);
-            }
+            fence_proxy_async_smem();
+            arrive_warp(&bar->y_full);
         }
         if (ok && g.final_state && row_in) {
 #pragma unroll
             for (int k = 0; k < KH; k += 4)
-                *reinterpret_cast<float4*>(g.final_state + srow + k) = make_float4(S[k], S[k + 1], S[k + 2], S[k + 3]);
+                *reinterpret_cast<float4*>(g.final_state + srow + k) =
+                    make_float4(S[k / 2].x, S[k / 2].y, S[k / 2 + 1].x, S[k / 2 + 1].y);
         }
     }
 
@@ -726,13 +832,11 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         for (int c = v_issued > kVStages ? v_issued - kVStages : 0; c < v_issued; ++c)
             mbar_wait_bounded(&bar->v_full[c % kVStages], (c / kVStages) & 1, p.drain_ns);
     }
-    if (warp == kMmaWarp && lane == 0) {
-        umma_commit(&bar->fin[0]);
-        mbar_wait_bounded(&bar->fin[0], 0, p.drain_ns);
-    }
-    if (tid == 32 * kStateWarps) {
-        umma_commit(&bar->fin[1]);
-        mbar_wait_bounded(&bar->fin[1], 0, p.drain_ns);
+    // every thread that issued MMAs: the chain's, and each group's
+    const int f = tid == 32 * kMmaWarp ? 0 : tid == 32 * kPrepWarp ? 1 : tid == 32 * (kPrepWarp + kGroupWarps) ? 2 : -1;
+    if (f >= 0) {
+        umma_commit(&bar->fin[f]);
+        mbar_wait_bounded(&bar->fin[f], 0, p.drain_ns);
     }
     tc_fence_before();
     __syncthreads();
