@@ -18,6 +18,7 @@ int check_gdr(const ss_gdr_dims* d, uint32_t flags) {
     if ((d->d_k != 64 && d->d_k != 128) || (d->d_v != 64 && d->d_v != 128)) return SS_ERR_UNSUPPORTED;
     if (d->nheads > 0 && (d->nheads_k == 0 || d->nheads % d->nheads_k)) return SS_ERR_INVALID_ARG;
     const int64_t lim = int64_t(1) << 27;   // (b, head) items times the blocks that share one stay below 2^31
+    if (double(d->batch) * double(d->nheads) * (double(d->seqlen) / 64.0 + 1.0) >= 2147483647.0) return SS_ERR_INVALID_ARG;
     if (d->batch >= lim || d->nheads >= lim || d->batch * d->nheads >= lim || d->seqlen >= (int64_t(1) << 31) - 256 ||
         double(d->batch) * double(d->seqlen) * double(d->nheads) * 128.0 > 2.0e18)
         return SS_ERR_INVALID_ARG;
@@ -73,34 +74,58 @@ bool head_map(CUtensorMap* m, const void* base, int64_t batch, int64_t L, int64_
     return make_map_bf16(m, base, 4, dims, strides, box, swizzle);
 }
 
+// Workspace: the status word's header, then a record per (item, chunk).
+struct GdrLayout {
+    int64_t nchunks;
+    size_t rec, total;
+};
+GdrLayout gdr_layout(const ss_gdr_dims* d, uint32_t flags) {
+    GdrLayout w{};
+    w.nchunks = ceil_div(d->seqlen, gdr::kC);
+    w.rec = kHeaderBytes;
+    w.total = w.rec;
+    if ((flags & SS_BF16) && d->seqlen >= kChunkedFrom)
+        w.total += static_cast<size_t>(d->batch * d->nheads * w.nchunks) * gdr::kRecBytes;
+    return w;
+}
+
+struct Maps {
+    CUtensorMap q, k, v, y;
+};
+
 template <int DK>
-int launch_tc(const gdr::Params& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-              const CUtensorMap& my, cudaStream_t stream) {
+int launch_tc(const gdr::Params& p, const Maps& m, cudaStream_t stream) {
+    auto prep = gdr::ss_gdr_prep_kernel<DK>;
     auto kern = gdr::ss_gdr_tc_kernel<DK>;
-    static std::atomic<bool> attr[kMaxDevices];
+    static std::atomic<bool> attr[2][kMaxDevices];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || set_smem_limit(kern, gdr::kSmemBytes, attr, dev) != SS_OK)
+    if (cudaGetDevice(&dev) != cudaSuccess || set_smem_limit(kern, gdr::kSmemBytes, attr[0], dev) != SS_OK ||
+        set_smem_limit(prep, gdr::kPrepSmem, attr[1], dev) != SS_OK)
         return SS_ERR_CUDA;
-    kern<<<static_cast<unsigned>(p.g.batch) * static_cast<unsigned>(p.g.H), gdr::kThreads, gdr::kSmemBytes, stream>>>(
-        p, mq, mk, mv, my);
+    const int64_t items = static_cast<int64_t>(p.g.batch) * p.g.H;
+    prep<<<static_cast<unsigned>(items * p.nchunks), gdr::kPrepThreads, gdr::kPrepSmem, stream>>>(p, m.q, m.k);
+    kern<<<static_cast<unsigned>(items), gdr::kThreads, gdr::kSmemBytes, stream>>>(p, m.q, m.k, m.v, m.y);
     return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
 int run_tc(const GdrParams& g, const ss_gdr_dims* d, uint32_t flags, const ss_launch* launch, cudaStream_t stream) {
+    const GdrLayout w = gdr_layout(d, flags);
     gdr::Params p{};
     p.g = g;
     p.status = static_cast<uint32_t*>(launch->workspace);
+    p.rec = static_cast<unsigned char*>(launch->workspace) + w.rec;
+    p.nchunks = w.nchunks;
     p.dv = static_cast<int>(d->d_v);
     p.test_drop = (flags & SS_TEST_DROP_CARRY) ? 1 : 0;
     p.wait_ns = launch->timeout_iters ? static_cast<uint64_t>(launch->timeout_iters) * 1000ull : kTmaWaitNs;
     p.drain_ns = kTmaWaitNs;
-    CUtensorMap mq, mk, mv, my;
-    if (!head_map(&mq, g.q, d->batch, d->seqlen, d->nheads_k, d->d_k, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !head_map(&mk, g.k, d->batch, d->seqlen, d->nheads_k, d->d_k, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !head_map(&mv, g.v, d->batch, d->seqlen, d->nheads, d->d_v, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !head_map(&my, g.y, d->batch, d->seqlen, d->nheads, d->d_v, d->d_v, CU_TENSOR_MAP_SWIZZLE_NONE))
+    Maps m;
+    if (!head_map(&m.q, g.q, d->batch, d->seqlen, d->nheads_k, d->d_k, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !head_map(&m.k, g.k, d->batch, d->seqlen, d->nheads_k, d->d_k, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !head_map(&m.v, g.v, d->batch, d->seqlen, d->nheads, d->d_v, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !head_map(&m.y, g.y, d->batch, d->seqlen, d->nheads, d->d_v, d->d_v, CU_TENSOR_MAP_SWIZZLE_NONE))
         return SS_ERR_CUDA;
-    return d->d_k == 128 ? launch_tc<128>(p, mq, mk, mv, my, stream) : launch_tc<64>(p, mq, mk, mv, my, stream);
+    return d->d_k == 128 ? launch_tc<128>(p, m, stream) : launch_tc<64>(p, m, stream);
 }
 
 }  // namespace
@@ -108,7 +133,7 @@ int run_tc(const GdrParams& g, const ss_gdr_dims* d, uint32_t flags, const ss_la
 extern "C" {
 
 size_t ss_gdr_fwd_workspace_bytes(const ss_gdr_dims* dims, uint32_t flags) {
-    return check_gdr(dims, flags) == SS_OK ? kHeaderBytes : 0;
+    return check_gdr(dims, flags) == SS_OK ? gdr_layout(dims, flags).total : 0;
 }
 
 int ss_gdr_fwd(const void* q, const void* k, const void* v, const void* dt, const float* dt_bias, const float* A,

@@ -5,34 +5,23 @@
 //   e_i = v_i - e^{G_i} S k̂_i - Σ_{j<i} e^{G_i - G_j} (k̂_i·k̂_j) β_j e_j
 // is one triangular system for all 64 corrections, so with A'_ij = e^{G_i - G_j} (k̂_i·k̂_j) β_j (j < i):
 //   E = T (V - diag(e^G) K̂ Sᵀ),  T = (I + A')^-1
-//   Y = diag(e^G) Q̂ Sᵀ + P diag(β) E,       P_ij = e^{G_i - G_j} q̂_i·k̂_j (j <= i)
+//   Y = diag(e^G) Q̂ Sᵀ + P E,       P_ij = e^{G_i - G_j} (q̂_i·k̂_j) β_j (j <= i)
 //   S <- e^{G_end} S + (diag(β e^{G_end - G}) E)ᵀ K̂
 // Every exponent is a difference G_i - G_j with j <= i, so nothing overflows; the differences are taken of 48-bit
-// values (pairs of floats of a 64-bit prefix sum), so a long decay keeps its near differences.  T does not depend
-// on S: it is computed chunks ahead, and what is left in the chain from chunk to chunk is three products and two
-// element-wise steps.
+// values (pairs of floats of a 64-bit prefix sum), so a long decay keeps its near differences.
 //
-// The products run transposed: the 128 TMEM lanes are the rows v of the state, and the columns are tokens or keys.
-//   KS, QS [v, i] = S Kᵀ, S Qᵀ      A: S (TMEM),  B: K and Q tiles in one, K-major
-//   E   [v, i] = Vᵀ Tᵀ + X Tᵀ       A: V tile, MN-major; X = -KS diag(e^G / |k|) (TMEM),  B: T tile, K-major
-//   dS  [v, k] = W K                A: W = E diag(β e^{G_end - G} / |k|) (TMEM),  B: K tile, MN-major
-//   Yᵀ  [v, i] = QS diag(scale e^G / |q|) + E (P β)ᵀ    off the chain, under the element-wise steps
-// so that the state, the right hand side and the corrections go from registers to TMEM and never through shared
-// memory, a thread owning one row v (four threads to a row, each with a quarter of the columns).  X is written over
-// KS, E's terms over E, S's terms over dS, by the thread that read them, which is what makes it fit in TMEM.
-// An MMA of 128 x N x 16 takes about 64 cycles for every N up to 128 (measured here), so operands are put side by
-// side to N = 128 where they share A: K with Q, and T's two terms, whose two halves of E the reader adds.
+// Two kernels.  What does not depend on S -- T, P and the factors -- is prepared for every chunk at once
+// (ss_gdr_prep_kernel, a block per chunk, four resident per SM) and left in the workspace, as the shared-memory
+// image that the second kernel copies in.  ss_gdr_tc_kernel then walks the chunks of a (b, h) in order; in its chain
+// from chunk to chunk remain three products and three element-wise steps.  With the preparation inside the second
+// kernel (two groups of four warps, up to two chunks ahead) its latency, about 14 000 cycles a chunk beside the
+// state's warps, set the pace: 8 700 cycles a chunk.
 //
 // Precision: q, k, v are bf16 values as given and unit lengths are factors of rows and columns, so they enter
 // exactly.  fp32 operands -- S, X, T, W, P, E -- enter as two bf16 terms, hi + lo (the product of two such pairs
 // without lo·lo): 16 bits, an error near 2^-18 a product.  One term for P and E would do for y's own rounding,
 // but not where keys repeat: the corrections are then differences of values, and P E cancels most of them.
 // Accumulation is fp32, the state is kept in fp32 registers.
-//
-// Warps: 0..15 state (above); 16..23 two groups that prepare (per-token scalars, K Kᵀ and Q Kᵀ, the inverse T), one
-// the even and one the odd chunks, up to two chunks ahead of the chain; 24 issues the chain's MMAs; 25 the TMA
-// loads (three tiles of K and Q, one of V in flight); 26 stores y.  They hand over through mbarriers.  Every wait
-// is bounded: one that runs out records SS_ERR_TIMEOUT and the CTA winds down.
 #pragma once
 
 #include "../../include/selscan.h"
@@ -58,62 +47,27 @@ using tc::tmem_ld32;
 using tc::umma;
 using tc::umma_commit;
 
-constexpr int kC = 64;                 // tokens of a chunk
-constexpr int kStages = 3;             // K, Q tiles in flight (they are prepared ahead)
-constexpr int kVStages = 1;            // V tiles in flight (read at a chunk's start alone)
-constexpr int kParts = 4;              // threads to a row of the state
-constexpr int kStateWarps = 4 * kParts, kGroupWarps = 4;
-constexpr int kPrepWarp = kStateWarps;                       // two groups
-constexpr int kMmaWarp = kPrepWarp + 2 * kGroupWarps, kLoadWarp = kMmaWarp + 1, kStoreWarp = kMmaWarp + 2;
-constexpr int kThreads = 32 * (kStoreWarp + 1);
-constexpr int kTok = kC / kParts;      // tokens of a state thread
+constexpr int kC = 64;                  // tokens of a chunk
+constexpr uint32_t kTile = 8192;        // 64 rows of 128 bytes, 128-byte swizzle
+constexpr int kPitchX = 36;             // floats from row to row of the inverse's scratch
 
-// TMEM columns.  A: KS, then X's terms over it, then W's; B: E in two halves, then its terms over the first; S: the
-// state's terms (of each 16 keys, hi then lo), then dS over them.
-constexpr uint32_t kColS = 0, kColA = 128, kColQS = 192, kColB = 256, kColY = 384, kColGram = 448;
-constexpr uint32_t kTmemCols = 512;
-
-// Shared memory: byte offsets from a 1024-aligned base.
-constexpr uint32_t kTile = 8192;                       // 64 rows of 128 bytes, 128-byte swizzle
-constexpr uint32_t kStageBytes = 4 * kTile;            // [K 0][Q 0][K 1][Q 1]
-constexpr uint32_t kOffV = kStages * kStageBytes;      // [V 0][V 1]
-constexpr uint32_t kVBytes = 2 * kTile;
-constexpr uint32_t kOffPrep = kOffV + kVStages * kVBytes;   // two buffers of [T hi][T lo][P hi][P lo]; while T is
-constexpr uint32_t kPrepBytes = 4 * kTile;                  // computed, fp32 [64][64] in the place of its terms
-constexpr uint32_t kOffY = kOffPrep + 2 * kPrepBytes;  // y [64][d_v] for the store
-constexpr uint32_t kOffXs = kOffY + 2 * kTile;         // block products of each group, fp32 [32][36]
-constexpr int kPitchX = 36;
-constexpr uint32_t kXsBytes = 32 * kPitchX * 4;
-constexpr uint32_t kOffScal = kOffXs + 2 * kXsBytes;
-constexpr int kScals = 4;              // buffers of per-token factors: chunk c's are written once K and Q of chunk c
-                                       // landed, in the place of chunk c - 3's, whose MMAs are done: its successor
-                                       // in the ring, chunk c - 4, was read before those were issued
-constexpr uint32_t kScalBytes = (3 * kC + 4) * 4;
-constexpr uint32_t kOffLocal = kOffScal + kScals * kScalBytes;   // what only a prepare group uses
-constexpr uint32_t kLocalBytes = 4 * kC * 4 + kC * 8;
-constexpr uint32_t kOffBar = kOffLocal + 2 * kLocalBytes;
-constexpr uint32_t kSmemBytes = kOffBar + 512 + 1024;
-static_assert(kOffScal % 16 == 0 && kOffLocal % 16 == 0 && kOffBar % 16 == 0, "aligned regions");
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-
-struct alignas(16) Scal {   // one chunk's factors, as the state warps read them
+struct alignas(16) Scal {   // one chunk's factors
     float ek[kC];           // -e^{G_i} / |k_i|
     float wk[kC];           // β_i e^{G_end - G_i} / |k_i|
     float qe[kC];           // scale e^{G_i} / |q_i|
     float end[4];           // e^{G_end}
+    float pad[60];
 };
-static_assert(sizeof(Scal) == kScalBytes, "layout");
-
-struct alignas(16) Local {  // one chunk's factors, for its prepare group
-    float gh[kC], gl[kC];   // log2 of the decay from the chunk's start, as a pair
-    float cb[kC];           // β_j / |k_j|
-    float cf[kC];           // β_j / |k_j| e^{G_31 - G_j}, j < 32
-    double G[kC];           // prefix sums over 32 tokens
-};
-static_assert(sizeof(Local) == kLocalBytes, "layout");
+// One chunk's record in the workspace: T and P, each as two bf16 terms in the swizzled layout that the MMAs read, then
+// the factors.
+constexpr uint32_t kRecT = 0, kRecP = 2 * kTile, kRecScal = 4 * kTile;
+constexpr uint32_t kRecBytes = kRecScal + sizeof(Scal);
+static_assert(sizeof(Scal) == 1024 && kRecBytes % 16 == 0, "records are copied whole");
 
 struct Params {
     GdrParams g;
+    unsigned char* rec;      // [items][nchunks] records
+    int64_t nchunks;         // chunks of g.L tokens
     uint32_t* status;
     int dv;
     int test_drop;
@@ -197,36 +151,16 @@ __device__ __forceinline__ void scale16(f32x2 (&v)[8], const float* f) {
     }
 }
 
-// Named barrier of a prepare group (128 threads).
-__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ bool group_any(int id, bool pred) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, %2, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(pred ? 1u : 0u), "r"(id)
-        : "memory");
-    return r != 0;
-}
 
-struct Bars {
-    uint64_t full[kStages];    // K and Q of a stage landed
-    uint64_t empty[kStages];   // the chunk's last MMA is done with the stage
-    uint64_t v_full[kVStages], v_empty[kVStages];   // V landed; its product done
-    uint64_t prep_full[2];     // T, P and the factors of a buffer written (4 warps)
-    uint64_t t_empty[2], p_empty[2];   // a buffer's T, P read by their last MMA
-    uint64_t gram, gram_free;  // K Kᵀ and Q Kᵀ of a chunk done; read (4 warps)
-    uint64_t ks, e, ds, pv;    // the chain's products done
-    uint64_t s_ready;          // S's terms written (state warps)
-    uint64_t x_ready, w_ready; // X's terms; W's and E's, and Y's first part, written (state warps)
-    uint64_t y_full, y_free;   // y staged (state warps); stored (1)
-    uint64_t fin[3];           // wind-down
-    uint32_t tmem;
-};
-static_assert(sizeof(Bars) <= 512, "barrier region");
+// The untiled bulk copies: shared memory to global memory, and back (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
 
 // Float offset of element (i, j) of the fp32 [64][64] matrix: 16-byte quads permuted within a row, so that the same
 // quad of eight consecutive rows lies in eight different banks.
@@ -239,11 +173,11 @@ __device__ __forceinline__ void axpy4(f32x2 (&acc)[2], float u, float4 w) {
 }
 __device__ __forceinline__ float4 quad(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-// (I + A')^-1 of the strictly lower triangular A' in `a`, in place, by a prepare group: the four 16-blocks on the
+// (I + A')^-1 of the strictly lower triangular A' in `a`, in place, by 128 threads: the four 16-blocks on the
 // diagonal row by row (x (I + A') = a unit row, from its last entry back: a subtracted row of A' per step, with no
 // sum to wait for), then T21 = -T22 A21 T11 of the two 32-blocks and of the whole.  fp32 throughout.  The 32 x 32
 // block above the diagonal is neither read nor written.
-__device__ __forceinline__ void invert64(float* a, float* xs, int pt, int id) {
+__device__ __forceinline__ void invert64(float* a, float* xs, int pt) {
     {
         const int o = 16 * (pt >> 5), i = pt & 15;
         float x[16];
@@ -269,7 +203,7 @@ __device__ __forceinline__ void invert64(float* a, float* xs, int pt, int id) {
                 *reinterpret_cast<float4*>(a + at(o + i, o + j)) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
         }
     }
-    group_sync(id);
+    __syncthreads();
     {   // 16-blocks: threads 64 m .. 64 m + 63 on the 32-block m, a quad of a row each
         const int m = pt >> 6, r = (pt & 63) >> 2, c = (pt & 3) * 4, o = 32 * m;
         float* x = xs + m * 16 * kPitchX + c;
@@ -288,7 +222,7 @@ __device__ __forceinline__ void invert64(float* a, float* xs, int pt, int id) {
             for (int e = 0; e < 4; ++e) axpy4(s, uu[e], quad(wc + (k + e) * kC + oc[(k + e) & 7]));
         }
         *reinterpret_cast<float4*>(x + r * kPitchX) = make_float4(-s[0].x, -s[0].y, -s[1].x, -s[1].y);
-        group_sync(id);
+        __syncthreads();
         s[0] = s[1] = pk2(0.0f, 0.0f);
 #pragma unroll
         for (int k = 0; k < 16; k += 4) {
@@ -299,7 +233,7 @@ __device__ __forceinline__ void invert64(float* a, float* xs, int pt, int id) {
         }
         *reinterpret_cast<float4*>(a + at(o + 16 + r, o + c)) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
     }
-    group_sync(id);
+    __syncthreads();
     {   // 32-blocks: a quad of two rows each
         const int r = (pt >> 3) * 2, c = (pt & 7) * 4, r7 = r & 7;   // (r even: row r + 1's permutation is r7 ^ 1)
         const float* ur = a + (32 + r) * kC;
@@ -321,7 +255,7 @@ __device__ __forceinline__ void invert64(float* a, float* xs, int pt, int id) {
         }
         *reinterpret_cast<float4*>(x + r * kPitchX) = make_float4(-s[0].x, -s[0].y, -s[1].x, -s[1].y);
         *reinterpret_cast<float4*>(x + (r + 1) * kPitchX) = make_float4(-w[0].x, -w[0].y, -w[1].x, -w[1].y);
-        group_sync(id);
+        __syncthreads();
         s[0] = s[1] = w[0] = w[1] = pk2(0.0f, 0.0f);
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
@@ -337,7 +271,7 @@ __device__ __forceinline__ void invert64(float* a, float* xs, int pt, int id) {
         *reinterpret_cast<float4*>(a + at(32 + r, c)) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
         *reinterpret_cast<float4*>(a + at(33 + r, c)) = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
     }
-    group_sync(id);
+    __syncthreads();
 }
 
 // v[i] for a runtime i < 32: a tree of selects on the bits of i.
@@ -354,6 +288,294 @@ __device__ __forceinline__ float pick32(const float (&v)[32], int i) {
     return (i & 1) ? a[1] : a[0];
 }
 
+// ------------------------------------------------------------------------------------------ preparation
+constexpr int kPrepThreads = 128;
+
+struct alignas(16) Local {
+    float gh[kC], gl[kC];   // log2 of the decay from the chunk's start, as a pair
+    float cb[kC];           // β_j / |k_j|
+    float cf[kC];           // β_j / |k_j| e^{G_31 - G_j}, j < 32
+    double G[kC];           // prefix sums over 32 tokens
+    uint64_t full, gram;
+    uint32_t tmem, pad[3];
+};
+// Shared memory: [K 0][Q 0][K 1][Q 1], P's terms over the first two once K and Q have been read; T as fp32 [64][64],
+// then T's terms in its place; the factors; scratch.
+constexpr uint32_t kPrepT = 4 * kTile, kPrepScal = 6 * kTile, kPrepXs = kPrepScal + sizeof(Scal);
+constexpr uint32_t kPrepLocal = kPrepXs + 32 * kPitchX * 4;
+constexpr uint32_t kPrepSmem = kPrepLocal + sizeof(Local) + 1024;
+
+// Grid: one block per (item, chunk), a sequence's chunks together.  Bound by the latency of the triangular inverse
+// (fp32, about 75 000 multiply-adds in a dozen dependent steps), which the four resident blocks hide for one another.
+template <int DK>
+__global__ void __launch_bounds__(kPrepThreads)
+ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_q,
+                   const __grid_constant__ CUtensorMap tm_k) {
+    constexpr int KB = DK / 64;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    unsigned char* gbase = smem_raw + (base - raw);
+    Scal& sc = *reinterpret_cast<Scal*>(gbase + kPrepScal);
+    Local& lo = *reinterpret_cast<Local*>(gbase + kPrepLocal);
+    float* const a = reinterpret_cast<float*>(gbase + kPrepT);
+    float* const xs = reinterpret_cast<float*>(gbase + kPrepXs);
+
+    const GdrParams& g = p.g;
+    const int pt = threadIdx.x, lane = pt & 31, warp = pt >> 5, i = pt & 63, rb = warp & 1;   // row i, its 32-block
+    const bool is_q = pt >= 64;
+    const int64_t item = blockIdx.x / p.nchunks, c = blockIdx.x % p.nchunks;
+    const int b = static_cast<int>(item / g.H), h = static_cast<int>(item % g.H), hk = h / (g.H / g.Hk);
+    const int64_t left = gdr_len(g, b) - c * kC;
+    if (left <= 0) return;
+    const int valid = left < kC ? static_cast<int>(left) : kC;
+
+    if (pt == 0) {
+        mbar_init(&lo.full, 1);
+        mbar_init(&lo.gram, 1);
+        fence_mbar_init();
+        mbar_arrive_expect_tx(&lo.full, 2 * KB * kTile);
+        for (int kb = 0; kb < KB; ++kb) {
+            tma_load_4d(base + (2 * kb) * kTile, &tm_k, 64 * kb, hk, static_cast<int>(c) * kC, b, &lo.full);
+            tma_load_4d(base + (2 * kb + 1) * kTile, &tm_q, 64 * kb, hk, static_cast<int>(c) * kC, b, &lo.full);
+        }
+    }
+    if (warp == 0) {
+        tc::tmem_alloc(&lo.tmem, kC);
+        tc::tmem_relinquish();
+    }
+    float be = 0.0f;
+    double G = 0.0;
+    if (!is_q) {   // the gates, while K and Q come in
+        const int64_t o = (static_cast<int64_t>(b) * g.L + c * kC + i) * g.H + h;
+        float delta = 0.0f;
+        if (i < valid) {
+            delta = gdr_delta(to_f32(static_cast<const __nv_bfloat16*>(g.dt)[o]), g.dt_bias ? g.dt_bias[h] : 0.0f, g.softplus);
+            be = gdr_beta(to_f32(static_cast<const __nv_bfloat16*>(g.beta)[o]), g.sigmoid);
+        }
+        G = static_cast<double>(delta) * static_cast<double>(g.A[h]) * 1.4426950408889634074;   // log2 α
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const double v = __shfl_up_sync(0xffffffffu, G, s);
+            if (lane >= s) G += v;
+        }
+        lo.G[i] = G;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = lo.tmem;
+    bool got = mbar_wait_bounded(&lo.full, 0, p.wait_ns);
+    if (valid < kC) {   // rows behind the end, whatever they hold, become zero rows
+        if (i >= valid && got) {
+            for (int w = 0; w < 8 * KB; ++w)
+                sts128(base + (2 * (w >> 3) + (is_q ? 1 : 0)) * kTile + i * 128 + (w & 7) * 16, make_uint4(0, 0, 0, 0));
+            fence_proxy_async_smem();
+        }
+        __syncthreads();
+    }
+    const bool issued = got && pt == 0;
+    if (issued) {   // [K; Q] Kᵀ: lanes 0..63 K's rows, 64..127 Q's
+#pragma unroll
+        for (int ks = 0; ks < DK / 16; ++ks) {
+            const uint32_t off = (ks >> 2) * 2 * kTile + (ks & 3) * 32;
+            umma(tmem, sdesc(base + off, 16, 1024), sdesc(base + off, 16, 1024), idesc(kC, false), ks > 0);
+        }
+        umma_commit(&lo.gram);
+    }
+    const double first = lo.G[31], end = first + lo.G[63];
+    float rn = 1.0f;   // 1 / |row i| of K, or of Q
+    if (!is_q) {
+        if (i >= 32) G += first;
+        const float hi = static_cast<float>(G);
+        lo.gh[i] = hi;
+        lo.gl[i] = static_cast<float>(G - static_cast<double>(hi));
+        if (i == 0) sc.end[0] = exp2f(static_cast<float>(end));
+    } else if (g.l2norm) {
+        f32x2 q0 = pk2(0.0f, 0.0f), q1 = q0;
+#pragma unroll
+        for (int w = 0; w < 8 * KB; ++w) {
+            const uint4 x = lds128(chunk_addr(base + (2 * (w >> 3) + 1) * kTile, i, w & 7));
+            const f32x2 x0 = pk2(lo_f(x.x), hi_f(x.x)), x1 = pk2(lo_f(x.y), hi_f(x.y));
+            const f32x2 x2 = pk2(lo_f(x.z), hi_f(x.z)), x3 = pk2(lo_f(x.w), hi_f(x.w));
+            q0 = fma2(x0, x0, fma2(x2, x2, q0));
+            q1 = fma2(x1, x1, fma2(x3, x3, q1));
+        }
+        rn = 1.0f / sqrtf((q0.x + q0.y) + (q1.x + q1.y) + kGdrL2Eps);
+    }
+    if (got) got = mbar_wait_bounded(&lo.gram, 0, p.wait_ns);
+    const bool bad = __syncthreads_or(!got) != 0;
+    if (bad) {
+        if (pt == 0 && p.status) atomicCAS(p.status, 0u, static_cast<uint32_t>(SS_ERR_TIMEOUT));
+    } else {
+        tc_fence_after();
+        const uint32_t src = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        float v[32];
+        tmem_ld32(src + 32 * rb, v);   // the block on the diagonal
+        if (!is_q) {                   // |k_i|² is K Kᵀ's own diagonal
+            if (g.l2norm) rn = 1.0f / sqrtf(pick32(v, lane) + kGdrL2Eps);
+            lo.cb[i] = be * rn;
+            if (rb == 0) lo.cf[i] = be * rn * exp2f(static_cast<float>(first - G));
+            sc.ek[i] = -exp2f(static_cast<float>(G)) * rn;
+            sc.wk[i] = be * exp2f(static_cast<float>(end - G)) * rn;
+        }
+        __syncthreads();
+        const float gh = lo.gh[i], gl = lo.gl[i];
+        const float row = is_q ? rn * g.scale : rn;
+        if (is_q) sc.qe[i] = exp2f(gh) * row;
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk) {
+            // first the block on the diagonal, then (rows 32..63) the block left of it; above the diagonal P is zero
+            if (blk == 1) {
+                if (rb == 0) {
+                    if (is_q)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            sts128(chunk_addr(base, i, 4 + w), make_uint4(0, 0, 0, 0));
+                            sts128(chunk_addr(base + kTile, i, 4 + w), make_uint4(0, 0, 0, 0));
+                        }
+                    break;
+                }
+                tmem_ld32(src, v);
+            }
+            const int j0 = blk == 0 ? 32 * rb : 0;
+            if (blk == 0) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 h4 = quad(lo.gh + j0 + e), l4 = quad(lo.gl + j0 + e), c4 = quad(lo.cb + j0 + e);
+                    const f32x2 hh[2] = {pk2(h4.x, h4.y), pk2(h4.z, h4.w)}, ll[2] = {pk2(l4.x, l4.y), pk2(l4.z, l4.w)};
+                    const f32x2 cc[2] = {pk2(c4.x, c4.y), pk2(c4.z, c4.w)};
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const f32x2 m1 = pk2(-1.0f, -1.0f);
+                        const f32x2 d = add2(fma2(hh[f], m1, pk2(gh, gh)), fma2(ll[f], m1, pk2(gl, gl)));
+                        const f32x2 w = mul2(mul2(pk2(v[e + 2 * f], v[e + 2 * f + 1]), cc[f]), pk2(row, row));
+                        const f32x2 r = mul2(w, pk2(ex2_approx(d.x), ex2_approx(d.y)));
+                        const int k = e + 2 * f - (is_q ? 1 : 0);   // P keeps its diagonal
+                        v[e + 2 * f] = k < lane ? r.x : 0.0f;
+                        v[e + 2 * f + 1] = k + 1 < lane ? r.y : 0.0f;
+                    }
+                }
+            } else {   // j < 32 <= i: both factors of e^{G_i - G_31} e^{G_31 - G_j} lie between the product and 1
+                const float rf = row * exp2f(static_cast<float>((static_cast<double>(gh) + static_cast<double>(gl)) - first));
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 c4 = quad(lo.cf + e);
+                    const f32x2 r0 = mul2(mul2(pk2(v[e], v[e + 1]), pk2(c4.x, c4.y)), pk2(rf, rf));
+                    const f32x2 r1 = mul2(mul2(pk2(v[e + 2], v[e + 3]), pk2(c4.z, c4.w)), pk2(rf, rf));
+                    v[e] = r0.x;
+                    v[e + 1] = r0.y;
+                    v[e + 2] = r1.x;
+                    v[e + 3] = r1.y;
+                }
+            }
+            if (is_q) {   // (K and Q have been read: by the MMAs, and by the lengths before the barriers above)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t hw[4], lw[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) split2(pk2(v[8 * w + 2 * e], v[8 * w + 2 * e + 1]), hw[e], lw[e]);
+                    sts128(chunk_addr(base, i, j0 / 8 + w), make_uint4(hw[0], hw[1], hw[2], hw[3]));
+                    sts128(chunk_addr(base + kTile, i, j0 / 8 + w), make_uint4(lw[0], lw[1], lw[2], lw[3]));
+                }
+            } else {
+#pragma unroll
+                for (int w = 0; w < 8; ++w)
+                    *reinterpret_cast<float4*>(a + at(i, j0 + 4 * w)) =
+                        make_float4(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
+            }
+        }
+        __syncthreads();
+        invert64(a, xs, pt);
+        {   // T as two bf16 terms in its own place: half a row each (row pt & 63), read by all first
+            const int hf = pt >> 6;
+            float4 u[8];
+#pragma unroll
+            for (int w = 0; w < 8; ++w)   // (the block above the diagonal holds nothing)
+                u[w] = i >= 32 || hf == 0 ? quad(a + at(i, 32 * hf + 4 * w)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                uint32_t hw[4], lw[4];
+                split2(pk2(u[2 * w].x, u[2 * w].y), hw[0], lw[0]);
+                split2(pk2(u[2 * w].z, u[2 * w].w), hw[1], lw[1]);
+                split2(pk2(u[2 * w + 1].x, u[2 * w + 1].y), hw[2], lw[2]);
+                split2(pk2(u[2 * w + 1].z, u[2 * w + 1].w), hw[3], lw[3]);
+                sts128(chunk_addr(base + kPrepT, i, 4 * hf + w), make_uint4(hw[0], hw[1], hw[2], hw[3]));
+                sts128(chunk_addr(base + kPrepT + kTile, i, 4 * hf + w), make_uint4(lw[0], lw[1], lw[2], lw[3]));
+            }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (pt == 0) {
+        if (!bad) {
+            unsigned char* r = p.rec + (item * p.nchunks + c) * kRecBytes;
+            bulk_store(r + kRecT, base + kPrepT, 2 * kTile);
+            bulk_store(r + kRecP, base, 2 * kTile);
+            bulk_store(r + kRecScal, base + kPrepScal, sizeof(Scal));
+            tc::bulk_commit();
+            bulk_wait0();
+        } else {   // what is still in flight ends before the shared memory and the TMEM columns go
+            mbar_wait_bounded(&lo.full, 0, p.drain_ns);
+            if (issued) mbar_wait_bounded(&lo.gram, 0, p.drain_ns);
+        }
+    }
+    __syncwarp();
+    if (warp == 0) {
+        tc_fence_after();
+        tc::tmem_dealloc(tmem, kC);
+    }
+}
+
+// ------------------------------------------------------------------------------------------------ chain
+// The products run transposed: the 128 TMEM lanes are the rows v of the state, and the columns are tokens or keys.
+//   KS, QS [v, i] = S Kᵀ, S Qᵀ      A: S (TMEM),  B: K and Q tiles in one, K-major
+//   E   [v, i] = Vᵀ Tᵀ + X Tᵀ       A: V tile, MN-major; X = -KS diag(e^G / |k|) (TMEM),  B: T tile, K-major
+//   dS  [v, k] = W K                A: W = E diag(β e^{G_end - G} / |k|) (TMEM),  B: K tile, MN-major
+//   Yᵀ  [v, i] = QS diag(scale e^G / |q|) + E Pᵀ    off the chain, under the element-wise steps
+// so that the state, the right hand side and the corrections go from registers to TMEM and never through shared
+// memory, a thread owning one row v (four threads to a row, each with a quarter of the columns).  X is written over
+// KS, E's terms over E, S's terms over dS, by the thread that read them, which is what makes it fit in TMEM.
+// An MMA of 128 x N x 16 takes about 64 cycles for every N up to 128 (measured here), so operands are put side by
+// side to N = 128 where they share A: K with Q, and T's two terms, whose two halves of E the reader adds.
+//
+// Warps: 0..15 state (above); 16 issues the MMAs; 17 the loads (two chunks in flight); 18 stores y.  They hand over
+// through mbarriers.  Every wait is bounded: one that runs out records SS_ERR_TIMEOUT and the CTA winds down.
+constexpr int kParts = 4;              // threads to a row of the state
+constexpr int kStateWarps = 4 * kParts;
+constexpr int kMmaWarp = kStateWarps, kLoadWarp = kMmaWarp + 1, kStoreWarp = kMmaWarp + 2;
+constexpr int kThreads = 32 * (kStoreWarp + 1);
+constexpr int kTok = kC / kParts;      // tokens of a state thread
+constexpr int kStages = 2;             // chunks in flight
+
+// TMEM columns.  A: KS, then X's terms over it, then W's; B: E in two halves, then its terms over the first; S: the
+// state's terms (of each 16 keys, hi then lo), then dS over them.
+constexpr uint32_t kColS = 0, kColA = 128, kColQS = 192, kColB = 256, kColY = 384;
+constexpr uint32_t kTmemCols = 512;
+
+// Shared memory: byte offsets from a 1024-aligned base.  A stage: [K 0][Q 0][K 1][Q 1][V 0][V 1][record]
+constexpr uint32_t kOffV = 4 * kTile, kOffRec = 6 * kTile;
+constexpr uint32_t kStageBytes = kOffRec + kRecBytes;
+static_assert(kStageBytes % 1024 == 0, "swizzled tiles");
+constexpr uint32_t kOffY = kStages * kStageBytes;      // y [64][d_v] for the store
+constexpr uint32_t kOffBar = kOffY + 2 * kTile;
+constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+struct Bars {
+    uint64_t full[kStages];    // K, Q, V and the record of a stage landed
+    uint64_t empty[kStages];   // the chunk's last MMA is done with the stage
+    uint64_t ks, e, ds, pv;    // the chain's products done
+    uint64_t s_ready;          // S's terms written (state warps)
+    uint64_t x_ready, w_ready; // X's terms; W's and E's, and Y's first part, written (state warps)
+    uint64_t y_full, y_free;   // y staged (state warps); stored (1)
+    uint64_t fin;              // wind-down
+    uint32_t tmem;
+};
+static_assert(sizeof(Bars) <= 256, "barrier region");
+
 // Grid: one CTA per (b, h).
 template <int DK>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -367,13 +589,14 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
     const uint32_t base = (raw + 1023u) & ~1023u;
     unsigned char* gbase = smem_raw + (base - raw);
     Bars* const bar = reinterpret_cast<Bars*>(gbase + kOffBar);
-    Scal* const scal = reinterpret_cast<Scal*>(gbase + kOffScal);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const GdrParams& g = p.g;
     const int item = blockIdx.x, b = item / g.H, h = item % g.H, hk = h / (g.H / g.Hk);
     const int64_t len = gdr_len(g, b);
     const int nchunk = static_cast<int>((len + kC - 1) / kC);
+    // the last chunk of a sequence that ends before the tensor does: other tokens follow in its tile
+    const int ragged = (len % kC != 0 && len < g.L) ? nchunk - 1 : -1;
     const uint64_t lim = p.wait_ns;
 
     if (tid == 0) {
@@ -381,20 +604,10 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             mbar_init(&bar->full[i], 1);
             mbar_init(&bar->empty[i], 1);
         }
-        for (int i = 0; i < kVStages; ++i) {
-            mbar_init(&bar->v_full[i], 1);
-            mbar_init(&bar->v_empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar->prep_full[i], kGroupWarps);
-            mbar_init(&bar->t_empty[i], 1);
-            mbar_init(&bar->p_empty[i], 1);
-        }
-        uint64_t* one[] = {&bar->ks, &bar->e, &bar->ds, &bar->pv, &bar->gram, &bar->y_free, bar->fin, bar->fin + 1, bar->fin + 2};
+        uint64_t* one[] = {&bar->ks, &bar->e, &bar->ds, &bar->pv, &bar->y_free, &bar->fin};
         for (uint64_t* x : one) mbar_init(x, 1);
         uint64_t* all[] = {&bar->s_ready, &bar->x_ready, &bar->w_ready, &bar->y_full};
         for (uint64_t* x : all) mbar_init(x, kStateWarps);
-        mbar_init(&bar->gram_free, kGroupWarps);
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -424,7 +637,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         __syncwarp();
         if (lane == 0) mbar_arrive(x);
     };
-    int issued = 0, v_issued = 0;   // loads of the load thread
+    int issued = 0;   // loads of the load thread
 
     if (warp == kLoadWarp) {
         // ============================================================ loads (one thread)
@@ -433,20 +646,19 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_v);
             for (int c = 0; c < nchunk; ++c) {
-                const int s = c % kStages, vs = c % kVStages;
+                const int s = c % kStages;
                 if (c >= kStages && !wait1(&bar->empty[s], ((c / kStages) - 1) & 1)) break;
                 const uint32_t st = base + s * kStageBytes;
-                mbar_arrive_expect_tx(&bar->full[s], 2 * KB * kTile);
+                uint64_t* f = &bar->full[s];
+                mbar_arrive_expect_tx(f, 2 * KB * kTile + kC * p.dv * 2 + kRecBytes);
                 for (int kb = 0; kb < KB; ++kb) {
-                    tma_load_4d(st + (2 * kb) * kTile, &tm_k, 64 * kb, hk, c * kC, b, &bar->full[s]);
-                    tma_load_4d(st + (2 * kb + 1) * kTile, &tm_q, 64 * kb, hk, c * kC, b, &bar->full[s]);
+                    tma_load_4d(st + (2 * kb) * kTile, &tm_k, 64 * kb, hk, c * kC, b, f);
+                    tma_load_4d(st + (2 * kb + 1) * kTile, &tm_q, 64 * kb, hk, c * kC, b, f);
                 }
-                issued = c + 1;
-                if (c >= kVStages && !wait1(&bar->v_empty[vs], ((c / kVStages) - 1) & 1)) break;
-                mbar_arrive_expect_tx(&bar->v_full[vs], kC * p.dv * 2);
                 for (int vb = 0; vb < p.dv / 64; ++vb)
-                    tma_load_4d(base + kOffV + vs * kVBytes + vb * kTile, &tm_v, 64 * vb, h, c * kC, b, &bar->v_full[vs]);
-                v_issued = c + 1;
+                    tma_load_4d(st + kOffV + vb * kTile, &tm_v, 64 * vb, h, c * kC, b, f);
+                bulk_load(st + kOffRec, p.rec + (item * p.nchunks + c) * kRecBytes, kRecBytes, f);
+                issued = c + 1;
             }
         }
         __syncwarp();
@@ -454,14 +666,14 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         // ============================================================ y
         for (int c = 0; c < nchunk; ++c) {
             if (!wait_warp(&bar->y_full, c & 1)) break;
-            const int64_t t0 = static_cast<int64_t>(c) * kC;
-            if (t0 + kC <= len || len == g.L) {   // rows behind the tensor's end are clipped by the copy
+            if (c != ragged) {   // rows behind the tensor's end are clipped by the copy
                 if (lane == 0) {
                     tc::tma_store_4d(&tm_y, base + kOffY, 0, h, c * kC, b);
                     tc::bulk_commit();
                     tc::bulk_wait_read0();
                 }
-            } else {                              // rows behind the sequence's end stay as they are
+            } else {             // rows behind the sequence's end stay as they are
+                const int64_t t0 = static_cast<int64_t>(c) * kC;
                 const int quads = p.dv / 8, n = static_cast<int>(len - t0) * quads;
                 __nv_bfloat16* y = static_cast<__nv_bfloat16*>(g.y);
                 for (int i = lane; i < n; i += 32) {
@@ -475,23 +687,21 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         if (lane == 0) bulk_wait0();
         __syncwarp();
     } else if (warp == kMmaWarp) {
-        // ============================================================ the chain's MMAs (one thread)
+        // ============================================================ MMAs (one thread)
         if (lane == 0) {
             const uint32_t vlbo = p.dv == 128 ? kTile : 0;   // d_v 64: the lanes 64.. repeat the rows 0..63
             for (int c = 0; c < nchunk; ++c) {
-                const int s = c % kStages, pb = c & 1, vs = c % kVStages;
-                const uint32_t par = c & 1, st = base + s * kStageBytes, vt = base + kOffV + vs * kVBytes;
-                const uint32_t pr = base + kOffPrep + pb * kPrepBytes;
-                if (!wait1(&bar->prep_full[pb], (c >> 1) & 1)) break;   // (K and Q landed, rows behind the end zero)
-                if (!wait1(&bar->v_full[vs], (c / kVStages) & 1)) break;
+                const int s = c % kStages;
+                const uint32_t par = c & 1, st = base + s * kStageBytes, pr = st + kOffRec;
+                if (!wait1(&bar->full[s], (c / kStages) & 1)) break;
+                if (c == ragged && !wait1(&bar->s_ready, par)) break;   // rows behind the end are zeroed by then
                 if (c > 0 && !wait1(&bar->pv, (c - 1) & 1)) break;      // the last chunk's E is read
                 tc_fence_after();
                 // E = Vᵀ Tᵀ, T's terms side by side
 #pragma unroll
                 for (int j = 0; j < kC / 16; ++j)
-                    umma(tmem + kColB, sdesc(vt + 2048u * j, vlbo, 1024), sdesc(pr + 32u * j, 16, 1024),
+                    umma(tmem + kColB, sdesc(st + kOffV + 2048u * j, vlbo, 1024), sdesc(pr + kRecT + 32u * j, 16, 1024),
                          idesc(2 * kC, false, true), j > 0);
-                umma_commit(&bar->v_empty[vs]);
                 if (!wait1(&bar->s_ready, par)) break;
                 tc_fence_after();
                 // KS and QS: S's terms of 16 keys in 16 columns, K and Q of a 64-key block side by side
@@ -507,11 +717,11 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 // E += X Tᵀ
 #pragma unroll
                 for (int j = 0; j < kC / 16; ++j) {
-                    umma_ts(tmem + kColB, tmem + kColA + 16 * j, sdesc(pr + 32u * j, 16, 1024), idesc(2 * kC, false), 1);
-                    umma_ts(tmem + kColB, tmem + kColA + 16 * j + 8, sdesc(pr + 32u * j, 16, 1024), idesc(kC, false), 1);
+                    const uint64_t bd = sdesc(pr + kRecT + 32u * j, 16, 1024);
+                    umma_ts(tmem + kColB, tmem + kColA + 16 * j, bd, idesc(2 * kC, false), 1);
+                    umma_ts(tmem + kColB, tmem + kColA + 16 * j + 8, bd, idesc(kC, false), 1);
                 }
                 umma_commit(&bar->e);
-                umma_commit(&bar->t_empty[pb]);
                 if (!wait1(&bar->w_ready, par)) break;
                 tc_fence_after();
                 // dS = W K over the columns of S's terms
@@ -522,217 +732,20 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                     umma_ts(tmem + kColS, tmem + kColA + 16 * j + 8, bd, idesc(DK, true), 1);
                 }
                 umma_commit(&bar->ds);
-                // Yᵀ += E (P β)ᵀ: tokens 16 j .. 16 j + 15 reach the rows i >= 16 j of P alone
+                // Yᵀ += E Pᵀ: tokens 16 j .. 16 j + 15 reach the rows i >= 16 j of P alone
 #pragma unroll
                 for (int j = 0; j < kC / 16; ++j) {
-                    const uint32_t n = kC - 16 * j, row = 2 * kTile + 2048u * j + 32u * j;
+                    const uint32_t n = kC - 16 * j, row = pr + kRecP + 2048u * j + 32u * j;
                     const uint32_t d = tmem + kColY + 16 * j, x = tmem + kColB + 16 * j;
-                    umma_ts(d, x, sdesc(pr + row, 16, 1024), idesc(n, false), 1);
-                    umma_ts(d, x, sdesc(pr + kTile + row, 16, 1024), idesc(n, false), 1);
-                    umma_ts(d, x + 8, sdesc(pr + row, 16, 1024), idesc(n, false), 1);
+                    umma_ts(d, x, sdesc(row, 16, 1024), idesc(n, false), 1);
+                    umma_ts(d, x, sdesc(row + kTile, 16, 1024), idesc(n, false), 1);
+                    umma_ts(d, x + 8, sdesc(row, 16, 1024), idesc(n, false), 1);
                 }
                 umma_commit(&bar->pv);
                 umma_commit(&bar->empty[s]);
-                umma_commit(&bar->p_empty[pb]);
             }
         }
         __syncwarp();
-    } else if (warp >= kPrepWarp) {
-        // ============================================================ prepare groups
-        const int grp = (warp - kPrepWarp) >> 2, id = 1 + grp;
-        const int pt = tid - 32 * (kPrepWarp + 4 * grp), i = pt & 63, rb = (pt >> 5) & 1;   // row i, its 32-block rb
-        const bool is_q = pt >= 64;
-        Local& lo = reinterpret_cast<Local*>(gbase + kOffLocal)[grp];
-        float* const xs = reinterpret_cast<float*>(gbase + kOffXs + grp * kXsBytes);
-        const uint32_t pr = base + kOffPrep + grp * kPrepBytes;
-        float* const a = reinterpret_cast<float*>(gbase + kOffPrep + grp * kPrepBytes);
-        const uint32_t gram = tmem + kColGram;
-        const float Ah = g.A[h], bias = g.dt_bias ? g.dt_bias[h] : 0.0f;
-        const __nv_bfloat16* dtp = static_cast<const __nv_bfloat16*>(g.dt);
-        const __nv_bfloat16* bep = static_cast<const __nv_bfloat16*>(g.beta);
-        float dt_n = 0.0f, be_n = 0.0f;
-        auto fetch = [&](int c) {   // the raw gates of this thread's token
-            const int64_t t = static_cast<int64_t>(c) * kC + i;
-            if (!is_q && t < len) {
-                const int64_t o = (static_cast<int64_t>(b) * g.L + t) * g.H + h;
-                dt_n = to_f32(dtp[o]);
-                be_n = to_f32(bep[o]);
-            }
-        };
-        if (grp < nchunk) fetch(grp);
-        for (int c = grp; c < nchunk; c += 2) {
-            const int s = c % kStages;
-            const uint32_t st = base + s * kStageBytes, ph = (c >> 1) & 1;
-            Scal& sc = scal[c % kScals];
-            const int64_t left = len - static_cast<int64_t>(c) * kC;
-            const int valid = left < kC ? static_cast<int>(left) : kC;
-            bool got = mbar_wait_bounded(&bar->full[s], (c / kStages) & 1, lim);
-            if (got && valid < kC) got = mbar_wait_bounded(&bar->v_full[c % kVStages], (c / kVStages) & 1, lim);
-            if (got && c >= 1) got = mbar_wait_bounded(&bar->gram_free, (c - 1) & 1, lim);   // the other group's
-            if (valid < kC && i >= valid && got) {   // rows behind the end, whatever they hold, become zero rows
-                for (int w = 0; w < 8 * KB; ++w)
-                    sts128(st + (2 * (w >> 3) + (is_q ? 1 : 0)) * kTile + i * 128 + (w & 7) * 16, make_uint4(0, 0, 0, 0));
-                if (!is_q)
-                    for (int w = 0; w < p.dv / 8; ++w)
-                        sts128(base + kOffV + (c % kVStages) * kVBytes + (w >> 3) * kTile + i * 128 + (w & 7) * 16,
-                               make_uint4(0, 0, 0, 0));
-                fence_proxy_async_smem();
-            }
-            tc_fence_before();
-            if (group_any(id, !got)) {
-                if (pt == 0) record();
-                break;
-            }
-            if (pt == 0) {   // [K; Q] Kᵀ: lanes 0..63 K's rows, 64..127 Q's
-                tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * 2 * kTile + (ks & 3) * 32;
-                    umma(gram, sdesc(st + off, 16, 1024), sdesc(st + off, 16, 1024), idesc(kC, false), ks > 0);
-                }
-                umma_commit(&bar->gram);
-            }
-            double G = 0.0;
-            float rn = 1.0f, be = 0.0f;   // 1 / |row i| of K, or of Q
-            if (!is_q) {
-                const bool in = i < valid;
-                const float delta = in ? gdr_delta(dt_n, bias, g.softplus) : 0.0f;
-                be = in ? gdr_beta(be_n, g.sigmoid) : 0.0f;
-                if (c + 2 < nchunk) fetch(c + 2);
-                G = static_cast<double>(delta) * static_cast<double>(Ah) * 1.4426950408889634074;   // log2 α
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double v = __shfl_up_sync(0xffffffffu, G, o);
-                    if (lane >= o) G += v;
-                }
-                lo.G[i] = G;
-            } else if (g.l2norm) {
-                f32x2 q0 = pk2(0.0f, 0.0f), q1 = q0;
-#pragma unroll
-                for (int w = 0; w < 8 * KB; ++w) {
-                    const uint4 x = lds128(chunk_addr(st + (2 * (w >> 3) + 1) * kTile, i, w & 7));
-                    const f32x2 x0 = pk2(lo_f(x.x), hi_f(x.x)), x1 = pk2(lo_f(x.y), hi_f(x.y));
-                    const f32x2 x2 = pk2(lo_f(x.z), hi_f(x.z)), x3 = pk2(lo_f(x.w), hi_f(x.w));
-                    q0 = fma2(x0, x0, fma2(x2, x2, q0));
-                    q1 = fma2(x1, x1, fma2(x3, x3, q1));
-                }
-                rn = 1.0f / sqrtf((q0.x + q0.y) + (q1.x + q1.y) + kGdrL2Eps);
-            }
-            group_sync(id);
-            const double first = lo.G[31];
-            if (!is_q) {
-                const double end = first + lo.G[63];
-                if (i >= 32) G += first;
-                const float hi = static_cast<float>(G);
-                lo.gh[i] = hi;
-                lo.gl[i] = static_cast<float>(G - static_cast<double>(hi));
-                sc.ek[i] = -exp2f(hi);
-                sc.wk[i] = be * exp2f(static_cast<float>(end - G));
-                if (i == 0) sc.end[0] = exp2f(static_cast<float>(end));
-            }
-            got = mbar_wait_bounded(&bar->gram, c & 1, lim);
-            if (got && c >= 2) got = mbar_wait_bounded(is_q ? &bar->p_empty[grp] : &bar->t_empty[grp], ph ^ 1, lim);
-            if (group_any(id, !got)) {
-                if (pt == 0) record();
-                break;
-            }
-            tc_fence_after();
-            const uint32_t src = gram + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-            float v[32];
-            tmem_ld32(src + 32 * rb, v);   // the block on the diagonal
-            if (!is_q) {                   // |k_i|² is K Kᵀ's own diagonal
-                if (g.l2norm) rn = 1.0f / sqrtf(pick32(v, lane) + kGdrL2Eps);
-                lo.cb[i] = be * rn;
-                if (rb == 0) lo.cf[i] = be * rn * exp2f(static_cast<float>(first - G));
-                sc.ek[i] *= rn;
-                sc.wk[i] *= rn;
-            }
-            group_sync(id);
-            const float gh = lo.gh[i], gl = lo.gl[i];
-            const float row = is_q ? rn * g.scale : rn;
-            if (is_q) sc.qe[i] = exp2f(gh) * row;
-#pragma unroll
-            for (int blk = 0; blk < 2; ++blk) {
-                // first the block on the diagonal, then (rows 32..63) the block left of it
-                if (blk == 1) {
-                    if (rb == 0) break;
-                    tmem_ld32(src, v);
-                }
-                const int j0 = blk == 0 ? 32 * rb : 0;
-                if (blk == 0) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 h4 = quad(lo.gh + j0 + e), l4 = quad(lo.gl + j0 + e), c4 = quad(lo.cb + j0 + e);
-                        const f32x2 hh[2] = {pk2(h4.x, h4.y), pk2(h4.z, h4.w)}, ll[2] = {pk2(l4.x, l4.y), pk2(l4.z, l4.w)};
-                        const f32x2 cc[2] = {pk2(c4.x, c4.y), pk2(c4.z, c4.w)};
-#pragma unroll
-                        for (int f = 0; f < 2; ++f) {
-                            const f32x2 m1 = pk2(-1.0f, -1.0f);
-                            const f32x2 d = add2(fma2(hh[f], m1, pk2(gh, gh)), fma2(ll[f], m1, pk2(gl, gl)));
-                            const f32x2 w = mul2(mul2(pk2(v[e + 2 * f], v[e + 2 * f + 1]), cc[f]), pk2(row, row));
-                            const f32x2 r = mul2(w, pk2(ex2_approx(d.x), ex2_approx(d.y)));
-                            const int k = e + 2 * f - (is_q ? 1 : 0);   // P keeps its diagonal
-                            v[e + 2 * f] = k < lane ? r.x : 0.0f;
-                            v[e + 2 * f + 1] = k + 1 < lane ? r.y : 0.0f;
-                        }
-                    }
-                } else {   // j < 32 <= i: both factors of e^{G_i - G_31} e^{G_31 - G_j} lie between the product and 1
-                    const float rf = row * exp2f(static_cast<float>((static_cast<double>(gh) + static_cast<double>(gl)) - first));
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 c4 = quad(lo.cf + e);
-                        const f32x2 r0 = mul2(mul2(pk2(v[e], v[e + 1]), pk2(c4.x, c4.y)), pk2(rf, rf));
-                        const f32x2 r1 = mul2(mul2(pk2(v[e + 2], v[e + 3]), pk2(c4.z, c4.w)), pk2(rf, rf));
-                        v[e] = r0.x;
-                        v[e + 1] = r0.y;
-                        v[e + 2] = r1.x;
-                        v[e + 3] = r1.y;
-                    }
-                }
-                if (is_q) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t hw[4], lw[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) split2(pk2(v[8 * w + 2 * e], v[8 * w + 2 * e + 1]), hw[e], lw[e]);
-                        sts128(chunk_addr(pr + 2 * kTile, i, j0 / 8 + w), make_uint4(hw[0], hw[1], hw[2], hw[3]));
-                        sts128(chunk_addr(pr + 3 * kTile, i, j0 / 8 + w), make_uint4(lw[0], lw[1], lw[2], lw[3]));
-                    }
-                } else {
-#pragma unroll
-                    for (int w = 0; w < 8; ++w)
-                        *reinterpret_cast<float4*>(a + at(i, j0 + 4 * w)) =
-                            make_float4(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar->gram_free);
-            group_sync(id);
-            invert64(a, xs, pt, id);
-            {   // T as two bf16 terms in its own place: half a row each (thread pt: row pt & 63), read by all first
-                const int r = pt & 63, hf = pt >> 6;
-                float4 u[8];
-#pragma unroll
-                for (int w = 0; w < 8; ++w)   // (the block above the diagonal holds nothing)
-                    u[w] = r >= 32 || hf == 0 ? quad(a + at(r, 32 * hf + 4 * w)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                group_sync(id);
-                {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t hw[4], lw[4];
-                        split2(pk2(u[2 * w].x, u[2 * w].y), hw[0], lw[0]);
-                        split2(pk2(u[2 * w].z, u[2 * w].w), hw[1], lw[1]);
-                        split2(pk2(u[2 * w + 1].x, u[2 * w + 1].y), hw[2], lw[2]);
-                        split2(pk2(u[2 * w + 1].z, u[2 * w + 1].w), hw[3], lw[3]);
-                        sts128(chunk_addr(pr, r, 4 * hf + w), make_uint4(hw[0], hw[1], hw[2], hw[3]));
-                        sts128(chunk_addr(pr + kTile, r, 4 * hf + w), make_uint4(lw[0], lw[1], lw[2], lw[3]));
-                    }
-                }
-            }
-            fence_proxy_async_smem();
-            arrive_warp(&bar->prep_full[grp]);
-        }
     } else {
         // ============================================================ state warps
         const int v = (warp & 3) * 32 + lane, part = warp >> 2;
@@ -751,13 +764,40 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         for (int k = 0; k < KH; k += 16) store_terms(tl + kColS + part * KH + k, S + k / 2);
         tmem_wait_st();
         tc_fence_before();
-        arrive_warp(&bar->s_ready);
         bool ok = true;
         for (int c = 0; c < nchunk; ++c) {
-            const int pb = c & 1;
-            const uint32_t par = c & 1;
-            const Scal& sc = scal[c % kScals];
-            ok = wait_warp(&bar->prep_full[pb], (c >> 1) & 1) && wait_warp(&bar->ks, par);
+            const int s = c % kStages;
+            const uint32_t par = c & 1, st = base + s * kStageBytes;
+            const Scal& sc = *reinterpret_cast<const Scal*>(gbase + s * kStageBytes + kOffRec + kRecScal);
+            if (c == ragged) {   // rows of K and V behind the end, whatever they hold, become zero rows
+                ok = wait_warp(&bar->full[s], (c / kStages) & 1);
+                if (!ok) break;
+                const int n0 = static_cast<int>(len - static_cast<int64_t>(c) * kC);
+                for (int i = n0 * 8 + tid; i < kC * 8; i += 32 * kStateWarps) {
+                    for (int kb = 0; kb < KB; ++kb) sts128(st + 2 * kb * kTile + 16 * i, make_uint4(0, 0, 0, 0));
+                    for (int vb = 0; vb < p.dv / 64; ++vb) sts128(st + kOffV + vb * kTile + 16 * i, make_uint4(0, 0, 0, 0));
+                }
+                fence_proxy_async_smem();
+            }
+            arrive_warp(&bar->s_ready);
+            if (c > 0) {   // the last chunk's y, while this one's K Sᵀ runs
+                ok = (c == 1 || wait_warp(&bar->y_free, c & 1)) && wait_warp(&bar->pv, par ^ 1);
+                if (!ok) break;
+                tc_fence_after();
+                f32x2 x[8];
+                tmem_ld16(tl + kColY + kTok * part, x);
+                if (row_in) {
+                    __nv_bfloat16* ys = reinterpret_cast<__nv_bfloat16*>(gbase + kOffY) + kTok * part * p.dv + v;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        ys[2 * e * p.dv] = __float2bfloat16_rn(x[e].x);
+                        ys[(2 * e + 1) * p.dv] = __float2bfloat16_rn(x[e].y);
+                    }
+                }
+                fence_proxy_async_smem();
+                arrive_warp(&bar->y_full);
+            }
+            ok = wait_warp(&bar->full[s], (c / kStages) & 1) && wait_warp(&bar->ks, par);
             if (!ok) break;
             tc_fence_after();
             f32x2 x[8];
@@ -798,23 +838,24 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             }
             tmem_wait_st();
             tc_fence_before();
-            arrive_warp(&bar->s_ready);
-            // y, while the next chunk's K Sᵀ runs
-            ok = (c == 0 || wait_warp(&bar->y_free, (c - 1) & 1)) && wait_warp(&bar->pv, par);
-            if (!ok) break;
-            tc_fence_after();
-            tmem_ld16(tl + kColY + kTok * part, x);
-            tc_fence_before();
-            if (row_in) {
-                __nv_bfloat16* ys = reinterpret_cast<__nv_bfloat16*>(gbase + kOffY) + kTok * part * p.dv + v;
+        }
+        if (ok && nchunk > 0) {   // the last chunk's y
+            ok = (nchunk == 1 || wait_warp(&bar->y_free, nchunk & 1)) && wait_warp(&bar->pv, (nchunk - 1) & 1);
+            if (ok) {
+                tc_fence_after();
+                f32x2 x[8];
+                tmem_ld16(tl + kColY + kTok * part, x);
+                if (row_in) {
+                    __nv_bfloat16* ys = reinterpret_cast<__nv_bfloat16*>(gbase + kOffY) + kTok * part * p.dv + v;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    ys[2 * e * p.dv] = __float2bfloat16_rn(x[e].x);
-                    ys[(2 * e + 1) * p.dv] = __float2bfloat16_rn(x[e].y);
+                    for (int e = 0; e < 8; ++e) {
+                        ys[2 * e * p.dv] = __float2bfloat16_rn(x[e].x);
+                        ys[(2 * e + 1) * p.dv] = __float2bfloat16_rn(x[e].y);
+                    }
                 }
+                fence_proxy_async_smem();
+                arrive_warp(&bar->y_full);
             }
-            fence_proxy_async_smem();
-            arrive_warp(&bar->y_full);
         }
         if (ok && g.final_state && row_in) {
 #pragma unroll
@@ -822,6 +863,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 *reinterpret_cast<float4*>(g.final_state + srow + k) =
                     make_float4(S[k / 2].x, S[k / 2].y, S[k / 2 + 1].x, S[k / 2 + 1].y);
         }
+        tc_fence_before();
     }
 
     // Wind-down: loads in flight land before the shared memory goes, MMAs end before the TMEM columns do.
@@ -829,14 +871,10 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
     if (warp == kLoadWarp && lane == 0) {
         for (int c = issued > kStages ? issued - kStages : 0; c < issued; ++c)
             mbar_wait_bounded(&bar->full[c % kStages], (c / kStages) & 1, p.drain_ns);
-        for (int c = v_issued > kVStages ? v_issued - kVStages : 0; c < v_issued; ++c)
-            mbar_wait_bounded(&bar->v_full[c % kVStages], (c / kVStages) & 1, p.drain_ns);
     }
-    // every thread that issued MMAs: the chain's, and each group's
-    const int f = tid == 32 * kMmaWarp ? 0 : tid == 32 * kPrepWarp ? 1 : tid == 32 * (kPrepWarp + kGroupWarps) ? 2 : -1;
-    if (f >= 0) {
-        umma_commit(&bar->fin[f]);
-        mbar_wait_bounded(&bar->fin[f], 0, p.drain_ns);
+    if (tid == 32 * kMmaWarp) {
+        umma_commit(&bar->fin);
+        mbar_wait_bounded(&bar->fin, 0, p.drain_ns);
     }
     tc_fence_before();
     __syncthreads();

@@ -1,4 +1,6 @@
 """GPU tests of the gated delta rule's forward and step against the 64-bit oracle (token by token)."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -186,7 +188,8 @@ def test_bounded_wait_reports_timeout_and_context_survives():
     """A hand-over that is never signalled (SS_TEST_DROP_CARRY: the first block's first product) runs the bounded
     waits out: the call reports SS_ERR_TIMEOUT, and the next call on the same context is right."""
     x = gdr_inputs(2, 300, 2, 2, 128, 128, seed=5)
-    ws = torch.zeros(4096, dtype=torch.uint8, device="cuda:0")
+    need = ss.lib().ss_gdr_fwd_workspace_bytes(ctypes.byref(ss.ss_gdr_dims(2, 300, 2, 2, 128, 128)), ss.SS_BF16)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda:0")
     ss.ss_gdr_fwd(*call_args(x), dt_bias=x["dt_bias"], workspace=ws, timeout_iters=200,
                   extra_flags=ss.SS_TEST_DROP_CARRY)
     assert ss.ss_check(ws) == ss.SS_ERR_TIMEOUT
