@@ -538,8 +538,11 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
 // so that the state, the right hand side and the corrections go from registers to TMEM and never through shared
 // memory, a thread owning one row v (four threads to a row, each with a quarter of the columns).  X is written over
 // KS, E's terms over E, S's terms over dS, by the thread that read them, which is what makes it fit in TMEM.
-// An MMA of 128 x N x 16 takes about 64 cycles for every N up to 128 (measured here), so operands are put side by
-// side to N = 128 where they share A: K with Q, and T's two terms, whose two halves of E the reader adds.
+// An MMA of 128 x N x 16 takes about 58 cycles for every N up to 128 (measured here; 100 where N changes from one to
+// the next, as when the zero blocks of T and P are left out), so operands are put side by side to N = 128 where they
+// share A: K with Q, T's two terms, P's two terms, and the reader adds the two halves of E and of Y.  The order of
+// issue keeps the chain's products first: E's part from V follows KS, Y's follows dS, and S's terms are handed over
+// in two halves, so that KS starts on the first.
 //
 // Warps: 0..15 state (above); 16 issues the MMAs; 17 the loads (two chunks in flight); 18 stores y.  They hand over
 // through mbarriers.  Every wait is bounded: one that runs out records SS_ERR_TIMEOUT and the CTA winds down.
@@ -551,7 +554,7 @@ constexpr int kTok = kC / kParts;      // tokens of a state thread
 constexpr int kStages = 2;             // chunks in flight
 
 // TMEM columns.  A: KS, then X's terms over it, then W's; B: E in two halves, then its terms over the first; S: the
-// state's terms (of each 16 keys, hi then lo), then dS over them.
+// state's terms (of each 16 keys, hi then lo), then dS over them; Y: in two halves.
 constexpr uint32_t kColS = 0, kColA = 128, kColQS = 192, kColB = 256, kColY = 384;
 constexpr uint32_t kTmemCols = 512;
 
@@ -568,8 +571,8 @@ struct Bars {
     uint64_t full[kStages];    // K, Q, V and the record of a stage landed
     uint64_t empty[kStages];   // the chunk's last MMA is done with the stage
     uint64_t ks, e, ds, pv;    // the chain's products done
-    uint64_t s_ready;          // S's terms written (state warps)
-    uint64_t x_ready, w_ready; // X's terms; W's and E's, and Y's first part, written (state warps)
+    uint64_t s_ready[2];       // S's terms written: of the first 16 keys of each thread, of the others (state warps)
+    uint64_t x_ready, w_ready, e_ready;   // X's terms, W's, E's and Y's first part written (state warps)
     uint64_t y_full, y_free;   // y staged (state warps); stored (1)
     uint64_t fin;              // wind-down
     uint32_t tmem;
@@ -606,7 +609,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         }
         uint64_t* one[] = {&bar->ks, &bar->e, &bar->ds, &bar->pv, &bar->y_free, &bar->fin};
         for (uint64_t* x : one) mbar_init(x, 1);
-        uint64_t* all[] = {&bar->s_ready, &bar->x_ready, &bar->w_ready, &bar->y_full};
+        uint64_t* all[] = {bar->s_ready, bar->s_ready + 1, &bar->x_ready, &bar->w_ready, &bar->e_ready, &bar->y_full};
         for (uint64_t* x : all) mbar_init(x, kStateWarps);
         fence_mbar_init();
     }
@@ -694,24 +697,31 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 const int s = c % kStages;
                 const uint32_t par = c & 1, st = base + s * kStageBytes, pr = st + kOffRec;
                 if (!wait1(&bar->full[s], (c / kStages) & 1)) break;
-                if (c == ragged && !wait1(&bar->s_ready, par)) break;   // rows behind the end are zeroed by then
-                if (c > 0 && !wait1(&bar->pv, (c - 1) & 1)) break;      // the last chunk's E is read
+                // KS and QS: S's terms of 16 keys in 16 columns, K and Q of a 64-key block side by side
+                auto ks_step = [&](int ks) {
+                    const uint64_t bd = sdesc(st + (ks >> 2) * 2 * kTile + (ks & 3) * 32, 16, 1024);
+                    umma_ts(tmem + kColA, tmem + kColS + 16 * ks, bd, idesc(2 * kC, false), ks > 0);
+                    umma_ts(tmem + kColA, tmem + kColS + 16 * ks + 8, bd, idesc(2 * kC, false), 1);
+                };
+                constexpr int kStep = KH / 16;   // (the rows behind a sequence's end are zeroed before s_ready)
+                if (!wait1(&bar->s_ready[0], par)) break;
                 tc_fence_after();
-                // E = Vᵀ Tᵀ, T's terms side by side
+#pragma unroll
+                for (int ks = 0; ks < DK / 16; ks += kStep) ks_step(ks);
+                if (!wait1(&bar->s_ready[1], par)) break;
+                tc_fence_after();
+                if (kStep == 2) {
+#pragma unroll
+                    for (int ks = 1; ks < DK / 16; ks += 2) ks_step(ks);
+                }
+                if (!(p.test_drop && blockIdx.x == 0 && c == 0)) umma_commit(&bar->ks);
+                // E = Vᵀ Tᵀ, T's terms side by side, once the last chunk's E is read
+                if (c > 0 && !wait1(&bar->pv, (c - 1) & 1)) break;
+                tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < kC / 16; ++j)
                     umma(tmem + kColB, sdesc(st + kOffV + 2048u * j, vlbo, 1024), sdesc(pr + kRecT + 32u * j, 16, 1024),
                          idesc(2 * kC, false, true), j > 0);
-                if (!wait1(&bar->s_ready, par)) break;
-                tc_fence_after();
-                // KS and QS: S's terms of 16 keys in 16 columns, K and Q of a 64-key block side by side
-#pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks) {
-                    const uint64_t bd = sdesc(st + (ks >> 2) * 2 * kTile + (ks & 3) * 32, 16, 1024);
-                    umma_ts(tmem + kColA, tmem + kColS + 16 * ks, bd, idesc(2 * kC, false), ks > 0);
-                    umma_ts(tmem + kColA, tmem + kColS + 16 * ks + 8, bd, idesc(2 * kC, false), 1);
-                }
-                if (!(p.test_drop && blockIdx.x == 0 && c == 0)) umma_commit(&bar->ks);
                 if (!wait1(&bar->x_ready, par)) break;
                 tc_fence_after();
                 // E += X Tᵀ
@@ -732,14 +742,14 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                     umma_ts(tmem + kColS, tmem + kColA + 16 * j + 8, bd, idesc(DK, true), 1);
                 }
                 umma_commit(&bar->ds);
-                // Yᵀ += E Pᵀ: tokens 16 j .. 16 j + 15 reach the rows i >= 16 j of P alone
+                if (!wait1(&bar->e_ready, par)) break;
+                tc_fence_after();
+                // Yᵀ += E Pᵀ
 #pragma unroll
                 for (int j = 0; j < kC / 16; ++j) {
-                    const uint32_t n = kC - 16 * j, row = pr + kRecP + 2048u * j + 32u * j;
-                    const uint32_t d = tmem + kColY + 16 * j, x = tmem + kColB + 16 * j;
-                    umma_ts(d, x, sdesc(row, 16, 1024), idesc(n, false), 1);
-                    umma_ts(d, x, sdesc(row + kTile, 16, 1024), idesc(n, false), 1);
-                    umma_ts(d, x + 8, sdesc(row, 16, 1024), idesc(n, false), 1);
+                    const uint64_t bd = sdesc(pr + kRecP + 32u * j, 16, 1024);
+                    umma_ts(tmem + kColY, tmem + kColB + 16 * j, bd, idesc(2 * kC, false), 1);
+                    umma_ts(tmem + kColY, tmem + kColB + 16 * j + 8, bd, idesc(kC, false), 1);
                 }
                 umma_commit(&bar->pv);
                 umma_commit(&bar->empty[s]);
@@ -779,13 +789,18 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 }
                 fence_proxy_async_smem();
             }
-            arrive_warp(&bar->s_ready);
+            if (c == 0 || c == ragged) {   // (else: handed over below)
+                arrive_warp(&bar->s_ready[0]);
+                arrive_warp(&bar->s_ready[1]);
+            }
             if (c > 0) {   // the last chunk's y, while this one's K Sᵀ runs
                 ok = (c == 1 || wait_warp(&bar->y_free, c & 1)) && wait_warp(&bar->pv, par ^ 1);
                 if (!ok) break;
                 tc_fence_after();
-                f32x2 x[8];
-                tmem_ld16(tl + kColY + kTok * part, x);
+                f32x2 x[8], w[8];
+                tmem_ld16x2(tl + kColY + kTok * part, tl + kColY + kC + kTok * part, x, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = add2(x[e], w[e]);
                 if (row_in) {
                     __nv_bfloat16* ys = reinterpret_cast<__nv_bfloat16*>(gbase + kOffY) + kTok * part * p.dv + v;
 #pragma unroll
@@ -810,6 +825,11 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             tmem_ld16(tl + kColQS + kTok * part, x);  // y's part from the entering state, while E is multiplied
             scale16(x, sc.qe + kTok * part);
             tmem_st16(tl + kColY + kTok * part, x);
+            {
+                const uint32_t zero[8] = {};
+                tmem_st8(tl + kColY + kC + kTok * part, zero);
+                tmem_st8(tl + kColY + kC + kTok * part + 8, zero);
+            }
             ok = wait_warp(&bar->e, par);
             if (!ok) break;
             tc_fence_after();
@@ -819,13 +839,21 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = add2(x[e], w[e]);
             }
-            store_terms(tl + kColB + kTok * part, x);
-            scale16(x, sc.wk + kTok * part);
-            store_terms(tl + kColA + kTok * part, x);
+            {
+                f32x2 w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = x[e];
+                scale16(w, sc.wk + kTok * part);
+                store_terms(tl + kColA + kTok * part, w);
+            }
+            const float end = sc.end[0];
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(&bar->w_ready);
-            const float end = sc.end[0];
+            store_terms(tl + kColB + kTok * part, x);
+            tmem_wait_st();
+            tc_fence_before();
+            arrive_warp(&bar->e_ready);
             ok = wait_warp(&bar->ds, par);
             if (!ok) break;
             tc_fence_after();
@@ -835,6 +863,12 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
 #pragma unroll
                 for (int e = 0; e < 8; ++e) S[k / 2 + e] = fma2(pk2(end, end), S[k / 2 + e], x[e]);
                 store_terms(tl + kColS + part * KH + k, S + k / 2);
+                if (c + 1 != ragged && c + 1 < nchunk) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    arrive_warp(&bar->s_ready[k / 16]);
+                    if (KH == 16) arrive_warp(&bar->s_ready[1]);
+                }
             }
             tmem_wait_st();
             tc_fence_before();
@@ -843,8 +877,10 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             ok = (nchunk == 1 || wait_warp(&bar->y_free, nchunk & 1)) && wait_warp(&bar->pv, (nchunk - 1) & 1);
             if (ok) {
                 tc_fence_after();
-                f32x2 x[8];
-                tmem_ld16(tl + kColY + kTok * part, x);
+                f32x2 x[8], w[8];
+                tmem_ld16x2(tl + kColY + kTok * part, tl + kColY + kC + kTok * part, x, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = add2(x[e], w[e]);
                 if (row_in) {
                     __nv_bfloat16* ys = reinterpret_cast<__nv_bfloat16*>(gbase + kOffY) + kTok * part * p.dv + v;
 #pragma unroll
