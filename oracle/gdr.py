@@ -62,7 +62,8 @@ def gdr_fwd(q, k, v, dt, A, beta, dt_bias=None, h_init=None, seqlens=None, scale
 
 def gdr_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, h_init=None, dfinal=None, seqlens=None, scale=1.0, softplus=True,
             beta_sigmoid=True, qk_l2norm=True):
-    """Gradients of sum(dy y) + sum(dfinal final_state) as a dict."""
+    """Gradients of sum(dy y) + sum(dfinal final_state) as a dict, and of each token Δ, the gradient of log α, and the
+    sum of absolute values whose signed sum that gradient is (what a rounding of its terms is relative to)."""
     p = _Prep(q, k, v, dt, A, beta, dt_bias, seqlens, scale, softplus, beta_sigmoid, qk_l2norm)
     B, L, H, dv = v.shape
     dk = q.shape[3]
@@ -74,7 +75,7 @@ def gdr_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, h_init=None, dfinal=None, se
     dy = np.where(p.live[..., None, None], dy, 0.0)
     dS = np.zeros_like(S) if dfinal is None else np.array(dfinal, dtype=np.float64)
     dq, dk_, dv_ = np.zeros(p.qr.shape), np.zeros(p.kr.shape), np.zeros(v.shape)
-    db, dla = np.zeros(dt.shape), np.zeros(dt.shape)
+    db, dla, size = np.zeros(dt.shape), np.zeros(dt.shape), np.zeros(dt.shape)
     for t in reversed(range(L)):
         Sd, e, S1 = kept[t]
         kt, qt, b1 = p.kr[:, t], p.qr[:, t], p.beta[:, t, :, None]
@@ -87,6 +88,7 @@ def gdr_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, h_init=None, dfinal=None, se
         dk_[:, t] = b1 * np.einsum("bhv,bhvk->bhk", e, dS) - np.einsum("bhv,bhvk->bhk", de, Sd)
         dv_[:, t] = de
         dla[:, t] = (dSd * Sd).sum((-1, -2))
+        size[:, t] = np.abs(dSd * Sd).sum((-1, -2))
         dS = p.alpha[:, t, :, None, None] * dSd
     m = p.live[..., None]
     db, dla = np.where(m, db, 0.0), np.where(m, dla, 0.0)
@@ -98,7 +100,7 @@ def gdr_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, h_init=None, dfinal=None, se
     ddt = dla * A * (_sigmoid(p.pre) if softplus else 1.0)
     return {"dq": dq, "dk": dk_, "dv": dv_, "ddt": ddt, "dA": (dla * p.delta).sum((0, 1)),
             "dbeta": db * (p.beta * (1.0 - p.beta) if beta_sigmoid else 1.0), "ddt_bias": ddt.sum((0, 1)),
-            "dinitial_state": dS}
+            "dinitial_state": dS, "delta": p.delta, "dlog_alpha": dla, "dlog_alpha_size": size}
 
 
 def norm_fwd(x, weight=None, bias=None, eps=1e-5):

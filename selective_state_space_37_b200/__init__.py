@@ -28,7 +28,7 @@ from ._binding import (D_STATE, EXPORTED, LIB_PATH, SS_BF16, SS_DELTA_SOFTPLUS,
                        fwd_workspace_bytes, lib, ss_bwd, ss_check, ss_dims, ss_fwd, ss_fwd_conv,
                        ss_launch, ss_step, ss_step_conv, status_string, workspace_for,
                        ss_fwd_host, fwd_host_workspace_bytes, clear_workspaces, SS_BETA_SIGMOID, SS_QK_L2NORM,
-                       ss_gdr_dims, ss_gdr_fwd, ss_gdr_step, ss_norm_dims, ss_norm_fwd, ss_norm_bwd,
+                       ss_gdr_dims, ss_gdr_fwd, ss_gdr_step, ss_gdr_bwd, ss_norm_dims, ss_norm_fwd, ss_norm_bwd,
                        ss_block_fwd_prenorm)
 
 __all__ = ["ss_fwd", "ss_fwd_host", "fwd_host_workspace_bytes", "ss_step", "ss_bwd", "ss_fwd_conv", "ss_step_conv", "ss_block_fwd", "ss_ssd_fwd",
@@ -38,5 +38,5 @@ __all__ = ["ss_fwd", "ss_fwd_host", "fwd_host_workspace_bytes", "ss_step", "ss_b
            "D_STATE", "EXPORTED", "LIB_PATH", "SS_OK", "SS_ERR_INVALID_ARG",
            "SS_ERR_UNSUPPORTED", "SS_ERR_CUDA", "SS_ERR_TIMEOUT", "SS_ERR_WORKSPACE",
            "SS_BF16", "SS_DELTA_SOFTPLUS", "SS_SYNC_CHECK", "SS_FORCE_GENERAL_A",
-           "SS_TEST_DROP_CARRY", "SS_BETA_SIGMOID", "SS_QK_L2NORM", "ss_gdr_dims", "ss_gdr_fwd", "ss_gdr_step",
+           "SS_TEST_DROP_CARRY", "SS_BETA_SIGMOID", "SS_QK_L2NORM", "ss_gdr_dims", "ss_gdr_fwd", "ss_gdr_step", "ss_gdr_bwd",
            "ss_norm_dims", "ss_norm_fwd", "ss_norm_bwd", "ss_block_fwd_prenorm"]

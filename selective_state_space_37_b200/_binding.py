@@ -39,7 +39,7 @@ EXPORTED = ("ss_fwd", "ss_step", "ss_fwd_workspace_bytes", "ss_fwd_chunk_len", "
             "ss_status_string", "ss_version", "ss_fwd_noalloc", "ss_bwd", "ss_bwd_workspace_bytes",
             "ss_fwd_conv", "ss_step_conv", "ss_block_fwd", "ss_block_scratch_bytes", "ss_ssd_fwd",
             "ss_fwd_host", "ss_fwd_host_workspace_bytes", "ss_ssd_fwd_workspace_bytes", "ss_fwd_with_state",
-            "ss_gdr_fwd", "ss_gdr_fwd_workspace_bytes", "ss_gdr_step", "ss_norm_fwd", "ss_norm_bwd",
+            "ss_gdr_fwd", "ss_gdr_fwd_workspace_bytes", "ss_gdr_step", "ss_gdr_bwd", "ss_gdr_bwd_workspace_bytes", "ss_norm_fwd", "ss_norm_bwd",
             "ss_norm_bwd_workspace_bytes", "ss_block_fwd_prenorm", "ss_block_prenorm_scratch_bytes")
 
 
@@ -162,17 +162,19 @@ def lib():
         u32, f32, lp = ctypes.c_uint32, ctypes.c_float, ctypes.POINTER(ss_launch)
         L.ss_gdr_fwd.argtypes = [vp, vp, vp, vp, f32p, f32p, vp, f32p, vp, vp, f32p, f32, u32, gp, lp]
         L.ss_gdr_step.argtypes = [f32p, vp, vp, vp, vp, f32p, f32p, vp, vp, f32, u32, gp, lp]
+        L.ss_gdr_bwd.argtypes = [vp] * 19 + [f32, u32, gp, lp]
         L.ss_norm_fwd.argtypes = [vp, f32p, f32p, vp, f32p, f32p, f32, u32, np_, lp]
         L.ss_norm_bwd.argtypes = [vp, vp, f32p, f32p, f32p, vp, f32p, f32p, u32, np_, lp]
         L.ss_block_fwd_prenorm.argtypes = [vp, f32p, f32p, f32, vp, ctypes.POINTER(ss_block_weights),
                                            ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_size_t, vp]
-        for f in (L.ss_gdr_fwd, L.ss_gdr_step, L.ss_norm_fwd, L.ss_norm_bwd, L.ss_block_fwd_prenorm):
+        for f in (L.ss_gdr_fwd, L.ss_gdr_step, L.ss_gdr_bwd, L.ss_norm_fwd, L.ss_norm_bwd, L.ss_block_fwd_prenorm):
             f.restype = ctypes.c_int
         L.ss_gdr_fwd_workspace_bytes.argtypes = [gp, u32]
         L.ss_norm_bwd_workspace_bytes.argtypes = [np_, u32]
         L.ss_block_prenorm_scratch_bytes.argtypes = [ctypes.POINTER(ss_block_weights), ctypes.c_int64,
                                                      ctypes.c_int64]
-        for f in (L.ss_gdr_fwd_workspace_bytes, L.ss_norm_bwd_workspace_bytes, L.ss_block_prenorm_scratch_bytes):
+        L.ss_gdr_bwd_workspace_bytes.argtypes = [gp, u32]
+        for f in (L.ss_gdr_fwd_workspace_bytes, L.ss_gdr_bwd_workspace_bytes, L.ss_norm_bwd_workspace_bytes, L.ss_block_prenorm_scratch_bytes):
             f.restype = ctypes.c_size_t
         _lib = L
     return _lib
@@ -698,6 +700,50 @@ def ss_gdr_step(state, q, k, v, dt, A, beta, dt_bias=None, *, scale=None, softpl
     if rc != SS_OK:
         raise SelscanError(rc, "ss_gdr_step")
     return y
+
+
+@_on_device
+def ss_gdr_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, initial_state=None, dfinal_state=None, seqlens=None, *,
+               scale=None, softplus=True, beta_sigmoid=True, qk_l2norm=True, grads=None, workspace=None, stream=None,
+               sync_check=False, timeout_iters=0, extra_flags=0):
+    """Backward of ss_gdr_fwd (bf16) through libselscan's ss_gdr_bwd.  Its inputs, dy like v and dfinal_state
+    [batch, nheads, d_v, d_k] fp32 or None.  Returns a dict with dq, dk, dv, ddt, dbeta (bf16, shaped like
+    what they are of), dA, ddt_bias (fp32; the latter with dt_bias) and dinitial_state (fp32, with
+    initial_state); `grads` may supply output tensors by name."""
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, L, nheads_k, d_k]")
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"ss_gdr_bwd takes bfloat16, got {q.dtype}")
+    batch, L = q.shape[:2]
+    dims, flags = _gdr_setup(q, k, v, dt, A, beta, dt_bias, q.dtype, softplus, beta_sigmoid, qk_l2norm, (batch, L))
+    dev = q.device
+    states = (batch, dims.nheads, dims.d_v, dims.d_k)
+    _check(dy, "dy", v.shape, v.dtype, dev)
+    _check(initial_state, "initial_state", states, torch.float32, dev)
+    _check(dfinal_state, "dfinal_state", states, torch.float32, dev)
+    _check(seqlens, "seqlens", (batch,), torch.int32, dev)
+    like = {"dq": q, "dk": k, "dv": v, "ddt": dt, "dbeta": beta, "dA": A}
+    if dt_bias is not None:
+        like["ddt_bias"] = dt_bias
+    if initial_state is not None:
+        like["dinitial_state"] = initial_state
+    g = {}
+    for name, t in like.items():
+        given = (grads or {}).get(name)
+        g[name] = torch.empty_like(t) if given is None else given
+        _check(g[name], name, t.shape, t.dtype, dev)
+    flags |= (SS_SYNC_CHECK if sync_check else 0) | int(extra_flags)
+    need = int(lib().ss_gdr_bwd_workspace_bytes(ctypes.byref(dims), flags))
+    launch = _launch_for(need, dev, stream, workspace, timeout_iters)
+    rc = lib().ss_gdr_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(beta),
+                          _ptr(initial_state), _ptr(seqlens), _ptr(dy), _ptr(dfinal_state), _ptr(g["dq"]),
+                          _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["ddt"]), _ptr(g["dbeta"]), _ptr(g["dA"]),
+                          _ptr(g.get("ddt_bias")), _ptr(g.get("dinitial_state")),
+                          dims.d_k ** -0.5 if scale is None else float(scale), flags, ctypes.byref(dims),
+                          ctypes.byref(launch))
+    if rc != SS_OK:
+        raise SelscanError(rc, "ss_gdr_bwd")
+    return g
 
 
 @_on_device

@@ -1,6 +1,7 @@
 // gdr.cu -- the gated delta rule's entry points (ss_gdr_fwd, ss_gdr_step, ss_gdr_bwd): argument checks,
 // workspace layout, choice of kernel and launches.
 #include "common.cuh"
+#include "gdr_bwd.cuh"
 #include "gdr_rec.cuh"
 #include "gdr_tc.cuh"
 #include "host.cuh"
@@ -96,7 +97,7 @@ struct Maps {
 template <int DK>
 int launch_tc(const gdr::Params& p, const Maps& m, cudaStream_t stream) {
     auto prep = gdr::ss_gdr_prep_kernel<DK>;
-    auto kern = gdr::ss_gdr_tc_kernel<DK>;
+    auto kern = gdr::ss_gdr_tc_kernel<DK, false>;
     static std::atomic<bool> attr[2][kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || set_smem_limit(kern, gdr::kSmemBytes, attr[0], dev) != SS_OK ||
@@ -115,6 +116,7 @@ int run_tc(const GdrParams& g, const ss_gdr_dims* d, uint32_t flags, const ss_la
     p.status = static_cast<uint32_t*>(launch->workspace);
     p.rec = static_cast<unsigned char*>(launch->workspace) + w.rec;
     p.nchunks = w.nchunks;
+    p.rec_bytes = gdr::kRecBytes;
     p.dv = static_cast<int>(d->d_v);
     p.test_drop = (flags & SS_TEST_DROP_CARRY) ? 1 : 0;
     p.wait_ns = launch->timeout_iters ? static_cast<uint64_t>(launch->timeout_iters) * 1000ull : kTmaWaitNs;
@@ -126,6 +128,59 @@ int run_tc(const GdrParams& g, const ss_gdr_dims* d, uint32_t flags, const ss_la
         !head_map(&m.y, g.y, d->batch, d->seqlen, d->nheads, d->d_v, d->d_v, CU_TENSOR_MAP_SWIZZLE_NONE))
         return SS_ERR_CUDA;
     return d->d_k == 128 ? launch_tc<128>(p, m, stream) : launch_tc<64>(p, m, stream);
+}
+
+// The backward pass's workspace: header, records, what the chains keep, the tokens' sums, the items' shares.
+struct GdrBwdLayout {
+    int64_t nchunks;
+    size_t rec, keep, dots, part, total;
+};
+GdrBwdLayout gdr_bwd_layout(const ss_gdr_dims* d) {
+    GdrBwdLayout w{};
+    auto al = [](size_t x) { return (x + 1023) & ~static_cast<size_t>(1023); };
+    w.nchunks = ceil_div(d->seqlen, gdr::kC);
+    const size_t items = static_cast<size_t>(d->batch * d->nheads), n = static_cast<size_t>(w.nchunks);
+    w.rec = 1024;
+    w.keep = w.rec + al(items * n * gdr::kRecBwdBytes);
+    w.dots = w.keep + al(items * (n + 1) * gdr::kKeepBytes);
+    w.part = w.dots + al((3 * items * n * gdr::kC + items * n) * sizeof(float));
+    w.total = w.part + al(items * 2 * sizeof(float));
+    return w;
+}
+
+struct GdrGrads {
+    __nv_bfloat16 *dq, *dk, *dv, *ddt, *dbeta;
+    float *dA, *ddt_bias;
+};
+
+template <int DK>
+int launch_bwd(const gdr::Params& p, const Maps& m, const CUtensorMap& mo, const CUtensorMap& mo_plain,
+               const CUtensorMap& mdv, const CUtensorMap& mdv_plain, const GdrGrads& o, float* part,
+               cudaStream_t stream) {
+    auto prep = gdr::ss_gdr_prep_kernel<DK>;
+    auto fwd = gdr::ss_gdr_tc_kernel<DK, true>;
+    auto rev = gdr::ss_gdr_rev_kernel<DK>;
+    auto grad = gdr::ss_gdr_grad_kernel<DK>;
+    static std::atomic<bool> attr[4][kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || set_smem_limit(prep, gdr::kPrepSmem, attr[0], dev) != SS_OK ||
+        set_smem_limit(fwd, gdr::kSmemBytes, attr[1], dev) != SS_OK ||
+        set_smem_limit(rev, gdr::kRevSmem, attr[2], dev) != SS_OK ||
+        set_smem_limit(grad, gdr::kGradSmem, attr[3], dev) != SS_OK)
+        return SS_ERR_CUDA;
+    const int64_t items = static_cast<int64_t>(p.g.batch) * p.g.H;
+    const unsigned n = static_cast<unsigned>(items);
+    prep<<<static_cast<unsigned>(items * p.nchunks), gdr::kPrepThreads, gdr::kPrepSmem, stream>>>(p, m.q, m.k);
+    fwd<<<n, gdr::kThreads, gdr::kSmemBytes, stream>>>(p, m.q, m.k, m.v, mo_plain);
+    rev<<<n, gdr::kThreads, gdr::kRevSmem, stream>>>(p, m.q, m.k, m.v, mo, mdv_plain);
+    gdr::GradParams gp{p, o.dq, o.dk, o.dv};
+    const int64_t blocks = static_cast<int64_t>(p.g.batch) * p.g.Hk * p.nchunks;
+    grad<<<static_cast<unsigned>(blocks), gdr::kGradThreads, gdr::kGradSmem, stream>>>(gp, m.q, m.k, mo, mdv);
+    gdr::GateParams gt{p, o.ddt, o.dbeta, part};
+    gdr::ss_gdr_gate_kernel<<<n, 256, 0, stream>>>(gt);
+    gdr::ss_gdr_head_kernel<<<static_cast<unsigned>(ceil_div(p.g.H, 128)), 128, 0, stream>>>(part, p.g.batch, p.g.H, o.dA,
+                                                                                        o.ddt_bias);
+    return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
 }  // namespace
@@ -181,6 +236,82 @@ int ss_gdr_step(float* state, const void* q, const void* k, const void* v, const
     if (rc != SS_OK) return rc;
     if ((flags & SS_SYNC_CHECK) && cudaStreamSynchronize(stream) != cudaSuccess) return SS_ERR_CUDA;
     return SS_OK;
+}
+
+size_t ss_gdr_bwd_workspace_bytes(const ss_gdr_dims* dims, uint32_t flags) {
+    if (check_gdr(dims, flags) != SS_OK || !(flags & SS_BF16)) return 0;
+    return gdr_bwd_layout(dims).total;
+}
+
+int ss_gdr_bwd(const void* q, const void* k, const void* v, const void* dt, const float* dt_bias, const float* A,
+               const void* beta, const float* h_init, const int32_t* seqlens, const void* dy, const float* dfinal_state,
+               void* dq, void* dk, void* dv, void* ddt, void* dbeta, float* dA, float* ddt_bias, float* dh_init,
+               float scale, uint32_t flags, const ss_gdr_dims* dims, const ss_launch* launch) {
+    if (!launch) return SS_ERR_INVALID_ARG;
+    int rc = check_gdr(dims, flags);
+    if (rc != SS_OK) return rc;
+    if (!(flags & SS_BF16)) return SS_ERR_UNSUPPORTED;
+    const int64_t L = dims->seqlen, items = dims->batch * dims->nheads;
+    if (dims->nheads == 0) return SS_OK;
+    if (!A || !dA || (ddt_bias && !dt_bias)) return SS_ERR_INVALID_ARG;
+    if (dims->batch > 0 && L > 0 &&
+        (!q || !k || !v || !dt || !beta || !dy || !dq || !dk || !dv || !ddt || !dbeta))
+        return SS_ERR_INVALID_ARG;
+    const void* ptrs[] = {q, k, v, dt, dt_bias, A, beta, h_init, seqlens, dy, dfinal_state,
+                          dq, dk, dv, ddt, dbeta, dA, ddt_bias, dh_init};
+    for (const void* x : ptrs)
+        if (!aligned16(x)) return SS_ERR_INVALID_ARG;
+    if (!launch->workspace || launch->workspace_bytes < gdr_bwd_layout(dims).total || !aligned16(launch->workspace))
+        return SS_ERR_WORKSPACE;
+    cudaStream_t stream = static_cast<cudaStream_t>(launch->stream);
+    unsigned char* ws = static_cast<unsigned char*>(launch->workspace);
+    if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), stream) != cudaSuccess) return SS_ERR_CUDA;
+    if (L == 0 || dims->batch == 0) {   // no token: the final state is the entering one
+        const size_t n = static_cast<size_t>(dims->nheads) * sizeof(float);
+        const size_t st = static_cast<size_t>(items * dims->d_k * dims->d_v) * sizeof(float);
+        cudaError_t e = cudaMemsetAsync(dA, 0, n, stream);
+        if (e == cudaSuccess && ddt_bias) e = cudaMemsetAsync(ddt_bias, 0, n, stream);
+        if (e == cudaSuccess && dh_init && st)
+            e = dfinal_state ? cudaMemcpyAsync(dh_init, dfinal_state, st, cudaMemcpyDeviceToDevice, stream)
+                             : cudaMemsetAsync(dh_init, 0, st, stream);
+        if (e != cudaSuccess) return SS_ERR_CUDA;
+    } else {
+        const GdrBwdLayout w = gdr_bwd_layout(dims);
+        gdr::Params p{};
+        p.g = gdr_params(q, k, v, dt, dt_bias, A, beta, scale, flags, dims, L);
+        p.g.h_init = h_init;
+        p.g.seqlens = seqlens;
+        p.rec = ws + w.rec;
+        p.nchunks = w.nchunks;
+        p.rec_bytes = gdr::kRecBwdBytes;
+        p.keep = ws + w.keep;
+        p.dots = reinterpret_cast<float*>(ws + w.dots);
+        p.dfinal = dfinal_state;
+        p.dinit = dh_init;
+        p.status = reinterpret_cast<uint32_t*>(ws);
+        p.dv = static_cast<int>(dims->d_v);
+        p.test_drop = (flags & SS_TEST_DROP_CARRY) ? 1 : 0;
+        p.wait_ns = launch->timeout_iters ? static_cast<uint64_t>(launch->timeout_iters) * 1000ull : kTmaWaitNs;
+        p.drain_ns = kTmaWaitNs;
+        Maps m;
+        CUtensorMap mo, mo_plain, mdv, mdv_plain;
+        const int64_t B = dims->batch, H = dims->nheads, dvw = dims->d_v;
+        if (!head_map(&m.q, q, B, L, dims->nheads_k, dims->d_k, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !head_map(&m.k, k, B, L, dims->nheads_k, dims->d_k, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !head_map(&m.v, v, B, L, H, dvw, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !head_map(&mo, dy, B, L, H, dvw, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !head_map(&mo_plain, dy, B, L, H, dvw, dvw, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+            !head_map(&mdv, dv, B, L, H, dvw, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !head_map(&mdv_plain, dv, B, L, H, dvw, dvw, CU_TENSOR_MAP_SWIZZLE_NONE))
+            return SS_ERR_CUDA;
+        const GdrGrads o{static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv),
+                         static_cast<__nv_bfloat16*>(ddt), static_cast<__nv_bfloat16*>(dbeta), dA, ddt_bias};
+        float* part = reinterpret_cast<float*>(ws + w.part);
+        rc = dims->d_k == 128 ? launch_bwd<128>(p, m, mo, mo_plain, mdv, mdv_plain, o, part, stream)
+                              : launch_bwd<64>(p, m, mo, mo_plain, mdv, mdv_plain, o, part, stream);
+        if (rc != SS_OK) return rc;
+    }
+    return (flags & SS_SYNC_CHECK) ? ss_check(launch) : SS_OK;
 }
 
 }  // extern "C"

@@ -64,10 +64,29 @@ constexpr uint32_t kRecT = 0, kRecP = 2 * kTile, kRecScal = 4 * kTile;
 constexpr uint32_t kRecBytes = kRecScal + sizeof(Scal);
 static_assert(sizeof(Scal) == 1024 && kRecBytes % 16 == 0, "records are copied whole");
 
+struct alignas(16) Local {  // what a chunk's decay factors are made of (the backward pass keeps it behind the record)
+    float gh[kC], gl[kC];   // log2 of the decay from the chunk's start, as a pair
+    float cb[kC];           // β_j / |k_j|
+    float cf[kC];           // β_j / |k_j| e^{G_31 - G_j}, j < 32
+    float rk[kC], rq[kC];   // 1 / |k_i|, scale / |q_i|
+};
+constexpr uint32_t kRecLocal = kRecBytes, kRecBwdBytes = kRecBytes + 2048;
+static_assert(sizeof(Local) <= 2048, "record");
+
+// What the backward pass keeps of a chunk, beside its record: images of tiles in the swizzled layout of the MMAs.
+//   E [64 tokens][128], S0 hi and lo [128 rows v][128 keys] (the entering state's terms), dS1 [128][128] (bf16)
+constexpr uint32_t kKeepE = 0, kKeepShi = 2 * kTile, kKeepSlo = 6 * kTile, kKeepD = 10 * kTile, kKeepBytes = 14 * kTile;
+
 struct Params {
     GdrParams g;
     unsigned char* rec;      // [items][nchunks] records
     int64_t nchunks;         // chunks of g.L tokens
+    uint32_t rec_bytes;      // from record to record
+    // backward pass
+    unsigned char* keep;     // [items][nchunks + 1]
+    float* dots;             // [4][items][nchunks * 64]: dO·O, dV·V, dV·E of each token; <dS1, S1> of each chunk
+    const float* dfinal;     // [batch, H, d_v, d_k] or null
+    float* dinit;            // [batch, H, d_v, d_k] or null
     uint32_t* status;
     int dv;
     int test_drop;
@@ -288,22 +307,57 @@ __device__ __forceinline__ float pick32(const float (&v)[32], int i) {
     return (i & 1) ? a[1] : a[0];
 }
 
+// v_e *= row · cb_j e^{G_i - G_j}, j = j0 + e, for the 32 columns of row i's block on the diagonal; zero from the
+// diagonal on (incl: above it).  `r` is i's place in the block.
+__device__ __forceinline__ void decay_diagonal(float (&v)[32], const Local& lo, int j0, float gh, float gl, float row,
+                                               int r, bool incl) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        const float4 h4 = quad(lo.gh + j0 + e), l4 = quad(lo.gl + j0 + e), c4 = quad(lo.cb + j0 + e);
+        const f32x2 hh[2] = {pk2(h4.x, h4.y), pk2(h4.z, h4.w)}, ll[2] = {pk2(l4.x, l4.y), pk2(l4.z, l4.w)};
+        const f32x2 cc[2] = {pk2(c4.x, c4.y), pk2(c4.z, c4.w)};
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const f32x2 m1 = pk2(-1.0f, -1.0f);
+            const f32x2 d = add2(fma2(hh[f], m1, pk2(gh, gh)), fma2(ll[f], m1, pk2(gl, gl)));
+            const f32x2 w = mul2(mul2(pk2(v[e + 2 * f], v[e + 2 * f + 1]), cc[f]), pk2(row, row));
+            const f32x2 x = mul2(w, pk2(ex2_approx(d.x), ex2_approx(d.y)));
+            const int k = e + 2 * f - (incl ? 1 : 0);
+            v[e + 2 * f] = k < r ? x.x : 0.0f;
+            v[e + 2 * f + 1] = k + 1 < r ? x.y : 0.0f;
+        }
+    }
+}
+// The same for j < 32 <= i: both factors of e^{G_i - G_31} e^{G_31 - G_j} lie between the product and 1.
+__device__ __forceinline__ void decay_left(float (&v)[32], const Local& lo, float gh, float gl, float row) {
+    const float rf = row * exp2f((gh - lo.gh[31]) + (gl - lo.gl[31]));
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        const float4 c4 = quad(lo.cf + e);
+        const f32x2 r0 = mul2(mul2(pk2(v[e], v[e + 1]), pk2(c4.x, c4.y)), pk2(rf, rf));
+        const f32x2 r1 = mul2(mul2(pk2(v[e + 2], v[e + 3]), pk2(c4.z, c4.w)), pk2(rf, rf));
+        v[e] = r0.x;
+        v[e + 1] = r0.y;
+        v[e + 2] = r1.x;
+        v[e + 3] = r1.y;
+    }
+}
+
 // ------------------------------------------------------------------------------------------ preparation
 constexpr int kPrepThreads = 128;
 
-struct alignas(16) Local {
-    float gh[kC], gl[kC];   // log2 of the decay from the chunk's start, as a pair
-    float cb[kC];           // β_j / |k_j|
-    float cf[kC];           // β_j / |k_j| e^{G_31 - G_j}, j < 32
+struct alignas(16) PrepSmem {
     double G[kC];           // prefix sums over 32 tokens
     uint64_t full, gram;
     uint32_t tmem, pad[3];
 };
 // Shared memory: [K 0][Q 0][K 1][Q 1], P's terms over the first two once K and Q have been read; T as fp32 [64][64],
-// then T's terms in its place; the factors; scratch.
-constexpr uint32_t kPrepT = 4 * kTile, kPrepScal = 6 * kTile, kPrepXs = kPrepScal + sizeof(Scal);
-constexpr uint32_t kPrepLocal = kPrepXs + 32 * kPitchX * 4;
-constexpr uint32_t kPrepSmem = kPrepLocal + sizeof(Local) + 1024;
+// then T's terms in its place, with scratch over K 1; the factors.
+constexpr uint32_t kPrepXs = 2 * kTile, kPrepT = 4 * kTile, kPrepScal = 6 * kTile;
+constexpr uint32_t kPrepLocal = kPrepScal + sizeof(Scal);
+constexpr uint32_t kPrepState = kPrepLocal + 2048;
+constexpr uint32_t kPrepSmem = kPrepState + sizeof(PrepSmem) + 1024;
+static_assert(4 * (kPrepSmem + 1024) <= 228 * 1024, "four resident blocks");
 
 // Grid: one block per (item, chunk), a sequence's chunks together.  Bound by the latency of the triangular inverse
 // (fp32, about 75 000 multiply-adds in a dozen dependent steps), which the four resident blocks hide for one another.
@@ -318,6 +372,7 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
     unsigned char* gbase = smem_raw + (base - raw);
     Scal& sc = *reinterpret_cast<Scal*>(gbase + kPrepScal);
     Local& lo = *reinterpret_cast<Local*>(gbase + kPrepLocal);
+    PrepSmem& ps = *reinterpret_cast<PrepSmem*>(gbase + kPrepState);
     float* const a = reinterpret_cast<float*>(gbase + kPrepT);
     float* const xs = reinterpret_cast<float*>(gbase + kPrepXs);
 
@@ -331,17 +386,17 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
     const int valid = left < kC ? static_cast<int>(left) : kC;
 
     if (pt == 0) {
-        mbar_init(&lo.full, 1);
-        mbar_init(&lo.gram, 1);
+        mbar_init(&ps.full, 1);
+        mbar_init(&ps.gram, 1);
         fence_mbar_init();
-        mbar_arrive_expect_tx(&lo.full, 2 * KB * kTile);
+        mbar_arrive_expect_tx(&ps.full, 2 * KB * kTile);
         for (int kb = 0; kb < KB; ++kb) {
-            tma_load_4d(base + (2 * kb) * kTile, &tm_k, 64 * kb, hk, static_cast<int>(c) * kC, b, &lo.full);
-            tma_load_4d(base + (2 * kb + 1) * kTile, &tm_q, 64 * kb, hk, static_cast<int>(c) * kC, b, &lo.full);
+            tma_load_4d(base + (2 * kb) * kTile, &tm_k, 64 * kb, hk, static_cast<int>(c) * kC, b, &ps.full);
+            tma_load_4d(base + (2 * kb + 1) * kTile, &tm_q, 64 * kb, hk, static_cast<int>(c) * kC, b, &ps.full);
         }
     }
     if (warp == 0) {
-        tc::tmem_alloc(&lo.tmem, kC);
+        tc::tmem_alloc(&ps.tmem, kC);
         tc::tmem_relinquish();
     }
     float be = 0.0f;
@@ -352,6 +407,8 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
         if (i < valid) {
             delta = gdr_delta(to_f32(static_cast<const __nv_bfloat16*>(g.dt)[o]), g.dt_bias ? g.dt_bias[h] : 0.0f, g.softplus);
             be = gdr_beta(to_f32(static_cast<const __nv_bfloat16*>(g.beta)[o]), g.sigmoid);
+            // β's gradient is a quotient by β; 1e-20 stands for a β of zero there, and changes nothing else
+            if (p.keep && !g.sigmoid && fabsf(be) < 1e-20f) be = 1e-20f;
         }
         G = static_cast<double>(delta) * static_cast<double>(g.A[h]) * 1.4426950408889634074;   // log2 α
 #pragma unroll
@@ -359,13 +416,13 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
             const double v = __shfl_up_sync(0xffffffffu, G, s);
             if (lane >= s) G += v;
         }
-        lo.G[i] = G;
+        ps.G[i] = G;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = lo.tmem;
-    bool got = mbar_wait_bounded(&lo.full, 0, p.wait_ns);
+    const uint32_t tmem = ps.tmem;
+    bool got = mbar_wait_bounded(&ps.full, 0, p.wait_ns);
     if (valid < kC) {   // rows behind the end, whatever they hold, become zero rows
         if (i >= valid && got) {
             for (int w = 0; w < 8 * KB; ++w)
@@ -381,9 +438,9 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
             const uint32_t off = (ks >> 2) * 2 * kTile + (ks & 3) * 32;
             umma(tmem, sdesc(base + off, 16, 1024), sdesc(base + off, 16, 1024), idesc(kC, false), ks > 0);
         }
-        umma_commit(&lo.gram);
+        umma_commit(&ps.gram);
     }
-    const double first = lo.G[31], end = first + lo.G[63];
+    const double first = ps.G[31], end = first + ps.G[63];
     float rn = 1.0f;   // 1 / |row i| of K, or of Q
     if (!is_q) {
         if (i >= 32) G += first;
@@ -403,7 +460,7 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
         }
         rn = 1.0f / sqrtf((q0.x + q0.y) + (q1.x + q1.y) + kGdrL2Eps);
     }
-    if (got) got = mbar_wait_bounded(&lo.gram, 0, p.wait_ns);
+    if (got) got = mbar_wait_bounded(&ps.gram, 0, p.wait_ns);
     const bool bad = __syncthreads_or(!got) != 0;
     if (bad) {
         if (pt == 0 && p.status) atomicCAS(p.status, 0u, static_cast<uint32_t>(SS_ERR_TIMEOUT));
@@ -414,6 +471,7 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
         tmem_ld32(src + 32 * rb, v);   // the block on the diagonal
         if (!is_q) {                   // |k_i|² is K Kᵀ's own diagonal
             if (g.l2norm) rn = 1.0f / sqrtf(pick32(v, lane) + kGdrL2Eps);
+            lo.rk[i] = rn;
             lo.cb[i] = be * rn;
             if (rb == 0) lo.cf[i] = be * rn * exp2f(static_cast<float>(first - G));
             sc.ek[i] = -exp2f(static_cast<float>(G)) * rn;
@@ -422,7 +480,10 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
         __syncthreads();
         const float gh = lo.gh[i], gl = lo.gl[i];
         const float row = is_q ? rn * g.scale : rn;
-        if (is_q) sc.qe[i] = exp2f(gh) * row;
+        if (is_q) {
+            sc.qe[i] = exp2f(gh) * row;
+            lo.rq[i] = row;
+        }
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
             // first the block on the diagonal, then (rows 32..63) the block left of it; above the diagonal P is zero
@@ -439,36 +500,8 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
                 tmem_ld32(src, v);
             }
             const int j0 = blk == 0 ? 32 * rb : 0;
-            if (blk == 0) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 h4 = quad(lo.gh + j0 + e), l4 = quad(lo.gl + j0 + e), c4 = quad(lo.cb + j0 + e);
-                    const f32x2 hh[2] = {pk2(h4.x, h4.y), pk2(h4.z, h4.w)}, ll[2] = {pk2(l4.x, l4.y), pk2(l4.z, l4.w)};
-                    const f32x2 cc[2] = {pk2(c4.x, c4.y), pk2(c4.z, c4.w)};
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        const f32x2 m1 = pk2(-1.0f, -1.0f);
-                        const f32x2 d = add2(fma2(hh[f], m1, pk2(gh, gh)), fma2(ll[f], m1, pk2(gl, gl)));
-                        const f32x2 w = mul2(mul2(pk2(v[e + 2 * f], v[e + 2 * f + 1]), cc[f]), pk2(row, row));
-                        const f32x2 r = mul2(w, pk2(ex2_approx(d.x), ex2_approx(d.y)));
-                        const int k = e + 2 * f - (is_q ? 1 : 0);   // P keeps its diagonal
-                        v[e + 2 * f] = k < lane ? r.x : 0.0f;
-                        v[e + 2 * f + 1] = k + 1 < lane ? r.y : 0.0f;
-                    }
-                }
-            } else {   // j < 32 <= i: both factors of e^{G_i - G_31} e^{G_31 - G_j} lie between the product and 1
-                const float rf = row * exp2f(static_cast<float>((static_cast<double>(gh) + static_cast<double>(gl)) - first));
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 c4 = quad(lo.cf + e);
-                    const f32x2 r0 = mul2(mul2(pk2(v[e], v[e + 1]), pk2(c4.x, c4.y)), pk2(rf, rf));
-                    const f32x2 r1 = mul2(mul2(pk2(v[e + 2], v[e + 3]), pk2(c4.z, c4.w)), pk2(rf, rf));
-                    v[e] = r0.x;
-                    v[e + 1] = r0.y;
-                    v[e + 2] = r1.x;
-                    v[e + 3] = r1.y;
-                }
-            }
+            if (blk == 0) decay_diagonal(v, lo, j0, gh, gl, row, lane, is_q);
+            else decay_left(v, lo, gh, gl, row);
             if (is_q) {   // (K and Q have been read: by the MMAs, and by the lengths before the barriers above)
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
@@ -511,15 +544,16 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
     __syncthreads();
     if (pt == 0) {
         if (!bad) {
-            unsigned char* r = p.rec + (item * p.nchunks + c) * kRecBytes;
+            unsigned char* r = p.rec + (item * p.nchunks + c) * p.rec_bytes;
             bulk_store(r + kRecT, base + kPrepT, 2 * kTile);
             bulk_store(r + kRecP, base, 2 * kTile);
             bulk_store(r + kRecScal, base + kPrepScal, sizeof(Scal));
+            if (p.keep) bulk_store(r + kRecLocal, base + kPrepLocal, sizeof(Local));
             tc::bulk_commit();
             bulk_wait0();
         } else {   // what is still in flight ends before the shared memory and the TMEM columns go
-            mbar_wait_bounded(&lo.full, 0, p.drain_ns);
-            if (issued) mbar_wait_bounded(&lo.gram, 0, p.drain_ns);
+            mbar_wait_bounded(&ps.full, 0, p.drain_ns);
+            if (issued) mbar_wait_bounded(&ps.gram, 0, p.drain_ns);
         }
     }
     __syncwarp();
@@ -563,9 +597,40 @@ constexpr uint32_t kOffV = 4 * kTile, kOffRec = 6 * kTile;
 constexpr uint32_t kStageBytes = kOffRec + kRecBytes;
 static_assert(kStageBytes % 1024 == 0, "swizzled tiles");
 constexpr uint32_t kOffY = kStages * kStageBytes;      // y [64][d_v] for the store
-constexpr uint32_t kOffBar = kOffY + 2 * kTile;
+constexpr uint32_t kOffE = kOffY + 2 * kTile;          // backward: dO in y's place, E [2 blocks of 64 rows] for its store
+constexpr uint32_t kOffDot = kOffE + 2 * kTile;        // and the row sums of the four lane groups, [4][64]
+constexpr uint32_t kOffBar = kOffDot + 4 * kC * 4;
 constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// Σ over a warp's lanes of each of 16 values, by halving: after it lane l holds the sum of value (l >> 1) (both lanes
+// of a pair the same).
+__device__ __forceinline__ float lane_sums16(float (&v)[16], int lane) {
+#pragma unroll
+    for (int o = 16, n = 8; n > 0; o >>= 1, n >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (e >= n) break;
+            const float keep = up ? v[e + n] : v[e], give = up ? v[e] : v[e + n];
+            v[e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    }
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+// 16 values' terms (hi then lo words) to two images of [rows][64-wide blocks]: chunks 2 m, 2 m + 1 of row r.
+__device__ __forceinline__ void keep_terms(unsigned char* hi_img, unsigned char* lo_img, int r, int key, const f32x2* v) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split2(v[e], hi[e], lo[e]);
+    const uint32_t blk = static_cast<uint32_t>(key >> 6) * 2 * kTile;   // 128 rows of 128 bytes
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t o = chunk_addr(blk, r, ((key & 63) >> 3) + h);
+        *reinterpret_cast<uint4*>(hi_img + o) = make_uint4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]);
+        if (lo_img) *reinterpret_cast<uint4*>(lo_img + o) = make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
+    }
+}
 
 struct Bars {
     uint64_t full[kStages];    // K, Q, V and the record of a stage landed
@@ -573,14 +638,16 @@ struct Bars {
     uint64_t ks, e, ds, pv;    // the chain's products done
     uint64_t s_ready[2];       // S's terms written: of the first 16 keys of each thread, of the others (state warps)
     uint64_t x_ready, w_ready, e_ready;   // X's terms, W's, E's and Y's first part written (state warps)
-    uint64_t y_full, y_free;   // y staged (state warps); stored (1)
+    uint64_t y_full, y_free;   // y staged (state warps); stored (1).  Backward: dO read (state warps); landed (1)
+    uint64_t e_full, e_free;   // backward: E staged (state warps); stored (1)
     uint64_t fin;              // wind-down
     uint32_t tmem;
 };
 static_assert(sizeof(Bars) <= 256, "barrier region");
 
-// Grid: one CTA per (b, h).
-template <int DK>
+// Grid: one CTA per (b, h).  BWD: the backward pass's forward half.  y is not written (tm_y reads dO); what is kept of
+// each chunk is E, the entering state's terms, and dO_i · O_i of its tokens in fp32.
+template <int DK, bool BWD>
 __global__ void __launch_bounds__(kThreads, 1)
 ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_q,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -607,9 +674,9 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             mbar_init(&bar->full[i], 1);
             mbar_init(&bar->empty[i], 1);
         }
-        uint64_t* one[] = {&bar->ks, &bar->e, &bar->ds, &bar->pv, &bar->y_free, &bar->fin};
+        uint64_t* one[] = {&bar->ks, &bar->e, &bar->ds, &bar->pv, &bar->y_free, &bar->e_free, &bar->fin};
         for (uint64_t* x : one) mbar_init(x, 1);
-        uint64_t* all[] = {bar->s_ready, bar->s_ready + 1, &bar->x_ready, &bar->w_ready, &bar->e_ready, &bar->y_full};
+        uint64_t* all[] = {bar->s_ready, bar->s_ready + 1, &bar->x_ready, &bar->w_ready, &bar->e_ready, &bar->y_full, &bar->e_full};
         for (uint64_t* x : all) mbar_init(x, kStateWarps);
         fence_mbar_init();
     }
@@ -640,7 +707,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         __syncwarp();
         if (lane == 0) mbar_arrive(x);
     };
-    int issued = 0;   // loads of the load thread
+    int issued = 0, do_issued = 0;   // loads of the load thread, of the store warp
 
     if (warp == kLoadWarp) {
         // ============================================================ loads (one thread)
@@ -660,14 +727,37 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 }
                 for (int vb = 0; vb < p.dv / 64; ++vb)
                     tma_load_4d(st + kOffV + vb * kTile, &tm_v, 64 * vb, h, c * kC, b, f);
-                bulk_load(st + kOffRec, p.rec + (item * p.nchunks + c) * kRecBytes, kRecBytes, f);
+                bulk_load(st + kOffRec, p.rec + (item * p.nchunks + c) * p.rec_bytes, kRecBytes, f);
                 issued = c + 1;
             }
         }
         __syncwarp();
     } else if (warp == kStoreWarp) {
-        // ============================================================ y
-        for (int c = 0; c < nchunk; ++c) {
+        // ============================================================ y; backward: dO in, E out
+        for (int c = 0; BWD && c <= nchunk; ++c) {
+            // dO of chunk c once chunk c - 1's was read, E of chunk c once it was staged
+            if (c > 0) {
+                if (!wait_warp(&bar->y_full, (c - 1) & 1)) break;
+                const float* q = reinterpret_cast<const float*>(gbase + kOffDot);   // the four lane groups, in order
+                float* out = p.dots + (item * p.nchunks + c - 1) * kC;
+                for (int i = lane; i < kC; i += 32) out[i] = (q[i] + q[kC + i]) + (q[2 * kC + i] + q[3 * kC + i]);
+                __syncwarp();
+            }
+            if (c == nchunk) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar->y_free, kC * p.dv * 2);
+                tma_load_4d(base + kOffY, &tm_y, 0, h, c * kC, b, &bar->y_free);
+            }
+            do_issued = c + 1;
+            if (!wait_warp(&bar->e_full, c & 1)) break;
+            if (lane == 0) {
+                bulk_store(p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes + kKeepE, base + kOffE, 2 * kTile);
+                tc::bulk_commit();
+                tc::bulk_wait_read0();
+            }
+            arrive_warp(&bar->e_free);
+        }
+        for (int c = 0; !BWD && c < nchunk; ++c) {
             if (!wait_warp(&bar->y_full, c & 1)) break;
             if (c != ragged) {   // rows behind the tensor's end are clipped by the copy
                 if (lane == 0) {
@@ -774,6 +864,44 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         for (int k = 0; k < KH; k += 16) store_terms(tl + kColS + part * KH + k, S + k / 2);
         tmem_wait_st();
         tc_fence_before();
+        auto keep_state = [&](int c) {   // the terms of the state that enters chunk c
+            unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
+#pragma unroll
+            for (int k = 0; k < KH; k += 16) keep_terms(kp + kKeepShi, kp + kKeepSlo, v, part * KH + k, S + k / 2);
+        };
+        auto finish_y = [&](int c) {     // chunk c's y, or its dO·O
+            if (BWD ? !wait_warp(&bar->y_free, c & 1) : (c > 0 && !wait_warp(&bar->y_free, (c - 1) & 1))) return false;
+            if (!wait_warp(&bar->pv, c & 1)) return false;
+            tc_fence_after();
+            f32x2 x[8], w[8];
+            tmem_ld16x2(tl + kColY + kTok * part, tl + kColY + kC + kTok * part, x, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = add2(x[e], w[e]);
+            __nv_bfloat16* ys = reinterpret_cast<__nv_bfloat16*>(gbase + kOffY) + kTok * part * p.dv + v;
+            if (BWD) {
+                float d[16];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    d[2 * e] = row_in ? x[e].x * __bfloat162float(ys[2 * e * p.dv]) : 0.0f;
+                    d[2 * e + 1] = row_in ? x[e].y * __bfloat162float(ys[(2 * e + 1) * p.dv]) : 0.0f;
+                }
+                float* dots = reinterpret_cast<float*>(gbase + kOffDot);
+                const float sum = lane_sums16(d, lane);
+                if (!(lane & 1)) dots[(warp & 3) * kC + kTok * part + (lane >> 1)] = sum;
+                arrive_warp(&bar->y_full);
+                return true;
+            }
+            if (row_in) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    ys[2 * e * p.dv] = __float2bfloat16_rn(x[e].x);
+                    ys[(2 * e + 1) * p.dv] = __float2bfloat16_rn(x[e].y);
+                }
+            }
+            fence_proxy_async_smem();
+            arrive_warp(&bar->y_full);
+            return true;
+        };
         bool ok = true;
         for (int c = 0; c < nchunk; ++c) {
             const int s = c % kStages;
@@ -793,24 +921,10 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 arrive_warp(&bar->s_ready[0]);
                 arrive_warp(&bar->s_ready[1]);
             }
+            if (BWD) keep_state(c);
             if (c > 0) {   // the last chunk's y, while this one's K Sᵀ runs
-                ok = (c == 1 || wait_warp(&bar->y_free, c & 1)) && wait_warp(&bar->pv, par ^ 1);
+                ok = finish_y(c - 1);
                 if (!ok) break;
-                tc_fence_after();
-                f32x2 x[8], w[8];
-                tmem_ld16x2(tl + kColY + kTok * part, tl + kColY + kC + kTok * part, x, w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = add2(x[e], w[e]);
-                if (row_in) {
-                    __nv_bfloat16* ys = reinterpret_cast<__nv_bfloat16*>(gbase + kOffY) + kTok * part * p.dv + v;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        ys[2 * e * p.dv] = __float2bfloat16_rn(x[e].x);
-                        ys[(2 * e + 1) * p.dv] = __float2bfloat16_rn(x[e].y);
-                    }
-                }
-                fence_proxy_async_smem();
-                arrive_warp(&bar->y_full);
             }
             ok = wait_warp(&bar->full[s], (c / kStages) & 1) && wait_warp(&bar->ks, par);
             if (!ok) break;
@@ -854,6 +968,19 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(&bar->e_ready);
+            if (BWD) {   // E's hi terms, staged as the image that the gradient kernel reads
+                ok = c == 0 || wait_warp(&bar->e_free, (c - 1) & 1);
+                if (!ok) break;
+                const uint32_t img = base + kOffE + static_cast<uint32_t>(v >> 6) * kTile;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int t = kTok * part + e;
+                    *reinterpret_cast<__nv_bfloat16*>(smem_raw + (chunk_addr(img, t, (v & 63) >> 3) + 2 * (v & 7) - raw)) =
+                        __float2bfloat16_rn((e & 1) ? x[e >> 1].y : x[e >> 1].x);
+                }
+                fence_proxy_async_smem();
+                arrive_warp(&bar->e_full);
+            }
             ok = wait_warp(&bar->ds, par);
             if (!ok) break;
             tc_fence_after();
@@ -873,26 +1000,8 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             tmem_wait_st();
             tc_fence_before();
         }
-        if (ok && nchunk > 0) {   // the last chunk's y
-            ok = (nchunk == 1 || wait_warp(&bar->y_free, nchunk & 1)) && wait_warp(&bar->pv, (nchunk - 1) & 1);
-            if (ok) {
-                tc_fence_after();
-                f32x2 x[8], w[8];
-                tmem_ld16x2(tl + kColY + kTok * part, tl + kColY + kC + kTok * part, x, w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = add2(x[e], w[e]);
-                if (row_in) {
-                    __nv_bfloat16* ys = reinterpret_cast<__nv_bfloat16*>(gbase + kOffY) + kTok * part * p.dv + v;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        ys[2 * e * p.dv] = __float2bfloat16_rn(x[e].x);
-                        ys[(2 * e + 1) * p.dv] = __float2bfloat16_rn(x[e].y);
-                    }
-                }
-                fence_proxy_async_smem();
-                arrive_warp(&bar->y_full);
-            }
-        }
+        if (ok && nchunk > 0) ok = finish_y(nchunk - 1);
+        if (BWD && ok) keep_state(nchunk);
         if (ok && g.final_state && row_in) {
 #pragma unroll
             for (int k = 0; k < KH; k += 4)
@@ -908,6 +1017,8 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         for (int c = issued > kStages ? issued - kStages : 0; c < issued; ++c)
             mbar_wait_bounded(&bar->full[c % kStages], (c / kStages) & 1, p.drain_ns);
     }
+    if (BWD && warp == kStoreWarp && lane == 0 && do_issued > 0)
+        mbar_wait_bounded(&bar->y_free, (do_issued - 1) & 1, p.drain_ns);
     if (tid == 32 * kMmaWarp) {
         umma_commit(&bar->fin);
         mbar_wait_bounded(&bar->fin, 0, p.drain_ns);
