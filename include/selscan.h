@@ -379,7 +379,7 @@ SS_API int ss_gdr_step(float* state, const void* q, const void* k, const void* v
  * sums are added in a fixed order: the same call gives the same bits.  Outputs overlap
  * neither the inputs nor one another (dh_init may be dfinal_state).
  * Workspace: launch->workspace of at least ss_gdr_bwd_workspace_bytes() bytes (about
- * 148 KB per 64 tokens of a head: the chunks' states and their adjoints), 16-byte
+ * 230 KB per 64 tokens of a head: the chunks' states and their adjoints), 16-byte
  * aligned; its first word is the status word, as in ss_gdr_fwd.  Errors: as ss_gdr_fwd. */
 SS_API int ss_gdr_bwd(const void* q, const void* k, const void* v, const void* dt, const float* dt_bias,
                       const float* A, const void* beta, const float* h_init, const int32_t* seqlens,

@@ -97,7 +97,7 @@ struct Maps {
 template <int DK>
 int launch_tc(const gdr::Params& p, const Maps& m, cudaStream_t stream) {
     auto prep = gdr::ss_gdr_prep_kernel<DK>;
-    auto kern = gdr::ss_gdr_tc_kernel<DK, false>;
+    auto kern = gdr::ss_gdr_tc_kernel<DK, true>;
     static std::atomic<bool> attr[2][kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || set_smem_limit(kern, gdr::kSmemBytes, attr[0], dev) != SS_OK ||
@@ -143,7 +143,7 @@ GdrBwdLayout gdr_bwd_layout(const ss_gdr_dims* d) {
     w.rec = 1024;
     w.keep = w.rec + al(items * n * gdr::kRecBwdBytes);
     w.dots = w.keep + al(items * (n + 1) * gdr::kKeepBytes);
-    w.part = w.dots + al((3 * items * n * gdr::kC + items * n) * sizeof(float));
+    w.part = w.dots + al((4 * items * n * gdr::kC + items * (n + 1)) * sizeof(float));
     w.total = w.part + al(items * 2 * sizeof(float));
     return w;
 }
@@ -154,11 +154,10 @@ struct GdrGrads {
 };
 
 template <int DK>
-int launch_bwd(const gdr::Params& p, const Maps& m, const CUtensorMap& mo, const CUtensorMap& mo_plain,
-               const CUtensorMap& mdv, const CUtensorMap& mdv_plain, const GdrGrads& o, float* part,
+int launch_bwd(const gdr::Params& p, const Maps& m, const CUtensorMap& mo, const GdrGrads& o, float* part,
                cudaStream_t stream) {
     auto prep = gdr::ss_gdr_prep_kernel<DK>;
-    auto fwd = gdr::ss_gdr_tc_kernel<DK, true>;
+    auto fwd = gdr::ss_gdr_tc_kernel<DK, false>;
     auto rev = gdr::ss_gdr_rev_kernel<DK>;
     auto grad = gdr::ss_gdr_grad_kernel<DK>;
     static std::atomic<bool> attr[4][kMaxDevices];
@@ -171,11 +170,11 @@ int launch_bwd(const gdr::Params& p, const Maps& m, const CUtensorMap& mo, const
     const int64_t items = static_cast<int64_t>(p.g.batch) * p.g.H;
     const unsigned n = static_cast<unsigned>(items);
     prep<<<static_cast<unsigned>(items * p.nchunks), gdr::kPrepThreads, gdr::kPrepSmem, stream>>>(p, m.q, m.k);
-    fwd<<<n, gdr::kThreads, gdr::kSmemBytes, stream>>>(p, m.q, m.k, m.v, mo_plain);
-    rev<<<n, gdr::kThreads, gdr::kRevSmem, stream>>>(p, m.q, m.k, m.v, mo, mdv_plain);
+    fwd<<<n, gdr::kThreads, gdr::kSmemBytes, stream>>>(p, m.q, m.k, m.v, m.v);
+    rev<<<n, gdr::kThreads, gdr::kRevSmem, stream>>>(p, m.q, m.k, mo);
     gdr::GradParams gp{p, o.dq, o.dk, o.dv};
     const int64_t blocks = static_cast<int64_t>(p.g.batch) * p.g.Hk * p.nchunks;
-    grad<<<static_cast<unsigned>(blocks), gdr::kGradThreads, gdr::kGradSmem, stream>>>(gp, m.q, m.k, mo, mdv);
+    grad<<<static_cast<unsigned>(blocks), gdr::kGradThreads, gdr::kGradSmem, stream>>>(gp, m.q, m.k, mo);
     gdr::GateParams gt{p, o.ddt, o.dbeta, part};
     gdr::ss_gdr_gate_kernel<<<n, 256, 0, stream>>>(gt);
     gdr::ss_gdr_head_kernel<<<static_cast<unsigned>(ceil_div(p.g.H, 128)), 128, 0, stream>>>(part, p.g.batch, p.g.H, o.dA,
@@ -294,21 +293,18 @@ int ss_gdr_bwd(const void* q, const void* k, const void* v, const void* dt, cons
         p.wait_ns = launch->timeout_iters ? static_cast<uint64_t>(launch->timeout_iters) * 1000ull : kTmaWaitNs;
         p.drain_ns = kTmaWaitNs;
         Maps m;
-        CUtensorMap mo, mo_plain, mdv, mdv_plain;
+        CUtensorMap mo;
         const int64_t B = dims->batch, H = dims->nheads, dvw = dims->d_v;
         if (!head_map(&m.q, q, B, L, dims->nheads_k, dims->d_k, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !head_map(&m.k, k, B, L, dims->nheads_k, dims->d_k, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !head_map(&m.v, v, B, L, H, dvw, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !head_map(&mo, dy, B, L, H, dvw, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !head_map(&mo_plain, dy, B, L, H, dvw, dvw, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-            !head_map(&mdv, dv, B, L, H, dvw, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !head_map(&mdv_plain, dv, B, L, H, dvw, dvw, CU_TENSOR_MAP_SWIZZLE_NONE))
+            !head_map(&mo, dy, B, L, H, dvw, 64, CU_TENSOR_MAP_SWIZZLE_128B))
             return SS_ERR_CUDA;
         const GdrGrads o{static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv),
                          static_cast<__nv_bfloat16*>(ddt), static_cast<__nv_bfloat16*>(dbeta), dA, ddt_bias};
         float* part = reinterpret_cast<float*>(ws + w.part);
-        rc = dims->d_k == 128 ? launch_bwd<128>(p, m, mo, mo_plain, mdv, mdv_plain, o, part, stream)
-                              : launch_bwd<64>(p, m, mo, mo_plain, mdv, mdv_plain, o, part, stream);
+        rc = dims->d_k == 128 ? launch_bwd<128>(p, m, mo, o, part, stream)
+                              : launch_bwd<64>(p, m, mo, o, part, stream);
         if (rc != SS_OK) return rc;
     }
     return (flags & SS_SYNC_CHECK) ? ss_check(launch) : SS_OK;

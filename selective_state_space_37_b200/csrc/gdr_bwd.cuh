@@ -10,14 +10,17 @@
 // parallel over chunks (ss_gdr_grad_kernel), with S the entering state and dS the leaving one's adjoint, kept by the
 // two chains:
 //   M^P_ij = (dO_i·E_j) e^{G_i - G_j} β_j (j <= i),   M^A_ij = -(dV_i·E_j) e^{G_i - G_j} β_j (j < i)
-//   dQ̂ = diag(e^G) dO S + M^P K̂,    dK̂ = -diag(e^G) dV S + diag(β e^{G_end - G}) E dS + M^Pᵀ Q̂ + M^A K̂ + M^Aᵀ K̂
-// and for the gates, with <S, dS> of the state that leaves the chunk (every term of Y and of S that carries e^{G_i}
-// is a term of dO_i·Y_i, and every e^{-G_i} one of dV_i·V_i, which is what makes the sums this short):
-//   dlog α_t = <S, dS> + Σ_{i >= t} (dO_i·Y_i - dV_i·V_i) over the chunk,     dβ_j = dV_j·E_j / β_j
-// A chunk's sum starts from its own <S, dS>, so rounding does not pile up over a long sequence.
+//   dQ̂ = [diag(e^G) dO S + M^P K̂]
+//   dK̂ = [-diag(e^G) dV S + M^A K̂] + [diag(β e^{G_end - G}) E dS + M^Pᵀ Q̂ + M^Aᵀ K̂]
+// For the gates: a token's decay stands in every path that crosses it, so the gradient of log α changes from a token
+// to the next by what ends and what begins there.  With R_t = q̂_t·dq̂_t + k̂_t·(the first bracket of dk̂_t), where
+// paths end, and C_t = k̂_t·(the second), where they begin, and S, dS at the chunk's start:
+//   dlog α_0 = <S, dS>,   dlog α_t+1 = dlog α_t - R_t + C_t,        dβ_j = dV_j·E_j / β_j
+// Every term carries its decay, so a head that forgets fast has small terms and not the difference of large ones (as
+// Σ (dO·Y - dV·V), which is the same sum, would be); and each chunk starts from its own <S, dS>.
 //
-// Precision: the chain as in the forward (fp32 operands as two bf16 terms; the sums for the gates in fp32).  dQ and
-// dK leave as bf16, and their products read E, dV, S, dS, M rounded once to bf16.
+// Precision: fp32 operands enter every product as two bf16 terms, as in the forward; the gates' gradients are sums
+// over all tokens and come out in fp32.
 #pragma once
 
 #include "gdr_tc.cuh"
@@ -29,33 +32,28 @@ namespace gdr {
 // TMEM columns.  S: dS's terms, then its update; A: K dSᵀ, then dE's terms over it; R: Pᵀ dO in two halves (P's terms);
 // V: Tᵀ dE in two halves, then the terms of -e^G dV over the first; O: the terms of scale e^G dO.
 constexpr uint32_t kRevS = 0, kRevA = 128, kRevR = 192, kRevV = 320, kRevO = 448;
-// Shared memory: two stages of [K 0][Q 0][K 1][Q 1][record]; then, once each, dO and V (swizzled blocks), E's image, and
-// dV staged for its store.
+// Shared memory: two stages of [K 0][Q 0][K 1][Q 1][record]; two of dO (swizzled blocks); the warps' <S, dS>.
 constexpr uint32_t kRevStage = 4 * kTile + kRecBytes, kRevOffRec = 4 * kTile;
-constexpr uint32_t kRevOffO = 2 * kRevStage, kRevOffV = kRevOffO + 2 * kTile, kRevOffE = kRevOffV + 2 * kTile;
-constexpr uint32_t kRevOffOut = kRevOffE + 2 * kTile, kRevOffDot = kRevOffOut + 2 * kTile;
-constexpr uint32_t kRevOffBar = kRevOffDot + 2 * 4 * kC * 4 + 2 * 16 * 4;
+constexpr uint32_t kRevOffO = 2 * kRevStage, kRevOffDot = kRevOffO + 4 * kTile;
+constexpr uint32_t kRevOffBar = kRevOffDot + 16 * 4;
 constexpr uint32_t kRevSmem = kRevOffBar + 256 + 1024;
 static_assert(kRevStage % 1024 == 0 && kRevSmem <= 227 * 1024, "shared memory");
 
 struct RevBars {
-    uint64_t full[2], empty[2];      // K, Q and the record of a stage
-    uint64_t o_full, o_free;         // dO landed; read (state warps, after its product)
-    uint64_t ve_full, ve_free;       // V and E landed; read (state warps)
+    uint64_t full[2], empty[2];      // K, Q, dO and the record of a stage
     uint64_t ks, e, ds;              // products done
     uint64_t s_ready[2], x_ready, w_ready;
-    uint64_t out_full, out_free;     // dV and the sums staged (state warps); stored (1)
+    uint64_t dot, dot_free;          // a step's <S, dS> of every warp written; read (1)
     uint64_t fin;
     uint32_t tmem;
 };
 static_assert(sizeof(RevBars) <= 256, "barrier region");
 
-// Grid: one CTA per (b, h).  tm_o reads dO and tm_v V in swizzled blocks, tm_dv writes dV unswizzled.
+// Grid: one CTA per (b, h).  Of a chunk dV and the leaving state's adjoint are kept.
 template <int DK>
 __global__ void __launch_bounds__(kThreads, 1)
 ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_q,
-                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_dv) {
+                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_o) {
     constexpr int KB = DK / 64, KH = DK / kParts;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -70,14 +68,10 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
     const int nchunk = static_cast<int>((len + kC - 1) / kC);
     const bool ragged = len % kC != 0 && len < g.L;   // other tokens follow in the last chunk's tiles
     const uint64_t lim = p.wait_ns;
-    const int64_t toks = p.nchunks * kC;
-
     if (tid == 0) {
-        uint64_t* one[] = {bar->full, bar->full + 1, bar->empty, bar->empty + 1, &bar->o_full, &bar->ve_full, &bar->ks,
-                           &bar->e,   &bar->ds,      &bar->out_free, &bar->fin};
+        uint64_t* one[] = {bar->full, bar->full + 1, bar->empty, bar->empty + 1, &bar->ks, &bar->e, &bar->ds, &bar->dot_free, &bar->fin};
         for (uint64_t* x : one) mbar_init(x, 1);
-        uint64_t* all[] = {&bar->o_free, &bar->ve_free, bar->s_ready, bar->s_ready + 1, &bar->x_ready, &bar->w_ready,
-                           &bar->out_full};
+        uint64_t* all[] = {bar->s_ready, bar->s_ready + 1, &bar->x_ready, &bar->w_ready, &bar->dot};
         for (uint64_t* x : all) mbar_init(x, kStateWarps);
         fence_mbar_init();
     }
@@ -107,7 +101,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
         __syncwarp();
         if (lane == 0) mbar_arrive(x);
     };
-    int issued = 0, o_issued = 0, ve_issued = 0;
+    int issued = 0;
 
     // Step n handles chunk nchunk - 1 - n.
     if (warp == kLoadWarp) {
@@ -117,54 +111,29 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 if (n >= 2 && !wait1(&bar->empty[s], ((n >> 1) - 1) & 1)) break;
                 const uint32_t st = base + s * kRevStage;
                 uint64_t* f = &bar->full[s];
-                mbar_arrive_expect_tx(f, 2 * KB * kTile + kRecBytes);
+                mbar_arrive_expect_tx(f, 2 * KB * kTile + kC * p.dv * 2 + kRecBytes);
                 for (int kb = 0; kb < KB; ++kb) {
                     tma_load_4d(st + (2 * kb) * kTile, &tm_k, 64 * kb, hk, c * kC, b, f);
                     tma_load_4d(st + (2 * kb + 1) * kTile, &tm_q, 64 * kb, hk, c * kC, b, f);
                 }
+                for (int vb = 0; vb < p.dv / 64; ++vb)
+                    tma_load_4d(base + kRevOffO + (2 * s + vb) * kTile, &tm_o, 64 * vb, h, c * kC, b, f);
                 bulk_load(st + kRevOffRec, p.rec + (item * p.nchunks + c) * p.rec_bytes, kRecBytes, f);
                 issued = n + 1;
-                if (n >= 1 && !wait1(&bar->o_free, (n - 1) & 1)) break;
-                mbar_arrive_expect_tx(&bar->o_full, kC * p.dv * 2);
-                for (int vb = 0; vb < p.dv / 64; ++vb)
-                    tma_load_4d(base + kRevOffO + vb * kTile, &tm_o, 64 * vb, h, c * kC, b, &bar->o_full);
-                o_issued = n + 1;
-                if (n >= 1 && !wait1(&bar->ve_free, (n - 1) & 1)) break;
-                mbar_arrive_expect_tx(&bar->ve_full, kC * p.dv * 4);
-                for (int vb = 0; vb < p.dv / 64; ++vb)
-                    tma_load_4d(base + kRevOffV + vb * kTile, &tm_v, 64 * vb, h, c * kC, b, &bar->ve_full);
-                bulk_load(base + kRevOffE, p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes + kKeepE, kC * p.dv * 2,
-                          &bar->ve_full);
-                ve_issued = n + 1;
             }
         }
         __syncwarp();
     } else if (warp == kStoreWarp) {
-        for (int n = 0; n < nchunk; ++n) {
-            const int c = nchunk - 1 - n;
-            if (!wait_warp(&bar->out_full, n & 1)) break;
-            if (lane == 0) {   // rows behind a sequence's end are zero rows: dO is zero there
-                tc::tma_store_4d(&tm_dv, base + kRevOffOut, 0, h, c * kC, b);
-                tc::bulk_commit();
-            }
-            const float* q = reinterpret_cast<const float*>(gbase + kRevOffDot);
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {   // dV·V, dV·E: the four lane groups, in order
-                const float* d = q + w * 4 * kC;
-                float* out = p.dots + (w + 1) * (static_cast<int64_t>(g.batch) * g.H * toks) + item * toks + static_cast<int64_t>(c) * kC;
-                for (int i = lane; i < kC; i += 32) out[i] = (d[i] + d[kC + i]) + (d[2 * kC + i] + d[3 * kC + i]);
-            }
-            float a = q[8 * kC + (n & 1) * 16 + (lane & 15)];   // <S, dS>: the sixteen warps' sums
+        // <S, dS> at the states between the chunks, from the last to the first: the sixteen warps' sums, in order of a tree
+        for (int n = 0; n <= nchunk; ++n) {
+            if (!wait_warp(&bar->dot, n & 1)) break;
+            float a = reinterpret_cast<const float*>(gbase + kRevOffDot)[lane & 15];
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-            if (lane == 0) {
-                p.dots[3 * (static_cast<int64_t>(g.batch) * g.H * toks) + item * p.nchunks + c] = a;
-                tc::bulk_wait_read0();
-            }
-            arrive_warp(&bar->out_free);
+            if (lane == 0)
+                p.dots[4 * (static_cast<int64_t>(g.batch) * g.H * p.nchunks * kC) + item * (p.nchunks + 1) + nchunk - n] = a;
+            arrive_warp(&bar->dot_free);
         }
-        if (lane == 0) bulk_wait0();
-        __syncwarp();
     } else if (warp == kMmaWarp) {
         if (lane == 0) {
             const uint32_t lbo = p.dv == 128 ? kTile : 0;   // d_v 64: the lanes 64.. repeat the rows 0..63
@@ -172,13 +141,13 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 const int s = n & 1;
                 const uint32_t par = n & 1, st = base + s * kRevStage, pr = st + kRevOffRec;
                 if (!wait1(&bar->full[s], (n >> 1) & 1)) break;
-                if (!wait1(&bar->o_full, par)) break;
+                const uint32_t ot = base + kRevOffO + 2 * s * kTile;
                 if (n == 0 && !wait1(&bar->s_ready[0], 0)) break;   // the tiles' rows behind the end are zero by then
                 tc_fence_after();
                 // R = dOᵀ P, P's terms side by side (their columns were read before dE's terms were handed over)
 #pragma unroll
                 for (int j = 0; j < kC / 16; ++j)
-                    umma(tmem + kRevR, sdesc(base + kRevOffO + 2048u * j, lbo, 1024), sdesc(pr + kRecP + 2048u * j, kTile, 1024),
+                    umma(tmem + kRevR, sdesc(ot + 2048u * j, lbo, 1024), sdesc(pr + kRecP + 2048u * j, kTile, 1024),
                          idesc(2 * kC, true, true), j > 0);
                 auto ks_step = [&](int ks) {
                     const uint64_t bd = sdesc(st + (ks >> 2) * 2 * kTile + (ks & 3) * 32, 16, 1024);
@@ -196,7 +165,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
 #pragma unroll
                     for (int ks = 1; ks < DK / 16; ks += 2) ks_step(ks);
                 }
-                umma_commit(&bar->ks);
+                if (!(p.test_drop && blockIdx.x == 0 && n == 0)) umma_commit(&bar->ks);
                 if (!wait1(&bar->x_ready, par)) break;
                 tc_fence_after();
                 // Vᵀ = dEᵀ T
@@ -250,7 +219,32 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             const uint32_t a = chunk_addr(off + static_cast<uint32_t>(v >> 6) * kTile, t, (v & 63) >> 3) + 2 * (v & 7);
             return row_in ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(gbase + a)) : 0.0f;
         };
-        float* const dots = reinterpret_cast<float*>(gbase + kRevOffDot);
+        // this warp's part of <S, dS> of the state that enters chunk c (leaves chunk c - 1), dS being the registers'
+        auto dot_state = [&](int c, int n) {
+            const unsigned char* sp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
+            float dot = 0.0f;
+#pragma unroll
+            for (int k = 0; k < KH; k += 8) {
+                const int key = part * KH + k;
+                const uint32_t o = chunk_addr(static_cast<uint32_t>(key >> 6) * 2 * kTile, v, (key & 63) >> 3);
+                const uint4 hi = *reinterpret_cast<const uint4*>(sp + kKeepS + o);
+                const uint4 lo = *reinterpret_cast<const uint4*>(sp + kKeepSlo + o);
+                const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const f32x2 d = S[k / 2 + e];
+                    dot = fmaf(d.x, lo_f(hw[e]) + lo_f(lw[e]), dot);
+                    dot = fmaf(d.y, hi_f(hw[e]) + hi_f(lw[e]), dot);
+                }
+            }
+            if (!row_in) dot = 0.0f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            if (n > 0 && !wait_warp(&bar->dot_free, (n - 1) & 1)) return false;
+            if (lane == 0) reinterpret_cast<float*>(gbase + kRevOffDot)[warp] = dot;
+            arrive_warp(&bar->dot);
+            return true;
+        };
         bool ok = true;
         for (int n = 0; n < nchunk; ++n) {
             const int c = nchunk - 1 - n, s = n & 1;
@@ -258,15 +252,13 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             const Scal& sc = *reinterpret_cast<const Scal*>(gbase + s * kRevStage + kRevOffRec + kRecScal);
             if (n == 0) {
                 if (ragged) {   // rows behind the end, whatever they hold, become zero rows
-                    ok = wait_warp(&bar->full[0], 0) && wait_warp(&bar->o_full, 0) && wait_warp(&bar->ve_full, 0);
+                    ok = wait_warp(&bar->full[0], 0);
                     if (!ok) break;
                     const int n0 = static_cast<int>(len - static_cast<int64_t>(c) * kC);
                     for (int i = n0 * 8 + tid; i < kC * 8; i += 32 * kStateWarps) {
                         for (int kb = 0; kb < 2 * KB; ++kb) sts128(st + kb * kTile + 16 * i, make_uint4(0, 0, 0, 0));
-                        for (int vb = 0; vb < p.dv / 64; ++vb) {
+                        for (int vb = 0; vb < p.dv / 64; ++vb)
                             sts128(base + kRevOffO + vb * kTile + 16 * i, make_uint4(0, 0, 0, 0));
-                            sts128(base + kRevOffV + vb * kTile + 16 * i, make_uint4(0, 0, 0, 0));
-                        }
                     }
                     fence_proxy_async_smem();
                 }
@@ -274,40 +266,20 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 arrive_warp(&bar->s_ready[1]);
                 // (the zero rows of other warps' share are visible behind the product's own barrier)
             }
-            {   // keep dS, and <S, dS> of the state that leaves the chunk
+            {   // keep dS, and its product with the state that leaves the chunk
                 unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
-                const unsigned char* sp = kp + kKeepBytes;
-                float dot = 0.0f;
 #pragma unroll
-                for (int k = 0; k < KH; k += 16) {
-                    const int key = part * KH + k;
-                    keep_terms(kp + kKeepD, nullptr, v, key, S + k / 2);
-#pragma unroll
-                    for (int h2 = 0; h2 < 2; ++h2) {
-                        const uint32_t o = chunk_addr(static_cast<uint32_t>(key >> 6) * 2 * kTile, v, ((key & 63) >> 3) + h2);
-                        const uint4 hi = *reinterpret_cast<const uint4*>(sp + kKeepShi + o);
-                        const uint4 lo = *reinterpret_cast<const uint4*>(sp + kKeepSlo + o);
-                        const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const f32x2 d = S[k / 2 + 4 * h2 + e];
-                            dot = fmaf(d.x, lo_f(hw[e]) + lo_f(lw[e]), dot);
-                            dot = fmaf(d.y, hi_f(hw[e]) + hi_f(lw[e]), dot);
-                        }
-                    }
-                }
-                if (!row_in) dot = 0.0f;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                // (two buffers: the sums of step n - 1 may still wait for their store)
-                if (lane == 0) dots[8 * kC + (n & 1) * 16 + warp] = dot;
+                for (int k = 0; k < KH; k += 16) keep_terms(kp + kKeepD, kp + kKeepDlo, v, part * KH + k, S + k / 2);
+                ok = dot_state(c + 1, n);
+                if (!ok) break;
             }
-            ok = wait_warp(&bar->full[s], (n >> 1) & 1) && wait_warp(&bar->o_full, par);
+            ok = wait_warp(&bar->full[s], (n >> 1) & 1);
+            const uint32_t ot = kRevOffO + 2 * s * kTile;
             if (!ok) break;
             f32x2 x[8];
             if (!(n == 0 && ragged)) {   // scale e^G dO (in a ragged chunk once every warp's zero rows are written)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = pk2(val(kRevOffO, 2 * e), val(kRevOffO, 2 * e + 1));
+                for (int e = 0; e < 8; ++e) x[e] = pk2(val(ot, 2 * e), val(ot, 2 * e + 1));
                 scale16(x, sc.qe + kTok * part);
                 store_terms(tl + kRevO + kTok * part, x);
             }
@@ -316,7 +288,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             tc_fence_after();
             if (n == 0 && ragged) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = pk2(val(kRevOffO, 2 * e), val(kRevOffO, 2 * e + 1));
+                for (int e = 0; e < 8; ++e) x[e] = pk2(val(ot, 2 * e), val(ot, 2 * e + 1));
                 scale16(x, sc.qe + kTok * part);
                 store_terms(tl + kRevO + kTok * part, x);
             }
@@ -334,11 +306,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             store_terms(tl + kRevA + kTok * part, x);
             tmem_wait_st();
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bar->x_ready);
-                mbar_arrive(&bar->o_free);
-            }
+            arrive_warp(&bar->x_ready);
             ok = wait_warp(&bar->e, par);
             if (!ok) break;
             tc_fence_after();
@@ -357,35 +325,9 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(&bar->w_ready);
-            // dV, and its products with V and E, while dS is multiplied
-            ok = wait_warp(&bar->ve_full, par) && (n == 0 || wait_warp(&bar->out_free, (n - 1) & 1));
-            if (!ok) break;
-            if (row_in) {
-                __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(gbase + kRevOffOut) + kTok * part * p.dv + v;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    o[2 * e * p.dv] = __float2bfloat16_rn(x[e].x);
-                    o[(2 * e + 1) * p.dv] = __float2bfloat16_rn(x[e].y);
-                }
-            }
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                float d[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    d[e] = ((e & 1) ? x[e >> 1].y : x[e >> 1].x) * val(w == 0 ? kRevOffV : kRevOffE, e);
-                if (!row_in) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) d[e] = 0.0f;
-                }
-                const float sum = lane_sums16(d, lane);
-                if (!(lane & 1)) dots[(4 * w + (warp & 3)) * kC + kTok * part + (lane >> 1)] = sum;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bar->ve_free);
-                mbar_arrive(&bar->out_full);
+            {   // dV, while dS is multiplied
+                unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
+                keep_terms(kp + kKeepV, kp + kKeepVlo, v, kTok * part, x);
             }
             ok = wait_warp(&bar->ds, par);
             if (!ok) break;
@@ -406,6 +348,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             tmem_wait_st();
             tc_fence_before();
         }
+        if (ok) ok = dot_state(0, nchunk);
         if (ok && p.dinit && row_in) {
 #pragma unroll
             for (int k = 0; k < KH; k += 4)
@@ -418,8 +361,6 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
     if (warp == kLoadWarp && lane == 0) {
         for (int n = issued > 2 ? issued - 2 : 0; n < issued; ++n)
             mbar_wait_bounded(&bar->full[n & 1], (n >> 1) & 1, p.drain_ns);
-        if (o_issued) mbar_wait_bounded(&bar->o_full, (o_issued - 1) & 1, p.drain_ns);
-        if (ve_issued) mbar_wait_bounded(&bar->ve_full, (ve_issued - 1) & 1, p.drain_ns);
     }
     if (tid == 32 * kMmaWarp) {
         umma_commit(&bar->fin);
@@ -435,29 +376,34 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
 
 // ------------------------------------------------------------------------------------ gradients of q and k
 // One block per (b, key head, chunk); the value heads that share the key head one after the other, their sums in
-// fp32 registers.  Per value head (M = 128 lanes, two 64-row operands on top of one another):
-//   D1 [dO; dV] S              -> columns   0 .. 127 (K: d_v)
-//   D3 [E; .] dS               ->         128 .. 255 (K: d_v; lanes 64.. are not read)
-//   D2 [dO; dV] Eᵀ             ->         384 .. 447 (K: d_v), read into M^P, M^A (bf16, shared memory)
+// fp32 registers.  Per value head (M = 128 lanes, two 64-row operands on top of one another; every operand but dO, K
+// and Q in two terms):
+//   D2 [dO; dV] Eᵀ             -> columns 384 .. 447 (K: d_v), read into M^P, M^A (two bf16 terms, shared memory)
+//   D1 [dO; dV] S              ->           0 .. 127 (K: d_v)
 //   D4 [M^P; M^A] K            ->         256 .. 383 (K: 64 tokens)
-//   D5 [M^P; M^A]ᵀ [Q; K]      ->         384 .. 511 (K: 128; lanes 64.. are not read)
+//   D5 [M^P; M^A]ᵀ [Q; K]      ->         384 .. 511 (K: 128; lanes 64.. repeat the rows 0..63)
+//   D3 E dS                    ->         128 .. 255 (K: d_v; likewise)
 //   dq~ = qe D1 + D4 (lanes 0..63),   dk~ = ek D1 + D4 (lanes 64..127) + wk D3 + D5 (lanes 0..63)
-// (ek carries the minus of -e^G.)  Bound by latency: loads, two rounds of products, and the M's between them.
+// (ek carries the minus of -e^G), and of each token the products of these brackets with its own q and k.  dV comes
+// from the chain transposed and is turned in shared memory; S and dS pass through one buffer.  Bound by what it reads
+// (the chains' states, 176 KB a chunk) and by the latency of its stages.
 constexpr int kGradThreads = 256;
 constexpr uint32_t kGK = 0;                       // [K 0][Q 0][K 1][Q 1]
-constexpr uint32_t kGO = 4 * kTile;               // [dO 0][dV 0][dO 1][dV 1]
-constexpr uint32_t kGE = 8 * kTile;               // [E 0][E 1] (an operand of 128 rows reads on into S: not used)
-constexpr uint32_t kGS = 10 * kTile;              // S: two blocks of 128 rows
-constexpr uint32_t kGD = 14 * kTile;              // dS
-constexpr uint32_t kGM = 18 * kTile;              // [M^P][M^A], 64 rows of 64 each
-constexpr uint32_t kGX = 20 * kTile;              // dk~'s other half, fp32 [64][DK + 4]
-constexpr uint32_t kGScal = kGX + 64 * 132 * 4;   // Scal, Local (one copy from the record)
-constexpr uint32_t kGBar = kGScal + 1024 + 2048;
+constexpr uint32_t kG1 = 4 * kTile;               // [dO 0][dV hi 0][dO 1][dV hi 1]
+constexpr uint32_t kG2 = 8 * kTile;               // [0][dV lo 0][0][dV lo 1]; then [M^P lo][M^A lo] over its first half
+constexpr uint32_t kGE = 12 * kTile;              // Eᵀ hi, lo: 128 rows each
+constexpr uint32_t kGS = 16 * kTile;              // dVᵀ hi, lo; then S hi, lo; then dS hi, lo (two blocks of 128 rows each);
+                                                  // then dk~'s other bracket, fp32 [64][132]
+constexpr uint32_t kGM = 24 * kTile;              // [M^P hi][M^A hi], 64 rows of 64 each
+constexpr uint32_t kGScal = 26 * kTile;           // Scal, Local (one copy from the record)
+constexpr uint32_t kGRed = kGScal + 1024 + sizeof(Local);   // row products of the two halves, [3][2][64]
+constexpr uint32_t kGBar = kGRed + 3 * 2 * kC * 4;
 constexpr uint32_t kGradSmem = kGBar + 128 + 1024;
+constexpr int kGPitch = 132;
 static_assert(kGradSmem <= 227 * 1024, "shared memory");
 
 struct GradBars {
-    uint64_t qk, in, m1, m2;
+    uint64_t qk, in, s, d, m2, m1, m5, m3, fin;
     uint32_t tmem;
 };
 
@@ -466,11 +412,22 @@ struct GradParams {
     __nv_bfloat16 *dq, *dk, *dv;
 };
 
+// Four 8 x 8 bf16 blocks, each lane giving a row's address: loaded transposed, and stored.
+__device__ __forceinline__ void turn8x4(uint32_t src, uint32_t dst) {
+    uint32_t r0, r1, r2, r3;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(src)
+                 : "memory");
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(r0), "r"(r1), "r"(r2),
+                 "r"(r3)
+                 : "memory");
+}
+
 template <int DK>
 __global__ void __launch_bounds__(kGradThreads, 1)
 ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant__ CUtensorMap tm_q,
-                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_o,
-                   const __grid_constant__ CUtensorMap tm_dv) {
+                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_o) {
     constexpr int KB = DK / 64, CN = DK / 2;   // CN: columns of a thread
     const Params& p = gp.p;
     const GdrParams& g = p.g;
@@ -501,10 +458,8 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
         return;
     }
     if (tid == 0) {
-        mbar_init(&bar->qk, 1);
-        mbar_init(&bar->in, 1);
-        mbar_init(&bar->m1, 1);
-        mbar_init(&bar->m2, 1);
+        uint64_t* all[] = {&bar->qk, &bar->in, &bar->s, &bar->d, &bar->m2, &bar->m1, &bar->m5, &bar->m3, &bar->fin};
+        for (uint64_t* x : all) mbar_init(x, 1);
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -515,7 +470,26 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar->tmem;
-    const int t = static_cast<int>(t0);
+    const int t = static_cast<int>(t0), vb = p.dv / 64, vs = p.dv / 16;
+    // thread: lane row r of TMEM (token i; q's bracket below 64, k's first from 64 on), columns CN · half ..
+    const int r = (warp & 3) * 32 + lane, half = warp >> 2, i = r & 63, rb = (r >> 5) & 1;
+    const bool is_k = r >= 64;
+    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const int64_t plane = static_cast<int64_t>(g.batch) * g.H * p.nchunks * kC;
+    auto load_in = [&](int64_t item, int h) {   // dVᵀ, E, dO and the factors
+        const unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
+        mbar_arrive_expect_tx(&bar->in, 8 * kTile + vb * kTile + 1024 + sizeof(Local));
+        bulk_load(base + kGS, kp + kKeepV, 4 * kTile, &bar->in);
+        bulk_load(base + kGE, kp + kKeepE, 4 * kTile, &bar->in);
+        for (int w = 0; w < vb; ++w) tma_load_4d(base + kG1 + 2 * w * kTile, &tm_o, 64 * w, h, t, b, &bar->in);
+        bulk_load(base + kGScal, p.rec + (item * p.nchunks + c) * p.rec_bytes + kRecScal, 1024 + sizeof(Local), &bar->in);
+    };
+    auto load_states = [&](int64_t item, uint32_t hi, uint32_t lo_off, uint64_t* f) {
+        const unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
+        mbar_arrive_expect_tx(f, 4 * KB * kTile);
+        bulk_load(base + kGS, kp + hi, 2 * KB * kTile, f);
+        bulk_load(base + kGS + 4 * kTile, kp + lo_off, 2 * KB * kTile, f);
+    };
     if (tid == 0) {
         mbar_arrive_expect_tx(&bar->qk, 2 * KB * kTile);
         for (int kb = 0; kb < KB; ++kb) {
@@ -523,80 +497,125 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
             tma_load_4d(base + kGK + (2 * kb + 1) * kTile, &tm_q, 64 * kb, hk, t, b, &bar->qk);
         }
     }
-    // thread: lane row r of TMEM (token r & 63; dq~ below 64, dk~ from 64 on), columns CN · half ..
-    const int r = (warp & 3) * 32 + lane, half = warp >> 2, i = r & 63, rb = (r >> 5) & 1;
-    const bool is_k = r >= 64;
-    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    // Σ over this thread's columns of its row of Q or K (own) times d
+    auto row_product = [&](uint32_t own, const float (&d)[CN]) {
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int w = 0; w < CN / 8; ++w) {
+            const int col = CN * half + 8 * w;
+            const uint4 q = lds128(chunk_addr(own + (col >> 6) * 2 * kTile, i, (col & 63) >> 3));
+            const uint32_t a[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s0 = fmaf(lo_f(a[e]), d[8 * w + 2 * e], s0);
+                s1 = fmaf(hi_f(a[e]), d[8 * w + 2 * e + 1], s1);
+            }
+        }
+        return s0 + s1;
+    };
     float acc[CN];   // dq~ or dk~ of this thread's row and columns
 #pragma unroll
     for (int e = 0; e < CN; ++e) acc[e] = 0.0f;
-    float* const xch = reinterpret_cast<float*>(gbase + kGX);
+    float* const xch = reinterpret_cast<float*>(gbase + kGS);
+    float* const red = reinterpret_cast<float*>(gbase + kGRed);
+    const uint32_t own = base + kGK + (is_k ? 0 : kTile);   // this row of K or Q
     bool bad = false;
-    for (int j = 0; j < rep && !bad; ++j) {
+    int stage = 0;   // what thread 0 has in flight, for the wind-down
+    for (int j = 0; j < rep; ++j) {
         const int h = hk * rep + j;
         const int64_t item = static_cast<int64_t>(b) * g.H + h;
         const uint32_t par = j & 1;
+        auto wait_all = [&](uint64_t* x, uint32_t ph) {   // every thread; a uniform outcome
+            const bool got = mbar_wait_bounded(x, ph, p.wait_ns);
+            bad = __syncthreads_or(!got) != 0;
+            return !bad;
+        };
         if (tid == 0) {
-            const unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
-            const uint32_t vb = p.dv / 64;
-            mbar_arrive_expect_tx(&bar->in, vb * 3 * kTile + 2 * KB * 2 * kTile + 1024 + sizeof(Local));
-            for (uint32_t w = 0; w < vb; ++w) {
-                tma_load_4d(base + kGO + 2 * w * kTile, &tm_o, 64 * w, h, t, b, &bar->in);
-                tma_load_4d(base + kGO + (2 * w + 1) * kTile, &tm_dv, 64 * w, h, t, b, &bar->in);
-            }
-            bulk_load(base + kGE, kp + kKeepE, vb * kTile, &bar->in);
-            bulk_load(base + kGS, kp + kKeepShi, KB * 2 * kTile, &bar->in);
-            bulk_load(base + kGD, kp + kKeepD, KB * 2 * kTile, &bar->in);
-            bulk_load(base + kGScal, p.rec + (item * p.nchunks + c) * p.rec_bytes + kRecScal, 1024 + sizeof(Local), &bar->in);
+            load_in(item, h);
+            stage = 4 * j + 1;
         }
-        bool got = mbar_wait_bounded(&bar->in, par, p.wait_ns);
-        if (j == 0) {
-            got = mbar_wait_bounded(&bar->qk, 0, p.wait_ns) && got;
+        if (j == 0 && !wait_all(&bar->qk, 0)) break;
+        if (!wait_all(&bar->in, par)) break;
+        // dV's rows (its terms turned), zero rows under the lo terms, and behind the sequence's end
+        for (int w = warp; w < 4 * vb * 8; w += 8) {   // four 8-row groups of v by 8 tokens, hi then lo
+            const int term = w / (2 * vb * 8), x = w % (2 * vb * 8), vg = (x >> 3) * 4, tc8 = x & 7;
+            const int m = vg + (lane >> 3), l7 = lane & 7;
+            turn8x4(chunk_addr(base + kGS + term * 2 * kTile, 8 * m + l7, tc8),
+                    chunk_addr(base + (term ? kG2 : kG1) + (2 * (m >> 3) + 1) * kTile, 8 * tc8 + l7, m & 7));
         }
-        if (valid < kC && got) {   // rows behind the sequence's end: K, Q (once) and dO become zero rows (dV has them)
+        for (int w = tid; w < 512; w += kGradThreads)
+            for (int x = 0; x < vb; ++x) sts128(base + kG2 + 2 * x * kTile + 16 * w, make_uint4(0, 0, 0, 0));
+        if (valid < kC) {   // K, Q (once) and dO (dV has them)
             for (int w = valid * 8 + tid; w < kC * 8; w += kGradThreads) {
                 for (int kb = 0; kb < 2 * KB && j == 0; ++kb) sts128(base + kGK + kb * kTile + 16 * w, make_uint4(0, 0, 0, 0));
-                for (int vb = 0; vb < p.dv / 64; ++vb) sts128(base + kGO + 2 * vb * kTile + 16 * w, make_uint4(0, 0, 0, 0));
+                for (int x = 0; x < vb; ++x) sts128(base + kG1 + 2 * x * kTile + 16 * w, make_uint4(0, 0, 0, 0));
             }
-            fence_proxy_async_smem();
         }
-        bad = __syncthreads_or(!got) != 0;
-        if (bad) break;
+        fence_proxy_async_smem();
+        __syncthreads();
+        auto a_off = [](int ks) { return (ks >> 2) * 2 * kTile + (ks & 3) * 32u; };   // 16 columns of a stacked operand
         if (tid == 0) {
-            const int vs = p.dv / 16;
-            for (int ks = 0; ks < vs; ++ks) {   // D2 first: the M's wait for it
-                const uint32_t o = (ks >> 2) * 2 * kTile + (ks & 3) * 32, e = (ks >> 2) * kTile + (ks & 3) * 32;
-                umma(tmem + 384, sdesc(base + kGO + o, 16, 1024), sdesc(base + kGE + e, 16, 1024), idesc(kC, false), ks > 0);
-            }
-            umma_commit(&bar->m1);
+            load_states(item, kKeepS, kKeepSlo, &bar->s);
+            stage = 4 * j + 2;
             for (int ks = 0; ks < vs; ++ks) {
-                const uint32_t o = (ks >> 2) * 2 * kTile + (ks & 3) * 32, e = (ks >> 2) * kTile + (ks & 3) * 32;
-                umma(tmem, sdesc(base + kGO + o, 16, 1024), sdesc(base + kGS + 2048u * ks, 2 * kTile, 1024), idesc(DK, true), ks > 0);
-                umma(tmem + 128, sdesc(base + kGE + e, 16, 1024), sdesc(base + kGD + 2048u * ks, 2 * kTile, 1024), idesc(DK, true), ks > 0);
+                const uint64_t e = sdesc(base + kGE + 2048u * ks, 0, 1024), el = sdesc(base + kGE + 2 * kTile + 2048u * ks, 0, 1024);
+                const uint64_t a = sdesc(base + kG1 + a_off(ks), 16, 1024);
+                umma(tmem + 384, a, e, idesc(kC, true), ks > 0);
+                umma(tmem + 384, a, el, idesc(kC, true), 1);
+                umma(tmem + 384, sdesc(base + kG2 + a_off(ks), 16, 1024), e, idesc(kC, true), 1);
             }
+            umma_commit(&bar->m2);
         }
-        got = mbar_wait_bounded(&bar->m1, par, p.wait_ns);
-        bad = __syncthreads_or(!got) != 0;
-        if (bad) break;
+        // v's gradient: dV's hi terms are its values rounded to bf16
+        for (int w = tid; w < rows * vb * 8; w += kGradThreads) {
+            const int row = w / (vb * 8), q = w % (vb * 8);
+            *reinterpret_cast<uint4*>(gp.dv + ((static_cast<int64_t>(b) * g.L + t0 + row) * g.H + h) * p.dv + 8 * q) =
+                lds128(chunk_addr(base + kG1 + (2 * (q >> 3) + 1) * kTile, row, q & 7));
+        }
+        if (!wait_all(&bar->m2, par)) break;
         tc_fence_after();
-        {   // M^P (rows 0..63), M^A (64..127): one 32-column block per thread
-            const uint32_t blk = base + kGM + (is_k ? kTile : 0);
-            float v[32];
+        float v[32];   // M^P (rows 0..63), M^A (64..127): one 32-column block per thread
+        {
             const bool diag = half == rb;
             if (diag || half < rb) {
                 tmem_ld32(tl + 384 + 32 * half, v);
                 const float row = is_k ? -lo.rk[i] : lo.rq[i];
-                if (diag) decay_diagonal(v, lo, 32 * rb, lo.gh[i], lo.gl[i], row, i & 31, !is_k);
-                else decay_left(v, lo, lo.gh[i], lo.gl[i], row);
+                if (diag) {
+                    if (is_k) p.dots[3 * plane + (item * p.nchunks + c) * kC + i] = pick32(v, i & 31);   // dV·E
+                    decay_diagonal(v, lo, 32 * rb, lo.gh[i], lo.gl[i], row, i & 31, !is_k);
+                } else {
+                    decay_left(v, lo, lo.gh[i], lo.gl[i], row);
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = 0.0f;
             }
+        }
+        if (!wait_all(&bar->s, par)) break;
+        if (tid == 0) {
+            tc_fence_after();
+            for (int ks = 0; ks < vs; ++ks) {
+                const uint64_t sh = sdesc(base + kGS + 2048u * ks, 2 * kTile, 1024);
+                const uint64_t a = sdesc(base + kG1 + a_off(ks), 16, 1024);
+                umma(tmem, a, sh, idesc(DK, true), ks > 0);
+                umma(tmem, a, sdesc(base + kGS + 4 * kTile + 2048u * ks, 2 * kTile, 1024), idesc(DK, true), 1);
+                umma(tmem, sdesc(base + kG2 + a_off(ks), 16, 1024), sh, idesc(DK, true), 1);
+            }
+            umma_commit(&bar->m1);
+        }
+        if (!wait_all(&bar->m1, par)) break;   // S and dV's lo terms are read
+        if (tid == 0) {
+            load_states(item, kKeepD, kKeepDlo, &bar->d);
+            stage = 4 * j + 3;
+        }
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-                sts128(chunk_addr(blk, i, 4 * half + w),
-                       make_uint4(pk(v[8 * w], v[8 * w + 1]), pk(v[8 * w + 2], v[8 * w + 3]), pk(v[8 * w + 4], v[8 * w + 5]),
-                                  pk(v[8 * w + 6], v[8 * w + 7])));
+        for (int w = 0; w < 4; ++w) {
+            uint32_t hw[4], lw[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split2(pk2(v[8 * w + 2 * e], v[8 * w + 2 * e + 1]), hw[e], lw[e]);
+            const uint32_t o = chunk_addr(is_k ? kTile : 0, i, 4 * half + w);
+            sts128(base + kGM + o, make_uint4(hw[0], hw[1], hw[2], hw[3]));
+            sts128(base + kG2 + o, make_uint4(lw[0], lw[1], lw[2], lw[3]));
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -604,69 +623,98 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
         if (tid == 0) {
             tc_fence_after();
 #pragma unroll
-            for (int ks = 0; ks < kC / 16; ++ks)
-                umma(tmem + 256, sdesc(base + kGM + 32u * ks, 16, 1024), sdesc(base + kGK + 2048u * ks, 2 * kTile, 1024),
-                     idesc(DK, true), ks > 0);
+            for (int w = 0; w < 2; ++w) {   // M's hi terms, then its lo terms
+                const uint32_t mt = base + (w ? kG2 : kGM);
 #pragma unroll
-            for (int ks = 0; ks < 2 * kC / 16; ++ks) {   // rows r of [M^P; M^A] with rows r of [Q; K]
-                const uint32_t qk = base + kGK + (ks < 4 ? kTile : 0) + 2048u * (ks & 3);
-                umma(tmem + 384, sdesc(base + kGM + 2048u * ks, 0, 1024), sdesc(qk, 2 * kTile, 1024), idesc(DK, true, true), ks > 0);
+                for (int ks = 0; ks < kC / 16; ++ks)
+                    umma(tmem + 256, sdesc(mt + 32u * ks, 16, 1024), sdesc(base + kGK + 2048u * ks, 2 * kTile, 1024),
+                         idesc(DK, true), w + ks > 0);
+#pragma unroll
+                for (int ks = 0; ks < 2 * kC / 16; ++ks) {   // rows r of [M^P; M^A] with rows r of [Q; K]
+                    const uint32_t qk = base + kGK + (ks < 4 ? kTile : 0) + 2048u * (ks & 3);
+                    umma(tmem + 384, sdesc(mt + 2048u * ks, 0, 1024), sdesc(qk, 2 * kTile, 1024), idesc(DK, true, true), w + ks > 0);
+                }
             }
-            umma_commit(&bar->m2);
+            umma_commit(&bar->m5);
         }
-        got = mbar_wait_bounded(&bar->m2, par, p.wait_ns);
-        bad = __syncthreads_or(!got) != 0;
-        if (bad) break;
+        if (!wait_all(&bar->d, par)) break;
+        if (tid == 0) {
+            for (int ks = 0; ks < vs; ++ks) {
+                const uint64_t dh = sdesc(base + kGS + 2048u * ks, 2 * kTile, 1024);
+                const uint64_t e = sdesc(base + kGE + 2048u * ks, 0, 1024), el = sdesc(base + kGE + 2 * kTile + 2048u * ks, 0, 1024);
+                umma(tmem + 128, e, dh, idesc(DK, true, true), ks > 0);
+                umma(tmem + 128, e, sdesc(base + kGS + 4 * kTile + 2048u * ks, 2 * kTile, 1024), idesc(DK, true, true), 1);
+                umma(tmem + 128, el, dh, idesc(DK, true, true), 1);
+            }
+            umma_commit(&bar->m3);
+        }
+        if (!wait_all(&bar->m5, par)) break;
         tc_fence_after();
-        const float f1 = is_k ? sc.ek[i] : sc.qe[i], f3 = sc.wk[i];
+        const int64_t tok = (item * p.nchunks + c) * kC + i;
+        float d[CN];
+        {
+            const float f1 = is_k ? sc.ek[i] : sc.qe[i];
 #pragma unroll
-        for (int e = 0; e < CN; e += 32) {
-            float v[32], w[32];
-            tmem_ld32(tl + CN * half + e, v);
-            tmem_ld32(tl + 256 + CN * half + e, w);
+            for (int e = 0; e < CN; e += 32) {
+                float w[32];
+                tmem_ld32(tl + CN * half + e, v);
+                tmem_ld32(tl + 256 + CN * half + e, w);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) acc[e + x] += fmaf(f1, v[x], w[x]);
-            if (!is_k) {   // dk~'s terms that lie in the lanes below 64
+                for (int x = 0; x < 32; ++x) {
+                    d[e + x] = fmaf(f1, v[x], w[x]);
+                    acc[e + x] += d[e + x];
+                }
+            }
+            red[(is_k ? 2 : 0) * kC + half * kC + i] = row_product(own, d);
+        }
+        if (!wait_all(&bar->m3, par)) break;   // (dS is read: its buffer takes dk~'s other bracket)
+        tc_fence_after();
+        if (!is_k) {
+            const float f3 = sc.wk[i];
+#pragma unroll
+            for (int e = 0; e < CN; e += 32) {
+                float w[32];
                 tmem_ld32(tl + 128 + CN * half + e, v);
                 tmem_ld32(tl + 384 + CN * half + e, w);
 #pragma unroll
+                for (int x = 0; x < 32; ++x) d[e + x] = fmaf(f3, v[x], w[x]);
+#pragma unroll
                 for (int x = 0; x < 32; x += 4)
-                    *reinterpret_cast<float4*>(xch + i * 132 + CN * half + e + x) =
-                        make_float4(fmaf(f3, v[x], w[x]), fmaf(f3, v[x + 1], w[x + 1]), fmaf(f3, v[x + 2], w[x + 2]),
-                                    fmaf(f3, v[x + 3], w[x + 3]));
+                    *reinterpret_cast<float4*>(xch + i * kGPitch + CN * half + e + x) =
+                        make_float4(d[e + x], d[e + x + 1], d[e + x + 2], d[e + x + 3]);
             }
+            red[4 * kC + half * kC + i] = row_product(base + kGK, d);
         }
         tc_fence_before();
         __syncthreads();
         if (is_k) {
 #pragma unroll
             for (int x = 0; x < CN; x += 4) {
-                const float4 q = quad(xch + i * 132 + CN * half + x);
+                const float4 q = quad(xch + i * kGPitch + CN * half + x);
                 acc[x] += q.x;
                 acc[x + 1] += q.y;
                 acc[x + 2] += q.z;
                 acc[x + 3] += q.w;
             }
+        } else if (half == 0) {   // q's row product, k's two
+#pragma unroll
+            for (int w = 0; w < 3; ++w) p.dots[w * plane + tok] = red[2 * w * kC + i] + red[(2 * w + 1) * kC + i];
         }
-        // (the next head's loads overwrite nothing that is still read: the barrier above, and xch is written two
-        // barriers later)
+        fence_proxy_async_smem();   // the exchange was written and read before the next head's loads land there
+        __syncthreads();
     }
     if (!bad) {
         // the unit length's own derivative: d = d~ - x (x·d~) / |x|²; the row's two halves meet in shared memory
-        const uint32_t own = base + kGK + (is_k ? 0 : kTile);   // this row of K or Q
         float x2 = 0.0f, xd = 0.0f;
-        __syncthreads();
         if (g.l2norm) {
+            xd = row_product(own, acc);
 #pragma unroll
             for (int w = 0; w < CN / 8; ++w) {
                 const int col = CN * half + 8 * w;
                 const uint4 q = lds128(chunk_addr(own + (col >> 6) * 2 * kTile, i, (col & 63) >> 3));
                 const uint32_t a[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x2 = fmaf(lo_f(a[e]), lo_f(a[e]), fmaf(hi_f(a[e]), hi_f(a[e]), x2));
-                    xd = fmaf(lo_f(a[e]), acc[8 * w + 2 * e], fmaf(hi_f(a[e]), acc[8 * w + 2 * e + 1], xd));
-                }
+                for (int e = 0; e < 4; ++e) x2 = fmaf(lo_f(a[e]), lo_f(a[e]), fmaf(hi_f(a[e]), hi_f(a[e]), x2));
             }
             xch[2 * (128 * half + r)] = x2;
             xch[2 * (128 * half + r) + 1] = xd;
@@ -698,15 +746,16 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
                     live ? make_uint4(pk(a[0], a[1]), pk(a[2], a[3]), pk(a[4], a[5]), pk(a[6], a[7])) : make_uint4(0, 0, 0, 0);
             }
         }
-    } else {
-        if (tid == 0) {
-            if (p.status) atomicCAS(p.status, 0u, static_cast<uint32_t>(SS_ERR_TIMEOUT));
-            // what is in flight ends before the shared memory and the TMEM columns go
-            mbar_wait_bounded(&bar->qk, 0, p.drain_ns);
-            for (uint32_t q = 0; q < 2; ++q) mbar_wait_bounded(&bar->in, q, p.drain_ns);
-            umma_commit(&bar->m2);
-            for (uint32_t q = 0; q < 2; ++q) mbar_wait_bounded(&bar->m2, q, p.drain_ns);
-        }
+    } else if (tid == 0) {
+        if (p.status) atomicCAS(p.status, 0u, static_cast<uint32_t>(SS_ERR_TIMEOUT));
+        // what is in flight ends before the shared memory and the TMEM columns go
+        const uint32_t ph = static_cast<uint32_t>((stage - 1) >> 2) & 1;
+        mbar_wait_bounded(&bar->qk, 0, p.drain_ns);
+        mbar_wait_bounded(&bar->in, ph, p.drain_ns);
+        if ((stage & 3) >= 2) mbar_wait_bounded(&bar->s, ph, p.drain_ns);
+        if ((stage & 3) == 3) mbar_wait_bounded(&bar->d, ph, p.drain_ns);
+        umma_commit(&bar->fin);
+        mbar_wait_bounded(&bar->fin, 0, p.drain_ns);
     }
     tc_fence_before();
     __syncthreads();
@@ -723,7 +772,7 @@ struct GateParams {
     float* part;              // [items][2]: this item's share of dA and ddt_bias
 };
 
-// One block per (b, h); a warp per chunk, two tokens per lane, the suffix sum by shuffles.
+// One block per (b, h); a warp per chunk, two tokens per lane, the prefix sum by shuffles.
 __global__ void __launch_bounds__(256) ss_gdr_gate_kernel(const __grid_constant__ GateParams gt) {
     const Params& p = gt.p;
     const GdrParams& g = p.g;
@@ -738,20 +787,22 @@ __global__ void __launch_bounds__(256) ss_gdr_gate_kernel(const __grid_constant_
         const int64_t t = c * kC + 2 * lane;
         float r[2], ve[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < 2; ++e) {   // what begins at a token less what ends there
             const bool in = t + e < len;
             const float* d = p.dots + item * toks + t + e;
-            r[e] = in ? d[0] - d[plane] : 0.0f;
-            ve[e] = in ? d[2 * plane] : 0.0f;
+            r[e] = in ? d[2 * plane] - d[0] - d[plane] : 0.0f;
+            ve[e] = in ? d[3 * plane] : 0.0f;
         }
-        float s = r[0] + r[1];   // suffix sums over the lanes
+        float s = r[0] + r[1];   // prefix sums over the lanes
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float v = __shfl_down_sync(0xffffffffu, s, o);
-            if (lane + o < 32) s += v;
+            const float v = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += v;
         }
-        const float anchor = c * kC < len ? p.dots[3 * plane + item * p.nchunks + c] : 0.0f;
-        const float dla[2] = {anchor + s, anchor + (s - r[0])};
+        const float before = __shfl_up_sync(0xffffffffu, s, 1);
+        const float start = c * kC < len ? p.dots[4 * plane + item * (p.nchunks + 1) + c] : 0.0f;
+        const float first = start + (lane ? before : 0.0f);
+        const float dla[2] = {first, first + r[0]};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             if (t + e >= g.L) continue;
@@ -760,10 +811,8 @@ __global__ void __launch_bounds__(256) ss_gdr_gate_kernel(const __grid_constant_
             if (t + e < len) {
                 const float pre = to_f32(static_cast<const __nv_bfloat16*>(g.dt)[o]) + bias;
                 const float delta = g.softplus ? softplus_accurate(pre) : pre;
-                // the decay of the first token meets a state of zero
-                const float d = (t + e == 0 && !g.h_init) ? 0.0f : dla[e];
-                ddt = d * A * (g.softplus ? 1.0f / (1.0f + expf(-pre)) : 1.0f);
-                sa += static_cast<double>(d) * static_cast<double>(delta);
+                ddt = dla[e] * A * (g.softplus ? 1.0f / (1.0f + expf(-pre)) : 1.0f);
+                sa += static_cast<double>(dla[e]) * static_cast<double>(delta);
                 sb += static_cast<double>(ddt);
                 const float raw = to_f32(static_cast<const __nv_bfloat16*>(g.beta)[o]);
                 if (g.sigmoid) {

@@ -73,9 +73,12 @@ struct alignas(16) Local {  // what a chunk's decay factors are made of (the bac
 constexpr uint32_t kRecLocal = kRecBytes, kRecBwdBytes = kRecBytes + 2048;
 static_assert(sizeof(Local) <= 2048, "record");
 
-// What the backward pass keeps of a chunk, beside its record: images of tiles in the swizzled layout of the MMAs.
-//   E [64 tokens][128], S0 hi and lo [128 rows v][128 keys] (the entering state's terms), dS1 [128][128] (bf16)
-constexpr uint32_t kKeepE = 0, kKeepShi = 2 * kTile, kKeepSlo = 6 * kTile, kKeepD = 10 * kTile, kKeepBytes = 14 * kTile;
+// What the backward pass keeps of a chunk, beside its record: images of tiles in the swizzled layout of the MMAs, each
+// value as two bf16 terms.  Eᵀ, dVᵀ: [128 rows v][64 tokens]; S (entering), dS (of the leaving state): [128 rows v]
+// [d_k keys].
+constexpr uint32_t kKeepE = 0, kKeepElo = 2 * kTile, kKeepV = 4 * kTile, kKeepVlo = 6 * kTile;
+constexpr uint32_t kKeepS = 8 * kTile, kKeepSlo = 12 * kTile, kKeepD = 16 * kTile, kKeepDlo = 20 * kTile;
+constexpr uint32_t kKeepBytes = 24 * kTile;
 
 struct Params {
     GdrParams g;
@@ -84,7 +87,8 @@ struct Params {
     uint32_t rec_bytes;      // from record to record
     // backward pass
     unsigned char* keep;     // [items][nchunks + 1]
-    float* dots;             // [4][items][nchunks * 64]: dO·O, dV·V, dV·E of each token; <dS1, S1> of each chunk
+    float* dots;             // [4][items][nchunks * 64] of each token, then [items][nchunks + 1]: <S, dS> of the
+                             // states between the chunks
     const float* dfinal;     // [batch, H, d_v, d_k] or null
     float* dinit;            // [batch, H, d_v, d_k] or null
     uint32_t* status;
@@ -597,27 +601,10 @@ constexpr uint32_t kOffV = 4 * kTile, kOffRec = 6 * kTile;
 constexpr uint32_t kStageBytes = kOffRec + kRecBytes;
 static_assert(kStageBytes % 1024 == 0, "swizzled tiles");
 constexpr uint32_t kOffY = kStages * kStageBytes;      // y [64][d_v] for the store
-constexpr uint32_t kOffE = kOffY + 2 * kTile;          // backward: dO in y's place, E [2 blocks of 64 rows] for its store
-constexpr uint32_t kOffDot = kOffE + 2 * kTile;        // and the row sums of the four lane groups, [4][64]
-constexpr uint32_t kOffBar = kOffDot + 4 * kC * 4;
+constexpr uint32_t kOffBar = kOffY + 2 * kTile;
 constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
-// Σ over a warp's lanes of each of 16 values, by halving: after it lane l holds the sum of value (l >> 1) (both lanes
-// of a pair the same).
-__device__ __forceinline__ float lane_sums16(float (&v)[16], int lane) {
-#pragma unroll
-    for (int o = 16, n = 8; n > 0; o >>= 1, n >>= 1) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (e >= n) break;
-            const float keep = up ? v[e + n] : v[e], give = up ? v[e] : v[e + n];
-            v[e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-        }
-    }
-    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
-}
 // 16 values' terms (hi then lo words) to two images of [rows][64-wide blocks]: chunks 2 m, 2 m + 1 of row r.
 __device__ __forceinline__ void keep_terms(unsigned char* hi_img, unsigned char* lo_img, int r, int key, const f32x2* v) {
     uint32_t hi[8], lo[8];
@@ -628,7 +615,7 @@ __device__ __forceinline__ void keep_terms(unsigned char* hi_img, unsigned char*
     for (int h = 0; h < 2; ++h) {
         const uint32_t o = chunk_addr(blk, r, ((key & 63) >> 3) + h);
         *reinterpret_cast<uint4*>(hi_img + o) = make_uint4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]);
-        if (lo_img) *reinterpret_cast<uint4*>(lo_img + o) = make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
+        *reinterpret_cast<uint4*>(lo_img + o) = make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
     }
 }
 
@@ -638,16 +625,15 @@ struct Bars {
     uint64_t ks, e, ds, pv;    // the chain's products done
     uint64_t s_ready[2];       // S's terms written: of the first 16 keys of each thread, of the others (state warps)
     uint64_t x_ready, w_ready, e_ready;   // X's terms, W's, E's and Y's first part written (state warps)
-    uint64_t y_full, y_free;   // y staged (state warps); stored (1).  Backward: dO read (state warps); landed (1)
-    uint64_t e_full, e_free;   // backward: E staged (state warps); stored (1)
+    uint64_t y_full, y_free;   // y staged (state warps); stored (1)
     uint64_t fin;              // wind-down
     uint32_t tmem;
 };
 static_assert(sizeof(Bars) <= 256, "barrier region");
 
-// Grid: one CTA per (b, h).  BWD: the backward pass's forward half.  y is not written (tm_y reads dO); what is kept of
-// each chunk is E, the entering state's terms, and dO_i · O_i of its tokens in fp32.
-template <int DK, bool BWD>
+// Grid: one CTA per (b, h).  Y false: the backward pass's forward half.  There is no y, and with it no QS and no
+// product with P; E and the entering state's terms of every chunk are kept.
+template <int DK, bool Y>
 __global__ void __launch_bounds__(kThreads, 1)
 ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_q,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -674,9 +660,9 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             mbar_init(&bar->full[i], 1);
             mbar_init(&bar->empty[i], 1);
         }
-        uint64_t* one[] = {&bar->ks, &bar->e, &bar->ds, &bar->pv, &bar->y_free, &bar->e_free, &bar->fin};
+        uint64_t* one[] = {&bar->ks, &bar->e, &bar->ds, &bar->pv, &bar->y_free, &bar->fin};
         for (uint64_t* x : one) mbar_init(x, 1);
-        uint64_t* all[] = {bar->s_ready, bar->s_ready + 1, &bar->x_ready, &bar->w_ready, &bar->e_ready, &bar->y_full, &bar->e_full};
+        uint64_t* all[] = {bar->s_ready, bar->s_ready + 1, &bar->x_ready, &bar->w_ready, &bar->e_ready, &bar->y_full};
         for (uint64_t* x : all) mbar_init(x, kStateWarps);
         fence_mbar_init();
     }
@@ -707,7 +693,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         __syncwarp();
         if (lane == 0) mbar_arrive(x);
     };
-    int issued = 0, do_issued = 0;   // loads of the load thread, of the store warp
+    int issued = 0;   // loads of the load thread
 
     if (warp == kLoadWarp) {
         // ============================================================ loads (one thread)
@@ -720,10 +706,10 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 if (c >= kStages && !wait1(&bar->empty[s], ((c / kStages) - 1) & 1)) break;
                 const uint32_t st = base + s * kStageBytes;
                 uint64_t* f = &bar->full[s];
-                mbar_arrive_expect_tx(f, 2 * KB * kTile + kC * p.dv * 2 + kRecBytes);
+                mbar_arrive_expect_tx(f, (Y ? 2 : 1) * KB * kTile + kC * p.dv * 2 + kRecBytes);
                 for (int kb = 0; kb < KB; ++kb) {
                     tma_load_4d(st + (2 * kb) * kTile, &tm_k, 64 * kb, hk, c * kC, b, f);
-                    tma_load_4d(st + (2 * kb + 1) * kTile, &tm_q, 64 * kb, hk, c * kC, b, f);
+                    if (Y) tma_load_4d(st + (2 * kb + 1) * kTile, &tm_q, 64 * kb, hk, c * kC, b, f);
                 }
                 for (int vb = 0; vb < p.dv / 64; ++vb)
                     tma_load_4d(st + kOffV + vb * kTile, &tm_v, 64 * vb, h, c * kC, b, f);
@@ -733,31 +719,8 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         }
         __syncwarp();
     } else if (warp == kStoreWarp) {
-        // ============================================================ y; backward: dO in, E out
-        for (int c = 0; BWD && c <= nchunk; ++c) {
-            // dO of chunk c once chunk c - 1's was read, E of chunk c once it was staged
-            if (c > 0) {
-                if (!wait_warp(&bar->y_full, (c - 1) & 1)) break;
-                const float* q = reinterpret_cast<const float*>(gbase + kOffDot);   // the four lane groups, in order
-                float* out = p.dots + (item * p.nchunks + c - 1) * kC;
-                for (int i = lane; i < kC; i += 32) out[i] = (q[i] + q[kC + i]) + (q[2 * kC + i] + q[3 * kC + i]);
-                __syncwarp();
-            }
-            if (c == nchunk) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bar->y_free, kC * p.dv * 2);
-                tma_load_4d(base + kOffY, &tm_y, 0, h, c * kC, b, &bar->y_free);
-            }
-            do_issued = c + 1;
-            if (!wait_warp(&bar->e_full, c & 1)) break;
-            if (lane == 0) {
-                bulk_store(p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes + kKeepE, base + kOffE, 2 * kTile);
-                tc::bulk_commit();
-                tc::bulk_wait_read0();
-            }
-            arrive_warp(&bar->e_free);
-        }
-        for (int c = 0; !BWD && c < nchunk; ++c) {
+        // ============================================================ y
+        for (int c = 0; Y && c < nchunk; ++c) {
             if (!wait_warp(&bar->y_full, c & 1)) break;
             if (c != ragged) {   // rows behind the tensor's end are clipped by the copy
                 if (lane == 0) {
@@ -790,8 +753,8 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 // KS and QS: S's terms of 16 keys in 16 columns, K and Q of a 64-key block side by side
                 auto ks_step = [&](int ks) {
                     const uint64_t bd = sdesc(st + (ks >> 2) * 2 * kTile + (ks & 3) * 32, 16, 1024);
-                    umma_ts(tmem + kColA, tmem + kColS + 16 * ks, bd, idesc(2 * kC, false), ks > 0);
-                    umma_ts(tmem + kColA, tmem + kColS + 16 * ks + 8, bd, idesc(2 * kC, false), 1);
+                    umma_ts(tmem + kColA, tmem + kColS + 16 * ks, bd, idesc(Y ? 2 * kC : kC, false), ks > 0);
+                    umma_ts(tmem + kColA, tmem + kColS + 16 * ks + 8, bd, idesc(Y ? 2 * kC : kC, false), 1);
                 };
                 constexpr int kStep = KH / 16;   // (the rows behind a sequence's end are zeroed before s_ready)
                 if (!wait1(&bar->s_ready[0], par)) break;
@@ -806,7 +769,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 }
                 if (!(p.test_drop && blockIdx.x == 0 && c == 0)) umma_commit(&bar->ks);
                 // E = Vᵀ Tᵀ, T's terms side by side, once the last chunk's E is read
-                if (c > 0 && !wait1(&bar->pv, (c - 1) & 1)) break;
+                if (Y && c > 0 && !wait1(&bar->pv, (c - 1) & 1)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < kC / 16; ++j)
@@ -832,16 +795,17 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                     umma_ts(tmem + kColS, tmem + kColA + 16 * j + 8, bd, idesc(DK, true), 1);
                 }
                 umma_commit(&bar->ds);
-                if (!wait1(&bar->e_ready, par)) break;
-                tc_fence_after();
-                // Yᵀ += E Pᵀ
+                if (Y) {   // Yᵀ += E Pᵀ
+                    if (!wait1(&bar->e_ready, par)) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int j = 0; j < kC / 16; ++j) {
-                    const uint64_t bd = sdesc(pr + kRecP + 32u * j, 16, 1024);
-                    umma_ts(tmem + kColY, tmem + kColB + 16 * j, bd, idesc(2 * kC, false), 1);
-                    umma_ts(tmem + kColY, tmem + kColB + 16 * j + 8, bd, idesc(kC, false), 1);
+                    for (int j = 0; j < kC / 16; ++j) {
+                        const uint64_t bd = sdesc(pr + kRecP + 32u * j, 16, 1024);
+                        umma_ts(tmem + kColY, tmem + kColB + 16 * j, bd, idesc(2 * kC, false), 1);
+                        umma_ts(tmem + kColY, tmem + kColB + 16 * j + 8, bd, idesc(kC, false), 1);
+                    }
+                    umma_commit(&bar->pv);
                 }
-                umma_commit(&bar->pv);
                 umma_commit(&bar->empty[s]);
             }
         }
@@ -867,10 +831,10 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         auto keep_state = [&](int c) {   // the terms of the state that enters chunk c
             unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
 #pragma unroll
-            for (int k = 0; k < KH; k += 16) keep_terms(kp + kKeepShi, kp + kKeepSlo, v, part * KH + k, S + k / 2);
+            for (int k = 0; k < KH; k += 16) keep_terms(kp + kKeepS, kp + kKeepSlo, v, part * KH + k, S + k / 2);
         };
-        auto finish_y = [&](int c) {     // chunk c's y, or its dO·O
-            if (BWD ? !wait_warp(&bar->y_free, c & 1) : (c > 0 && !wait_warp(&bar->y_free, (c - 1) & 1))) return false;
+        auto finish_y = [&](int c) {     // chunk c's y
+            if (c > 0 && !wait_warp(&bar->y_free, (c - 1) & 1)) return false;
             if (!wait_warp(&bar->pv, c & 1)) return false;
             tc_fence_after();
             f32x2 x[8], w[8];
@@ -878,19 +842,6 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = add2(x[e], w[e]);
             __nv_bfloat16* ys = reinterpret_cast<__nv_bfloat16*>(gbase + kOffY) + kTok * part * p.dv + v;
-            if (BWD) {
-                float d[16];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    d[2 * e] = row_in ? x[e].x * __bfloat162float(ys[2 * e * p.dv]) : 0.0f;
-                    d[2 * e + 1] = row_in ? x[e].y * __bfloat162float(ys[(2 * e + 1) * p.dv]) : 0.0f;
-                }
-                float* dots = reinterpret_cast<float*>(gbase + kOffDot);
-                const float sum = lane_sums16(d, lane);
-                if (!(lane & 1)) dots[(warp & 3) * kC + kTok * part + (lane >> 1)] = sum;
-                arrive_warp(&bar->y_full);
-                return true;
-            }
             if (row_in) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -921,8 +872,8 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 arrive_warp(&bar->s_ready[0]);
                 arrive_warp(&bar->s_ready[1]);
             }
-            if (BWD) keep_state(c);
-            if (c > 0) {   // the last chunk's y, while this one's K Sᵀ runs
+            if (!Y) keep_state(c);
+            if (Y && c > 0) {   // the last chunk's y, while this one's K Sᵀ runs
                 ok = finish_y(c - 1);
                 if (!ok) break;
             }
@@ -936,11 +887,11 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(&bar->x_ready);
-            tmem_ld16(tl + kColQS + kTok * part, x);  // y's part from the entering state, while E is multiplied
-            scale16(x, sc.qe + kTok * part);
-            tmem_st16(tl + kColY + kTok * part, x);
-            {
+            if (Y) {   // y's part from the entering state, while E is multiplied
                 const uint32_t zero[8] = {};
+                tmem_ld16(tl + kColQS + kTok * part, x);
+                scale16(x, sc.qe + kTok * part);
+                tmem_st16(tl + kColY + kTok * part, x);
                 tmem_st8(tl + kColY + kC + kTok * part, zero);
                 tmem_st8(tl + kColY + kC + kTok * part + 8, zero);
             }
@@ -964,22 +915,14 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(&bar->w_ready);
-            store_terms(tl + kColB + kTok * part, x);
-            tmem_wait_st();
-            tc_fence_before();
-            arrive_warp(&bar->e_ready);
-            if (BWD) {   // E's hi terms, staged as the image that the gradient kernel reads
-                ok = c == 0 || wait_warp(&bar->e_free, (c - 1) & 1);
-                if (!ok) break;
-                const uint32_t img = base + kOffE + static_cast<uint32_t>(v >> 6) * kTile;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int t = kTok * part + e;
-                    *reinterpret_cast<__nv_bfloat16*>(smem_raw + (chunk_addr(img, t, (v & 63) >> 3) + 2 * (v & 7) - raw)) =
-                        __float2bfloat16_rn((e & 1) ? x[e >> 1].y : x[e >> 1].x);
-                }
-                fence_proxy_async_smem();
-                arrive_warp(&bar->e_full);
+            if (Y) {
+                store_terms(tl + kColB + kTok * part, x);
+                tmem_wait_st();
+                tc_fence_before();
+                arrive_warp(&bar->e_ready);
+            } else {
+                unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
+                keep_terms(kp + kKeepE, kp + kKeepElo, v, kTok * part, x);
             }
             ok = wait_warp(&bar->ds, par);
             if (!ok) break;
@@ -1000,8 +943,8 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             tmem_wait_st();
             tc_fence_before();
         }
-        if (ok && nchunk > 0) ok = finish_y(nchunk - 1);
-        if (BWD && ok) keep_state(nchunk);
+        if (Y && ok && nchunk > 0) ok = finish_y(nchunk - 1);
+        if (!Y && ok) keep_state(nchunk);
         if (ok && g.final_state && row_in) {
 #pragma unroll
             for (int k = 0; k < KH; k += 4)
@@ -1017,8 +960,6 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         for (int c = issued > kStages ? issued - kStages : 0; c < issued; ++c)
             mbar_wait_bounded(&bar->full[c % kStages], (c / kStages) & 1, p.drain_ns);
     }
-    if (BWD && warp == kStoreWarp && lane == 0 && do_issued > 0)
-        mbar_wait_bounded(&bar->y_free, (do_issued - 1) & 1, p.drain_ns);
     if (tid == 32 * kMmaWarp) {
         umma_commit(&bar->fin);
         mbar_wait_bounded(&bar->fin, 0, p.drain_ns);
