@@ -100,12 +100,12 @@ int launch_tc(const gdr::Params& p, const Maps& m, cudaStream_t stream) {
     auto kern = gdr::ss_gdr_tc_kernel<DK, true>;
     static std::atomic<bool> attr[2][kMaxDevices];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || set_smem_limit(kern, gdr::kSmemBytes, attr[0], dev) != SS_OK ||
+    if (cudaGetDevice(&dev) != cudaSuccess || set_smem_limit(kern, gdr::Smem<true>::kBytes, attr[0], dev) != SS_OK ||
         set_smem_limit(prep, gdr::kPrepSmem, attr[1], dev) != SS_OK)
         return SS_ERR_CUDA;
     const int64_t items = static_cast<int64_t>(p.g.batch) * p.g.H;
     prep<<<static_cast<unsigned>(items * p.nchunks), gdr::kPrepThreads, gdr::kPrepSmem, stream>>>(p, m.q, m.k);
-    kern<<<static_cast<unsigned>(items), gdr::kThreads, gdr::kSmemBytes, stream>>>(p, m.q, m.k, m.v, m.y);
+    kern<<<static_cast<unsigned>(items), gdr::kThreads, gdr::Smem<true>::kBytes, stream>>>(p, m.q, m.k, m.v, m.y);
     return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
@@ -163,14 +163,14 @@ int launch_bwd(const gdr::Params& p, const Maps& m, const CUtensorMap& mo, const
     static std::atomic<bool> attr[4][kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || set_smem_limit(prep, gdr::kPrepSmem, attr[0], dev) != SS_OK ||
-        set_smem_limit(fwd, gdr::kSmemBytes, attr[1], dev) != SS_OK ||
+        set_smem_limit(fwd, gdr::Smem<false>::kBytes, attr[1], dev) != SS_OK ||
         set_smem_limit(rev, gdr::kRevSmem, attr[2], dev) != SS_OK ||
         set_smem_limit(grad, gdr::kGradSmem, attr[3], dev) != SS_OK)
         return SS_ERR_CUDA;
     const int64_t items = static_cast<int64_t>(p.g.batch) * p.g.H;
     const unsigned n = static_cast<unsigned>(items);
     prep<<<static_cast<unsigned>(items * p.nchunks), gdr::kPrepThreads, gdr::kPrepSmem, stream>>>(p, m.q, m.k);
-    fwd<<<n, gdr::kThreads, gdr::kSmemBytes, stream>>>(p, m.q, m.k, m.v, m.v);
+    fwd<<<n, gdr::kThreads, gdr::Smem<false>::kBytes, stream>>>(p, m.q, m.k, m.v, m.v);
     rev<<<n, gdr::kThreads, gdr::kRevSmem, stream>>>(p, m.q, m.k, mo);
     gdr::GradParams gp{p, o.dq, o.dk, o.dv};
     const int64_t blocks = static_cast<int64_t>(p.g.batch) * p.g.Hk * p.nchunks;

@@ -32,18 +32,21 @@ namespace gdr {
 // TMEM columns.  S: dS's terms, then its update; A: K dSᵀ, then dE's terms over it; R: Pᵀ dO in two halves (P's terms);
 // V: Tᵀ dE in two halves, then the terms of -e^G dV over the first; O: the terms of scale e^G dO.
 constexpr uint32_t kRevS = 0, kRevA = 128, kRevR = 192, kRevV = 320, kRevO = 448;
-// Shared memory: two stages of [K 0][Q 0][K 1][Q 1][record]; two of dO (swizzled blocks); the warps' <S, dS>.
+// Shared memory: two stages of [K 0][Q 0][K 1][Q 1][record]; dO (swizzled blocks); two images in and out: S's terms
+// come in for their product with dS, dS's terms take their place and go out, then dVᵀ's; the warps' <S, dS>.
 constexpr uint32_t kRevStage = 4 * kTile + kRecBytes, kRevOffRec = 4 * kTile;
-constexpr uint32_t kRevOffO = 2 * kRevStage, kRevOffDot = kRevOffO + 4 * kTile;
+constexpr uint32_t kRevOffO = 2 * kRevStage, kRevOffImg = kRevOffO + 2 * kTile, kRevOffDot = kRevOffImg + 8 * kTile;
 constexpr uint32_t kRevOffBar = kRevOffDot + 16 * 4;
 constexpr uint32_t kRevSmem = kRevOffBar + 256 + 1024;
 static_assert(kRevStage % 1024 == 0 && kRevSmem <= 227 * 1024, "shared memory");
 
 struct RevBars {
-    uint64_t full[2], empty[2];      // K, Q, dO and the record of a stage
+    uint64_t full[2], empty[2];      // K, Q and the record of a stage
+    uint64_t o_full, o_free;         // dO landed; read (state warps, behind its product)
+    uint64_t s_in;                   // S's terms landed
+    uint64_t img_full, img_free;     // dS's terms staged, then dV's (state warps); stored (1)
     uint64_t ks, e, ds;              // products done
     uint64_t s_ready[2], x_ready, w_ready;
-    uint64_t dot, dot_free;          // a step's <S, dS> of every warp written; read (1)
     uint64_t fin;
     uint32_t tmem;
 };
@@ -69,9 +72,11 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
     const bool ragged = len % kC != 0 && len < g.L;   // other tokens follow in the last chunk's tiles
     const uint64_t lim = p.wait_ns;
     if (tid == 0) {
-        uint64_t* one[] = {bar->full, bar->full + 1, bar->empty, bar->empty + 1, &bar->ks, &bar->e, &bar->ds, &bar->dot_free, &bar->fin};
+        uint64_t* one[] = {bar->full, bar->full + 1, bar->empty, bar->empty + 1, &bar->o_full, &bar->s_in,
+                           &bar->img_free, &bar->ks, &bar->e, &bar->ds, &bar->fin};
         for (uint64_t* x : one) mbar_init(x, 1);
-        uint64_t* all[] = {bar->s_ready, bar->s_ready + 1, &bar->x_ready, &bar->w_ready, &bar->dot};
+        uint64_t* all[] = {bar->s_ready, bar->s_ready + 1, &bar->x_ready, &bar->w_ready, &bar->o_free,
+                           &bar->img_full};
         for (uint64_t* x : all) mbar_init(x, kStateWarps);
         fence_mbar_init();
     }
@@ -101,7 +106,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
         __syncwarp();
         if (lane == 0) mbar_arrive(x);
     };
-    int issued = 0;
+    int issued = 0, o_issued = 0, s_issued = 0;
 
     // Step n handles chunk nchunk - 1 - n.
     if (warp == kLoadWarp) {
@@ -111,29 +116,58 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 if (n >= 2 && !wait1(&bar->empty[s], ((n >> 1) - 1) & 1)) break;
                 const uint32_t st = base + s * kRevStage;
                 uint64_t* f = &bar->full[s];
-                mbar_arrive_expect_tx(f, 2 * KB * kTile + kC * p.dv * 2 + kRecBytes);
+                mbar_arrive_expect_tx(f, 2 * KB * kTile + kRecBytes);
                 for (int kb = 0; kb < KB; ++kb) {
                     tma_load_4d(st + (2 * kb) * kTile, &tm_k, 64 * kb, hk, c * kC, b, f);
                     tma_load_4d(st + (2 * kb + 1) * kTile, &tm_q, 64 * kb, hk, c * kC, b, f);
                 }
-                for (int vb = 0; vb < p.dv / 64; ++vb)
-                    tma_load_4d(base + kRevOffO + (2 * s + vb) * kTile, &tm_o, 64 * vb, h, c * kC, b, f);
                 bulk_load(st + kRevOffRec, p.rec + (item * p.nchunks + c) * p.rec_bytes, kRecBytes, f);
                 issued = n + 1;
+                if (n >= 1 && !wait1(&bar->o_free, (n - 1) & 1)) break;
+                mbar_arrive_expect_tx(&bar->o_full, kC * p.dv * 2);
+                for (int vb = 0; vb < p.dv / 64; ++vb)
+                    tma_load_4d(base + kRevOffO + vb * kTile, &tm_o, 64 * vb, h, c * kC, b, &bar->o_full);
+                o_issued = n + 1;
             }
         }
         __syncwarp();
     } else if (warp == kStoreWarp) {
-        // <S, dS> at the states between the chunks, from the last to the first: the sixteen warps' sums, in order of a tree
+        // the images: S's terms of a state between two chunks in, dS's out, dV's out; from the last state to the first
         for (int n = 0; n <= nchunk; ++n) {
-            if (!wait_warp(&bar->dot, n & 1)) break;
-            float a = reinterpret_cast<const float*>(gbase + kRevOffDot)[lane & 15];
+            const int c = nchunk - n;   // the state that enters chunk c
+            unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar->s_in, 4 * KB * kTile);
+                bulk_load(base + kRevOffImg, kp + kKeepS, 2 * KB * kTile, &bar->s_in);
+                bulk_load(base + kRevOffImg + 4 * kTile, kp + kKeepSlo, 2 * KB * kTile, &bar->s_in);
+            }
+            s_issued = n + 1;
+            kp -= kKeepBytes;           // the chunk that this state leaves
+            if (!wait_warp(&bar->img_full, 0)) break;   // (two a step)
+            float a = reinterpret_cast<const float*>(gbase + kRevOffDot)[lane & 15];   // the sixteen warps' sums
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-            if (lane == 0)
-                p.dots[4 * (static_cast<int64_t>(g.batch) * g.H * p.nchunks * kC) + item * (p.nchunks + 1) + nchunk - n] = a;
-            arrive_warp(&bar->dot_free);
+            if (lane == 0) {
+                p.dots[4 * (static_cast<int64_t>(g.batch) * g.H * p.nchunks * kC) + item * (p.nchunks + 1) + c] = a;
+                if (n < nchunk) {
+                    bulk_store(kp + kKeepD, base + kRevOffImg, 2 * KB * kTile);
+                    bulk_store(kp + kKeepDlo, base + kRevOffImg + 4 * kTile, 2 * KB * kTile);
+                    tc::bulk_commit();
+                    tc::bulk_wait_read0();
+                }
+            }
+            if (n == nchunk) break;
+            arrive_warp(&bar->img_free);
+            if (!wait_warp(&bar->img_full, 1)) break;
+            if (lane == 0) {
+                bulk_store(kp + kKeepV, base + kRevOffImg, 4 * kTile);
+                tc::bulk_commit();
+                tc::bulk_wait_read0();
+            }
+            __syncwarp();
         }
+        if (lane == 0) bulk_wait0();
+        __syncwarp();
     } else if (warp == kMmaWarp) {
         if (lane == 0) {
             const uint32_t lbo = p.dv == 128 ? kTile : 0;   // d_v 64: the lanes 64.. repeat the rows 0..63
@@ -141,7 +175,8 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 const int s = n & 1;
                 const uint32_t par = n & 1, st = base + s * kRevStage, pr = st + kRevOffRec;
                 if (!wait1(&bar->full[s], (n >> 1) & 1)) break;
-                const uint32_t ot = base + kRevOffO + 2 * s * kTile;
+                const uint32_t ot = base + kRevOffO;
+                if (!wait1(&bar->o_full, par)) break;
                 if (n == 0 && !wait1(&bar->s_ready[0], 0)) break;   // the tiles' rows behind the end are zero by then
                 tc_fence_after();
                 // R = dOᵀ P, P's terms side by side (their columns were read before dE's terms were handed over)
@@ -219,16 +254,16 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             const uint32_t a = chunk_addr(off + static_cast<uint32_t>(v >> 6) * kTile, t, (v & 63) >> 3) + 2 * (v & 7);
             return row_in ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(gbase + a)) : 0.0f;
         };
-        // this warp's part of <S, dS> of the state that enters chunk c (leaves chunk c - 1), dS being the registers'
-        auto dot_state = [&](int c, int n) {
-            const unsigned char* sp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
+        // dS (the registers') with the state whose terms landed at step n: this warp's part of the product, then dS's
+        // terms in their place
+        auto meet_state = [&](int n) {
+            if (!wait_warp(&bar->s_in, n & 1)) return false;
             float dot = 0.0f;
 #pragma unroll
             for (int k = 0; k < KH; k += 8) {
                 const int key = part * KH + k;
-                const uint32_t o = chunk_addr(static_cast<uint32_t>(key >> 6) * 2 * kTile, v, (key & 63) >> 3);
-                const uint4 hi = *reinterpret_cast<const uint4*>(sp + kKeepS + o);
-                const uint4 lo = *reinterpret_cast<const uint4*>(sp + kKeepSlo + o);
+                const uint32_t o = chunk_addr(base + kRevOffImg + static_cast<uint32_t>(key >> 6) * 2 * kTile, v, (key & 63) >> 3);
+                const uint4 hi = lds128(o), lo = lds128(o + 4 * kTile);
                 const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -240,9 +275,12 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             if (!row_in) dot = 0.0f;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            if (n > 0 && !wait_warp(&bar->dot_free, (n - 1) & 1)) return false;
             if (lane == 0) reinterpret_cast<float*>(gbase + kRevOffDot)[warp] = dot;
-            arrive_warp(&bar->dot);
+#pragma unroll
+            for (int k = 0; k < KH; k += 16)   // (a thread's own values' places)
+                stage_terms(base + kRevOffImg, base + kRevOffImg + 4 * kTile, v, part * KH + k, S + k / 2);
+            fence_proxy_async_smem();
+            arrive_warp(&bar->img_full);
             return true;
         };
         bool ok = true;
@@ -252,7 +290,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             const Scal& sc = *reinterpret_cast<const Scal*>(gbase + s * kRevStage + kRevOffRec + kRecScal);
             if (n == 0) {
                 if (ragged) {   // rows behind the end, whatever they hold, become zero rows
-                    ok = wait_warp(&bar->full[0], 0);
+                    ok = wait_warp(&bar->full[0], 0) && wait_warp(&bar->o_full, 0);
                     if (!ok) break;
                     const int n0 = static_cast<int>(len - static_cast<int64_t>(c) * kC);
                     for (int i = n0 * 8 + tid; i < kC * 8; i += 32 * kStateWarps) {
@@ -266,15 +304,10 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 arrive_warp(&bar->s_ready[1]);
                 // (the zero rows of other warps' share are visible behind the product's own barrier)
             }
-            {   // keep dS, and its product with the state that leaves the chunk
-                unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
-#pragma unroll
-                for (int k = 0; k < KH; k += 16) keep_terms(kp + kKeepD, kp + kKeepDlo, v, part * KH + k, S + k / 2);
-                ok = dot_state(c + 1, n);
-                if (!ok) break;
-            }
-            ok = wait_warp(&bar->full[s], (n >> 1) & 1);
-            const uint32_t ot = kRevOffO + 2 * s * kTile;
+            ok = meet_state(n);
+            if (!ok) break;
+            ok = wait_warp(&bar->full[s], (n >> 1) & 1) && wait_warp(&bar->o_full, par);
+            const uint32_t ot = kRevOffO;
             if (!ok) break;
             f32x2 x[8];
             if (!(n == 0 && ragged)) {   // scale e^G dO (in a ragged chunk once every warp's zero rows are written)
@@ -306,7 +339,11 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             store_terms(tl + kRevA + kTok * part, x);
             tmem_wait_st();
             tc_fence_before();
-            arrive_warp(&bar->x_ready);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bar->x_ready);
+                mbar_arrive(&bar->o_free);
+            }
             ok = wait_warp(&bar->e, par);
             if (!ok) break;
             tc_fence_after();
@@ -325,10 +362,11 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(&bar->w_ready);
-            {   // dV, while dS is multiplied
-                unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
-                keep_terms(kp + kKeepV, kp + kKeepVlo, v, kTok * part, x);
-            }
+            ok = wait_warp(&bar->img_free, par);   // dV's terms, once dS's have left, while dS is multiplied
+            if (!ok) break;
+            stage_terms(base + kRevOffImg, base + kRevOffImg + 2 * kTile, v, kTok * part, x);
+            fence_proxy_async_smem();
+            arrive_warp(&bar->img_full);
             ok = wait_warp(&bar->ds, par);
             if (!ok) break;
             tc_fence_after();
@@ -348,7 +386,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             tmem_wait_st();
             tc_fence_before();
         }
-        if (ok) ok = dot_state(0, nchunk);
+        if (ok) ok = meet_state(nchunk);
         if (ok && p.dinit && row_in) {
 #pragma unroll
             for (int k = 0; k < KH; k += 4)
@@ -361,7 +399,9 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
     if (warp == kLoadWarp && lane == 0) {
         for (int n = issued > 2 ? issued - 2 : 0; n < issued; ++n)
             mbar_wait_bounded(&bar->full[n & 1], (n >> 1) & 1, p.drain_ns);
+        if (o_issued) mbar_wait_bounded(&bar->o_full, (o_issued - 1) & 1, p.drain_ns);
     }
+    if (warp == kStoreWarp && lane == 0 && s_issued) mbar_wait_bounded(&bar->s_in, (s_issued - 1) & 1, p.drain_ns);
     if (tid == 32 * kMmaWarp) {
         umma_commit(&bar->fin);
         mbar_wait_bounded(&bar->fin, 0, p.drain_ns);

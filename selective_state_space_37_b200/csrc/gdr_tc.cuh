@@ -596,26 +596,33 @@ constexpr int kStages = 2;             // chunks in flight
 constexpr uint32_t kColS = 0, kColA = 128, kColQS = 192, kColB = 256, kColY = 384;
 constexpr uint32_t kTmemCols = 512;
 
-// Shared memory: byte offsets from a 1024-aligned base.  A stage: [K 0][Q 0][K 1][Q 1][V 0][V 1][record]
-constexpr uint32_t kOffV = 4 * kTile, kOffRec = 6 * kTile;
-constexpr uint32_t kStageBytes = kOffRec + kRecBytes;
-static_assert(kStageBytes % 1024 == 0, "swizzled tiles");
-constexpr uint32_t kOffY = kStages * kStageBytes;      // y [64][d_v] for the store
-constexpr uint32_t kOffBar = kOffY + 2 * kTile;
-constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+// Shared memory: byte offsets from a 1024-aligned base.  A stage: [K 0][Q 0][K 1][Q 1][V 0][V 1][record]; then y
+// [64][d_v] for its store.  Without y there is no Q and of the record only T and the factors, and what is kept is
+// staged for its store: E's two images, then S's.
+template <bool Y>
+struct Smem {
+    static constexpr uint32_t kPair = Y ? 2 * kTile : kTile;   // from K's first block of keys to its second
+    static constexpr uint32_t kV = 2 * kPair, kRec = kV + 2 * kTile;
+    static constexpr uint32_t kFactors = kRec + (Y ? kRecScal : 2 * kTile);
+    static constexpr uint32_t kStage = kFactors + sizeof(Scal);
+    static constexpr uint32_t kOut = kStages * kStage;
+    static constexpr uint32_t kBar = kOut + (Y ? 2 : 12) * kTile;
+    static constexpr uint32_t kBytes = kBar + 256 + 1024;
+    static_assert(kStage % 1024 == 0 && kBytes <= 227 * 1024, "shared memory");
+};
 
-// 16 values' terms (hi then lo words) to two images of [rows][64-wide blocks]: chunks 2 m, 2 m + 1 of row r.
-__device__ __forceinline__ void keep_terms(unsigned char* hi_img, unsigned char* lo_img, int r, int key, const f32x2* v) {
+// 16 values' terms to two images in shared memory (rows of 128 bytes in 64-wide blocks of 128 rows): the 16 columns
+// from `col` on of row r.
+__device__ __forceinline__ void stage_terms(uint32_t hi_img, uint32_t lo_img, int r, int col, const f32x2* v) {
     uint32_t hi[8], lo[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) split2(v[e], hi[e], lo[e]);
-    const uint32_t blk = static_cast<uint32_t>(key >> 6) * 2 * kTile;   // 128 rows of 128 bytes
+    const uint32_t blk = static_cast<uint32_t>(col >> 6) * 2 * kTile;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const uint32_t o = chunk_addr(blk, r, ((key & 63) >> 3) + h);
-        *reinterpret_cast<uint4*>(hi_img + o) = make_uint4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]);
-        *reinterpret_cast<uint4*>(lo_img + o) = make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
+        const uint32_t o = chunk_addr(blk, r, ((col & 63) >> 3) + h);
+        sts128(hi_img + o, make_uint4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]));
+        sts128(lo_img + o, make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]));
     }
 }
 
@@ -625,7 +632,7 @@ struct Bars {
     uint64_t ks, e, ds, pv;    // the chain's products done
     uint64_t s_ready[2];       // S's terms written: of the first 16 keys of each thread, of the others (state warps)
     uint64_t x_ready, w_ready, e_ready;   // X's terms, W's, E's and Y's first part written (state warps)
-    uint64_t y_full, y_free;   // y staged (state warps); stored (1)
+    uint64_t y_full, y_free;   // y staged (state warps); stored (1).  Without y: a chunk's S, then its E
     uint64_t fin;              // wind-down
     uint32_t tmem;
 };
@@ -638,13 +645,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_q,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ CUtensorMap tm_y) {
+    using M = Smem<Y>;
     constexpr int KB = DK / 64;       // 64-wide blocks of a K or Q row
     constexpr int KH = DK / kParts;   // keys of a state thread
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     unsigned char* gbase = smem_raw + (base - raw);
-    Bars* const bar = reinterpret_cast<Bars*>(gbase + kOffBar);
+    Bars* const bar = reinterpret_cast<Bars*>(gbase + M::kBar);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const GdrParams& g = p.g;
@@ -704,27 +712,47 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             for (int c = 0; c < nchunk; ++c) {
                 const int s = c % kStages;
                 if (c >= kStages && !wait1(&bar->empty[s], ((c / kStages) - 1) & 1)) break;
-                const uint32_t st = base + s * kStageBytes;
+                const uint32_t st = base + s * M::kStage;
                 uint64_t* f = &bar->full[s];
-                mbar_arrive_expect_tx(f, (Y ? 2 : 1) * KB * kTile + kC * p.dv * 2 + kRecBytes);
+                mbar_arrive_expect_tx(f, (Y ? 2 : 1) * KB * kTile + kC * p.dv * 2 + (M::kStage - M::kRec));
                 for (int kb = 0; kb < KB; ++kb) {
-                    tma_load_4d(st + (2 * kb) * kTile, &tm_k, 64 * kb, hk, c * kC, b, f);
-                    if (Y) tma_load_4d(st + (2 * kb + 1) * kTile, &tm_q, 64 * kb, hk, c * kC, b, f);
+                    tma_load_4d(st + kb * M::kPair, &tm_k, 64 * kb, hk, c * kC, b, f);
+                    if (Y) tma_load_4d(st + kb * M::kPair + kTile, &tm_q, 64 * kb, hk, c * kC, b, f);
                 }
                 for (int vb = 0; vb < p.dv / 64; ++vb)
-                    tma_load_4d(st + kOffV + vb * kTile, &tm_v, 64 * vb, h, c * kC, b, f);
-                bulk_load(st + kOffRec, p.rec + (item * p.nchunks + c) * p.rec_bytes, kRecBytes, f);
+                    tma_load_4d(st + M::kV + vb * kTile, &tm_v, 64 * vb, h, c * kC, b, f);
+                const unsigned char* r = p.rec + (item * p.nchunks + c) * p.rec_bytes;
+                if (Y) {
+                    bulk_load(st + M::kRec, r, kRecBytes, f);
+                } else {
+                    bulk_load(st + M::kRec, r + kRecT, 2 * kTile, f);
+                    bulk_load(st + M::kFactors, r + kRecScal, sizeof(Scal), f);
+                }
                 issued = c + 1;
             }
         }
         __syncwarp();
     } else if (warp == kStoreWarp) {
-        // ============================================================ y
+        // ============================================================ y, or what is kept
+        for (int n = 0; !Y && n < 2 * nchunk + 1; ++n) {   // S of chunk n / 2, then its E; at last the final state
+            if (!wait_warp(&bar->y_full, n & 1)) break;
+            if (lane == 0) {
+                unsigned char* kp = p.keep + (item * (p.nchunks + 1) + (n >> 1)) * kKeepBytes;
+                if (n & 1) bulk_store(kp + kKeepE, base + M::kOut, 4 * kTile);
+                else {
+                    bulk_store(kp + kKeepS, base + M::kOut + 4 * kTile, 2 * KB * kTile);
+                    bulk_store(kp + kKeepSlo, base + M::kOut + 8 * kTile, 2 * KB * kTile);
+                }
+                tc::bulk_commit();
+                tc::bulk_wait_read0();
+            }
+            arrive_warp(&bar->y_free);
+        }
         for (int c = 0; Y && c < nchunk; ++c) {
             if (!wait_warp(&bar->y_full, c & 1)) break;
             if (c != ragged) {   // rows behind the tensor's end are clipped by the copy
                 if (lane == 0) {
-                    tc::tma_store_4d(&tm_y, base + kOffY, 0, h, c * kC, b);
+                    tc::tma_store_4d(&tm_y, base + M::kOut, 0, h, c * kC, b);
                     tc::bulk_commit();
                     tc::bulk_wait_read0();
                 }
@@ -735,7 +763,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 for (int i = lane; i < n; i += 32) {
                     const int r = i / quads, q = i % quads;
                     *reinterpret_cast<uint4*>(y + ((static_cast<int64_t>(b) * g.L + t0 + r) * g.H + h) * p.dv + 8 * q) =
-                        lds128(base + kOffY + (r * p.dv + 8 * q) * 2);
+                        lds128(base + M::kOut + (r * p.dv + 8 * q) * 2);
                 }
             }
             arrive_warp(&bar->y_free);
@@ -748,11 +776,11 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             const uint32_t vlbo = p.dv == 128 ? kTile : 0;   // d_v 64: the lanes 64.. repeat the rows 0..63
             for (int c = 0; c < nchunk; ++c) {
                 const int s = c % kStages;
-                const uint32_t par = c & 1, st = base + s * kStageBytes, pr = st + kOffRec;
+                const uint32_t par = c & 1, st = base + s * M::kStage, pr = st + M::kRec;
                 if (!wait1(&bar->full[s], (c / kStages) & 1)) break;
                 // KS and QS: S's terms of 16 keys in 16 columns, K and Q of a 64-key block side by side
                 auto ks_step = [&](int ks) {
-                    const uint64_t bd = sdesc(st + (ks >> 2) * 2 * kTile + (ks & 3) * 32, 16, 1024);
+                    const uint64_t bd = sdesc(st + (ks >> 2) * M::kPair + (ks & 3) * 32, 16, 1024);
                     umma_ts(tmem + kColA, tmem + kColS + 16 * ks, bd, idesc(Y ? 2 * kC : kC, false), ks > 0);
                     umma_ts(tmem + kColA, tmem + kColS + 16 * ks + 8, bd, idesc(Y ? 2 * kC : kC, false), 1);
                 };
@@ -773,7 +801,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < kC / 16; ++j)
-                    umma(tmem + kColB, sdesc(st + kOffV + 2048u * j, vlbo, 1024), sdesc(pr + kRecT + 32u * j, 16, 1024),
+                    umma(tmem + kColB, sdesc(st + M::kV + 2048u * j, vlbo, 1024), sdesc(pr + kRecT + 32u * j, 16, 1024),
                          idesc(2 * kC, false, true), j > 0);
                 if (!wait1(&bar->x_ready, par)) break;
                 tc_fence_after();
@@ -790,7 +818,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 // dS = W K over the columns of S's terms
 #pragma unroll
                 for (int j = 0; j < kC / 16; ++j) {
-                    const uint64_t bd = sdesc(st + 2048u * j, 2 * kTile, 1024);
+                    const uint64_t bd = sdesc(st + 2048u * j, M::kPair, 1024);
                     umma_ts(tmem + kColS, tmem + kColA + 16 * j, bd, idesc(DK, true), j > 0);
                     umma_ts(tmem + kColS, tmem + kColA + 16 * j + 8, bd, idesc(DK, true), 1);
                 }
@@ -828,10 +856,15 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         for (int k = 0; k < KH; k += 16) store_terms(tl + kColS + part * KH + k, S + k / 2);
         tmem_wait_st();
         tc_fence_before();
-        auto keep_state = [&](int c) {   // the terms of the state that enters chunk c
-            unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
+        // the terms of the state that enters chunk c, and those of its E (without y); the stores are one behind another
+        auto keep_state = [&](int c) {
+            if (c > 0 && !wait_warp(&bar->y_free, 1)) return false;   // chunk c - 1's E, store 2 c - 1
 #pragma unroll
-            for (int k = 0; k < KH; k += 16) keep_terms(kp + kKeepS, kp + kKeepSlo, v, part * KH + k, S + k / 2);
+            for (int k = 0; k < KH; k += 16)
+                stage_terms(base + M::kOut + 4 * kTile, base + M::kOut + 8 * kTile, v, part * KH + k, S + k / 2);
+            fence_proxy_async_smem();
+            arrive_warp(&bar->y_full);
+            return true;
         };
         auto finish_y = [&](int c) {     // chunk c's y
             if (c > 0 && !wait_warp(&bar->y_free, (c - 1) & 1)) return false;
@@ -841,7 +874,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             tmem_ld16x2(tl + kColY + kTok * part, tl + kColY + kC + kTok * part, x, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = add2(x[e], w[e]);
-            __nv_bfloat16* ys = reinterpret_cast<__nv_bfloat16*>(gbase + kOffY) + kTok * part * p.dv + v;
+            __nv_bfloat16* ys = reinterpret_cast<__nv_bfloat16*>(gbase + M::kOut) + kTok * part * p.dv + v;
             if (row_in) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -856,15 +889,15 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         bool ok = true;
         for (int c = 0; c < nchunk; ++c) {
             const int s = c % kStages;
-            const uint32_t par = c & 1, st = base + s * kStageBytes;
-            const Scal& sc = *reinterpret_cast<const Scal*>(gbase + s * kStageBytes + kOffRec + kRecScal);
+            const uint32_t par = c & 1, st = base + s * M::kStage;
+            const Scal& sc = *reinterpret_cast<const Scal*>(gbase + s * M::kStage + M::kFactors);
             if (c == ragged) {   // rows of K and V behind the end, whatever they hold, become zero rows
                 ok = wait_warp(&bar->full[s], (c / kStages) & 1);
                 if (!ok) break;
                 const int n0 = static_cast<int>(len - static_cast<int64_t>(c) * kC);
                 for (int i = n0 * 8 + tid; i < kC * 8; i += 32 * kStateWarps) {
-                    for (int kb = 0; kb < KB; ++kb) sts128(st + 2 * kb * kTile + 16 * i, make_uint4(0, 0, 0, 0));
-                    for (int vb = 0; vb < p.dv / 64; ++vb) sts128(st + kOffV + vb * kTile + 16 * i, make_uint4(0, 0, 0, 0));
+                    for (int kb = 0; kb < KB; ++kb) sts128(st + kb * M::kPair + 16 * i, make_uint4(0, 0, 0, 0));
+                    for (int vb = 0; vb < p.dv / 64; ++vb) sts128(st + M::kV + vb * kTile + 16 * i, make_uint4(0, 0, 0, 0));
                 }
                 fence_proxy_async_smem();
             }
@@ -872,7 +905,10 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 arrive_warp(&bar->s_ready[0]);
                 arrive_warp(&bar->s_ready[1]);
             }
-            if (!Y) keep_state(c);
+            if (!Y) {
+                ok = keep_state(c);
+                if (!ok) break;
+            }
             if (Y && c > 0) {   // the last chunk's y, while this one's K Sᵀ runs
                 ok = finish_y(c - 1);
                 if (!ok) break;
@@ -921,8 +957,11 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 tc_fence_before();
                 arrive_warp(&bar->e_ready);
             } else {
-                unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
-                keep_terms(kp + kKeepE, kp + kKeepElo, v, kTok * part, x);
+                ok = wait_warp(&bar->y_free, 0);   // its S, store 2 c
+                if (!ok) break;
+                stage_terms(base + M::kOut, base + M::kOut + 2 * kTile, v, kTok * part, x);
+                fence_proxy_async_smem();
+                arrive_warp(&bar->y_full);
             }
             ok = wait_warp(&bar->ds, par);
             if (!ok) break;
@@ -944,7 +983,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             tc_fence_before();
         }
         if (Y && ok && nchunk > 0) ok = finish_y(nchunk - 1);
-        if (!Y && ok) keep_state(nchunk);
+        if (!Y && ok) ok = keep_state(nchunk);
         if (ok && g.final_state && row_in) {
 #pragma unroll
             for (int k = 0; k < KH; k += 4)
