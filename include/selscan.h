@@ -338,8 +338,11 @@ typedef struct ss_gdr_dims {
  *   launch       stream; workspace of at least ss_gdr_fwd_workspace_bytes() bytes,
  *                16-byte aligned (its first word is a status word that the call clears;
  *                see ss_ssd_fwd); timeout_iters bounds one wait in microseconds (0: two
- *                seconds); chunk_len > 0 fixes the length of the time segments that a
- *                bf16 sequence is cut into, 0 lets the library choose.
+ *                seconds); chunk_len > 0 fixes the length of the time segments that
+ *                bf16 sequences are cut into (rounded up to 64 steps, at most 16
+ *                segments), 0 lets the library choose: where batch x heads leaves SMs
+ *                idle, segments run in parallel, from entering states that a first
+ *                pass over them and a fold make exact up to rounding.
  * The state is fp32 throughout.  bf16 runs chunk by chunk (64 steps) as dense products
  * on the tensor cores, in which the fp32 operands (the state, the chunk's inverse and
  * its corrections) enter as two bf16 terms each; fp32, and short bf16 sequences, run
@@ -352,8 +355,9 @@ SS_API int ss_gdr_fwd(const void* q, const void* k, const void* v, const void* d
                       float* final_state, float scale, uint32_t flags, const ss_gdr_dims* dims,
                       const ss_launch* launch);
 
-/* Workspace bytes ss_gdr_fwd needs (0 for sizes it would reject). */
-SS_API size_t ss_gdr_fwd_workspace_bytes(const ss_gdr_dims* dims, uint32_t flags);
+/* Workspace bytes ss_gdr_fwd needs for these sizes, flags and launch->chunk_len on the current device (0 for sizes it
+ * would reject). */
+SS_API size_t ss_gdr_fwd_workspace_bytes(const ss_gdr_dims* dims, uint32_t flags, int32_t chunk_len);
 
 /* ss_gdr_step -- one token of the gated delta rule on a carried state.
  *   state        [batch, nheads, d_v, d_k] fp32, read and overwritten in place

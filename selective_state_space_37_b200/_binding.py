@@ -169,7 +169,7 @@ def lib():
                                            ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_size_t, vp]
         for f in (L.ss_gdr_fwd, L.ss_gdr_step, L.ss_gdr_bwd, L.ss_norm_fwd, L.ss_norm_bwd, L.ss_block_fwd_prenorm):
             f.restype = ctypes.c_int
-        L.ss_gdr_fwd_workspace_bytes.argtypes = [gp, u32]
+        L.ss_gdr_fwd_workspace_bytes.argtypes = [gp, u32, ctypes.c_int32]
         L.ss_norm_bwd_workspace_bytes.argtypes = [np_, u32]
         L.ss_block_prenorm_scratch_bytes.argtypes = [ctypes.POINTER(ss_block_weights), ctypes.c_int64,
                                                      ctypes.c_int64]
@@ -664,7 +664,7 @@ def ss_gdr_fwd(q, k, v, dt, A, beta, dt_bias=None, initial_state=None, seqlens=N
         final_state = torch.empty(states, dtype=torch.float32, device=dev)
     _check(final_state, "final_state", states, torch.float32, dev)
     flags |= (SS_SYNC_CHECK if sync_check else 0) | int(extra_flags)
-    need = int(lib().ss_gdr_fwd_workspace_bytes(ctypes.byref(dims), flags))
+    need = int(lib().ss_gdr_fwd_workspace_bytes(ctypes.byref(dims), flags, int(chunk_len)))
     launch = _launch_for(need, dev, stream, workspace, timeout_iters, chunk_len)
     rc = lib().ss_gdr_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(beta),
                           _ptr(initial_state), _ptr(seqlens), _ptr(y), _ptr(final_state),

@@ -75,18 +75,63 @@ bool head_map(CUtensorMap* m, const void* base, int64_t batch, int64_t L, int64_
     return make_map_bf16(m, base, 4, dims, strides, box, swizzle);
 }
 
-// Workspace: the status word's header, then a record per (item, chunk).
+// Time segments.  Items 0 .. n_whole - 1 run whole, the others are cut into nseg segments of cseg chunks: a state pass
+// (two runs for every segment but the first and the last), the fold, then every segment from its entering state.
+constexpr int64_t kGdrMaxSeg = 16;
+struct GdrPlan {
+    int64_t n_whole, nseg, cseg;
+};
+// The plan with the least chunk-times on the busiest SM (one CTA per SM).  A chunk of the state pass takes 0.8 of one
+// with y; the extra launches and the fold are charged 12 chunks (measured: 512 chunks of 16 items whole 1.55 ms, in 9
+// segments 0.52 ms; 160 items of 128 chunks whole 0.80 ms, the last wave's 12 in segments 0.54 ms).
+GdrPlan gdr_plan(int64_t items, int64_t nchunks, int32_t chunk_len) {
+    GdrPlan best{items, 1, nchunks};
+    if (items == 0 || nchunks < 2) return best;
+    if (chunk_len > 0) {
+        int64_t cs = std::max<int64_t>(1, ceil_div(chunk_len, gdr::kC));
+        if (ceil_div(nchunks, cs) > kGdrMaxSeg) cs = ceil_div(nchunks, kGdrMaxSeg);
+        const int64_t k = ceil_div(nchunks, cs);
+        return k > 1 ? GdrPlan{0, k, cs} : best;
+    }
+    const int64_t sms = sm_count_of_current_device(), tail = items % sms;
+    double cost = static_cast<double>(ceil_div(items, sms) * nchunks);
+    for (int64_t k = 2; k <= std::min(kGdrMaxSeg, nchunks); ++k) {
+        const int64_t cs = ceil_div(nchunks, k);
+        if (ceil_div(nchunks, cs) != k) continue;
+        for (const int64_t n : {items, tail}) {   // every item, or those of the last wave
+            if (n == 0) continue;
+            const double t = static_cast<double>((items - n) / sms * nchunks) +
+                             0.8 * static_cast<double>(ceil_div(n * std::max<int64_t>(1, 2 * k - 3), sms) * cs) +
+                             static_cast<double>(ceil_div(n * k, sms) * cs) + 12.0;
+            if (t < cost - 1e-9) {
+                cost = t;
+                best = GdrPlan{items - n, k, cs};
+            }
+        }
+    }
+    return best;
+}
+
+// Workspace: the status word's header, a record per (item, chunk), then the cut items' segment states.
 struct GdrLayout {
     int64_t nchunks;
-    size_t rec, total;
+    GdrPlan plan;
+    size_t rec, in, loc, map, total;
 };
-GdrLayout gdr_layout(const ss_gdr_dims* d, uint32_t flags) {
+GdrLayout gdr_layout(const ss_gdr_dims* d, uint32_t flags, int32_t chunk_len) {
     GdrLayout w{};
+    auto al = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+    const int64_t items = d->batch * d->nheads;
     w.nchunks = ceil_div(d->seqlen, gdr::kC);
-    w.rec = kHeaderBytes;
-    w.total = w.rec;
-    if ((flags & SS_BF16) && d->seqlen >= kChunkedFrom)
-        w.total += static_cast<size_t>(d->batch * d->nheads * w.nchunks) * gdr::kRecBytes;
+    w.plan = GdrPlan{items, 1, w.nchunks};
+    w.rec = w.total = kHeaderBytes;
+    if (!(flags & SS_BF16) || d->seqlen < kChunkedFrom) return w;
+    w.plan = gdr_plan(items, w.nchunks, chunk_len);
+    const size_t n = static_cast<size_t>((items - w.plan.n_whole) * (w.plan.nseg - 1));
+    w.in = w.rec + al(static_cast<size_t>(items * w.nchunks) * gdr::kRecBytes);
+    w.loc = w.in + al(n * static_cast<size_t>(d->d_v * d->d_k) * sizeof(float));
+    w.map = w.loc + al(n * static_cast<size_t>(d->d_v * d->d_k) * sizeof(float));
+    w.total = w.map + al(n * static_cast<size_t>(d->d_k * d->d_k) * sizeof(float));
     return w;
 }
 
@@ -98,20 +143,38 @@ template <int DK>
 int launch_tc(const gdr::Params& p, const Maps& m, cudaStream_t stream) {
     auto prep = gdr::ss_gdr_prep_kernel<DK>;
     auto kern = gdr::ss_gdr_tc_kernel<DK, true>;
-    static std::atomic<bool> attr[2][kMaxDevices];
+    auto state = gdr::ss_gdr_tc_kernel<DK, false>;
+    auto fold = gdr::ss_gdr_fold_kernel<DK>;
+    static std::atomic<bool> attr[4][kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || set_smem_limit(kern, gdr::Smem<true>::kBytes, attr[0], dev) != SS_OK ||
-        set_smem_limit(prep, gdr::kPrepSmem, attr[1], dev) != SS_OK)
+        set_smem_limit(prep, gdr::kPrepSmem, attr[1], dev) != SS_OK ||
+        set_smem_limit(state, gdr::Smem<false>::kBytes, attr[2], dev) != SS_OK ||
+        set_smem_limit(fold, sizeof(gdr::FoldSmem<DK>), attr[3], dev) != SS_OK)
         return SS_ERR_CUDA;
-    const int64_t items = static_cast<int64_t>(p.g.batch) * p.g.H;
+    const int64_t items = static_cast<int64_t>(p.g.batch) * p.g.H, cut = p.nseg > 1 ? items - p.n_whole : 0;
     prep<<<static_cast<unsigned>(items * p.nchunks), gdr::kPrepThreads, gdr::kPrepSmem, stream>>>(p, m.q, m.k);
-    kern<<<static_cast<unsigned>(items), gdr::kThreads, gdr::Smem<true>::kBytes, stream>>>(p, m.q, m.k, m.v, m.y);
+    if (cut > 0) {
+        state<<<static_cast<unsigned>(cut * (2 * p.nseg - 3)), gdr::kThreads, gdr::Smem<false>::kBytes, stream>>>(
+            p, m.q, m.k, m.v, m.v);
+        const dim3 grid(static_cast<unsigned>(cut), static_cast<unsigned>(p.dv / gdr::FoldSmem<DK>::kRows));
+        fold<<<grid, 256, sizeof(gdr::FoldSmem<DK>), stream>>>(p);
+    }
+    kern<<<static_cast<unsigned>(items - cut + cut * p.nseg), gdr::kThreads, gdr::Smem<true>::kBytes, stream>>>(
+        p, m.q, m.k, m.v, m.y);
     return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
 int run_tc(const GdrParams& g, const ss_gdr_dims* d, uint32_t flags, const ss_launch* launch, cudaStream_t stream) {
-    const GdrLayout w = gdr_layout(d, flags);
+    const GdrLayout w = gdr_layout(d, flags, launch->chunk_len);
+    unsigned char* ws = static_cast<unsigned char*>(launch->workspace);
     gdr::Params p{};
+    p.n_whole = static_cast<int>(w.plan.n_whole);
+    p.nseg = static_cast<int>(w.plan.nseg);
+    p.cseg = static_cast<int>(w.plan.cseg);
+    p.seg_in = reinterpret_cast<float*>(ws + w.in);
+    p.seg_loc = reinterpret_cast<float*>(ws + w.loc);
+    p.seg_map = reinterpret_cast<float*>(ws + w.map);
     p.g = g;
     p.status = static_cast<uint32_t*>(launch->workspace);
     p.rec = static_cast<unsigned char*>(launch->workspace) + w.rec;
@@ -186,8 +249,8 @@ int launch_bwd(const gdr::Params& p, const Maps& m, const CUtensorMap& mo, const
 
 extern "C" {
 
-size_t ss_gdr_fwd_workspace_bytes(const ss_gdr_dims* dims, uint32_t flags) {
-    return check_gdr(dims, flags) == SS_OK ? gdr_layout(dims, flags).total : 0;
+size_t ss_gdr_fwd_workspace_bytes(const ss_gdr_dims* dims, uint32_t flags, int32_t chunk_len) {
+    return check_gdr(dims, flags) == SS_OK ? gdr_layout(dims, flags, chunk_len).total : 0;
 }
 
 int ss_gdr_fwd(const void* q, const void* k, const void* v, const void* dt, const float* dt_bias, const float* A,
@@ -202,7 +265,7 @@ int ss_gdr_fwd(const void* q, const void* k, const void* v, const void* dt, cons
     const void* ptrs[] = {q, k, v, dt, dt_bias, A, beta, h_init, seqlens, y, final_state};
     for (const void* x : ptrs)
         if (!aligned16(x)) return SS_ERR_INVALID_ARG;
-    if (!launch->workspace || launch->workspace_bytes < ss_gdr_fwd_workspace_bytes(dims, flags) ||
+    if (!launch->workspace || launch->workspace_bytes < gdr_layout(dims, flags, launch->chunk_len).total ||
         !aligned16(launch->workspace))
         return SS_ERR_WORKSPACE;
     cudaStream_t stream = static_cast<cudaStream_t>(launch->stream);
@@ -282,6 +345,8 @@ int ss_gdr_bwd(const void* q, const void* k, const void* v, const void* dt, cons
         p.g.seqlens = seqlens;
         p.rec = ws + w.rec;
         p.nchunks = w.nchunks;
+        p.n_whole = static_cast<int>(items);
+        p.nseg = 1;
         p.rec_bytes = gdr::kRecBwdBytes;
         p.keep = ws + w.keep;
         p.dots = reinterpret_cast<float*>(ws + w.dots);

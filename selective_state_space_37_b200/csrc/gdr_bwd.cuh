@@ -19,7 +19,8 @@
 // Every term carries its decay, so a head that forgets fast has small terms and not the difference of large ones (as
 // Σ (dO·Y - dV·V), which is the same sum, would be); and each chunk starts from its own <S, dS>.
 //
-// Precision: fp32 operands enter every product as two bf16 terms, as in the forward; the gates' gradients are sums
+// Precision: fp32 operands enter every product as two bf16 terms, as in the forward, and those that go straight into
+// the adjoint as three; the gates' gradients are sums
 // over all tokens and come out in fp32.
 #pragma once
 
@@ -30,20 +31,19 @@ namespace gdr {
 
 // ---------------------------------------------------------------------------------------- the adjoint's chain
 // TMEM columns.  S: dS's terms, then its update; A: K dSᵀ, then dE's terms over it; R: Pᵀ dO in two halves (P's terms);
-// V: Tᵀ dE in two halves, then the terms of -e^G dV over the first; O: the terms of scale e^G dO.
+// V: Tᵀ dE in two halves, then the terms of -e^G dV over the first and its third over the second; O: the terms of
+// scale e^G dO, its third over R.
 constexpr uint32_t kRevS = 0, kRevA = 128, kRevR = 192, kRevV = 320, kRevO = 448;
-// Shared memory: two stages of [K 0][Q 0][K 1][Q 1][record]; dO (swizzled blocks); two images in and out: S's terms
-// come in for their product with dS, dS's terms take their place and go out, then dVᵀ's; the warps' <S, dS>.
+// Shared memory: two stages of [K 0][Q 0][K 1][Q 1][record]; dO (swizzled blocks); two images on their way out, dS's
+// terms and then dVᵀ's.
 constexpr uint32_t kRevStage = 4 * kTile + kRecBytes, kRevOffRec = 4 * kTile;
-constexpr uint32_t kRevOffO = 2 * kRevStage, kRevOffImg = kRevOffO + 2 * kTile, kRevOffDot = kRevOffImg + 8 * kTile;
-constexpr uint32_t kRevOffBar = kRevOffDot + 16 * 4;
+constexpr uint32_t kRevOffO = 2 * kRevStage, kRevOffImg = kRevOffO + 2 * kTile, kRevOffBar = kRevOffImg + 8 * kTile;
 constexpr uint32_t kRevSmem = kRevOffBar + 256 + 1024;
 static_assert(kRevStage % 1024 == 0 && kRevSmem <= 227 * 1024, "shared memory");
 
 struct RevBars {
     uint64_t full[2], empty[2];      // K, Q and the record of a stage
     uint64_t o_full, o_free;         // dO landed; read (state warps, behind its product)
-    uint64_t s_in;                   // S's terms landed
     uint64_t img_full, img_free;     // dS's terms staged, then dV's (state warps); stored (1)
     uint64_t ks, e, ds;              // products done
     uint64_t s_ready[2], x_ready, w_ready;
@@ -52,7 +52,7 @@ struct RevBars {
 };
 static_assert(sizeof(RevBars) <= 256, "barrier region");
 
-// Grid: one CTA per (b, h).  Of a chunk dV and the leaving state's adjoint are kept.
+// Grid: one CTA per (b, h).  dV of every chunk and the adjoints of the states between the chunks are kept.
 template <int DK>
 __global__ void __launch_bounds__(kThreads, 1)
 ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_q,
@@ -72,7 +72,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
     const bool ragged = len % kC != 0 && len < g.L;   // other tokens follow in the last chunk's tiles
     const uint64_t lim = p.wait_ns;
     if (tid == 0) {
-        uint64_t* one[] = {bar->full, bar->full + 1, bar->empty, bar->empty + 1, &bar->o_full, &bar->s_in,
+        uint64_t* one[] = {bar->full, bar->full + 1, bar->empty, bar->empty + 1, &bar->o_full,
                            &bar->img_free, &bar->ks, &bar->e, &bar->ds, &bar->fin};
         for (uint64_t* x : one) mbar_init(x, 1);
         uint64_t* all[] = {bar->s_ready, bar->s_ready + 1, &bar->x_ready, &bar->w_ready, &bar->o_free,
@@ -106,7 +106,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
         __syncwarp();
         if (lane == 0) mbar_arrive(x);
     };
-    int issued = 0, o_issued = 0, s_issued = 0;
+    int issued = 0, o_issued = 0;
 
     // Step n handles chunk nchunk - 1 - n.
     if (warp == kLoadWarp) {
@@ -132,39 +132,20 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
         }
         __syncwarp();
     } else if (warp == kStoreWarp) {
-        // the images: S's terms of a state between two chunks in, dS's out, dV's out; from the last state to the first
-        for (int n = 0; n <= nchunk; ++n) {
-            const int c = nchunk - n;   // the state that enters chunk c
-            unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
+        for (int n = 0; n < 2 * nchunk + 1; ++n) {   // dS of a state, dV of the chunk before it, and so on
+            if (!wait_warp(&bar->img_full, n & 1)) break;
             if (lane == 0) {
-                mbar_arrive_expect_tx(&bar->s_in, 4 * KB * kTile);
-                bulk_load(base + kRevOffImg, kp + kKeepS, 2 * KB * kTile, &bar->s_in);
-                bulk_load(base + kRevOffImg + 4 * kTile, kp + kKeepSlo, 2 * KB * kTile, &bar->s_in);
-            }
-            s_issued = n + 1;
-            kp -= kKeepBytes;           // the chunk that this state leaves
-            if (!wait_warp(&bar->img_full, 0)) break;   // (two a step)
-            float a = reinterpret_cast<const float*>(gbase + kRevOffDot)[lane & 15];   // the sixteen warps' sums
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-            if (lane == 0) {
-                p.dots[4 * (static_cast<int64_t>(g.batch) * g.H * p.nchunks * kC) + item * (p.nchunks + 1) + c] = a;
-                if (n < nchunk) {
+                unsigned char* kp = p.keep + (item * (p.nchunks + 1) + nchunk - ((n + 1) >> 1)) * kKeepBytes;
+                if (n & 1) {
+                    bulk_store(kp + kKeepV, base + kRevOffImg, 4 * kTile);
+                } else {
                     bulk_store(kp + kKeepD, base + kRevOffImg, 2 * KB * kTile);
                     bulk_store(kp + kKeepDlo, base + kRevOffImg + 4 * kTile, 2 * KB * kTile);
-                    tc::bulk_commit();
-                    tc::bulk_wait_read0();
                 }
-            }
-            if (n == nchunk) break;
-            arrive_warp(&bar->img_free);
-            if (!wait_warp(&bar->img_full, 1)) break;
-            if (lane == 0) {
-                bulk_store(kp + kKeepV, base + kRevOffImg, 4 * kTile);
                 tc::bulk_commit();
                 tc::bulk_wait_read0();
             }
-            __syncwarp();
+            arrive_warp(&bar->img_free);
         }
         if (lane == 0) bulk_wait0();
         __syncwarp();
@@ -208,24 +189,24 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 for (int j = 0; j < kC / 16; ++j) {
                     const uint64_t bd = sdesc(pr + kRecT + 2048u * j, kTile, 1024);
                     umma_ts(tmem + kRevV, tmem + kRevA + 16 * j, bd, idesc(2 * kC, true), j > 0);
-                    umma_ts(tmem + kRevV, tmem + kRevA + 16 * j + 8, bd, idesc(kC, true), 1);
+                    umma_ts(tmem + kRevV, tmem + kRevA + 16 * j + 8, bd, idesc(2 * kC, true), 1);
                 }
                 umma_commit(&bar->e);
                 // dS's update: (scale e^G dO)ᵀ Q, then (-e^G dV)ᵀ K, over the columns of dS's terms
 #pragma unroll
-                for (int j = 0; j < kC / 16; ++j) {
-                    const uint64_t bd = sdesc(st + kTile + 2048u * j, 2 * kTile, 1024);
-                    umma_ts(tmem + kRevS, tmem + kRevO + 16 * j, bd, idesc(DK, true), j > 0);
-                    umma_ts(tmem + kRevS, tmem + kRevO + 16 * j + 8, bd, idesc(DK, true), 1);
-                }
+                for (int w = 0; w < 3; ++w)
+#pragma unroll
+                    for (int j = 0; j < kC / 16; ++j)
+                        umma_ts(tmem + kRevS, tmem + (w == 0 ? kRevR : w == 1 ? kRevO + 8 : kRevO) + 16 * j,
+                                sdesc(st + kTile + 2048u * j, 2 * kTile, 1024), idesc(DK, true), w + j > 0);
                 if (!wait1(&bar->w_ready, par)) break;
                 tc_fence_after();
 #pragma unroll
-                for (int j = 0; j < kC / 16; ++j) {
-                    const uint64_t bd = sdesc(st + 2048u * j, 2 * kTile, 1024);
-                    umma_ts(tmem + kRevS, tmem + kRevV + 16 * j, bd, idesc(DK, true), 1);
-                    umma_ts(tmem + kRevS, tmem + kRevV + 16 * j + 8, bd, idesc(DK, true), 1);
-                }
+                for (int w = 0; w < 3; ++w)
+#pragma unroll
+                    for (int j = 0; j < kC / 16; ++j)
+                        umma_ts(tmem + kRevS, tmem + (w == 0 ? kRevV + kC : w == 1 ? kRevV + 8 : kRevV) + 16 * j,
+                                sdesc(st + 2048u * j, 2 * kTile, 1024), idesc(DK, true), 1);
                 umma_commit(&bar->ds);
                 umma_commit(&bar->empty[s]);
             }
@@ -254,30 +235,10 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             const uint32_t a = chunk_addr(off + static_cast<uint32_t>(v >> 6) * kTile, t, (v & 63) >> 3) + 2 * (v & 7);
             return row_in ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(gbase + a)) : 0.0f;
         };
-        // dS (the registers') with the state whose terms landed at step n: this warp's part of the product, then dS's
-        // terms in their place
-        auto meet_state = [&](int n) {
-            if (!wait_warp(&bar->s_in, n & 1)) return false;
-            float dot = 0.0f;
+        auto keep_state = [&](int n) {   // dS, store 2 n
+            if (n > 0 && !wait_warp(&bar->img_free, 1)) return false;
 #pragma unroll
-            for (int k = 0; k < KH; k += 8) {
-                const int key = part * KH + k;
-                const uint32_t o = chunk_addr(base + kRevOffImg + static_cast<uint32_t>(key >> 6) * 2 * kTile, v, (key & 63) >> 3);
-                const uint4 hi = lds128(o), lo = lds128(o + 4 * kTile);
-                const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const f32x2 d = S[k / 2 + e];
-                    dot = fmaf(d.x, lo_f(hw[e]) + lo_f(lw[e]), dot);
-                    dot = fmaf(d.y, hi_f(hw[e]) + hi_f(lw[e]), dot);
-                }
-            }
-            if (!row_in) dot = 0.0f;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            if (lane == 0) reinterpret_cast<float*>(gbase + kRevOffDot)[warp] = dot;
-#pragma unroll
-            for (int k = 0; k < KH; k += 16)   // (a thread's own values' places)
+            for (int k = 0; k < KH; k += 16)
                 stage_terms(base + kRevOffImg, base + kRevOffImg + 4 * kTile, v, part * KH + k, S + k / 2);
             fence_proxy_async_smem();
             arrive_warp(&bar->img_full);
@@ -304,27 +265,33 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 arrive_warp(&bar->s_ready[1]);
                 // (the zero rows of other warps' share are visible behind the product's own barrier)
             }
-            ok = meet_state(n);
+            ok = keep_state(n);
             if (!ok) break;
             ok = wait_warp(&bar->full[s], (n >> 1) & 1) && wait_warp(&bar->o_full, par);
             const uint32_t ot = kRevOffO;
             if (!ok) break;
             f32x2 x[8];
-            if (!(n == 0 && ragged)) {   // scale e^G dO (in a ragged chunk once every warp's zero rows are written)
+            uint32_t third[8];           // of scale e^G dO, until R's columns are free
+            auto scaled_do = [&]() {
+                f32x2 q[8];
+                uint32_t hi[8], lw[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = pk2(val(ot, 2 * e), val(ot, 2 * e + 1));
-                scale16(x, sc.qe + kTok * part);
-                store_terms(tl + kRevO + kTok * part, x);
-            }
+                for (int e = 0; e < 8; ++e) q[e] = pk2(val(ot, 2 * e), val(ot, 2 * e + 1));
+                scale16(q, sc.qe + kTok * part);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    hi[e] = pk(q[e].x, q[e].y);
+                    split2(fma2(pk2(lo_f(hi[e]), hi_f(hi[e])), pk2(-1.0f, -1.0f), q[e]), lw[e], third[e]);
+                }
+                tmem_st8(tl + kRevO + kTok * part, hi);
+                tmem_st8(tl + kRevO + kTok * part + 8, lw);
+            };
+            // (in a ragged chunk once every warp's zero rows are written)
+            if (!(n == 0 && ragged)) scaled_do();
             ok = wait_warp(&bar->ks, par);
             if (!ok) break;
             tc_fence_after();
-            if (n == 0 && ragged) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = pk2(val(ot, 2 * e), val(ot, 2 * e + 1));
-                scale16(x, sc.qe + kTok * part);
-                store_terms(tl + kRevO + kTok * part, x);
-            }
+            if (n == 0 && ragged) scaled_do();
             {
                 f32x2 w[8];
                 tmem_ld16(tl + kRevA + kTok * part, x);
@@ -336,6 +303,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = add2(x[e], w[e]);
             }
+            tmem_st8(tl + kRevR + kTok * part, third);
             store_terms(tl + kRevA + kTok * part, x);
             tmem_wait_st();
             tc_fence_before();
@@ -356,13 +324,13 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                     w[e] = x[e];
                 }
                 scale16(w, sc.ek + kTok * part);
-                store_terms(tl + kRevV + kTok * part, w);
+                store_terms3(tl + kRevV + kTok * part, tl + kRevV + kC + kTok * part, w);
             }
             const float end = sc.end[0];
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(&bar->w_ready);
-            ok = wait_warp(&bar->img_free, par);   // dV's terms, once dS's have left, while dS is multiplied
+            ok = wait_warp(&bar->img_free, 0);   // dV's terms, store 2 n + 1, while dS is multiplied
             if (!ok) break;
             stage_terms(base + kRevOffImg, base + kRevOffImg + 2 * kTile, v, kTok * part, x);
             fence_proxy_async_smem();
@@ -386,7 +354,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             tmem_wait_st();
             tc_fence_before();
         }
-        if (ok) ok = meet_state(nchunk);
+        if (ok) ok = keep_state(nchunk);
         if (ok && p.dinit && row_in) {
 #pragma unroll
             for (int k = 0; k < KH; k += 4)
@@ -401,7 +369,6 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             mbar_wait_bounded(&bar->full[n & 1], (n >> 1) & 1, p.drain_ns);
         if (o_issued) mbar_wait_bounded(&bar->o_full, (o_issued - 1) & 1, p.drain_ns);
     }
-    if (warp == kStoreWarp && lane == 0 && s_issued) mbar_wait_bounded(&bar->s_in, (s_issued - 1) & 1, p.drain_ns);
     if (tid == 32 * kMmaWarp) {
         umma_commit(&bar->fin);
         mbar_wait_bounded(&bar->fin, 0, p.drain_ns);
@@ -643,9 +610,36 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
             }
             umma_commit(&bar->m1);
         }
+        {   // <S, dS> of the entering state: S's terms here, dS's in memory, quad by quad in the images' common order
+            const unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
+            float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 2
+            for (int w = 0; w < 4 * KB; ++w) {
+                const uint32_t o = 16u * (tid + kGradThreads * w);
+                const uint4 dh = *reinterpret_cast<const uint4*>(kp + kKeepD + o), dl = *reinterpret_cast<const uint4*>(kp + kKeepDlo + o);
+                const uint4 sh = lds128(base + kGS + o), sl = lds128(base + kGS + 4 * kTile + o);
+                if (static_cast<int>((o >> 7) & 127) >= p.dv) continue;
+                const uint32_t a[4] = {dh.x, dh.y, dh.z, dh.w}, b2[4] = {dl.x, dl.y, dl.z, dl.w};
+                const uint32_t e2[4] = {sh.x, sh.y, sh.z, sh.w}, f[4] = {sl.x, sl.y, sl.z, sl.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s0 = fmaf(lo_f(a[e]) + lo_f(b2[e]), lo_f(e2[e]) + lo_f(f[e]), s0);
+                    s1 = fmaf(hi_f(a[e]) + hi_f(b2[e]), hi_f(e2[e]) + hi_f(f[e]), s1);
+                }
+            }
+            s0 += s1;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+            if (lane == 0) red[warp] = s0;
+        }
         if (!wait_all(&bar->m1, par)) break;   // S and dV's lo terms are read
         if (tid == 0) {
-            load_states(item, kKeepD, kKeepDlo, &bar->d);
+            float s = 0.0f;
+            for (int w = 0; w < 8; ++w) s += red[w];
+            p.dots[4 * plane + item * (p.nchunks + 1) + c] = s;
+        }
+        if (tid == 0) {
+            load_states(item, kKeepBytes + kKeepD, kKeepBytes + kKeepDlo, &bar->d);   // the leaving state's
             stage = 4 * j + 3;
         }
 #pragma unroll

@@ -18,9 +18,10 @@
 // state's warps, set the pace: 8 700 cycles a chunk.
 //
 // Precision: q, k, v are bf16 values as given and unit lengths are factors of rows and columns, so they enter
-// exactly.  fp32 operands -- S, X, T, W, P, E -- enter as two bf16 terms, hi + lo (the product of two such pairs
-// without lo·lo): 16 bits, an error near 2^-18 a product.  One term for P and E would do for y's own rounding,
-// but not where keys repeat: the corrections are then differences of values, and P E cancels most of them.
+// exactly.  fp32 operands -- S, X, T, P, E -- enter as two bf16 terms, hi + lo, of 16 bits, and W as three: what the
+// terms of W miss goes straight into the state (2.4e-6 of it on average with two), while S, X and T reach it through
+// products that the decay and the corrections make small (3e-7 together).  One term for P and E would do for y's own
+// rounding, but not where keys repeat: the corrections are then differences of values, and P E cancels most of them.
 // Accumulation is fp32, the state is kept in fp32 registers.
 #pragma once
 
@@ -74,8 +75,8 @@ constexpr uint32_t kRecLocal = kRecBytes, kRecBwdBytes = kRecBytes + 2048;
 static_assert(sizeof(Local) <= 2048, "record");
 
 // What the backward pass keeps of a chunk, beside its record: images of tiles in the swizzled layout of the MMAs, each
-// value as two bf16 terms.  Eᵀ, dVᵀ: [128 rows v][64 tokens]; S (entering), dS (of the leaving state): [128 rows v]
-// [d_k keys].
+// value as two bf16 terms.  Eᵀ, dVᵀ: [128 rows v][64 tokens]; S, the state that enters the chunk, and dS, its adjoint:
+// [128 rows v][d_k keys].  (The state that leaves the last chunk has a place behind it.)
 constexpr uint32_t kKeepE = 0, kKeepElo = 2 * kTile, kKeepV = 4 * kTile, kKeepVlo = 6 * kTile;
 constexpr uint32_t kKeepS = 8 * kTile, kKeepSlo = 12 * kTile, kKeepD = 16 * kTile, kKeepDlo = 20 * kTile;
 constexpr uint32_t kKeepBytes = 24 * kTile;
@@ -85,6 +86,11 @@ struct Params {
     unsigned char* rec;      // [items][nchunks] records
     int64_t nchunks;         // chunks of g.L tokens
     uint32_t rec_bytes;      // from record to record
+    // time segments: items n_whole .. are cut into nseg segments of cseg chunks
+    int n_whole, nseg, cseg;
+    float* seg_in;           // [cut items][nseg - 1][d_v][d_k]: the states that enter the segments 1 ..
+    float* seg_loc;          // [cut items][nseg - 1][d_v][d_k]: a segment's end from a zero (segment 0: the entering) state
+    float* seg_map;          // [cut items][nseg - 1][d_k][d_k]: its end from the unit matrix, without values
     // backward pass
     unsigned char* keep;     // [items][nchunks + 1]
     float* dots;             // [4][items][nchunks * 64] of each token, then [items][nchunks + 1]: <S, dS> of the
@@ -163,6 +169,19 @@ __device__ __forceinline__ void store_terms(uint32_t taddr, const f32x2* v) {
     for (int e = 0; e < 8; ++e) split2(v[e], hi[e], lo[e]);
     tmem_st8(taddr, hi);
     tmem_st8(taddr + 8, lo);
+}
+// The same in three terms, the third in the first 8 columns of `third`.
+__device__ __forceinline__ void store_terms3(uint32_t taddr, uint32_t third, const f32x2* v) {
+    uint32_t hi[8], lo[8], th[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        hi[e] = pk(v[e].x, v[e].y);
+        const f32x2 r = fma2(pk2(lo_f(hi[e]), hi_f(hi[e])), pk2(-1.0f, -1.0f), v[e]);
+        split2(r, lo[e], th[e]);
+    }
+    tmem_st8(taddr, hi);
+    tmem_st8(taddr + 8, lo);
+    tmem_st8(third, th);
 }
 // v *= f, 16 consecutive factors of shared memory (16-byte aligned).
 __device__ __forceinline__ void scale16(f32x2 (&v)[8], const float* f) {
@@ -591,7 +610,7 @@ constexpr int kThreads = 32 * (kStoreWarp + 1);
 constexpr int kTok = kC / kParts;      // tokens of a state thread
 constexpr int kStages = 2;             // chunks in flight
 
-// TMEM columns.  A: KS, then X's terms over it, then W's; B: E in two halves, then its terms over the first; S: the
+// TMEM columns.  A: KS, then X's terms over it, then W's (W's third over QS); B: E in two halves, then its terms over the first; S: the
 // state's terms (of each 16 keys, hi then lo), then dS over them; Y: in two halves.
 constexpr uint32_t kColS = 0, kColA = 128, kColQS = 192, kColB = 256, kColY = 384;
 constexpr uint32_t kTmemCols = 512;
@@ -638,8 +657,11 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 256, "barrier region");
 
-// Grid: one CTA per (b, h).  Y false: the backward pass's forward half.  There is no y, and with it no QS and no
-// product with P; E and the entering state's terms of every chunk are kept.
+// Y: CTAs 0 .. n_whole - 1 run the items 0 .. n_whole - 1 whole, the others a segment each, from the state that
+// enters it.  Y false: there is no y, and with it no QS and no product with P.  With p.keep it is the backward pass's
+// forward half, one CTA per item, and E and the entering state's terms of every chunk are kept; else it is the state
+// pass over the cut items' segments but the last.  A segment's end is S_in M + S_loc, row by row: S_loc is its end from
+// a zero state, and M its end from the unit matrix without values, a run of its own (the segment 0 needs none).
 template <int DK, bool Y>
 __global__ void __launch_bounds__(kThreads, 1)
 ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_q,
@@ -656,11 +678,28 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const GdrParams& g = p.g;
-    const int item = blockIdx.x, b = item / g.H, h = item % g.H, hk = h / (g.H / g.Hk);
+    int item = blockIdx.x, sg = 0, nseg = 1;
+    bool unit = false;                // a segment's map: from the unit matrix, without values
+    if (!Y && !p.keep) {
+        const int per = 2 * p.nseg - 3, x = item % per;
+        item = p.n_whole + item / per;
+        sg = x < p.nseg - 1 ? x : x - (p.nseg - 1) + 1;
+        unit = x >= p.nseg - 1;
+        nseg = p.nseg;
+    } else if (Y && item >= p.n_whole) {
+        const int x = item - p.n_whole;
+        item = p.n_whole + x / p.nseg;
+        sg = x % p.nseg;
+        nseg = p.nseg;
+    }
+    const int b = item / g.H, h = item % g.H, hk = h / (g.H / g.Hk);
+    const int rows = unit ? DK : p.dv;
     const int64_t len = gdr_len(g, b);
-    const int nchunk = static_cast<int>((len + kC - 1) / kC);
+    const int64_t all = (len + kC - 1) / kC, c0 = static_cast<int64_t>(sg) * (nseg > 1 ? p.cseg : 0);
+    const int nchunk = static_cast<int>(max(int64_t{0}, (nseg > 1 ? min(all - c0, static_cast<int64_t>(p.cseg)) : all)));
+    const int cbase = static_cast<int>(c0);   // chunk c of this CTA is the sequence's cbase + c
     // the last chunk of a sequence that ends before the tensor does: other tokens follow in its tile
-    const int ragged = (len % kC != 0 && len < g.L) ? nchunk - 1 : -1;
+    const int ragged = (len % kC != 0 && len < g.L) ? static_cast<int>(all - 1 - c0) : -1;
     const uint64_t lim = p.wait_ns;
 
     if (tid == 0) {
@@ -714,14 +753,15 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 if (c >= kStages && !wait1(&bar->empty[s], ((c / kStages) - 1) & 1)) break;
                 const uint32_t st = base + s * M::kStage;
                 uint64_t* f = &bar->full[s];
-                mbar_arrive_expect_tx(f, (Y ? 2 : 1) * KB * kTile + kC * p.dv * 2 + (M::kStage - M::kRec));
+                mbar_arrive_expect_tx(f, (Y ? 2 : 1) * KB * kTile + (unit ? 0 : kC * p.dv * 2) + (M::kStage - M::kRec));
+                const int t0 = (cbase + c) * kC;
                 for (int kb = 0; kb < KB; ++kb) {
-                    tma_load_4d(st + kb * M::kPair, &tm_k, 64 * kb, hk, c * kC, b, f);
-                    if (Y) tma_load_4d(st + kb * M::kPair + kTile, &tm_q, 64 * kb, hk, c * kC, b, f);
+                    tma_load_4d(st + kb * M::kPair, &tm_k, 64 * kb, hk, t0, b, f);
+                    if (Y) tma_load_4d(st + kb * M::kPair + kTile, &tm_q, 64 * kb, hk, t0, b, f);
                 }
-                for (int vb = 0; vb < p.dv / 64; ++vb)
-                    tma_load_4d(st + M::kV + vb * kTile, &tm_v, 64 * vb, h, c * kC, b, f);
-                const unsigned char* r = p.rec + (item * p.nchunks + c) * p.rec_bytes;
+                for (int vb = 0; !unit && vb < p.dv / 64; ++vb)
+                    tma_load_4d(st + M::kV + vb * kTile, &tm_v, 64 * vb, h, t0, b, f);
+                const unsigned char* r = p.rec + (item * p.nchunks + cbase + c) * p.rec_bytes;
                 if (Y) {
                     bulk_load(st + M::kRec, r, kRecBytes, f);
                 } else {
@@ -734,7 +774,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         __syncwarp();
     } else if (warp == kStoreWarp) {
         // ============================================================ y, or what is kept
-        for (int n = 0; !Y && n < 2 * nchunk + 1; ++n) {   // S of chunk n / 2, then its E; at last the final state
+        for (int n = 0; !Y && p.keep && n < 2 * nchunk + 1; ++n) {   // S of chunk n / 2, then its E; at last the final state
             if (!wait_warp(&bar->y_full, n & 1)) break;
             if (lane == 0) {
                 unsigned char* kp = p.keep + (item * (p.nchunks + 1) + (n >> 1)) * kKeepBytes;
@@ -752,12 +792,12 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             if (!wait_warp(&bar->y_full, c & 1)) break;
             if (c != ragged) {   // rows behind the tensor's end are clipped by the copy
                 if (lane == 0) {
-                    tc::tma_store_4d(&tm_y, base + M::kOut, 0, h, c * kC, b);
+                    tc::tma_store_4d(&tm_y, base + M::kOut, 0, h, (cbase + c) * kC, b);
                     tc::bulk_commit();
                     tc::bulk_wait_read0();
                 }
             } else {             // rows behind the sequence's end stay as they are
-                const int64_t t0 = static_cast<int64_t>(c) * kC;
+                const int64_t t0 = static_cast<int64_t>(cbase + c) * kC;
                 const int quads = p.dv / 8, n = static_cast<int>(len - t0) * quads;
                 __nv_bfloat16* y = static_cast<__nv_bfloat16*>(g.y);
                 for (int i = lane; i < n; i += 32) {
@@ -800,7 +840,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 if (Y && c > 0 && !wait1(&bar->pv, (c - 1) & 1)) break;
                 tc_fence_after();
 #pragma unroll
-                for (int j = 0; j < kC / 16; ++j)
+                for (int j = 0; j < (unit ? 0 : kC / 16); ++j)
                     umma(tmem + kColB, sdesc(st + M::kV + 2048u * j, vlbo, 1024), sdesc(pr + kRecT + 32u * j, 16, 1024),
                          idesc(2 * kC, false, true), j > 0);
                 if (!wait1(&bar->x_ready, par)) break;
@@ -809,19 +849,19 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
 #pragma unroll
                 for (int j = 0; j < kC / 16; ++j) {
                     const uint64_t bd = sdesc(pr + kRecT + 32u * j, 16, 1024);
-                    umma_ts(tmem + kColB, tmem + kColA + 16 * j, bd, idesc(2 * kC, false), 1);
-                    umma_ts(tmem + kColB, tmem + kColA + 16 * j + 8, bd, idesc(kC, false), 1);
+                    umma_ts(tmem + kColB, tmem + kColA + 16 * j, bd, idesc(2 * kC, false), unit && j == 0 ? 0 : 1);
+                    umma_ts(tmem + kColB, tmem + kColA + 16 * j + 8, bd, idesc(2 * kC, false), 1);
                 }
                 umma_commit(&bar->e);
                 if (!wait1(&bar->w_ready, par)) break;
                 tc_fence_after();
-                // dS = W K over the columns of S's terms
+                // dS = W K over the columns of S's terms, W's third terms (in QS's place) first
 #pragma unroll
-                for (int j = 0; j < kC / 16; ++j) {
-                    const uint64_t bd = sdesc(st + 2048u * j, M::kPair, 1024);
-                    umma_ts(tmem + kColS, tmem + kColA + 16 * j, bd, idesc(DK, true), j > 0);
-                    umma_ts(tmem + kColS, tmem + kColA + 16 * j + 8, bd, idesc(DK, true), 1);
-                }
+                for (int w = 0; w < 3; ++w)
+#pragma unroll
+                    for (int j = 0; j < kC / 16; ++j)
+                        umma_ts(tmem + kColS, tmem + (w == 0 ? kColQS : w == 1 ? kColA + 8 : kColA) + 16 * j,
+                                sdesc(st + 2048u * j, M::kPair, 1024), idesc(DK, true), w + j > 0);
                 umma_commit(&bar->ds);
                 if (Y) {   // Yᵀ += E Pᵀ
                     if (!wait1(&bar->e_ready, par)) break;
@@ -830,7 +870,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                     for (int j = 0; j < kC / 16; ++j) {
                         const uint64_t bd = sdesc(pr + kRecP + 32u * j, 16, 1024);
                         umma_ts(tmem + kColY, tmem + kColB + 16 * j, bd, idesc(2 * kC, false), 1);
-                        umma_ts(tmem + kColY, tmem + kColB + 16 * j + 8, bd, idesc(kC, false), 1);
+                        umma_ts(tmem + kColY, tmem + kColB + 16 * j + 8, bd, idesc(2 * kC, false), 1);
                     }
                     umma_commit(&bar->pv);
                 }
@@ -841,14 +881,25 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
     } else {
         // ============================================================ state warps
         const int v = (warp & 3) * 32 + lane, part = warp >> 2;
-        const bool row_in = v < p.dv;
+        const bool row_in = v < rows;
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const int64_t srow = (static_cast<int64_t>(item) * p.dv + v) * DK + part * KH;
+        // the entering state: the call's, a segment's, zero or the unit matrix; and where the leaving one goes
+        const int64_t cut = static_cast<int64_t>(item - p.n_whole) * (p.nseg - 1);
+        const float* from = sg == 0 ? (g.h_init ? g.h_init + srow : nullptr)
+                          : Y       ? p.seg_in + ((cut + sg - 1) * p.dv + v) * DK + part * KH : nullptr;
+        float* to = nullptr;
+        if (!Y && !p.keep) to = unit ? p.seg_map + ((cut + sg) * DK + v) * DK + part * KH : p.seg_loc + ((cut + sg) * p.dv + v) * DK + part * KH;
+        else if (g.final_state && sg == nseg - 1) to = g.final_state + srow;
         f32x2 S[KH / 2];
 #pragma unroll
         for (int k = 0; k < KH; k += 4) {
             float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (g.h_init && row_in) q = quad(g.h_init + srow + k);
+            if (from && row_in) q = quad(from + k);
+            if (unit) {
+                const int d = v - (part * KH + k);
+                q = make_float4(d == 0, d == 1, d == 2, d == 3);
+            }
             S[k / 2] = pk2(q.x, q.y);
             S[k / 2 + 1] = pk2(q.z, q.w);
         }
@@ -894,10 +945,10 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             if (c == ragged) {   // rows of K and V behind the end, whatever they hold, become zero rows
                 ok = wait_warp(&bar->full[s], (c / kStages) & 1);
                 if (!ok) break;
-                const int n0 = static_cast<int>(len - static_cast<int64_t>(c) * kC);
+                const int n0 = static_cast<int>(len - static_cast<int64_t>(cbase + c) * kC);
                 for (int i = n0 * 8 + tid; i < kC * 8; i += 32 * kStateWarps) {
                     for (int kb = 0; kb < KB; ++kb) sts128(st + kb * M::kPair + 16 * i, make_uint4(0, 0, 0, 0));
-                    for (int vb = 0; vb < p.dv / 64; ++vb) sts128(st + M::kV + vb * kTile + 16 * i, make_uint4(0, 0, 0, 0));
+                    for (int vb = 0; !unit && vb < p.dv / 64; ++vb) sts128(st + M::kV + vb * kTile + 16 * i, make_uint4(0, 0, 0, 0));
                 }
                 fence_proxy_async_smem();
             }
@@ -905,7 +956,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 arrive_warp(&bar->s_ready[0]);
                 arrive_warp(&bar->s_ready[1]);
             }
-            if (!Y) {
+            if (!Y && p.keep) {
                 ok = keep_state(c);
                 if (!ok) break;
             }
@@ -945,7 +996,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = x[e];
                 scale16(w, sc.wk + kTok * part);
-                store_terms(tl + kColA + kTok * part, w);
+                store_terms3(tl + kColA + kTok * part, tl + kColQS + kTok * part, w);
             }
             const float end = sc.end[0];
             tmem_wait_st();
@@ -956,7 +1007,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 tmem_wait_st();
                 tc_fence_before();
                 arrive_warp(&bar->e_ready);
-            } else {
+            } else if (p.keep) {
                 ok = wait_warp(&bar->y_free, 0);   // its S, store 2 c
                 if (!ok) break;
                 stage_terms(base + M::kOut, base + M::kOut + 2 * kTile, v, kTok * part, x);
@@ -983,11 +1034,11 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             tc_fence_before();
         }
         if (Y && ok && nchunk > 0) ok = finish_y(nchunk - 1);
-        if (!Y && ok) ok = keep_state(nchunk);
-        if (ok && g.final_state && row_in) {
+        if (!Y && p.keep && ok) ok = keep_state(nchunk);
+        if (ok && to && row_in) {
 #pragma unroll
             for (int k = 0; k < KH; k += 4)
-                *reinterpret_cast<float4*>(g.final_state + srow + k) =
+                *reinterpret_cast<float4*>(to + k) =
                     make_float4(S[k / 2].x, S[k / 2].y, S[k / 2 + 1].x, S[k / 2 + 1].y);
         }
         tc_fence_before();
@@ -1009,6 +1060,87 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         tc_fence_after();
         tc::tmem_dealloc(tmem, kTmemCols);
     }
+}
+
+// The states that enter the segments 1 .. nseg - 1 of the cut items: S_in(1) is the end of segment 0, and
+// S_in(s + 1) = S_in(s) M_s + S_loc(s), in fp32.  A chain over the segments, so the next map is copied to shared memory
+// under the product with this one; a thread has two rows of four keys, a warp whole rows.
+template <int DK>
+struct FoldSmem {
+    static constexpr int kRows = 8 * 2 * (128 / DK);   // rows of S per block of 256 threads
+    alignas(128) float map[2][DK * DK];
+    float row[kRows][DK];
+    uint64_t full[2];
+};
+template <int DK>
+__global__ void __launch_bounds__(256) ss_gdr_fold_kernel(const __grid_constant__ Params p) {
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    FoldSmem<DK>& sm = *reinterpret_cast<FoldSmem<DK>*>(smem_raw);
+    constexpr int Q = DK / 4;   // quads of a row
+    const int64_t it = static_cast<int64_t>(blockIdx.x) * (p.nseg - 1);
+    const int lane = threadIdx.x & 31, c = (lane % Q) * 4;
+    const int r0 = ((threadIdx.x >> 5) * (32 / Q) + lane / Q) * 2;   // rows r0, r0 + 1 of the block
+    const int64_t v0 = static_cast<int64_t>(blockIdx.y) * FoldSmem<DK>::kRows + r0;
+    constexpr uint32_t bytes = DK * DK * sizeof(float);
+    if (threadIdx.x == 0) {
+        mbar_init(&sm.full[0], 1);
+        mbar_init(&sm.full[1], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    auto fetch = [&](int seg) {
+        if (threadIdx.x != 0 || seg >= p.nseg - 1) return;
+        mbar_arrive_expect_tx(&sm.full[seg & 1], bytes);
+        bulk_load(smem_u32(sm.map[seg & 1]), p.seg_map + (it + seg) * DK * DK, bytes, &sm.full[seg & 1]);
+    };
+    fetch(1);
+    fetch(2);
+    auto at_state = [&](float* base, int seg, int r) { return base + ((it + seg) * p.dv + v0 + r) * DK + c; };
+    f32x2 s[2][2];
+    auto load_loc = [&](int seg) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float4 q = quad(at_state(p.seg_loc, seg, r));
+            s[r][0] = pk2(q.x, q.y);
+            s[r][1] = pk2(q.z, q.w);
+        }
+    };
+    auto store_in = [&](int seg) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            *reinterpret_cast<float4*>(at_state(p.seg_in, seg, r)) = make_float4(s[r][0].x, s[r][0].y, s[r][1].x, s[r][1].y);
+    };
+    load_loc(0);
+    store_in(0);
+    for (int seg = 1; seg < p.nseg - 1; ++seg) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            *reinterpret_cast<float4*>(&sm.row[r0 + r][c]) = make_float4(s[r][0].x, s[r][0].y, s[r][1].x, s[r][1].y);
+        load_loc(seg);
+        __syncwarp();   // (a row is one warp's)
+        // (segments seg use buffer seg & 1 from 1 on: buffer 1 first, in its phase 0)
+        const bool got = mbar_wait_bounded(&sm.full[seg & 1], ((seg - 1) >> 1) & 1, p.wait_ns);
+        if (!got && threadIdx.x == 0 && p.status) atomicCAS(p.status, 0u, static_cast<uint32_t>(SS_ERR_TIMEOUT));
+        const float* m = sm.map[seg & 1] + c;
+#pragma unroll 4
+        for (int k = 0; k < DK; k += 4) {
+            const float4 a = quad(&sm.row[r0][k]), b = quad(&sm.row[r0 + 1][k]);
+            const float aa[4] = {a.x, a.y, a.z, a.w}, bb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 q = quad(m + (k + e) * DK);
+                axpy4(s[0], aa[e], q);
+                axpy4(s[1], bb[e], q);
+            }
+        }
+        store_in(seg);
+        __syncthreads();   // the map is read
+        fetch(seg + 2);
+    }
+    // what is still in flight lands before the shared memory goes (after a wait that ran out)
+    if (threadIdx.x == 0)
+        for (int seg = max(1, p.nseg - 3); seg < p.nseg - 1; ++seg)
+            mbar_wait_bounded(&sm.full[seg & 1], ((seg - 1) >> 1) & 1, p.drain_ns);
 }
 
 }  // namespace gdr

@@ -188,10 +188,52 @@ def test_bounded_wait_reports_timeout_and_context_survives():
     """A hand-over that is never signalled (SS_TEST_DROP_CARRY: the first block's first product) runs the bounded
     waits out: the call reports SS_ERR_TIMEOUT, and the next call on the same context is right."""
     x = gdr_inputs(2, 300, 2, 2, 128, 128, seed=5)
-    need = ss.lib().ss_gdr_fwd_workspace_bytes(ctypes.byref(ss.ss_gdr_dims(2, 300, 2, 2, 128, 128)), ss.SS_BF16)
+    need = ss.lib().ss_gdr_fwd_workspace_bytes(ctypes.byref(ss.ss_gdr_dims(2, 300, 2, 2, 128, 128)), ss.SS_BF16, 0)
     ws = torch.zeros(need, dtype=torch.uint8, device="cuda:0")
     ss.ss_gdr_fwd(*call_args(x), dt_bias=x["dt_bias"], workspace=ws, timeout_iters=200,
                   extra_flags=ss.SS_TEST_DROP_CARRY)
     assert ss.ss_check(ws) == ss.SS_ERR_TIMEOUT
     check(x, 300, BF, workspace=ws)
     assert ss.ss_check(ws) == ss.SS_OK
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("L,seg", [(130, 64), (320, 128), (1000, 64), (700, 200)])
+def test_time_segments(L, seg, dk, dv):
+    """Forced segments (2 to 16): a state pass, the fold and the segments from their entering states."""
+    x = gdr_inputs(2, L, 4, 2, dk, dv, seed=L + dk, init=dv == 64)
+    check(x, L, BF, chunk_len=seg)
+
+
+def test_time_segments_of_a_padded_batch():
+    """Segments behind a sequence's end pass its state on."""
+    lens = [600, 0, 1, 64, 300, 599]
+    x = gdr_inputs(6, 600, 2, 2, 128, 128, seed=4, init=True)
+    for b, n in enumerate(lens):
+        for name in ("q", "k", "v", "dt", "beta"):
+            x[name][b, n:] = np.nan
+    y = torch.full_like(x["v"], 7.0)
+    lt = torch.tensor(lens, dtype=torch.int32, device="cuda:0")
+    y, S = ss.ss_gdr_fwd(*call_args(x), dt_bias=x["dt_bias"], initial_state=x["state"], seqlens=lt, y=y, chunk_len=128,
+                         sync_check=True)
+    yr, Sr = oracle_fwd(x, 128 ** -0.5, np.array(lens), **OPT)
+    for b, n in enumerate(lens):
+        assert bool((y[b, n:] == 7.0).all())
+        assert max_err(y[b, :n], yr[b, :n]) <= y_tol(600, BF)
+    assert max_err(S, Sr) <= state_tol(600, BF)
+    assert rms_err(S, Sr) <= 1e-5
+
+
+def test_segments_of_the_last_wave():
+    """More items than SMs: those of the last wave are cut, the others run whole; all give the whole sequence's
+    results (which the oracle checks elsewhere)."""
+    x = gdr_inputs(20, 512, 8, 4, 64, 64, seed=6)
+    y, S = ss.ss_gdr_fwd(*call_args(x), dt_bias=x["dt_bias"], sync_check=True)
+    st = None
+    ys = []
+    for i in range(0, 512, 64):   # token pieces of one chunk: no segments
+        part = [t[:, i:i + 64].contiguous() if t.dim() > 1 else t for t in call_args(x)]
+        yy, st = ss.ss_gdr_fwd(*part, dt_bias=x["dt_bias"], initial_state=st)
+        ys.append(yy)
+    assert rms_err(S, st.double().cpu().numpy()) <= 1e-5
+    assert max_err(y, torch.cat(ys, 1).double().cpu().numpy()) <= 2 * y_tol(512, BF)

@@ -36,7 +36,7 @@ BAD_DIMS = [((-1, 64, 4, 2, 128, 64), ss.SS_ERR_INVALID_ARG), ((2, -1, 4, 2, 128
 @pytest.mark.parametrize("dims,want", BAD_DIMS)
 def test_gdr_sizes_are_refused(L, dims, want):
     assert fwd(L, dims) == want
-    assert L.ss_gdr_fwd_workspace_bytes(ctypes.byref(ss.ss_gdr_dims(*dims)), ss.SS_BF16) == 0
+    assert L.ss_gdr_fwd_workspace_bytes(ctypes.byref(ss.ss_gdr_dims(*dims)), ss.SS_BF16, 0) == 0
 
 
 def test_gdr_fwd_refusals(L):
