@@ -185,7 +185,7 @@ def status_string(status: int) -> str:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()   # (a c_void_p argument takes the number)
 
 
 def _io_flag(t):
@@ -201,6 +201,8 @@ def _check(t, name, shape, dtype, device):
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return   # (small calls spend more time here than on the GPU)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
@@ -237,7 +239,8 @@ def clear_workspaces():
 
 def _stream_handle(stream, device):
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        index = torch.cuda.current_device() if device.index is None else device.index
+        return torch._C._cuda_getCurrentRawStream(index)   # torch.cuda.current_stream() without its object
     return stream.cuda_stream
 
 

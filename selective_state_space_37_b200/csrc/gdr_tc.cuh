@@ -402,8 +402,9 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
     const GdrParams& g = p.g;
     const int pt = threadIdx.x, lane = pt & 31, warp = pt >> 5, i = pt & 63, rb = warp & 1;   // row i, its 32-block
     const bool is_q = pt >= 64;
-    const int64_t item = blockIdx.x / p.nchunks, c = blockIdx.x % p.nchunks;
-    const int b = static_cast<int>(item / g.H), h = static_cast<int>(item % g.H), hk = h / (g.H / g.Hk);
+    const uint32_t nch = static_cast<uint32_t>(p.nchunks), H = static_cast<uint32_t>(g.H);   // (32-bit quotients)
+    const int64_t item = blockIdx.x / nch, c = blockIdx.x % nch;
+    const int b = static_cast<int>(blockIdx.x / nch / H), h = static_cast<int>(blockIdx.x / nch % H), hk = h / (g.H / g.Hk);
     const int64_t left = gdr_len(g, b) - c * kC;
     if (left <= 0) return;
     const int valid = left < kC ? static_cast<int>(left) : kC;
@@ -1074,7 +1075,7 @@ struct FoldSmem {
 };
 template <int DK>
 __global__ void __launch_bounds__(256) ss_gdr_fold_kernel(const __grid_constant__ Params p) {
-    extern __shared__ __align__(128) unsigned char smem_raw[];
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
     FoldSmem<DK>& sm = *reinterpret_cast<FoldSmem<DK>*>(smem_raw);
     constexpr int Q = DK / 4;   // quads of a row
     const int64_t it = static_cast<int64_t>(blockIdx.x) * (p.nseg - 1);

@@ -108,6 +108,48 @@ __device__ __forceinline__ void store_vec(IO* row, int64_t cols, int s, int t, i
     }
 }
 
+// The same, kept as it was loaded until it is used (so that the load's latency stays off the row it is fetched in).
+template <typename IO>
+struct RawVec {
+    uint32_t w[4];
+};
+template <typename IO, bool VEC>
+__device__ __forceinline__ void load_raw(const IO* row, int64_t cols, int s, int t, int T, RawVec<IO>& v) {
+    constexpr int N = VecOf<IO>::kN;
+    if (VEC) {
+        const int64_t c = col_of<IO, true>(s, 0, t, T);
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (c < cols) w = *reinterpret_cast<const uint4*>(row + c);
+        v.w[0] = w.x;
+        v.w[1] = w.y;
+        v.w[2] = w.z;
+        v.w[3] = w.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int64_t c = col_of<IO, false>(s, e, t, T);
+            if (sizeof(IO) == 2) {
+                const uint32_t b = c < cols ? reinterpret_cast<const unsigned short*>(row)[c] : 0u;
+                v.w[e >> 1] = (e & 1) ? v.w[e >> 1] | (b << 16) : b;
+            } else {
+                v.w[e & 3] = c < cols ? reinterpret_cast<const uint32_t*>(row)[c] : 0u;
+            }
+        }
+    }
+}
+template <typename IO>
+__device__ __forceinline__ void unpack_row(const RawVec<IO>& v, float (&f)[VecOf<IO>::kN]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (sizeof(IO) == 2) {
+            f[2 * e] = __uint_as_float(v.w[e] << 16);
+            f[2 * e + 1] = __uint_as_float(v.w[e] & 0xffff0000u);
+        } else {
+            f[e] = __uint_as_float(v.w[e]);
+        }
+    }
+}
+
 // fp32 parameters at a vector's columns (`other` behind the row's end or without a parameter).
 template <typename IO, bool VEC>
 __device__ __forceinline__ void load_par(const float* par, float other, int64_t cols, int s, int t, int T,
@@ -245,6 +287,101 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads) ss_norm_f
     }
 }
 
+// Forward, rows of whole 16-byte vectors that a warp holds: NV vectors per lane, all loaded before the first is used,
+// no barrier; the parameters lie in shared memory (their vectors' quads in planes, so that a warp's reads are
+// consecutive), loaded once by a block that walks rows.  32768 x 2560 bf16: see the host's choice.
+constexpr int kRowWarps = 8;
+template <typename IO, int NV>
+__global__ void __launch_bounds__(32 * kRowWarps, NV <= 8 ? 3 : 2) ss_norm_fwd_rows_kernel(const NormParams p) {
+    constexpr int N = VecOf<IO>::kN, P = N / 4;   // quads of parameters per vector
+    extern __shared__ float4 par[];               // [2][P][vecs]: weight, bias
+    const int lane = threadIdx.x & 31;
+    const int vecs = static_cast<int>(p.cols / N);
+    for (int i = threadIdx.x; i < 2 * P * vecs; i += 32 * kRowWarps) {
+        const int which = i / (P * vecs), q = (i / vecs) % P, v = i % vecs;
+        const float* src = which ? p.bias : p.weight;
+        const float other = which ? 0.0f : 1.0f;
+        par[i] = src ? reinterpret_cast<const float4*>(src)[v * P + q] : make_float4(other, other, other, other);
+    }
+    __syncthreads();
+    const float inv = 1.0f / static_cast<float>(p.cols);
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5); r < p.rows;
+         r += static_cast<int64_t>(gridDim.x) * kRowWarps) {
+        const uint4* row = reinterpret_cast<const uint4*>(static_cast<const IO*>(p.x) + r * p.cols);
+        uint4* out = reinterpret_cast<uint4*>(static_cast<IO*>(p.out) + r * p.cols);
+        uint4 raw[NV];
+#pragma unroll
+        for (int s = 0; s < NV; ++s) {
+            const int v = lane + 32 * s;
+            raw[s] = v < vecs ? __ldcs(row + v) : make_uint4(0, 0, 0, 0);
+        }
+        auto unpack = [](uint4 w, float (&f)[N]) {
+            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (sizeof(IO) == 2) {
+                    f[2 * e] = __uint_as_float(a[e] << 16);
+                    f[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
+                } else {
+                    f[e] = __uint_as_float(a[e]);
+                }
+            }
+        };
+        float f[N], sum = 0.0f, sq = 0.0f;
+#pragma unroll
+        for (int s = 0; s < NV; ++s) {
+            unpack(raw[s], f);
+            float t = 0.0f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) t += f[e];
+            sum += t;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float mu = sum * inv;
+#pragma unroll
+        for (int s = 0; s < NV; ++s) {
+            unpack(raw[s], f);
+            float t = 0.0f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) t = fmaf(f[e] - mu, f[e] - mu, t);
+            if (lane + 32 * s < vecs) sq += t;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        const float rs = 1.0f / sqrtf(fmaf(sq, inv, p.eps));
+#pragma unroll
+        for (int s = 0; s < NV; ++s) {
+            const int v = lane + 32 * s;
+            if (v >= vecs) continue;
+            unpack(raw[s], f);
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                const float4 w = par[q * vecs + v], b = par[(P + q) * vecs + v];
+                f[4 * q] = fmaf((f[4 * q] - mu) * rs, w.x, b.x);
+                f[4 * q + 1] = fmaf((f[4 * q + 1] - mu) * rs, w.y, b.y);
+                f[4 * q + 2] = fmaf((f[4 * q + 2] - mu) * rs, w.z, b.z);
+                f[4 * q + 3] = fmaf((f[4 * q + 3] - mu) * rs, w.w, b.w);
+            }
+            uint32_t a[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (sizeof(IO) == 2) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+                    a[e] = *reinterpret_cast<const uint32_t*>(&h);
+                } else {
+                    a[e] = __float_as_uint(f[e]);
+                }
+            }
+            __stcs(out + v, make_uint4(a[0], a[1], a[2], a[3]));
+        }
+        if (lane == 0) {
+            if (p.mean) p.mean[r] = mu;
+            if (p.rstd) p.rstd[r] = rs;
+        }
+    }
+}
+
 // dx, and (HELD) this block's partial sums of dw and db.  Without HELD the column sums are a kernel of their own.
 template <typename IO, bool VEC, bool WARP, bool HELD>
 __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads)
@@ -262,19 +399,34 @@ ss_norm_bwd_kernel(const NormParams p, int slots, int sums) {
 #pragma unroll
         for (int s = 0; s < kSlots; ++s) load_par<IO, VEC>(p.weight, 1.0f, C, s, t, T, w[s]);
     }
+    struct {
+        RawVec<IO> x[HELD ? kSlots : 1], g[HELD ? kSlots : 1];
+        float mu, rs;
+    } next;
+    auto fetch_row = [&](int64_t r) {
+#pragma unroll
+        for (int s = 0; s < (HELD ? kSlots : 0); ++s) {
+            load_raw<IO, VEC>(static_cast<const IO*>(p.x) + r * C, C, s, t, T, next.x[s]);
+            load_raw<IO, VEC>(static_cast<const IO*>(p.dy) + r * C, C, s, t, T, next.g[s]);
+        }
+        next.mu = p.mean[r];
+        next.rs = p.rstd[r];
+    };
+    if (HELD && first < p.rows) fetch_row(first);
     for (int64_t r = first; r < p.rows; r += step) {
         const IO* xrow = static_cast<const IO*>(p.x) + r * C;
         const IO* grow = static_cast<const IO*>(p.dy) + r * C;
         IO* out = static_cast<IO*>(p.out) + r * C;
-        const float mu = p.mean[r], rs = p.rstd[r];
+        const float mu = HELD ? next.mu : p.mean[r], rs = HELD ? next.rs : p.rstd[r];
         float x[HELD ? kSlots : 1][N], g[HELD ? kSlots : 1][N];
         float c1 = 0.0f, c2 = 0.0f;
         if (HELD) {
 #pragma unroll
             for (int s = 0; s < kSlots; ++s) {
-                load_vec<IO, VEC>(xrow, C, s, t, T, x[s]);
-                load_vec<IO, VEC>(grow, C, s, t, T, g[s]);
+                unpack_row<IO>(next.x[s], x[s]);
+                unpack_row<IO>(next.g[s], g[s]);
             }
+            if (r + step < p.rows) fetch_row(r + step);   // under this row's sums
 #pragma unroll
             for (int s = 0; s < kSlots; ++s)
 #pragma unroll
@@ -427,8 +579,22 @@ size_t norm_ws(const ss_norm_dims* dims, bool bf16) {
     return std::max<size_t>(256, static_cast<size_t>(pl.parts) * 2 * static_cast<size_t>(dims->cols) * sizeof(float));
 }
 
+// The row kernel for rows of `vecs` whole vectors, with the least NV that holds them; false if none does.
+template <typename IO, int NV, int... More>
+bool launch_rows(const NormParams& p, int64_t vecs, cudaStream_t stream) {
+    if (vecs <= 32 * NV) {
+        const size_t smem = static_cast<size_t>(p.cols) * 8;   // two parameters of 4 bytes per column, at most 32 KB
+        const int64_t blocks = ceil_div(p.rows, kRowWarps), most = 8 * sm_count_of_current_device();
+        ss_norm_fwd_rows_kernel<IO, NV><<<static_cast<unsigned>(std::min(blocks, most)), 32 * kRowWarps, smem, stream>>>(p);
+        return true;
+    }
+    if constexpr (sizeof...(More) > 0) return launch_rows<IO, More...>(p, vecs, stream);
+    return false;
+}
+
 template <typename IO, bool VEC>
 void launch_norm_fwd(const NormParams& p, const NormPlan& pl, cudaStream_t stream) {
+    if (VEC && launch_rows<IO, 1, 2, 3, 4, 6, 8, 10, 12, 16>(p, p.cols / VecOf<IO>::kN, stream)) return;
     const unsigned g = static_cast<unsigned>(pl.blocks), t = static_cast<unsigned>(pl.warp ? 32 * kWarpRows : pl.T);
     if (pl.warp) ss_norm_fwd_kernel<IO, VEC, true, true><<<g, t, 0, stream>>>(p, pl.slots);
     else if (pl.held) ss_norm_fwd_kernel<IO, VEC, false, true><<<g, t, 0, stream>>>(p, pl.slots);
