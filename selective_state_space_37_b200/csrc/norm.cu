@@ -174,29 +174,39 @@ __device__ __forceinline__ void load_par(const float* par, float other, int64_t 
     }
 }
 
-// Sums of a and b over the threads of a row (a warp, or the whole block), in every thread, in a fixed order.
+// Sums of a and b over the threads of a row (a warp, or the whole block of at most 16 warps), in every thread, in a
+// fixed order.  Behind the barrier every thread adds the warps' sums itself (a few wide reads: a second round of
+// shuffles costs more).
+struct RowSums {
+    float4 buf[2][2][4];   // two buffers: the next sum may start before every warp has read this one
+};
 template <bool WARP>
-__device__ __forceinline__ void row_sum2(float& a, float& b, float (&red)[2][2][32], int& flip) {
+__device__ __forceinline__ void row_sum2(float& a, float& b, RowSums& red, int& flip) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         a += __shfl_xor_sync(0xffffffffu, a, o);
         b += __shfl_xor_sync(0xffffffffu, b, o);
     }
     if (WARP) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
-    float (&buf)[2][32] = red[flip];   // two buffers: the next sum may start before every warp has read this one
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    float4 (&buf)[2][4] = red.buf[flip];
     flip ^= 1;
     if (lane == 0) {
-        buf[0][warp] = a;
-        buf[1][warp] = b;
+        reinterpret_cast<float*>(buf[0])[warp] = a;
+        reinterpret_cast<float*>(buf[1])[warp] = b;
+    }
+    if (threadIdx.x < 16 && threadIdx.x >= nw) {   // warps that are not there
+        reinterpret_cast<float*>(buf[0])[threadIdx.x] = 0.0f;
+        reinterpret_cast<float*>(buf[1])[threadIdx.x] = 0.0f;
     }
     __syncthreads();
-    a = lane < nw ? buf[0][lane] : 0.0f;
-    b = lane < nw ? buf[1][lane] : 0.0f;
+    a = b = 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
+    for (int q = 0; q < 4; ++q) {
+        if (4 * q >= nw) break;
+        const float4 x = buf[0][q], y = buf[1][q];
+        a += (x.x + x.y) + (x.z + x.w);
+        b += (y.x + y.y) + (y.z + y.w);
     }
 }
 
@@ -205,7 +215,7 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float (&red)[2][2][
 template <typename IO, bool VEC, bool WARP, bool HELD>
 __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads) ss_norm_fwd_kernel(const NormParams p, int slots) {
     constexpr int N = VecOf<IO>::kN, kSlots = VecOf<IO>::kSlots;
-    __shared__ float red[2][2][32];
+    __shared__ RowSums red;
     int flip = 0;
     const int T = WARP ? 32 : blockDim.x, t = WARP ? (threadIdx.x & 31) : threadIdx.x;
     const int64_t first = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
@@ -387,17 +397,25 @@ template <typename IO, bool VEC, bool WARP, bool HELD>
 __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads)
 ss_norm_bwd_kernel(const NormParams p, int slots, int sums) {
     constexpr int N = VecOf<IO>::kN, kSlots = VecOf<IO>::kSlots;
-    __shared__ float red[2][2][32];
+    __shared__ RowSums red;
     int flip = 0;
     const int T = WARP ? 32 : blockDim.x, t = WARP ? (threadIdx.x & 31) : threadIdx.x;
     const int64_t first = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
     const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * kWarpRows : gridDim.x;
     const int64_t C = p.cols;
     const float inv = 1.0f / static_cast<float>(C);
-    float w[HELD ? kSlots : 1][N], dw[HELD ? kSlots : 1][N] = {}, db[HELD ? kSlots : 1][N] = {};
+    constexpr int H = kHeld / 2;   // a thread's values as pairs
+    float w[1][N];
+    f32x2 w2[HELD ? H : 1], dw[HELD ? H : 1], db[HELD ? H : 1];
     if (HELD) {
 #pragma unroll
-        for (int s = 0; s < kSlots; ++s) load_par<IO, VEC>(p.weight, 1.0f, C, s, t, T, w[s]);
+        for (int s = 0; s < kSlots; ++s) {
+            load_par<IO, VEC>(p.weight, 1.0f, C, s, t, T, w[0]);
+#pragma unroll
+            for (int e = 0; e < N; e += 2) w2[(s * N + e) / 2] = pk2(w[0][e], w[0][e + 1]);
+        }
+#pragma unroll
+        for (int e = 0; e < H; ++e) dw[e] = db[e] = pk2(0.0f, 0.0f);
     }
     struct {
         RawVec<IO> x[HELD ? kSlots : 1], g[HELD ? kSlots : 1];
@@ -418,27 +436,30 @@ ss_norm_bwd_kernel(const NormParams p, int slots, int sums) {
         const IO* grow = static_cast<const IO*>(p.dy) + r * C;
         IO* out = static_cast<IO*>(p.out) + r * C;
         const float mu = HELD ? next.mu : p.mean[r], rs = HELD ? next.rs : p.rstd[r];
-        float x[HELD ? kSlots : 1][N], g[HELD ? kSlots : 1][N];
+        float x[1][N], g[1][N];
+        f32x2 xh[HELD ? H : 1], gw2[HELD ? H : 1];
         float c1 = 0.0f, c2 = 0.0f;
         if (HELD) {
+            f32x2 s1 = pk2(0.0f, 0.0f), s2 = s1;
 #pragma unroll
             for (int s = 0; s < kSlots; ++s) {
-                unpack_row<IO>(next.x[s], x[s]);
-                unpack_row<IO>(next.g[s], g[s]);
-            }
-            if (r + step < p.rows) fetch_row(r + step);   // under this row's sums
+                unpack_row<IO>(next.x[s], x[0]);
+                unpack_row<IO>(next.g[s], g[0]);
 #pragma unroll
-            for (int s = 0; s < kSlots; ++s)
-#pragma unroll
-                for (int e = 0; e < N; ++e) {   // behind the row's end g is zero, and with it every term
-                    const float xh = (x[s][e] - mu) * rs;
-                    dw[s][e] = fmaf(g[s][e], xh, dw[s][e]);
-                    db[s][e] += g[s][e];
-                    x[s][e] = xh;
-                    g[s][e] *= w[s][e];
-                    c1 += g[s][e];
-                    c2 = fmaf(g[s][e], xh, c2);
+                for (int e = 0; e < N; e += 2) {   // behind the row's end g is zero, and with it every term
+                    const int i = (s * N + e) / 2;
+                    const f32x2 gg = pk2(g[0][e], g[0][e + 1]);
+                    xh[i] = mul2(add2(pk2(x[0][e], x[0][e + 1]), pk2(-mu, -mu)), pk2(rs, rs));
+                    dw[i] = fma2(gg, xh[i], dw[i]);
+                    db[i] = add2(db[i], gg);
+                    gw2[i] = mul2(gg, w2[i]);
+                    s1 = add2(s1, gw2[i]);
+                    s2 = fma2(gw2[i], xh[i], s2);
                 }
+            }
+            c1 = s1.x + s1.y;
+            c2 = s2.x + s2.y;
+            if (r + step < p.rows) fetch_row(r + step);   // under this row's sums
         } else {
             for (int s = 0; s < slots; ++s) {
                 load_vec<IO, VEC>(xrow, C, s, t, T, x[0]);
@@ -459,8 +480,13 @@ ss_norm_bwd_kernel(const NormParams p, int slots, int sums) {
 #pragma unroll
             for (int s = 0; s < kSlots; ++s) {
 #pragma unroll
-                for (int e = 0; e < N; ++e) x[s][e] = rs * (g[s][e] - c1 - x[s][e] * c2);
-                store_vec<IO, VEC>(out, C, s, t, T, x[s]);
+                for (int e = 0; e < N; e += 2) {
+                    const int i = (s * N + e) / 2;
+                    const f32x2 d = mul2(fma2(xh[i], pk2(-c2, -c2), add2(gw2[i], pk2(-c1, -c1))), pk2(rs, rs));
+                    x[0][e] = d.x;
+                    x[0][e + 1] = d.y;
+                }
+                store_vec<IO, VEC>(out, C, s, t, T, x[0]);
             }
         } else {
             for (int s = 0; s < slots; ++s) {
@@ -482,8 +508,9 @@ ss_norm_bwd_kernel(const NormParams p, int slots, int sums) {
         for (int e = 0; e < N; ++e) {
             const int64_t c = col_of<IO, VEC>(s, e, t, T);
             if (c < C) {
-                pw[c] = dw[s][e];
-                pw[C + c] = db[s][e];
+                const f32x2 a = dw[(s * N + e) / 2], b = db[(s * N + e) / 2];
+                pw[c] = (e & 1) ? a.y : a.x;
+                pw[C + c] = (e & 1) ? b.y : b.x;
             }
         }
 }
@@ -554,9 +581,11 @@ NormPlan norm_plan(int64_t rows, int64_t cols, bool bf16, bool bwd) {
     const int64_t items = pl.warp ? ceil_div(rows, kWarpRows) : rows;
     const int threads = pl.warp ? 32 * kWarpRows : pl.T;
     const int64_t sms = sm_count_of_current_device();
-    // forward: a block per row while there are few, else resident blocks that walk rows with the parameters in
-    // registers; backward: as many blocks as are resident together (their partial rows are written and read once)
-    const int64_t resident = sms * std::max(1, (bwd ? 1024 : 2048) / threads);
+    // forward: a block per row while there are few, else blocks that walk rows with the parameters in registers;
+    // backward: as many blocks as are resident together (at 128 registers a thread; 32768 x 2560 bf16: 128 us with twice
+    // as many, 120 us so; rows through a ring of bulk copies in shared memory instead of the next row in registers:
+    // 117 us, not kept), and their partial rows are written and read once
+    const int64_t resident = sms * std::max(1, (bwd ? 512 : 2048) / threads);
     pl.blocks = std::max<int64_t>(1, std::min(items, resident));
     if (bwd && !pl.held) {
         pl.parts = std::max<int64_t>(1, std::min<int64_t>(rows, 64));
