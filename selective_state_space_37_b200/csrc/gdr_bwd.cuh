@@ -579,6 +579,19 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
             *reinterpret_cast<uint4*>(gp.dv + ((static_cast<int64_t>(b) * g.L + t0 + row) * g.H + h) * p.dv + 8 * q) =
                 lds128(chunk_addr(base + kG1 + (2 * (q >> 3) + 1) * kTile, row, q & 7));
         }
+        // <S, dS> of the entering state: dS's terms from memory, quad by quad in the order of S's image, fetched ahead
+        // in two batches
+        uint4 dh[2 * KB], dl[2 * KB];
+        auto fetch_ds = [&](int w0) {
+            const unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
+#pragma unroll
+            for (int w = 0; w < 2 * KB; ++w) {
+                const uint32_t o = 16u * (tid + kGradThreads * (w0 + w));
+                dh[w] = __ldg(reinterpret_cast<const uint4*>(kp + kKeepD + o));
+                dl[w] = __ldg(reinterpret_cast<const uint4*>(kp + kKeepDlo + o));
+            }
+        };
+        fetch_ds(0);
         if (!wait_all(&bar->m2, par)) break;
         tc_fence_after();
         float v[32];   // M^P (rows 0..63), M^A (64..127): one 32-column block per thread
@@ -610,22 +623,24 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
             }
             umma_commit(&bar->m1);
         }
-        {   // <S, dS> of the entering state: S's terms here, dS's in memory, quad by quad in the images' common order
-            const unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
+        {
             float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll 2
-            for (int w = 0; w < 4 * KB; ++w) {
-                const uint32_t o = 16u * (tid + kGradThreads * w);
-                const uint4 dh = *reinterpret_cast<const uint4*>(kp + kKeepD + o), dl = *reinterpret_cast<const uint4*>(kp + kKeepDlo + o);
-                const uint4 sh = lds128(base + kGS + o), sl = lds128(base + kGS + 4 * kTile + o);
-                if (static_cast<int>((o >> 7) & 127) >= p.dv) continue;
-                const uint32_t a[4] = {dh.x, dh.y, dh.z, dh.w}, b2[4] = {dl.x, dl.y, dl.z, dl.w};
-                const uint32_t e2[4] = {sh.x, sh.y, sh.z, sh.w}, f[4] = {sl.x, sl.y, sl.z, sl.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s0 = fmaf(lo_f(a[e]) + lo_f(b2[e]), lo_f(e2[e]) + lo_f(f[e]), s0);
-                    s1 = fmaf(hi_f(a[e]) + hi_f(b2[e]), hi_f(e2[e]) + hi_f(f[e]), s1);
+            for (int batch = 0; batch < 2; ++batch) {
+#pragma unroll
+                for (int w = 0; w < 2 * KB; ++w) {
+                    const uint32_t o = 16u * (tid + kGradThreads * (2 * KB * batch + w));
+                    const uint4 sh = lds128(base + kGS + o), sl = lds128(base + kGS + 4 * kTile + o);
+                    const bool in = static_cast<int>((o >> 7) & 127) < p.dv;
+                    const uint32_t a[4] = {dh[w].x, dh[w].y, dh[w].z, dh[w].w}, b2[4] = {dl[w].x, dl[w].y, dl[w].z, dl[w].w};
+                    const uint32_t e2[4] = {sh.x, sh.y, sh.z, sh.w}, f[4] = {sl.x, sl.y, sl.z, sl.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (in) s0 = fmaf(lo_f(a[e]) + lo_f(b2[e]), lo_f(e2[e]) + lo_f(f[e]), s0);
+                        if (in) s1 = fmaf(hi_f(a[e]) + hi_f(b2[e]), hi_f(e2[e]) + hi_f(f[e]), s1);
+                    }
                 }
+                if (batch == 0) fetch_ds(2 * KB);
             }
             s0 += s1;
 #pragma unroll
