@@ -86,7 +86,7 @@ struct GdrPlan {
 // segments 0.52 ms; 160 items of 128 chunks whole 0.80 ms, the last wave's 12 in segments 0.54 ms).
 GdrPlan gdr_plan(int64_t items, int64_t nchunks, int32_t chunk_len) {
     GdrPlan best{items, 1, nchunks};
-    if (items == 0 || nchunks < 2) return best;
+    if (items == 0 || nchunks < 2 || items * 2 * kGdrMaxSeg >= (int64_t(1) << 31)) return best;   // (a launch's blocks)
     if (chunk_len > 0) {
         int64_t cs = std::max<int64_t>(1, ceil_div(chunk_len, gdr::kC));
         if (ceil_div(nchunks, cs) > kGdrMaxSeg) cs = ceil_div(nchunks, kGdrMaxSeg);
@@ -116,7 +116,7 @@ GdrPlan gdr_plan(int64_t items, int64_t nchunks, int32_t chunk_len) {
 struct GdrLayout {
     int64_t nchunks;
     GdrPlan plan;
-    size_t rec, in, loc, map, total;
+    size_t rec, in, loc, map, first, total;
 };
 GdrLayout gdr_layout(const ss_gdr_dims* d, uint32_t flags, int32_t chunk_len) {
     GdrLayout w{};
@@ -131,7 +131,10 @@ GdrLayout gdr_layout(const ss_gdr_dims* d, uint32_t flags, int32_t chunk_len) {
     w.in = w.rec + al(static_cast<size_t>(items * w.nchunks) * gdr::kRecBytes);
     w.loc = w.in + al(n * static_cast<size_t>(d->d_v * d->d_k) * sizeof(float));
     w.map = w.loc + al(n * static_cast<size_t>(d->d_v * d->d_k) * sizeof(float));
-    w.total = w.map + al(n * static_cast<size_t>(d->d_k * d->d_k) * sizeof(float));
+    w.first = w.map + al(n * static_cast<size_t>(d->d_k * d->d_k) * sizeof(float));
+    w.total = w.first;
+    if (w.plan.nseg > 1)
+        w.total += al(static_cast<size_t>((items - w.plan.n_whole) * d->d_v * d->d_k) * sizeof(float));
     return w;
 }
 
@@ -175,6 +178,7 @@ int run_tc(const GdrParams& g, const ss_gdr_dims* d, uint32_t flags, const ss_la
     p.seg_in = reinterpret_cast<float*>(ws + w.in);
     p.seg_loc = reinterpret_cast<float*>(ws + w.loc);
     p.seg_map = reinterpret_cast<float*>(ws + w.map);
+    p.seg_first = reinterpret_cast<float*>(ws + w.first);
     p.g = g;
     p.status = static_cast<uint32_t*>(launch->workspace);
     p.rec = static_cast<unsigned char*>(launch->workspace) + w.rec;

@@ -11,7 +11,7 @@
 // values (pairs of floats of a 64-bit prefix sum), so a long decay keeps its near differences.
 //
 // Two kernels.  What does not depend on S -- T, P and the factors -- is prepared for every chunk at once
-// (ss_gdr_prep_kernel, a block per chunk, four resident per SM) and left in the workspace, as the shared-memory
+// (ss_gdr_prep_kernel, a block per chunk, five resident per SM) and left in the workspace, as the shared-memory
 // image that the second kernel copies in.  ss_gdr_tc_kernel then walks the chunks of a (b, h) in order; in its chain
 // from chunk to chunk remain three products and three element-wise steps.  With the preparation inside the second
 // kernel (two groups of four warps, up to two chunks ahead) its latency, about 14 000 cycles a chunk beside the
@@ -89,6 +89,8 @@ struct Params {
     // time segments: items n_whole .. are cut into nseg segments of cseg chunks
     int n_whole, nseg, cseg;
     float* seg_in;           // [cut items][nseg - 1][d_v][d_k]: the states that enter the segments 1 ..
+    float* seg_first;        // [cut items][d_v][d_k]: h_init, which the last segments may overwrite with the final state
+                             // before the first ones have read it
     float* seg_loc;          // [cut items][nseg - 1][d_v][d_k]: a segment's end from a zero (segment 0: the entering) state
     float* seg_map;          // [cut items][nseg - 1][d_k][d_k]: its end from the unit matrix, without values
     // backward pass
@@ -374,16 +376,15 @@ struct alignas(16) PrepSmem {
     uint64_t full, gram;
     uint32_t tmem, pad[3];
 };
-// Shared memory: [K 0][Q 0][K 1][Q 1], P's terms over the first two once K and Q have been read; T as fp32 [64][64],
-// then T's terms in its place, with scratch over K 1; the factors.
-constexpr uint32_t kPrepXs = 2 * kTile, kPrepT = 4 * kTile, kPrepScal = 6 * kTile;
-constexpr uint32_t kPrepLocal = kPrepScal + sizeof(Scal);
-constexpr uint32_t kPrepState = kPrepLocal + 2048;
-constexpr uint32_t kPrepSmem = kPrepState + sizeof(PrepSmem) + 1024;
-static_assert(4 * (kPrepSmem + 1024) <= 228 * 1024, "four resident blocks");
+// Shared memory: [K 0][Q 0][K 1][Q 1], of which P's terms take the first two tiles once K and Q have been read, and T
+// the others, first as fp32 [64][64] and then its terms; the factors; scratch.
+constexpr uint32_t kPrepT = 2 * kTile, kPrepScal = 4 * kTile, kPrepLocal = kPrepScal + sizeof(Scal);
+constexpr uint32_t kPrepState = kPrepLocal + 2048, kPrepXs = kPrepState + sizeof(PrepSmem);
+constexpr uint32_t kPrepSmem = kPrepXs + 32 * kPitchX * 4 + 1024;
+static_assert(kPrepXs % 16 == 0 && 5 * (kPrepSmem + 1024) <= 228 * 1024, "five resident blocks");
 
 // Grid: one block per (item, chunk), a sequence's chunks together.  Bound by the latency of the triangular inverse
-// (fp32, about 75 000 multiply-adds in a dozen dependent steps), which the four resident blocks hide for one another.
+// (fp32, about 75 000 multiply-adds in a dozen dependent steps), which the five resident blocks hide for one another.
 template <int DK>
 __global__ void __launch_bounds__(kPrepThreads)
 ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_q,
@@ -887,7 +888,8 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         const int64_t srow = (static_cast<int64_t>(item) * p.dv + v) * DK + part * KH;
         // the entering state: the call's, a segment's, zero or the unit matrix; and where the leaving one goes
         const int64_t cut = static_cast<int64_t>(item - p.n_whole) * (p.nseg - 1);
-        const float* from = sg == 0 ? (g.h_init ? g.h_init + srow : nullptr)
+        const int64_t first = (static_cast<int64_t>(item - p.n_whole) * p.dv + v) * DK + part * KH;
+        const float* from = sg == 0 ? (!g.h_init ? nullptr : Y && nseg > 1 ? p.seg_first + first : g.h_init + srow)
                           : Y       ? p.seg_in + ((cut + sg - 1) * p.dv + v) * DK + part * KH : nullptr;
         float* to = nullptr;
         if (!Y && !p.keep) to = unit ? p.seg_map + ((cut + sg) * DK + v) * DK + part * KH : p.seg_loc + ((cut + sg) * p.dv + v) * DK + part * KH;
@@ -897,6 +899,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
         for (int k = 0; k < KH; k += 4) {
             float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (from && row_in) q = quad(from + k);
+            if (!Y && nseg > 1 && from && row_in) *reinterpret_cast<float4*>(p.seg_first + first + k) = q;
             if (unit) {
                 const int d = v - (part * KH + k);
                 q = make_float4(d == 0, d == 1, d == 2, d == 3);

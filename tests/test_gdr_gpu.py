@@ -224,6 +224,15 @@ def test_time_segments_of_a_padded_batch():
     assert rms_err(S, Sr) <= 1e-5
 
 
+def test_time_segments_with_the_state_in_place():
+    """final_state = initial_state in segments: the first one's entering state is read from a copy."""
+    x = gdr_inputs(2, 640, 4, 2, 128, 128, seed=12, init=True)
+    y, S = ss.ss_gdr_fwd(*call_args(x), dt_bias=x["dt_bias"], initial_state=x["state"], chunk_len=64)
+    st = x["state"].clone()
+    y2, S2 = ss.ss_gdr_fwd(*call_args(x), dt_bias=x["dt_bias"], initial_state=st, final_state=st, chunk_len=64)
+    assert S2 is st and torch.equal(S, st) and torch.equal(y, y2)
+
+
 def test_segments_of_the_last_wave():
     """More items than SMs: those of the last wave are cut, the others run whole; all give the whole sequence's
     results (which the oracle checks elsewhere)."""
