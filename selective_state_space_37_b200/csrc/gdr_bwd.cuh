@@ -392,16 +392,16 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
 //   D3 E dS                    ->         128 .. 255 (K: d_v; likewise)
 //   dq~ = qe D1 + D4 (lanes 0..63),   dk~ = ek D1 + D4 (lanes 64..127) + wk D3 + D5 (lanes 0..63)
 // (ek carries the minus of -e^G), and of each token the products of these brackets with its own q and k.  dV comes
-// from the chain transposed and is turned in shared memory; S and dS pass through one buffer.  Bound by what it reads
-// (the chains' states, 176 KB a chunk) and by the latency of its stages.
+// from the chain transposed and is turned in shared memory; dO has no lo terms, so the products with dV's write the
+// lanes from 64 on alone; S and dS pass through one buffer.  Bound by the latency of its stages, one block per SM.
 constexpr int kGradThreads = 256;
 constexpr uint32_t kGK = 0;                       // [K 0][Q 0][K 1][Q 1]
 constexpr uint32_t kG1 = 4 * kTile;               // [dO 0][dV hi 0][dO 1][dV hi 1]
-constexpr uint32_t kG2 = 8 * kTile;               // [0][dV lo 0][0][dV lo 1]; then [M^P lo][M^A lo] over its first half
-constexpr uint32_t kGE = 12 * kTile;              // Eᵀ hi, lo: 128 rows each
-constexpr uint32_t kGS = 16 * kTile;              // dVᵀ hi, lo; then S hi, lo; then dS hi, lo (two blocks of 128 rows each);
-                                                  // then dk~'s other bracket, fp32 [64][132]
-constexpr uint32_t kGM = 24 * kTile;              // [M^P hi][M^A hi], 64 rows of 64 each
+constexpr uint32_t kG2 = 8 * kTile;               // [dV lo 0][dV lo 1]; then [M^P lo][M^A lo]
+constexpr uint32_t kGE = 10 * kTile;              // Eᵀ hi, lo: 128 rows each
+constexpr uint32_t kGS = 14 * kTile;              // S hi, lo; then dS hi, lo (two blocks of 128 rows each); then dk~'s
+                                                  // other bracket, fp32 [64][132]
+constexpr uint32_t kGM = 22 * kTile;              // dVᵀ hi, lo (128 rows each); then [M^P hi][M^A hi] over hi
 constexpr uint32_t kGScal = 26 * kTile;           // Scal, Local (one copy from the record)
 constexpr uint32_t kGRed = kGScal + 1024 + sizeof(Local);   // row products of the two halves, [3][2][64]
 constexpr uint32_t kGBar = kGRed + 3 * 2 * kC * 4;
@@ -429,6 +429,17 @@ __device__ __forceinline__ void turn8x4(uint32_t src, uint32_t dst) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(r0), "r"(r1), "r"(r2),
                  "r"(r3)
                  : "memory");
+}
+
+// D[tmem] += A · B in the lanes from 64 on; the others keep what they hold.
+__device__ __forceinline__ void umma_upper(uint32_t d, uint64_t a, uint64_t b, uint32_t id) {
+    const uint32_t off = 0xffffffffu, on = 0u;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, 1, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%4, %4, %5, %5}, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(off), "r"(on)
+        : "memory");
 }
 
 template <int DK>
@@ -486,7 +497,7 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
     auto load_in = [&](int64_t item, int h) {   // dVᵀ, E, dO and the factors
         const unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
         mbar_arrive_expect_tx(&bar->in, 8 * kTile + vb * kTile + 1024 + sizeof(Local));
-        bulk_load(base + kGS, kp + kKeepV, 4 * kTile, &bar->in);
+        bulk_load(base + kGM, kp + kKeepV, 4 * kTile, &bar->in);
         bulk_load(base + kGE, kp + kKeepE, 4 * kTile, &bar->in);
         for (int w = 0; w < vb; ++w) tma_load_4d(base + kG1 + 2 * w * kTile, &tm_o, 64 * w, h, t, b, &bar->in);
         bulk_load(base + kGScal, p.rec + (item * p.nchunks + c) * p.rec_bytes + kRecScal, 1024 + sizeof(Local), &bar->in);
@@ -539,19 +550,18 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
         };
         if (tid == 0) {
             load_in(item, h);
-            stage = 4 * j + 1;
+            load_states(item, kKeepS, kKeepSlo, &bar->s);
+            stage = 4 * j + 2;
         }
         if (j == 0 && !wait_all(&bar->qk, 0)) break;
         if (!wait_all(&bar->in, par)) break;
-        // dV's rows (its terms turned), zero rows under the lo terms, and behind the sequence's end
+        // dV's rows (its terms turned), and zero rows behind the sequence's end
         for (int w = warp; w < 4 * vb * 8; w += 8) {   // four 8-row groups of v by 8 tokens, hi then lo
             const int term = w / (2 * vb * 8), x = w % (2 * vb * 8), vg = (x >> 3) * 4, tc8 = x & 7;
             const int m = vg + (lane >> 3), l7 = lane & 7;
-            turn8x4(chunk_addr(base + kGS + term * 2 * kTile, 8 * m + l7, tc8),
-                    chunk_addr(base + (term ? kG2 : kG1) + (2 * (m >> 3) + 1) * kTile, 8 * tc8 + l7, m & 7));
+            turn8x4(chunk_addr(base + kGM + term * 2 * kTile, 8 * m + l7, tc8),
+                    chunk_addr(base + (term ? kG2 + (m >> 3) * kTile : kG1 + (2 * (m >> 3) + 1) * kTile), 8 * tc8 + l7, m & 7));
         }
-        for (int w = tid; w < 512; w += kGradThreads)
-            for (int x = 0; x < vb; ++x) sts128(base + kG2 + 2 * x * kTile + 16 * w, make_uint4(0, 0, 0, 0));
         if (valid < kC) {   // K, Q (once) and dO (dV has them)
             for (int w = valid * 8 + tid; w < kC * 8; w += kGradThreads) {
                 for (int kb = 0; kb < 2 * KB && j == 0; ++kb) sts128(base + kGK + kb * kTile + 16 * w, make_uint4(0, 0, 0, 0));
@@ -560,16 +570,15 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
         }
         fence_proxy_async_smem();
         __syncthreads();
-        auto a_off = [](int ks) { return (ks >> 2) * 2 * kTile + (ks & 3) * 32u; };   // 16 columns of a stacked operand
+        // 16 columns of [dO; dV hi], and of dV lo as the rows 64.. of an operand (whose others are not written out)
+        auto a_hi = [&](int ks) { return sdesc(base + kG1 + (ks >> 2) * 2 * kTile + (ks & 3) * 32u, 16, 1024); };
+        auto a_lo = [&](int ks) { return sdesc(base + kG2 - kTile + (ks >> 2) * kTile + (ks & 3) * 32u, 16, 1024); };
         if (tid == 0) {
-            load_states(item, kKeepS, kKeepSlo, &bar->s);
-            stage = 4 * j + 2;
             for (int ks = 0; ks < vs; ++ks) {
                 const uint64_t e = sdesc(base + kGE + 2048u * ks, 0, 1024), el = sdesc(base + kGE + 2 * kTile + 2048u * ks, 0, 1024);
-                const uint64_t a = sdesc(base + kG1 + a_off(ks), 16, 1024);
-                umma(tmem + 384, a, e, idesc(kC, true), ks > 0);
-                umma(tmem + 384, a, el, idesc(kC, true), 1);
-                umma(tmem + 384, sdesc(base + kG2 + a_off(ks), 16, 1024), e, idesc(kC, true), 1);
+                umma(tmem + 384, a_hi(ks), e, idesc(kC, true), ks > 0);
+                umma(tmem + 384, a_hi(ks), el, idesc(kC, true), 1);
+                umma_upper(tmem + 384, a_lo(ks), e, idesc(kC, true));
             }
             umma_commit(&bar->m2);
         }
@@ -616,10 +625,9 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
             tc_fence_after();
             for (int ks = 0; ks < vs; ++ks) {
                 const uint64_t sh = sdesc(base + kGS + 2048u * ks, 2 * kTile, 1024);
-                const uint64_t a = sdesc(base + kG1 + a_off(ks), 16, 1024);
-                umma(tmem, a, sh, idesc(DK, true), ks > 0);
-                umma(tmem, a, sdesc(base + kGS + 4 * kTile + 2048u * ks, 2 * kTile, 1024), idesc(DK, true), 1);
-                umma(tmem, sdesc(base + kG2 + a_off(ks), 16, 1024), sh, idesc(DK, true), 1);
+                umma(tmem, a_hi(ks), sh, idesc(DK, true), ks > 0);
+                umma(tmem, a_hi(ks), sdesc(base + kGS + 4 * kTile + 2048u * ks, 2 * kTile, 1024), idesc(DK, true), 1);
+                umma_upper(tmem, a_lo(ks), sh, idesc(DK, true));
             }
             umma_commit(&bar->m1);
         }
