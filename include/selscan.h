@@ -332,7 +332,8 @@ typedef struct ss_gdr_dims {
  *                (clamped to 0 .. seqlen).  Tokens behind its end are not used, whatever
  *                they hold, and their rows of y are left as they were.
  *   final_state  [batch, nheads, d_v, d_k] fp32, or NULL: S after a sequence's last
- *                token (h_init or zero for an empty one); may be h_init itself
+ *                token (h_init or zero for an empty one); may be h_init itself (y and
+ *                final_state overlap no other input, nor each other)
  *   flags        SS_BF16, SS_DELTA_SOFTPLUS, SS_BETA_SIGMOID, SS_QK_L2NORM, SS_SYNC_CHECK,
  *                SS_TEST_DROP_CARRY for tests
  *   launch       stream; workspace of at least ss_gdr_fwd_workspace_bytes() bytes,
@@ -362,7 +363,7 @@ SS_API size_t ss_gdr_fwd_workspace_bytes(const ss_gdr_dims* dims, uint32_t flags
 /* ss_gdr_step -- one token of the gated delta rule on a carried state.
  *   state        [batch, nheads, d_v, d_k] fp32, read and overwritten in place
  *   q, k [batch, nheads_k, d_k], v, y [batch, nheads, d_v], dt, beta [batch, nheads]
- * Everything else as in ss_gdr_fwd; dims->seqlen is ignored and launch->workspace is
+ * y overlaps no input.  Everything else as in ss_gdr_fwd; dims->seqlen is ignored and launch->workspace is
  * not used.  Token by token, ss_gdr_step gives ss_gdr_fwd up to rounding. */
 SS_API int ss_gdr_step(float* state, const void* q, const void* k, const void* v, const void* dt,
                        const float* dt_bias, const float* A, const void* beta, void* y, float scale,
@@ -414,8 +415,8 @@ SS_API int ss_norm_fwd(const void* x, const float* weight, const float* bias, vo
                        float eps, uint32_t flags, const ss_norm_dims* dims, const ss_launch* launch);
 
 /* ss_norm_bwd -- gradients of ss_norm_fwd's inputs from dy = dJ/dy.  With
- * x̂ = (x - μ) r and w = dy · weight, per row:
- *   dx = r (w - mean(w) - x̂ mean(w x̂)),  dweight = Σ_rows dy x̂,  dbias = Σ_rows dy
+ * x̂ = (x - μ) r and g = dy · weight, per row:
+ *   dx = r (g - mean(g) - x̂ mean(g x̂)),  dweight = Σ_rows dy x̂,  dbias = Σ_rows dy
  *   dy, x, dx       [rows, cols] element type; dx may be dy
  *   mean, rstd      [rows] fp32, as ss_norm_fwd wrote them
  *   weight          [cols] fp32 or NULL

@@ -246,15 +246,17 @@ def _stream_handle(stream, device):
 
 def _on_device(fn):
     """Runs a function with its first tensor's device current (the library launches on the current device)."""
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(first, *args, **kw):
-        dev = getattr(first, "device", None)
+    def call(*args, **kw):
+        dev = getattr(args[0] if args else kw.get(name), "device", None)
         if dev is None or dev.type != "cuda":
-            raise ValueError(f"{fn.__name__} runs on CUDA tensors only")
+            raise ValueError(f"{fn.__name__} runs on CUDA tensors only ({name})")
         if dev.index == torch.cuda.current_device():
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
         with torch.cuda.device(dev):
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
     return call
 
 
@@ -661,7 +663,10 @@ def ss_gdr_fwd(q, k, v, dt, A, beta, dt_bias=None, initial_state=None, seqlens=N
     _check(initial_state, "initial_state", states, torch.float32, dev)
     _check(seqlens, "seqlens", (batch,), torch.int32, dev)
     if y is None:
-        y = torch.empty_like(v) if seqlens is None else torch.zeros_like(v)
+        y = torch.empty_like(v)
+        if seqlens is not None:
+            with torch.cuda.stream(stream):   # (None: the current one)
+                y.zero_()
     _check(y, "y", v.shape, v.dtype, dev)
     if final_state is None and return_final_state:
         final_state = torch.empty(states, dtype=torch.float32, device=dev)

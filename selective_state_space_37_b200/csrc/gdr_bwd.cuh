@@ -859,7 +859,7 @@ __global__ void __launch_bounds__(256) ss_gdr_gate_kernel(const __grid_constant_
         const float before = __shfl_up_sync(0xffffffffu, s, 1);
         const float start = c * kC < len ? p.dots[4 * plane + item * (p.nchunks + 1) + c] : 0.0f;
         const float first = start + (lane ? before : 0.0f);
-        const float dla[2] = {first, first + r[0]};
+        float dla[2] = {first, first + r[0]};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             if (t + e >= g.L) continue;
@@ -868,6 +868,8 @@ __global__ void __launch_bounds__(256) ss_gdr_gate_kernel(const __grid_constant_
             if (t + e < len) {
                 const float pre = to_f32(static_cast<const __nv_bfloat16*>(g.dt)[o]) + bias;
                 const float delta = g.softplus ? softplus_accurate(pre) : pre;
+                // where α is zero in fp32 so is its gradient; the sums' rounding would be multiplied by a large Δ
+                if (delta * A < -104.0f) dla[e] = 0.0f;
                 ddt = dla[e] * A * (g.softplus ? 1.0f / (1.0f + expf(-pre)) : 1.0f);
                 sa += static_cast<double>(dla[e]) * static_cast<double>(delta);
                 sb += static_cast<double>(ddt);

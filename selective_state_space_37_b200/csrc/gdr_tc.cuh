@@ -436,6 +436,7 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
             if (p.keep && !g.sigmoid && fabsf(be) < 1e-20f) be = 1e-20f;
         }
         G = static_cast<double>(delta) * static_cast<double>(g.A[h]) * 1.4426950408889634074;   // log2 α
+        if (G < -2048.0) G = -2048.0;   // α is zero in fp32 from -150 down; the floor keeps differences of infinities out
 #pragma unroll
         for (int s = 1; s < 32; s <<= 1) {
             const double v = __shfl_up_sync(0xffffffffu, G, s);

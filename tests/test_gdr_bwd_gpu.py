@@ -132,6 +132,32 @@ def test_extreme_decays(A):
     assert np.all(np.abs(to_f64(g["dA"]) - want["dA"]) <= bA + 1e-30)
 
 
+@pytest.mark.parametrize("dt", [400.0, 3.0e38])
+def test_steps_that_empty_the_state(dt):
+    """Gates so large that Δ A, and its sums, leave fp32's range: no gradient passes them, and they have none."""
+    x = gdr_inputs(2, 140, 3, 3, 128, 128, seed=23, init=True)
+    x["dt"][0, ::9, 0] = dt
+    x["dt"][1, 5, :] = dt
+    x["dt"][:, -3:, 2] = dt
+    check(x, 3)
+
+
+def test_refusals():
+    x = gdr_inputs(2, 20, 2, 2, 64, 64, seed=2)
+    dy, _ = upstream(x, 1)
+    half = [t.float() if t.dim() > 1 else t for t in call_args(x)]
+    with pytest.raises(TypeError, match="bfloat16"):
+        ss.ss_gdr_bwd(*half, dy.float())
+    with pytest.raises(TypeError, match="dy"):
+        ss.ss_gdr_bwd(*call_args(x), dy.float())
+    with pytest.raises(ValueError, match="dq"):
+        ss.ss_gdr_bwd(*call_args(x), dy, grads={"dq": x["q"][:1].contiguous()})
+    with pytest.raises(ValueError, match="contiguous"):
+        ss.ss_gdr_bwd(x["q"].transpose(0, 1).contiguous().transpose(0, 1), *call_args(x)[1:], dy)
+    with pytest.raises(ss.SelscanError):
+        ss.ss_gdr_bwd(*call_args(x), dy, workspace=torch.empty(512, dtype=torch.uint8, device=DEV))
+
+
 def test_against_differences():
     """The gradients of the library's own forward: central differences of J along random directions of the fp32
     inputs (A, dt_bias, the states), whose outputs are fp32 where they matter (J of the final state alone)."""

@@ -113,6 +113,36 @@ def test_extreme_decays(dtype, A):
     check(x, 140, dtype)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("dt", [400.0, 3.0e38, float("inf")])
+@pytest.mark.parametrize("L", [10, 140])
+def test_steps_that_empty_the_state(L, dt, dtype):
+    """Gates so large that Δ A, and its sums, leave fp32's range: α is zero there and nowhere else."""
+    x = gdr_inputs(2, L, 3, 3, 128, 128, dtype, seed=23, init=True)
+    x["dt"][0, ::9, 0] = dt
+    x["dt"][1, 5, :] = dt
+    x["dt"][:, -3:, 2] = dt
+    check(x, L, dtype)
+
+
+def test_arguments_by_name_and_zeros_on_the_calls_stream():
+    """y, made by the call, is cleared on the stream that the call is given."""
+    x = gdr_inputs(3, 200, 2, 2, 64, 64, seed=41)
+    lens = torch.tensor([200, 3, 0], dtype=torch.int32, device="cuda:0")
+    names = ("q", "k", "v", "dt", "A", "beta", "dt_bias")
+    want, S = ss.ss_gdr_fwd(**{n: x[n] for n in names}, seqlens=lens)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for _ in range(3):
+        torch.empty_like(want).fill_(7.0)      # what the allocator hands out next
+        torch.cuda.synchronize()
+        y, S2 = ss.ss_gdr_fwd(**{n: x[n] for n in names}, seqlens=lens, stream=st)
+        st.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(S, S2)
+        assert not y[1, 3:].any() and not y[2].any()
+
+
 def test_equal_keys():
     """One key again and again with β = 1: the chunk's triangular system has no small entry."""
     x = gdr_inputs(1, 130, 2, 2, 128, 128, seed=31)

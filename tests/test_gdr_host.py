@@ -73,6 +73,78 @@ def test_gdr_step_refusals(L):
     assert step((0, 0, 4, 2, 64, 64)) == ss.SS_OK
 
 
+def test_gdr_bwd_refusals(L):
+    d = (2, 64, 4, 2, 128, 64)
+    need = L.ss_gdr_bwd_workspace_bytes(ctypes.byref(ss.ss_gdr_dims(*d)), ss.SS_BF16)
+    assert need > 0
+    assert L.ss_gdr_bwd_workspace_bytes(ctypes.byref(ss.ss_gdr_dims(*d)), 0) == 0
+
+    def bwd(dims=d, flags=ss.SS_BF16, ws=(0x900000, need), launch=True, **ptr):
+        names = ("q", "k", "v", "dt", "dt_bias", "A", "beta", "h_init", "seqlens", "dy", "dfinal_state", "dq", "dk",
+                 "dv", "ddt", "dbeta", "dA", "ddt_bias", "dh_init")
+        a = {n: 0x10000 * (i + 1) for i, n in enumerate(names)}
+        a.update(ptr)
+        la = ss.ss_launch(None, ws[0], ws[1], 0, 0)
+        return L.ss_gdr_bwd(*(P(v) if v else None for v in a.values()), 1.0, flags,
+                            None if dims is None else ctypes.byref(ss.ss_gdr_dims(*dims)),
+                            ctypes.byref(la) if launch else None)
+
+    bad = ss.SS_ERR_INVALID_ARG
+    assert bwd(None) == bad and bwd(launch=False) == bad
+    assert bwd(flags=0) == ss.SS_ERR_UNSUPPORTED
+    assert bwd(flags=ss.SS_BF16 | 1 << 12) == bad
+    for name in ("q", "k", "v", "dt", "A", "beta", "dy", "dq", "dk", "dv", "ddt", "dbeta", "dA"):
+        assert bwd(**{name: None}) == bad, name
+    for name in ("q", "dt_bias", "h_init", "seqlens", "dy", "dfinal_state", "dq", "dbeta", "dA", "ddt_bias", "dh_init"):
+        assert bwd(**{name: 0x700004}) == bad, name
+    assert bwd(dt_bias=None) == bad                       # a gradient of nothing
+    assert bwd(ws=(0x900000, need - 1)) == ss.SS_ERR_WORKSPACE
+    assert bwd(ws=(None, need)) == ss.SS_ERR_WORKSPACE
+    assert bwd(ws=(0x900004, need)) == ss.SS_ERR_WORKSPACE
+    for dims, want in BAD_DIMS:
+        assert bwd(dims) == want, dims
+        assert L.ss_gdr_bwd_workspace_bytes(ctypes.byref(ss.ss_gdr_dims(*dims)), ss.SS_BF16) == 0
+    assert bwd((2, 64, 0, 0, 128, 64)) == ss.SS_OK
+
+
+@pytest.mark.parametrize("L_,H", [(16, 1), (1000, 4), (100000, 16), (130, 300)])
+def test_gdr_workspace_grows_with_the_segments(L, L_, H):
+    """Records for every chunk, and states for the segments that a call is cut into; token by token needs neither."""
+    size = lambda n, f=ss.SS_BF16, cl=0: L.ss_gdr_fwd_workspace_bytes(  # noqa: E731
+        ctypes.byref(ss.ss_gdr_dims(1, n, H, H, 128, 128)), f, cl)
+    chunks = -(-L_ // 64)
+    whole = size(L_, cl=1 << 30)
+    assert whole >= H * chunks * 33 * 1024
+    assert size(L_, cl=64) >= whole + (H * min(chunks - 1, 1) * 3 * 65536 if chunks > 1 else 0)
+    assert size(L_) >= whole
+    assert size(L_, 0) == size(15) < 4096
+
+
+def test_prenorm_refusals(L):
+    w = ss.ss_block_weights()
+    for n, v in (("d_model", 64), ("d_inner", 128), ("dt_rank", 8)):
+        setattr(w, n, v)
+    for i, n in enumerate(("in_proj_x", "in_proj_z", "conv_w", "x_proj_dt", "x_proj_B", "x_proj_C", "dt_proj", "dt_bias",
+                           "A", "out_proj")):
+        setattr(w, n, 0x100000 * (i + 1))
+    need = L.ss_block_prenorm_scratch_bytes(ctypes.byref(w), 1, 16)
+    assert need > L.ss_block_scratch_bytes(ctypes.byref(w), 1, 16) > 0
+    assert L.ss_block_prenorm_scratch_bytes(ctypes.byref(w), -1, 16) == 0
+
+    def call(hidden=0x10000, nw=None, nb=None, eps=1e-5, out=0x20000, batch=1, scratch=0x30000, size=need):
+        return L.ss_block_fwd_prenorm(P(hidden) if hidden else None, P(nw) if nw else None, P(nb) if nb else None, eps,
+                                      P(out) if out else None, ctypes.byref(w), batch, 16,
+                                      P(scratch) if scratch else None, size, None)
+
+    bad = ss.SS_ERR_INVALID_ARG
+    assert call(hidden=None) == bad and call(out=None) == bad and call(batch=-1) == bad
+    assert call(hidden=0x10004) == bad and call(out=0x20004) == bad
+    assert call(nw=0x40004) == bad and call(nb=0x40004) == bad
+    assert call(eps=-1.0) == bad and call(eps=float("nan")) == bad
+    assert call(out=0x10000) == bad                       # out in hidden's place
+    assert call(scratch=None) != ss.SS_OK and call(size=need - 1) != ss.SS_OK
+
+
 def test_older_entry_points_refuse_the_new_flags(L):
     d = ss.ss_dims(0, 64, 128, 16)
     la = ss.ss_launch(None, None, 0, 0, 0)
@@ -128,3 +200,7 @@ def test_binding_checks():
         ss.ss_norm_bwd(torch.zeros(2, 8), torch.zeros(2, 8), torch.zeros(2), torch.zeros(2))
     with pytest.raises(ValueError, match="CUDA"):
         ss.ss_block_fwd_prenorm(torch.zeros(2, 8, 8), {})
+    with pytest.raises(ValueError, match="CUDA"):   # every argument by name
+        ss.ss_gdr_fwd(q=x, k=x, v=x, dt=g, A=A, beta=g)
+    with pytest.raises(ValueError, match="CUDA"):
+        ss.ss_norm_fwd(x=torch.zeros(2, 8))
