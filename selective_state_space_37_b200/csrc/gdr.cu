@@ -40,10 +40,12 @@ GdrParams gdr_params(const void* q, const void* k, const void* v, const void* dt
 
 template <typename IO, int DK>
 void launch_rec(const GdrParams& p, int dv, cudaStream_t stream) {
-    // four rows of the state per thread where the blocks still fill the GPU twice, else one
+    // Four rows of the state per thread from 1.25 blocks per SM on, else one.  d_k = d_v = 128, four rows against one:
+    // a decode step 3.0 / 2.3 us at 12 items, 4.2 / 4.0 at 96 (the border is at 93), 4.5 / 4.9 at 144, 206 / 255 at
+    // 10240; 256 tokens in fp32 256 / 185 us at 12 items, 310 / 364 at 96, 1650 / 2430 at 768.
     const int64_t items = static_cast<int64_t>(p.batch) * p.H;
     const int big = dv / (kGdrRecRows * 4);
-    if (items * big >= 2 * sm_count_of_current_device())
+    if (items * big * 4 >= 5 * sm_count_of_current_device())
         ss_gdr_rec_kernel<IO, DK, 4><<<static_cast<unsigned>(items * big), kGdrRecThreads, 0, stream>>>(p, dv, big);
     else
         ss_gdr_rec_kernel<IO, DK, 1><<<static_cast<unsigned>(items * big * 4), kGdrRecThreads, 0, stream>>>(p, dv, big * 4);
@@ -61,7 +63,9 @@ int run_rec(const GdrParams& p, const ss_gdr_dims* d, uint32_t flags, cudaStream
     return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
-// bf16 sequences of at least this many tokens run in chunks.
+// bf16 sequences of at least this many tokens run in chunks (token by token against in chunks, d_k = d_v = 128: at 8
+// tokens 10 / 21 us with 12 items, 18 / 23 with 96, 96 / 128 with 1280; at 16 tokens 17 / 22, 31 / 23 and 181 / 127; at
+// 24 tokens 24 / 21, 43 / 23 and 264 / 127).
 constexpr int64_t kChunkedFrom = 16;
 
 // 4-D map of a [batch, L, heads, d] bf16 tensor, boxes of `cols` x 64 tokens of one head.
@@ -82,8 +86,10 @@ struct GdrPlan {
     int64_t n_whole, nseg, cseg;
 };
 // The plan with the least chunk-times on the busiest SM (one CTA per SM).  A chunk of the state pass takes 0.8 of one
-// with y; the extra launches and the fold are charged 12 chunks (measured: 512 chunks of 16 items whole 1.55 ms, in 9
-// segments 0.52 ms; 160 items of 128 chunks whole 0.80 ms, the last wave's 12 in segments 0.54 ms).
+// with y; the extra launches are charged 3 chunks and the fold one per segment.  Whole call, items whole / in segments:
+// 16 items of 16 chunks 72 / 63 us in 4 (76 in 8), of 32 chunks 128 / 91 in 4, of 512 chunks 1795 / 695 in 9; 12 items
+// of 8 chunks 45 / 48 in 4 (runs whole); 160 items of 128 chunks 1210 / 934, the last wave's 12 items in segments (all
+// of them in 4: 1541).
 GdrPlan gdr_plan(int64_t items, int64_t nchunks, int32_t chunk_len) {
     GdrPlan best{items, 1, nchunks};
     if (items == 0 || nchunks < 2 || items * 2 * kGdrMaxSeg >= (int64_t(1) << 31)) return best;   // (a launch's blocks)
@@ -102,7 +108,7 @@ GdrPlan gdr_plan(int64_t items, int64_t nchunks, int32_t chunk_len) {
             if (n == 0) continue;
             const double t = static_cast<double>((items - n) / sms * nchunks) +
                              0.8 * static_cast<double>(ceil_div(n * std::max<int64_t>(1, 2 * k - 3), sms) * cs) +
-                             static_cast<double>(ceil_div(n * k, sms) * cs) + 12.0;
+                             static_cast<double>(ceil_div(n * k, sms) * cs) + 3.0 + static_cast<double>(k);
             if (t < cost - 1e-9) {
                 cost = t;
                 best = GdrPlan{items - n, k, cs};
@@ -337,7 +343,7 @@ int ss_gdr_bwd(const void* q, const void* k, const void* v, const void* dt, cons
         const size_t st = static_cast<size_t>(items * dims->d_k * dims->d_v) * sizeof(float);
         cudaError_t e = cudaMemsetAsync(dA, 0, n, stream);
         if (e == cudaSuccess && ddt_bias) e = cudaMemsetAsync(ddt_bias, 0, n, stream);
-        if (e == cudaSuccess && dh_init && st)
+        if (e == cudaSuccess && dh_init && st && dh_init != dfinal_state)
             e = dfinal_state ? cudaMemcpyAsync(dh_init, dfinal_state, st, cudaMemcpyDeviceToDevice, stream)
                              : cudaMemsetAsync(dh_init, 0, st, stream);
         if (e != cudaSuccess) return SS_ERR_CUDA;

@@ -299,7 +299,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads) ss_norm_f
 
 // Forward, rows of whole 16-byte vectors that a warp holds: NV vectors per lane, all loaded before the first is used,
 // no barrier; the parameters lie in shared memory (their vectors' quads in planes, so that a warp's reads are
-// consecutive), loaded once by a block that walks rows.  32768 x 2560 bf16: see the host's choice.
+// consecutive), loaded once by a block that walks rows.  32768 x 2560 bf16: 60 us, 5.6 TB/s, bound by HBM's
+// latency at 24 resident warps per SM.
 constexpr int kRowWarps = 8;
 template <typename IO, int NV>
 __global__ void __launch_bounds__(32 * kRowWarps, NV <= 8 ? 3 : 2) ss_norm_fwd_rows_kernel(const NormParams p) {
@@ -612,7 +613,10 @@ size_t norm_ws(const ss_norm_dims* dims, bool bf16) {
     return std::max<size_t>(256, static_cast<size_t>(pl.parts) * 2 * static_cast<size_t>(dims->cols) * sizeof(float));
 }
 
-// The row kernel for rows of `vecs` whole vectors, with the least NV that holds them; false if none does.
+// The row kernel for rows of `vecs` whole vectors, with the least NV that holds them; false if none does.  It is taken
+// where its blocks fill every SM (rows >= 8 per SM): fewer rows want a whole block each (row kernel / block kernel, us:
+// 16 x 2560 bf16 4.6 / 2.4, 592 x 2560 4.7 / 4.6, 1184 x 2560 5.0 / 6.6, 1184 x 768 3.2 / 2.9, 4736 x 768 6.0 / 8.3,
+// 1184 x 2048 fp32 5.1 / 5.3, 32768 x 2560 bf16 60 / 118).
 template <typename IO, int NV, int... More>
 bool launch_rows(const NormParams& p, int64_t vecs, cudaStream_t stream) {
     if (vecs <= 32 * NV) {
@@ -627,7 +631,9 @@ bool launch_rows(const NormParams& p, int64_t vecs, cudaStream_t stream) {
 
 template <typename IO, bool VEC>
 void launch_norm_fwd(const NormParams& p, const NormPlan& pl, cudaStream_t stream) {
-    if (VEC && launch_rows<IO, 1, 2, 3, 4, 6, 8, 10, 12, 16>(p, p.cols / VecOf<IO>::kN, stream)) return;
+    if (VEC && p.rows >= int64_t(kRowWarps) * sm_count_of_current_device() &&
+        launch_rows<IO, 1, 2, 3, 4, 6, 8, 10, 12, 16>(p, p.cols / VecOf<IO>::kN, stream))
+        return;
     const unsigned g = static_cast<unsigned>(pl.blocks), t = static_cast<unsigned>(pl.warp ? 32 * kWarpRows : pl.T);
     if (pl.warp) ss_norm_fwd_kernel<IO, VEC, true, true><<<g, t, 0, stream>>>(p, pl.slots);
     else if (pl.held) ss_norm_fwd_kernel<IO, VEC, false, true><<<g, t, 0, stream>>>(p, pl.slots);
