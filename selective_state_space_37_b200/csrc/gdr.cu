@@ -87,8 +87,8 @@ struct GdrPlan {
 };
 // The plan with the least chunk-times on the busiest SM (one CTA per SM).  A chunk of the state pass takes 0.8 of one
 // with y; the extra launches are charged 3 chunks and the fold one per segment.  Whole call, items whole / in segments:
-// 16 items of 16 chunks 72 / 63 us in 4 (76 in 8), of 32 chunks 128 / 91 in 4, of 512 chunks 1795 / 695 in 9; 12 items
-// of 8 chunks 45 / 48 in 4 (runs whole); 160 items of 128 chunks 1210 / 934, the last wave's 12 items in segments (all
+// 16 items of 16 chunks 72 / 62 us in 4 (75 in 8), of 32 chunks 127 / 84 in 6 (90 in 4), of 512 chunks 1795 / 695 in 9;
+// 12 items of 8 chunks 43 / 47 in 4 (runs whole); 160 items of 128 chunks 1210 / 934, the last wave's 12 items in segments (all
 // of them in 4: 1541).
 GdrPlan gdr_plan(int64_t items, int64_t nchunks, int32_t chunk_len) {
     GdrPlan best{items, 1, nchunks};
