@@ -5,6 +5,7 @@ kernels.  PyTorch supplies device memory (tensors, the cached workspace) and
 the current stream.  There is no CPU fallback: if the library is missing or a
 call fails, an exception is raised.
 """
+import contextlib
 import ctypes
 import functools
 import os
@@ -264,10 +265,12 @@ def _launch_for(need, dev, stream, workspace, timeout_iters=0, chunk_len=0):
     sh = _stream_handle(stream, dev)
     if workspace is None:
         # a captured graph gets a workspace of its own, from its memory pool: graphs may be replayed at once,
-        # and the cached buffer may have been replaced by a larger one by then
-        capturing = torch.cuda.is_current_stream_capturing()
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev) if capturing else \
-            workspace_for(need, dev, sh)
+        # and the cached buffer may have been replaced by a larger one by then.  On the call's stream, so that the
+        # allocator hands a replaced buffer out again behind the calls that used it
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev) if capturing else \
+                workspace_for(need, dev, sh)
     elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     return ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(timeout_iters),
@@ -735,6 +738,8 @@ def ss_gdr_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, initial_state=None, dfina
         like["ddt_bias"] = dt_bias
     if initial_state is not None:
         like["dinitial_state"] = initial_state
+    if grads and not like.keys() >= grads.keys():
+        raise ValueError(f"grads: no {sorted(grads.keys() - like.keys())} in this call's gradients {sorted(like)}")
     g = {}
     for name, t in like.items():
         given = (grads or {}).get(name)

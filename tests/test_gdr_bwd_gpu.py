@@ -152,6 +152,8 @@ def test_refusals():
         ss.ss_gdr_bwd(*call_args(x), dy.float())
     with pytest.raises(ValueError, match="dq"):
         ss.ss_gdr_bwd(*call_args(x), dy, grads={"dq": x["q"][:1].contiguous()})
+    with pytest.raises(ValueError, match="ddt_bias"):
+        ss.ss_gdr_bwd(*call_args(x), dy, grads={"ddt_bias": x["A"]})
     with pytest.raises(ValueError, match="contiguous"):
         ss.ss_gdr_bwd(x["q"].transpose(0, 1).contiguous().transpose(0, 1), *call_args(x)[1:], dy)
     with pytest.raises(ss.SelscanError):
