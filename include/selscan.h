@@ -371,28 +371,29 @@ SS_API int ss_gdr_step(float* state, const void* q, const void* k, const void* v
 
 /* ss_gdr_bwd -- gradients of ss_gdr_fwd's inputs, for a scalar J of its outputs:
  * dy = dJ/dy and dfinal_state = dJ/dfinal_state, with ss_gdr_fwd's q .. seqlens, scale
- * and flags.  bf16 only (SS_BF16; SS_ERR_UNSUPPORTED without it).
- *   dy            [batch, seqlen, nheads, d_v] bf16 (behind a sequence's end not used)
+ * and flags.
+ *   dy            [batch, seqlen, nheads, d_v] element type (behind a sequence's end not used)
  *   dfinal_state  [batch, nheads, d_v, d_k] fp32, or NULL (zero)
- *   dq, dk        [batch, seqlen, nheads_k, d_k] bf16, summed over the value heads of a key head
- *   dv            [batch, seqlen, nheads, d_v] bf16
- *   ddt, dbeta    [batch, seqlen, nheads] bf16: of the raw values
+ *   dq, dk        [batch, seqlen, nheads_k, d_k] element type, summed over the value heads of a key head
+ *   dv            [batch, seqlen, nheads, d_v] element type
+ *   ddt, dbeta    [batch, seqlen, nheads] element type: of the raw values
  *   dA, ddt_bias  [nheads] fp32, summed over batch and tokens; ddt_bias may be NULL (and
  *                 must be without dt_bias)
  *   dh_init       [batch, nheads, d_v, d_k] fp32, or NULL
  * Every output is written; behind a sequence's end the tokens' gradients are zero.  The
  * sums are added in a fixed order: the same call gives the same bits.  Outputs overlap
  * neither the inputs nor one another (dh_init may be dfinal_state).
- * Workspace: launch->workspace of at least ss_gdr_bwd_workspace_bytes() bytes (about
- * 230 KB per 64 tokens of a head: the chunks' states and their adjoints), 16-byte
- * aligned; its first word is the status word, as in ss_gdr_fwd.  Errors: as ss_gdr_fwd. */
+ * bf16 runs chunk by chunk on the tensor cores, fp32 and short bf16 sequences token by
+ * token in fp32.  Workspace: launch->workspace of at least ss_gdr_bwd_workspace_bytes()
+ * bytes (about 230 KB per 64 tokens of a head: the chunks' states and their adjoints;
+ * token by token up to 17 KB per token of a head), 16-byte aligned; its first word is the status word, as in ss_gdr_fwd.  Errors: as ss_gdr_fwd. */
 SS_API int ss_gdr_bwd(const void* q, const void* k, const void* v, const void* dt, const float* dt_bias,
                       const float* A, const void* beta, const float* h_init, const int32_t* seqlens,
                       const void* dy, const float* dfinal_state, void* dq, void* dk, void* dv, void* ddt,
                       void* dbeta, float* dA, float* ddt_bias, float* dh_init, float scale, uint32_t flags,
                       const ss_gdr_dims* dims, const ss_launch* launch);
 
-/* Workspace bytes ss_gdr_bwd needs (0 for sizes it would reject, or without SS_BF16). */
+/* Workspace bytes ss_gdr_bwd needs (0 for sizes it would reject). */
 SS_API size_t ss_gdr_bwd_workspace_bytes(const ss_gdr_dims* dims, uint32_t flags);
 
 /* Sizes of a layer norm: `rows` rows of `cols` consecutive values. */

@@ -717,14 +717,12 @@ def ss_gdr_step(state, q, k, v, dt, A, beta, dt_bias=None, *, scale=None, softpl
 def ss_gdr_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, initial_state=None, dfinal_state=None, seqlens=None, *,
                scale=None, softplus=True, beta_sigmoid=True, qk_l2norm=True, grads=None, workspace=None, stream=None,
                sync_check=False, timeout_iters=0, extra_flags=0):
-    """Backward of ss_gdr_fwd (bf16) through libselscan's ss_gdr_bwd.  Its inputs, dy like v and dfinal_state
-    [batch, nheads, d_v, d_k] fp32 or None.  Returns a dict with dq, dk, dv, ddt, dbeta (bf16, shaped like
-    what they are of), dA, ddt_bias (fp32; the latter with dt_bias) and dinitial_state (fp32, with
+    """Backward of ss_gdr_fwd through libselscan's ss_gdr_bwd.  Its inputs, dy like v and dfinal_state
+    [batch, nheads, d_v, d_k] fp32 or None.  Returns a dict with dq, dk, dv, ddt, dbeta (of the type and shape
+    of what they are of), dA, ddt_bias (fp32; the latter with dt_bias) and dinitial_state (fp32, with
     initial_state); `grads` may supply output tensors by name."""
     if q.dim() != 4:
         raise ValueError("q must be [batch, L, nheads_k, d_k]")
-    if q.dtype != torch.bfloat16:
-        raise TypeError(f"ss_gdr_bwd takes bfloat16, got {q.dtype}")
     batch, L = q.shape[:2]
     dims, flags = _gdr_setup(q, k, v, dt, A, beta, dt_bias, q.dtype, softplus, beta_sigmoid, qk_l2norm, (batch, L))
     dev = q.device

@@ -16,7 +16,7 @@ ROOT = os.path.dirname(os.path.dirname(HERE))
 LIB = os.path.join(HERE, "libselscan.so")
 SOURCES = ["selscan.cu", "gdr.cu", "norm.cu"]
 HEADERS = ["common.cuh", "cp_async.cuh", "fwd.cuh", "ssd_tc.cuh", "bwd.cuh", "step.cuh", "block.cuh", "ssd.cuh",
-           "host.cuh", "gdr_rec.cuh", "gdr_tc.cuh", "gdr_bwd.cuh"]
+           "host.cuh", "gdr_rec.cuh", "gdr_rec_bwd.cuh", "gdr_tc.cuh", "gdr_bwd.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 NVCC_FLAGS = [

@@ -3,6 +3,7 @@
 #include "common.cuh"
 #include "gdr_bwd.cuh"
 #include "gdr_rec.cuh"
+#include "gdr_rec_bwd.cuh"
 #include "gdr_tc.cuh"
 #include "host.cuh"
 
@@ -203,22 +204,57 @@ int run_tc(const GdrParams& g, const ss_gdr_dims* d, uint32_t flags, const ss_la
     return d->d_k == 128 ? launch_tc<128>(p, m, stream) : launch_tc<64>(p, m, stream);
 }
 
+// bf16 sequences of at least this many tokens run their backward pass in chunks (token by token against in chunks, d_k =
+// d_v = 128: at 4 tokens 24 / 52 us with 2 items, 39 / 54 with 96, 352 / 388 with 1280; at 8 tokens 33 / 53, 62 / 54 and
+// 646 / 389; at 16 tokens 51 / 53, 104 / 54 and 1238 / 393).
+constexpr int64_t kBwdChunkedFrom = 8;
+
 // The backward pass's workspace: header, records, what the chains keep, the tokens' sums, the items' shares.
+// (Token by token: header, kept states and corrections, the blocks' sums, the items' shares.)
 struct GdrBwdLayout {
+    bool chunks;
     int64_t nchunks;
     size_t rec, keep, dots, part, total;
 };
-GdrBwdLayout gdr_bwd_layout(const ss_gdr_dims* d) {
+GdrBwdLayout gdr_bwd_layout(const ss_gdr_dims* d, uint32_t flags) {
     GdrBwdLayout w{};
     auto al = [](size_t x) { return (x + 1023) & ~static_cast<size_t>(1023); };
     w.nchunks = ceil_div(d->seqlen, gdr::kC);
+    w.chunks = (flags & SS_BF16) && d->seqlen >= kBwdChunkedFrom;
     const size_t items = static_cast<size_t>(d->batch * d->nheads), n = static_cast<size_t>(w.nchunks);
     w.rec = 1024;
+    if (!w.chunks) {
+        const size_t L = static_cast<size_t>(d->seqlen), dv = static_cast<size_t>(d->d_v), dk = static_cast<size_t>(d->d_k);
+        w.keep = w.rec + al(items * ((L + kRecSeg - 1) / kRecSeg) * dv * dk * sizeof(float));
+        w.dots = w.keep + al(items * L * dv * sizeof(float));
+        w.part = w.dots + al(items * (dv / kGdrRecRows) * L * (2 * dk + 4) * sizeof(float));
+        w.total = w.part + al(items * 2 * sizeof(float));
+        return w;
+    }
     w.keep = w.rec + al(items * n * gdr::kRecBwdBytes);
     w.dots = w.keep + al(items * (n + 1) * gdr::kKeepBytes);
     w.part = w.dots + al((4 * items * n * gdr::kC + items * (n + 1)) * sizeof(float));
     w.total = w.part + al(items * 2 * sizeof(float));
     return w;
+}
+
+template <typename IO, int DK>
+int launch_rec_bwd(const GdrRecBwd& p, int dv, float* dA, float* ddt_bias, cudaStream_t stream) {
+    auto rev = ss_gdr_rec_rev_kernel<IO, DK>;
+    constexpr size_t smem = static_cast<size_t>(kRecSeg) * DK / 8 * kGdrRecThreads * sizeof(float);
+    static std::atomic<bool> attr[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || set_smem_limit(rev, smem, attr, dev) != SS_OK) return SS_ERR_CUDA;
+    const int rb = dv / kGdrRecRows;
+    const unsigned items = static_cast<unsigned>(p.g.batch) * static_cast<unsigned>(p.g.H), n = items * static_cast<unsigned>(rb);
+    ss_gdr_rec_keep_kernel<IO, DK><<<n, kGdrRecThreads, 0, stream>>>(p, dv, rb);
+    rev<<<n, kGdrRecThreads, smem, stream>>>(p, dv, rb);
+    const int64_t warps = static_cast<int64_t>(p.g.batch) * p.g.L * p.g.Hk;
+    ss_gdr_rec_fold_kernel<IO, DK><<<static_cast<unsigned>(ceil_div(warps, 4)), 128, 0, stream>>>(p, rb);
+    ss_gdr_rec_gate_kernel<IO><<<items, 256, 0, stream>>>(p, rb, DK);
+    gdr::ss_gdr_head_kernel<<<static_cast<unsigned>(ceil_div(p.g.H, 128)), 128, 0, stream>>>(p.part, p.g.batch, p.g.H, dA,
+                                                                                        ddt_bias);
+    return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
 struct GdrGrads {
@@ -311,8 +347,7 @@ int ss_gdr_step(float* state, const void* q, const void* k, const void* v, const
 }
 
 size_t ss_gdr_bwd_workspace_bytes(const ss_gdr_dims* dims, uint32_t flags) {
-    if (check_gdr(dims, flags) != SS_OK || !(flags & SS_BF16)) return 0;
-    return gdr_bwd_layout(dims).total;
+    return check_gdr(dims, flags) == SS_OK ? gdr_bwd_layout(dims, flags).total : 0;
 }
 
 int ss_gdr_bwd(const void* q, const void* k, const void* v, const void* dt, const float* dt_bias, const float* A,
@@ -322,7 +357,6 @@ int ss_gdr_bwd(const void* q, const void* k, const void* v, const void* dt, cons
     if (!launch) return SS_ERR_INVALID_ARG;
     int rc = check_gdr(dims, flags);
     if (rc != SS_OK) return rc;
-    if (!(flags & SS_BF16)) return SS_ERR_UNSUPPORTED;
     const int64_t L = dims->seqlen, items = dims->batch * dims->nheads;
     if (dims->nheads == 0) return SS_OK;
     if (!A || !dA || (ddt_bias && !dt_bias)) return SS_ERR_INVALID_ARG;
@@ -333,7 +367,7 @@ int ss_gdr_bwd(const void* q, const void* k, const void* v, const void* dt, cons
                           dq, dk, dv, ddt, dbeta, dA, ddt_bias, dh_init};
     for (const void* x : ptrs)
         if (!aligned16(x)) return SS_ERR_INVALID_ARG;
-    if (!launch->workspace || launch->workspace_bytes < gdr_bwd_layout(dims).total || !aligned16(launch->workspace))
+    if (!launch->workspace || launch->workspace_bytes < gdr_bwd_layout(dims, flags).total || !aligned16(launch->workspace))
         return SS_ERR_WORKSPACE;
     cudaStream_t stream = static_cast<cudaStream_t>(launch->stream);
     unsigned char* ws = static_cast<unsigned char*>(launch->workspace);
@@ -347,8 +381,26 @@ int ss_gdr_bwd(const void* q, const void* k, const void* v, const void* dt, cons
             e = dfinal_state ? cudaMemcpyAsync(dh_init, dfinal_state, st, cudaMemcpyDeviceToDevice, stream)
                              : cudaMemsetAsync(dh_init, 0, st, stream);
         if (e != cudaSuccess) return SS_ERR_CUDA;
+    } else if (const GdrBwdLayout w = gdr_bwd_layout(dims, flags); !w.chunks) {
+        GdrRecBwd p{};
+        p.g = gdr_params(q, k, v, dt, dt_bias, A, beta, scale, flags, dims, L);
+        p.g.h_init = h_init;
+        p.g.seqlens = seqlens;
+        p.dy = dy; p.dfinal = dfinal_state; p.dinit = dh_init;
+        p.dq = dq; p.dk = dk; p.dv = dv; p.ddt = ddt; p.dbeta = dbeta;
+        p.keep_s = reinterpret_cast<float*>(ws + w.rec);
+        p.keep_e = reinterpret_cast<float*>(ws + w.keep);
+        p.sums = reinterpret_cast<float*>(ws + w.dots);
+        p.part = reinterpret_cast<float*>(ws + w.part);
+        const int d = static_cast<int>(dims->d_v);
+        if (flags & SS_BF16)
+            rc = dims->d_k == 128 ? launch_rec_bwd<__nv_bfloat16, 128>(p, d, dA, ddt_bias, stream)
+                                  : launch_rec_bwd<__nv_bfloat16, 64>(p, d, dA, ddt_bias, stream);
+        else
+            rc = dims->d_k == 128 ? launch_rec_bwd<float, 128>(p, d, dA, ddt_bias, stream)
+                                  : launch_rec_bwd<float, 64>(p, d, dA, ddt_bias, stream);
+        if (rc != SS_OK) return rc;
     } else {
-        const GdrBwdLayout w = gdr_bwd_layout(dims);
         gdr::Params p{};
         p.g = gdr_params(q, k, v, dt, dt_bias, A, beta, scale, flags, dims, L);
         p.g.h_init = h_init;

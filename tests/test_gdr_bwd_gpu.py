@@ -145,9 +145,8 @@ def test_steps_that_empty_the_state(dt):
 def test_refusals():
     x = gdr_inputs(2, 20, 2, 2, 64, 64, seed=2)
     dy, _ = upstream(x, 1)
-    half = [t.float() if t.dim() > 1 else t for t in call_args(x)]
-    with pytest.raises(TypeError, match="bfloat16"):
-        ss.ss_gdr_bwd(*half, dy.float())
+    with pytest.raises(TypeError, match="float16"):
+        ss.ss_gdr_bwd(x["q"].half(), *call_args(x)[1:], dy)
     with pytest.raises(TypeError, match="dy"):
         ss.ss_gdr_bwd(*call_args(x), dy.float())
     with pytest.raises(ValueError, match="dq"):
