@@ -42,14 +42,15 @@ GdrParams gdr_params(const void* q, const void* k, const void* v, const void* dt
 template <typename IO, int DK>
 void launch_rec(const GdrParams& p, int dv, cudaStream_t stream) {
     // Four rows of the state per thread from 1.25 blocks per SM on, else one.  d_k = d_v = 128, four rows against one:
-    // a decode step 3.0 / 2.3 us at 12 items, 4.2 / 4.0 at 96 (the border is at 93), 4.5 / 4.9 at 144, 206 / 255 at
-    // 10240; 256 tokens in fp32 256 / 185 us at 12 items, 310 / 364 at 96, 1650 / 2430 at 768.
+    // a decode step 2.7 / 2.2 us at 12 items, 4.0 / 3.9 at 96 (the border is at 93), 4.2 / 4.8 at 144, 198 / 224 at
+    // 10240; 256 tokens in fp32 244 / 168 us at 12 items, 313 / 360 at 96, 1374 / 2269 at 768.
     const int64_t items = static_cast<int64_t>(p.batch) * p.H;
     const int big = dv / (kGdrRecRows * 4);
-    if (items * big * 4 >= 5 * sm_count_of_current_device())
-        ss_gdr_rec_kernel<IO, DK, 4><<<static_cast<unsigned>(items * big), kGdrRecThreads, 0, stream>>>(p, dv, big);
-    else
-        ss_gdr_rec_kernel<IO, DK, 1><<<static_cast<unsigned>(items * big * 4), kGdrRecThreads, 0, stream>>>(p, dv, big * 4);
+    const bool many = items * big * 4 >= 5 * sm_count_of_current_device();
+    const int rb = many ? big : 4 * big;
+    auto kern = p.L > 1 ? (many ? ss_gdr_rec_kernel<IO, DK, 4, true> : ss_gdr_rec_kernel<IO, DK, 1, true>)
+                        : (many ? ss_gdr_rec_kernel<IO, DK, 4, false> : ss_gdr_rec_kernel<IO, DK, 1, false>);
+    kern<<<static_cast<unsigned>(items * rb), kGdrRecThreads, 0, stream>>>(p, dv, rb);
 }
 
 int run_rec(const GdrParams& p, const ss_gdr_dims* d, uint32_t flags, cudaStream_t stream) {
@@ -65,8 +66,8 @@ int run_rec(const GdrParams& p, const ss_gdr_dims* d, uint32_t flags, cudaStream
 }
 
 // bf16 sequences of at least this many tokens run in chunks (token by token against in chunks, d_k = d_v = 128: at 8
-// tokens 10 / 21 us with 12 items, 18 / 23 with 96, 96 / 128 with 1280; at 16 tokens 17 / 22, 31 / 23 and 181 / 127; at
-// 24 tokens 24 / 21, 43 / 23 and 264 / 127).
+// tokens 10 / 21 us with 12 items, 16 / 23 with 96, 82 / 128 with 1280; at 16 tokens 15 / 22, 26 / 23 and 154 / 127; at
+// 24 tokens 21 / 21, 36 / 23 and 225 / 127).
 constexpr int64_t kChunkedFrom = 16;
 
 // 4-D map of a [batch, L, heads, d] bf16 tensor, boxes of `cols` x 64 tokens of one head.

@@ -9,8 +9,7 @@
 // Eight lanes share a row, each with the 16-byte quads l, l + 8, ... of it, so that a warp's accesses are
 // whole 128-byte lines and a dot product ends after three shuffles.
 // The decode step is bound by HBM (the fp32 state read and written: 8 d_k d_v bytes a head against 6 d_k d_v
-// operations), so a thread first loads all its rows and then computes: 10240 heads of 128 x 128 in 206 us, 6.5 TB/s.
-// A sequence is bound by a token's latency, 0.7 us at 12 items (no loads ahead: the tokens' vectors come from L1 and L2).
+// operations), so a thread first loads all its rows and then computes.
 #pragma once
 
 #include "common.cuh"
@@ -70,8 +69,12 @@ __device__ __forceinline__ float sum8(float v) {   // over the eight lanes of a 
     return v + __shfl_xor_sync(0xffffffffu, v, 4);
 }
 
-// Grid: x = (b, h) items times blocks of kGdrRecRows * R rows of S.
-template <typename IO, int DK, int R>
+// Grid: x = (b, h) items times blocks of kGdrRecRows * R rows of S.  SEQ: more than one token; a step without the loop
+// takes fewer registers, and more blocks are in flight (10240 heads of 128 x 128: 198 us, 6.8 TB/s, against 206 in bf16,
+// 201 against 234 in fp32).  Bound by HBM there, by a token's latency in a sequence: the sums over a row's lanes
+// run side by side (one after the other: 256 fp32 tokens of 12 items 185 against 172 us, of 768 items 1653 against 1375;
+// with the next token loaded and made ready under this one 184 and 1963).
+template <typename IO, int DK, int R, bool SEQ>
 __global__ void __launch_bounds__(kGdrRecThreads) ss_gdr_rec_kernel(const GdrParams p, int dv, int row_blocks) {
     constexpr int M = DK / 32;   // float4 quads of a row per lane
     const int item = blockIdx.x / row_blocks, rb = blockIdx.x % row_blocks;
@@ -105,41 +108,42 @@ __global__ void __launch_bounds__(kGdrRecThreads) ss_gdr_rec_kernel(const GdrPar
         const float dt = gdr_delta(to_f32(static_cast<const IO*>(p.dt)[tok * p.H + h]), bias, p.softplus);
         const float be = gdr_beta(to_f32(static_cast<const IO*>(p.beta)[tok * p.H + h]), p.sigmoid);
         const float al = expf(dt * A);
-        float kk = 0.0f, qq = 0.0f, kq = 0.0f;
+        // all sums side by side: the lengths enter as factors of the products, not of the vectors
+        float kk = 0.0f, qq = 0.0f, kq = 0.0f, sk[R], sq[R];
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             kk = fmaf(k[m].x, k[m].x, fmaf(k[m].y, k[m].y, fmaf(k[m].z, k[m].z, fmaf(k[m].w, k[m].w, kk))));
             qq = fmaf(q[m].x, q[m].x, fmaf(q[m].y, q[m].y, fmaf(q[m].z, q[m].z, fmaf(q[m].w, q[m].w, qq))));
             kq = fmaf(k[m].x, q[m].x, fmaf(k[m].y, q[m].y, fmaf(k[m].z, q[m].z, fmaf(k[m].w, q[m].w, kq))));
         }
-        kk = sum8(kk);
-        qq = sum8(qq);
-        kq = sum8(kq);
-        // the lengths enter as factors of the products, not of the vectors
-        const float rk = p.l2norm ? 1.0f / sqrtf(kk + kGdrL2Eps) : 1.0f;
-        const float rq = p.scale * (p.l2norm ? 1.0f / sqrtf(qq + kGdrL2Eps) : 1.0f);
-        float dk_[R], dq[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float a = 0.0f, c = 0.0f;
+            sk[r] = sq[r] = 0.0f;
 #pragma unroll
             for (int m = 0; m < M; ++m) {
-                a = fmaf(S[r][m].x, k[m].x, fmaf(S[r][m].y, k[m].y, fmaf(S[r][m].z, k[m].z, fmaf(S[r][m].w, k[m].w, a))));
-                c = fmaf(S[r][m].x, q[m].x, fmaf(S[r][m].y, q[m].y, fmaf(S[r][m].z, q[m].z, fmaf(S[r][m].w, q[m].w, c))));
+                const float4 s = S[r][m];
+                sk[r] = fmaf(s.x, k[m].x, fmaf(s.y, k[m].y, fmaf(s.z, k[m].z, fmaf(s.w, k[m].w, sk[r]))));
+                sq[r] = fmaf(s.x, q[m].x, fmaf(s.y, q[m].y, fmaf(s.z, q[m].z, fmaf(s.w, q[m].w, sq[r]))));
             }
-            dk_[r] = a;
-            dq[r] = c;
         }
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            dk_[r] = sum8(dk_[r]);
-            dq[r] = sum8(dq[r]);
+        for (int o = 1; o < 8; o <<= 1) {
+            kk += __shfl_xor_sync(0xffffffffu, kk, o);
+            qq += __shfl_xor_sync(0xffffffffu, qq, o);
+            kq += __shfl_xor_sync(0xffffffffu, kq, o);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                sk[r] += __shfl_xor_sync(0xffffffffu, sk[r], o);
+                sq[r] += __shfl_xor_sync(0xffffffffu, sq[r], o);
+            }
         }
+        const float rk = p.l2norm ? 1.0f / sqrtf(kk + kGdrL2Eps) : 1.0f;
+        const float rq = p.scale * (p.l2norm ? 1.0f / sqrtf(qq + kGdrL2Eps) : 1.0f);
         IO* yp = static_cast<IO*>(p.y) + (tok * p.H + h) * dv + r0;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const float w = be * rk * fmaf(-al * rk, dk_[r], v[r]);   // β e |k|^-1
-            if (l == 0) yp[r * kGdrRecRows] = from_f32<IO>(rq * fmaf(al, dq[r], kq * w));
+            const float w = be * rk * fmaf(-al * rk, sk[r], v[r]);   // β e / |k|
+            if (l == 0) yp[r * kGdrRecRows] = from_f32<IO>(rq * fmaf(al, sq[r], kq * w));
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 S[r][m].x = fmaf(w, k[m].x, al * S[r][m].x);
@@ -148,6 +152,7 @@ __global__ void __launch_bounds__(kGdrRecThreads) ss_gdr_rec_kernel(const GdrPar
                 S[r][m].w = fmaf(w, k[m].w, al * S[r][m].w);
             }
         }
+        if (!SEQ) break;
     }
     if (p.final_state) {
 #pragma unroll
