@@ -384,7 +384,9 @@ SS_API int ss_gdr_step(float* state, const void* q, const void* k, const void* v
  * sums are added in a fixed order: the same call gives the same bits.  Outputs overlap
  * neither the inputs nor one another (dh_init may be dfinal_state).
  * bf16 runs chunk by chunk on the tensor cores, fp32 and short bf16 sequences token by
- * token in fp32.  Workspace: launch->workspace of at least ss_gdr_bwd_workspace_bytes()
+ * token in fp32.  In chunks dA and ddt_bias, sums of terms of both signs, are off by a
+ * few 1e-6 of themselves, more where they nearly cancel (2^-15 of the terms' absolute
+ * sum at most); token by token as any fp32 sum.  Workspace: launch->workspace of at least ss_gdr_bwd_workspace_bytes()
  * bytes (about 230 KB per 64 tokens of a head: the chunks' states and their adjoints;
  * token by token up to 17 KB per token of a head), 16-byte aligned; its first word is the status word, as in ss_gdr_fwd.  Errors: as ss_gdr_fwd. */
 SS_API int ss_gdr_bwd(const void* q, const void* k, const void* v, const void* dt, const float* dt_bias,
