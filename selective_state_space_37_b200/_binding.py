@@ -262,6 +262,8 @@ def _on_device(fn):
 
 
 def _launch_for(need, dev, stream, workspace, timeout_iters=0, chunk_len=0):
+    """(the call's ss_launch, its workspace): the tensor is the caller's to hold until the library has returned, since
+    the cache may let go of it before (another thread's larger request on the same stream)."""
     sh = _stream_handle(stream, dev)
     if workspace is None:
         # a captured graph gets a workspace of its own, from its memory pool: graphs may be replayed at once,
@@ -274,7 +276,7 @@ def _launch_for(need, dev, stream, workspace, timeout_iters=0, chunk_len=0):
     elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     return ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(timeout_iters),
-                     int(chunk_len))
+                     int(chunk_len)), workspace
 
 
 def fwd_workspace_bytes(batch, seqlen, d_inner, bf16=True, chunk_len=0, d_state=D_STATE):
@@ -676,7 +678,7 @@ def ss_gdr_fwd(q, k, v, dt, A, beta, dt_bias=None, initial_state=None, seqlens=N
     _check(final_state, "final_state", states, torch.float32, dev)
     flags |= (SS_SYNC_CHECK if sync_check else 0) | int(extra_flags)
     need = int(lib().ss_gdr_fwd_workspace_bytes(ctypes.byref(dims), flags, int(chunk_len)))
-    launch = _launch_for(need, dev, stream, workspace, timeout_iters, chunk_len)
+    launch, workspace = _launch_for(need, dev, stream, workspace, timeout_iters, chunk_len)
     rc = lib().ss_gdr_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(beta),
                           _ptr(initial_state), _ptr(seqlens), _ptr(y), _ptr(final_state),
                           dims.d_k ** -0.5 if scale is None else float(scale), flags, ctypes.byref(dims),
@@ -745,7 +747,7 @@ def ss_gdr_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, initial_state=None, dfina
         _check(g[name], name, t.shape, t.dtype, dev)
     flags |= (SS_SYNC_CHECK if sync_check else 0) | int(extra_flags)
     need = int(lib().ss_gdr_bwd_workspace_bytes(ctypes.byref(dims), flags))
-    launch = _launch_for(need, dev, stream, workspace, timeout_iters)
+    launch, workspace = _launch_for(need, dev, stream, workspace, timeout_iters)
     rc = lib().ss_gdr_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(beta),
                           _ptr(initial_state), _ptr(seqlens), _ptr(dy), _ptr(dfinal_state), _ptr(g["dq"]),
                           _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["ddt"]), _ptr(g["dbeta"]), _ptr(g["dA"]),
@@ -810,7 +812,7 @@ def ss_norm_bwd(dy, x, mean, rstd, weight=None, *, dx=None, dweight=None, dbias=
     flags = _io_flag(x) | (SS_SYNC_CHECK if sync_check else 0)
     dims = ss_norm_dims(rows, cols)
     need = int(lib().ss_norm_bwd_workspace_bytes(ctypes.byref(dims), flags))
-    launch = _launch_for(need, dev, stream, workspace)
+    launch, workspace = _launch_for(need, dev, stream, workspace)
     rc = lib().ss_norm_bwd(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(g["dx"]),
                            _ptr(g.get("dweight")), _ptr(g.get("dbias")), flags, ctypes.byref(dims),
                            ctypes.byref(launch))
@@ -840,7 +842,7 @@ def ss_block_fwd_prenorm(hidden, weights, norm_weight=None, norm_bias=None, *, e
     need = int(lib().ss_block_prenorm_scratch_bytes(ctypes.byref(st), batch, L))
     if need == 0:
         raise SelscanError(SS_ERR_INVALID_ARG, "ss_block_fwd_prenorm")
-    launch = _launch_for(need, dev, stream, scratch)
+    launch, scratch = _launch_for(need, dev, stream, scratch)
     rc = lib().ss_block_fwd_prenorm(_ptr(hidden), _ptr(norm_weight), _ptr(norm_bias), float(eps), _ptr(out),
                                     ctypes.byref(st), batch, L, launch.workspace, launch.workspace_bytes,
                                     launch.stream)
