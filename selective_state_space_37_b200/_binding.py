@@ -221,15 +221,25 @@ def workspace_for(nbytes, device, stream_handle):
     """A cached device workspace of at least nbytes for (device, stream).
 
     One buffer per (device, stream), grown when a call needs more; calls on
-    one stream run in order, so they can share it.  A replaced buffer is
-    returned to torch's stream-ordered allocator.  clear_workspaces() drops
-    them all."""
+    one stream run in order (_in_turn keeps host threads' launches apart), so
+    they can share it.  A replaced buffer is returned to torch's
+    stream-ordered allocator.  clear_workspaces() drops them all."""
     key = (device.index, int(stream_handle))
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
         _ws_cache[key] = ws
     return ws
+
+
+_ws_locks = {}
+
+
+def _in_turn(device, stream):
+    """The lock of a (device, stream), held from a call's look-up of the cached workspace to its last launch: a call
+    is several launches on one workspace, and ctypes lets other threads run between them."""
+    key = (device.index, int(_stream_handle(stream, device)))
+    return _ws_locks.get(key) or _ws_locks.setdefault(key, threading.RLock())
 
 
 def clear_workspaces():
@@ -329,19 +339,20 @@ def ss_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, y=None, last_s
     sh = _stream_handle(stream, dev)
     dims = ss_dims(batch, L, d, D_STATE)
     need = int(lib().ss_fwd_workspace_bytes(ctypes.byref(dims), flags, int(chunk_len)))
-    if workspace is None:
-        workspace = workspace_for(need, dev, sh)
-    launch = ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                       int(timeout_iters), int(chunk_len))
-    if initial_state is not None:
-        _check(initial_state, "initial_state", (batch, d, D_STATE), torch.float32, dev)
-        rc = lib().ss_fwd_with_state(_ptr(u), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                                     _ptr(z), _ptr(initial_state), _ptr(y), _ptr(last_state), flags,
-                                     ctypes.byref(dims), ctypes.byref(launch))
-    else:
-        rc = lib().ss_fwd(_ptr(u), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                          _ptr(z), _ptr(y), _ptr(last_state), flags, ctypes.byref(dims),
-                          ctypes.byref(launch))
+    with _in_turn(dev, stream):
+        if workspace is None:
+            workspace = workspace_for(need, dev, sh)
+        launch = ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                           int(timeout_iters), int(chunk_len))
+        if initial_state is not None:
+            _check(initial_state, "initial_state", (batch, d, D_STATE), torch.float32, dev)
+            rc = lib().ss_fwd_with_state(_ptr(u), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+                                         _ptr(z), _ptr(initial_state), _ptr(y), _ptr(last_state), flags,
+                                         ctypes.byref(dims), ctypes.byref(launch))
+        else:
+            rc = lib().ss_fwd(_ptr(u), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+                              _ptr(z), _ptr(y), _ptr(last_state), flags, ctypes.byref(dims),
+                              ctypes.byref(launch))
     if rc != SS_OK:
         raise SelscanError(rc, "ss_fwd")
     return y, last_state
@@ -385,12 +396,13 @@ def ss_fwd_host(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, y=None, l
     sh = _stream_handle(stream, dev)
     dims = ss_dims(batch, L, d, D_STATE)
     need = int(lib().ss_fwd_host_workspace_bytes(ctypes.byref(dims), flags, int(rows_per_slice)))
-    if workspace is None:
-        workspace = workspace_for(need, dev, sh)
-    launch = ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(), 0, 0)
-    rc = lib().ss_fwd_host(_ptr(u), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                           _ptr(z), _ptr(y), _ptr(last_state), flags, ctypes.byref(dims),
-                           ctypes.byref(launch), int(rows_per_slice))
+    with _in_turn(dev, stream):
+        if workspace is None:
+            workspace = workspace_for(need, dev, sh)
+        launch = ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(), 0, 0)
+        rc = lib().ss_fwd_host(_ptr(u), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+                               _ptr(z), _ptr(y), _ptr(last_state), flags, ctypes.byref(dims),
+                               ctypes.byref(launch), int(rows_per_slice))
     if rc != SS_OK:
         raise SelscanError(rc, "ss_fwd_host")
     return y, last_state
@@ -449,13 +461,14 @@ def ss_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, dlast_state=N
     sh = _stream_handle(stream, dev)
     dims = ss_dims(batch, L, d, D_STATE)
     need = int(lib().ss_bwd_workspace_bytes(ctypes.byref(dims), flags))
-    if workspace is None:
-        workspace = workspace_for(need, dev, sh)
-    launch = ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(), 0, int(chunk_len))
-    rc = lib().ss_bwd(_ptr(u), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
-                      _ptr(dy), _ptr(dlast_state), _ptr(g["du"]), _ptr(g["ddelta"]), _ptr(g["dA"]),
-                      _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g.get("dD")), _ptr(g.get("dz")),
-                      _ptr(g.get("ddelta_bias")), flags, ctypes.byref(dims), ctypes.byref(launch))
+    with _in_turn(dev, stream):
+        if workspace is None:
+            workspace = workspace_for(need, dev, sh)
+        launch = ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(), 0, int(chunk_len))
+        rc = lib().ss_bwd(_ptr(u), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+                          _ptr(dy), _ptr(dlast_state), _ptr(g["du"]), _ptr(g["ddelta"]), _ptr(g["dA"]),
+                          _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g.get("dD")), _ptr(g.get("dz")),
+                          _ptr(g.get("ddelta_bias")), flags, ctypes.byref(dims), ctypes.byref(launch))
     if rc != SS_OK:
         raise SelscanError(rc, "ss_bwd")
     return {k: g[k] for k in shapes}
@@ -493,13 +506,14 @@ def ss_fwd_conv(x, conv_w, delta, A, B, C, D=None, z=None, delta_bias=None, conv
     sh = _stream_handle(stream, dev)
     dims = ss_dims(batch, L, d, D_STATE)
     need = int(lib().ss_fwd_workspace_bytes(ctypes.byref(dims), flags, int(chunk_len)))
-    if workspace is None:
-        workspace = workspace_for(need, dev, sh)
-    launch = ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                       int(timeout_iters), int(chunk_len))
-    rc = lib().ss_fwd_conv(_ptr(x), _ptr(conv_w), _ptr(conv_b), _ptr(delta), _ptr(delta_bias), _ptr(A),
-                           _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(y), _ptr(last_state), _ptr(conv_state),
-                           flags, ctypes.byref(dims), ctypes.byref(launch))
+    with _in_turn(dev, stream):
+        if workspace is None:
+            workspace = workspace_for(need, dev, sh)
+        launch = ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                           int(timeout_iters), int(chunk_len))
+        rc = lib().ss_fwd_conv(_ptr(x), _ptr(conv_w), _ptr(conv_b), _ptr(delta), _ptr(delta_bias), _ptr(A),
+                               _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(y), _ptr(last_state), _ptr(conv_state),
+                               flags, ctypes.byref(dims), ctypes.byref(launch))
     if rc != SS_OK:
         raise SelscanError(rc, "ss_fwd_conv")
     return y, last_state
@@ -574,10 +588,11 @@ def ss_block_fwd(hidden, weights, *, out=None, scratch=None, stream=None):
     need = int(lib().ss_block_scratch_bytes(ctypes.byref(st), batch, L))
     if need == 0:
         raise SelscanError(SS_ERR_INVALID_ARG, "ss_block_fwd")
-    if scratch is None:
-        scratch = workspace_for(need, dev, sh)
-    rc = lib().ss_block_fwd(_ptr(hidden), _ptr(out), ctypes.byref(st), batch, L, scratch.data_ptr(),
-                            scratch.numel() * scratch.element_size(), sh)
+    with _in_turn(dev, stream):
+        if scratch is None:
+            scratch = workspace_for(need, dev, sh)
+        rc = lib().ss_block_fwd(_ptr(hidden), _ptr(out), ctypes.byref(st), batch, L, scratch.data_ptr(),
+                                scratch.numel() * scratch.element_size(), sh)
     if rc != SS_OK:
         raise SelscanError(rc, "ss_block_fwd")
     return out
@@ -614,15 +629,16 @@ def ss_ssd_fwd(x, dt, A, B, C, D=None, dt_bias=None, *, softplus=True, y=None, f
     flags = (SS_DELTA_SOFTPLUS if softplus else 0) | (SS_SYNC_CHECK if sync_check else 0) | int(extra_flags)
     dims = ss_ssd_dims(batch, L, H, P, N)
     sh = _stream_handle(stream, dev)
-    if split:
-        if workspace is None:
-            workspace = workspace_for(int(lib().ss_ssd_fwd_workspace_bytes(ctypes.byref(dims), flags)), dev, sh)
-        launch = ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                           int(timeout_iters), int(chunk_len))
-    else:
-        launch = ss_launch(sh, None, 0, int(timeout_iters), int(chunk_len))
-    rc = lib().ss_ssd_fwd(_ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(y),
-                          _ptr(final_state), flags, ctypes.byref(dims), ctypes.byref(launch))
+    with _in_turn(dev, stream):
+        if split:
+            if workspace is None:
+                workspace = workspace_for(int(lib().ss_ssd_fwd_workspace_bytes(ctypes.byref(dims), flags)), dev, sh)
+            launch = ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                               int(timeout_iters), int(chunk_len))
+        else:
+            launch = ss_launch(sh, None, 0, int(timeout_iters), int(chunk_len))
+        rc = lib().ss_ssd_fwd(_ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(y),
+                              _ptr(final_state), flags, ctypes.byref(dims), ctypes.byref(launch))
     if rc != SS_OK:
         raise SelscanError(rc, "ss_ssd_fwd")
     return y, final_state
@@ -678,11 +694,12 @@ def ss_gdr_fwd(q, k, v, dt, A, beta, dt_bias=None, initial_state=None, seqlens=N
     _check(final_state, "final_state", states, torch.float32, dev)
     flags |= (SS_SYNC_CHECK if sync_check else 0) | int(extra_flags)
     need = int(lib().ss_gdr_fwd_workspace_bytes(ctypes.byref(dims), flags, int(chunk_len)))
-    launch, workspace = _launch_for(need, dev, stream, workspace, timeout_iters, chunk_len)
-    rc = lib().ss_gdr_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(beta),
-                          _ptr(initial_state), _ptr(seqlens), _ptr(y), _ptr(final_state),
-                          dims.d_k ** -0.5 if scale is None else float(scale), flags, ctypes.byref(dims),
-                          ctypes.byref(launch))
+    with _in_turn(dev, stream):
+        launch, workspace = _launch_for(need, dev, stream, workspace, timeout_iters, chunk_len)
+        rc = lib().ss_gdr_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(beta),
+                              _ptr(initial_state), _ptr(seqlens), _ptr(y), _ptr(final_state),
+                              dims.d_k ** -0.5 if scale is None else float(scale), flags, ctypes.byref(dims),
+                              ctypes.byref(launch))
     if rc != SS_OK:
         raise SelscanError(rc, "ss_gdr_fwd")
     return y, final_state
@@ -747,13 +764,14 @@ def ss_gdr_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, initial_state=None, dfina
         _check(g[name], name, t.shape, t.dtype, dev)
     flags |= (SS_SYNC_CHECK if sync_check else 0) | int(extra_flags)
     need = int(lib().ss_gdr_bwd_workspace_bytes(ctypes.byref(dims), flags))
-    launch, workspace = _launch_for(need, dev, stream, workspace, timeout_iters)
-    rc = lib().ss_gdr_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(beta),
-                          _ptr(initial_state), _ptr(seqlens), _ptr(dy), _ptr(dfinal_state), _ptr(g["dq"]),
-                          _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["ddt"]), _ptr(g["dbeta"]), _ptr(g["dA"]),
-                          _ptr(g.get("ddt_bias")), _ptr(g.get("dinitial_state")),
-                          dims.d_k ** -0.5 if scale is None else float(scale), flags, ctypes.byref(dims),
-                          ctypes.byref(launch))
+    with _in_turn(dev, stream):
+        launch, workspace = _launch_for(need, dev, stream, workspace, timeout_iters)
+        rc = lib().ss_gdr_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(beta),
+                              _ptr(initial_state), _ptr(seqlens), _ptr(dy), _ptr(dfinal_state), _ptr(g["dq"]),
+                              _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["ddt"]), _ptr(g["dbeta"]), _ptr(g["dA"]),
+                              _ptr(g.get("ddt_bias")), _ptr(g.get("dinitial_state")),
+                              dims.d_k ** -0.5 if scale is None else float(scale), flags, ctypes.byref(dims),
+                              ctypes.byref(launch))
     if rc != SS_OK:
         raise SelscanError(rc, "ss_gdr_bwd")
     return g
@@ -812,10 +830,11 @@ def ss_norm_bwd(dy, x, mean, rstd, weight=None, *, dx=None, dweight=None, dbias=
     flags = _io_flag(x) | (SS_SYNC_CHECK if sync_check else 0)
     dims = ss_norm_dims(rows, cols)
     need = int(lib().ss_norm_bwd_workspace_bytes(ctypes.byref(dims), flags))
-    launch, workspace = _launch_for(need, dev, stream, workspace)
-    rc = lib().ss_norm_bwd(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(g["dx"]),
-                           _ptr(g.get("dweight")), _ptr(g.get("dbias")), flags, ctypes.byref(dims),
-                           ctypes.byref(launch))
+    with _in_turn(dev, stream):
+        launch, workspace = _launch_for(need, dev, stream, workspace)
+        rc = lib().ss_norm_bwd(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(g["dx"]),
+                               _ptr(g.get("dweight")), _ptr(g.get("dbias")), flags, ctypes.byref(dims),
+                               ctypes.byref(launch))
     if rc != SS_OK:
         raise SelscanError(rc, "ss_norm_bwd")
     return g
@@ -842,10 +861,11 @@ def ss_block_fwd_prenorm(hidden, weights, norm_weight=None, norm_bias=None, *, e
     need = int(lib().ss_block_prenorm_scratch_bytes(ctypes.byref(st), batch, L))
     if need == 0:
         raise SelscanError(SS_ERR_INVALID_ARG, "ss_block_fwd_prenorm")
-    launch, scratch = _launch_for(need, dev, stream, scratch)
-    rc = lib().ss_block_fwd_prenorm(_ptr(hidden), _ptr(norm_weight), _ptr(norm_bias), float(eps), _ptr(out),
-                                    ctypes.byref(st), batch, L, launch.workspace, launch.workspace_bytes,
-                                    launch.stream)
+    with _in_turn(dev, stream):
+        launch, scratch = _launch_for(need, dev, stream, scratch)
+        rc = lib().ss_block_fwd_prenorm(_ptr(hidden), _ptr(norm_weight), _ptr(norm_bias), float(eps), _ptr(out),
+                                        ctypes.byref(st), batch, L, launch.workspace, launch.workspace_bytes,
+                                        launch.stream)
     if rc != SS_OK:
         raise SelscanError(rc, "ss_block_fwd_prenorm")
     return out

@@ -1,6 +1,8 @@
 """The binding's workspaces, without a GPU: CPU tensors stand for the device's and a recorder for the library, called
 behind the check for CUDA tensors."""
 import gc
+import threading
+import time
 import weakref
 
 import pytest
@@ -75,3 +77,49 @@ def test_workspace_lives_until_the_library_returns(name, fake, monkeypatch):
     fake(4096, on_call)
     CALLS[name]()
     assert alive == [True]
+
+
+def conv_call():
+    x, g, s = torch.zeros(1, 8, 64), torch.zeros(1, 8, 16), torch.zeros(64)
+    return bd.ss_fwd_conv(x, torch.zeros(64, 4), x, torch.zeros(64, 16), g, g, D=s, z=x, delta_bias=s)
+
+
+def ssd_call():
+    x, h, b = (torch.zeros(1, 8, *s, dtype=torch.bfloat16) for s in ((2, 64), (2,), (64,)))
+    return bd.ss_ssd_fwd(x, h, torch.zeros(2), b, b)
+
+
+SHARED = {**CALLS, "ss_fwd_conv": conv_call, "ss_ssd_fwd": ssd_call}
+
+
+@pytest.mark.parametrize("name", sorted(SHARED))
+def test_host_threads_on_one_stream_launch_in_turn(name, fake):
+    """Two threads' calls on one stream share a workspace: no launch of the second comes between the first one's."""
+    inside, most = [], []
+
+    def on_call(called, args):   # a call's launches take a while, without the interpreter's lock
+        inside.append(called)
+        most.append(len(inside))
+        time.sleep(0.02)
+        inside.pop()
+
+    fake(4096, on_call)
+    threads = [threading.Thread(target=SHARED[n]) for n in (name, "ss_gdr_bwd", name)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(10)
+    assert len(most) == 3 and max(most) == 1
+
+
+def test_streams_do_not_wait_for_one_another(fake, monkeypatch):
+    """The lock is the stream's: a call on another stream goes ahead."""
+    monkeypatch.setattr(bd, "_stream_handle", lambda stream, device: threading.get_ident())
+    both = threading.Barrier(2, timeout=10)
+    fake(4096, lambda called, args: both.wait() and None)
+    threads = [threading.Thread(target=CALLS["ss_norm_bwd"]) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(10)
+    assert not both.broken
