@@ -271,6 +271,15 @@ def _on_device(fn):
     return call
 
 
+def _empty(shape, dtype, dev, stream):
+    """An output of the call, on the call's stream: the allocator may hand out a block of the current stream's that work
+    queued there still uses."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _launch_for(need, dev, stream, workspace, timeout_iters=0, chunk_len=0):
     """(the call's ss_launch, its workspace): the tensor is the caller's to hold until the library has returned, since
     the cache may let go of it before (another thread's larger request on the same stream)."""
@@ -673,7 +682,7 @@ def ss_gdr_fwd(q, k, v, dt, A, beta, dt_bias=None, initial_state=None, seqlens=N
     all the same; d_k, d_v 64 or 128; nheads a multiple of nheads_k); A, dt_bias [nheads] fp32;
     initial_state [batch, nheads, d_v, d_k] fp32 or None; seqlens [batch] int32 on the device or None:
     the tokens of each sequence, the rows of y behind them staying as they were (zero when y is made
-    here).  scale defaults to d_k ** -0.5.  Returns (y, final_state or None); final_state may be
+    here).  With stream=, outputs that the call makes are that stream's.  scale defaults to d_k ** -0.5.  Returns (y, final_state or None); final_state may be
     initial_state."""
     if q.dim() != 4:
         raise ValueError("q must be [batch, L, nheads_k, d_k]")
@@ -684,13 +693,13 @@ def ss_gdr_fwd(q, k, v, dt, A, beta, dt_bias=None, initial_state=None, seqlens=N
     _check(initial_state, "initial_state", states, torch.float32, dev)
     _check(seqlens, "seqlens", (batch,), torch.int32, dev)
     if y is None:
-        y = torch.empty_like(v)
+        y = _empty(v.shape, v.dtype, dev, stream)
         if seqlens is not None:
             with torch.cuda.stream(stream):   # (None: the current one)
                 y.zero_()
     _check(y, "y", v.shape, v.dtype, dev)
     if final_state is None and return_final_state:
-        final_state = torch.empty(states, dtype=torch.float32, device=dev)
+        final_state = _empty(states, torch.float32, dev, stream)
     _check(final_state, "final_state", states, torch.float32, dev)
     flags |= (SS_SYNC_CHECK if sync_check else 0) | int(extra_flags)
     need = int(lib().ss_gdr_fwd_workspace_bytes(ctypes.byref(dims), flags, int(chunk_len)))
@@ -720,7 +729,7 @@ def ss_gdr_step(state, q, k, v, dt, A, beta, dt_bias=None, *, scale=None, softpl
                              (state.shape[0],))
     _check(state, "state", (dims.batch, dims.nheads, dims.d_v, dims.d_k), torch.float32, dev)
     if y is None:
-        y = torch.empty_like(v)
+        y = _empty(v.shape, v.dtype, dev, stream)
     _check(y, "y", v.shape, v.dtype, dev)
     flags |= SS_SYNC_CHECK if sync_check else 0
     launch = ss_launch(_stream_handle(stream, dev), None, 0, 0, 0)
@@ -760,7 +769,7 @@ def ss_gdr_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, initial_state=None, dfina
     g = {}
     for name, t in like.items():
         given = (grads or {}).get(name)
-        g[name] = torch.empty_like(t) if given is None else given
+        g[name] = _empty(t.shape, t.dtype, dev, stream) if given is None else given
         _check(g[name], name, t.shape, t.dtype, dev)
     flags |= (SS_SYNC_CHECK if sync_check else 0) | int(extra_flags)
     need = int(lib().ss_gdr_bwd_workspace_bytes(ctypes.byref(dims), flags))
@@ -791,10 +800,10 @@ def ss_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, y=None, stats=True, stre
     _check(weight, "weight", (cols,), torch.float32, dev)
     _check(bias, "bias", (cols,), torch.float32, dev)
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, x.dtype, dev, stream)
     _check(y, "y", x.shape, x.dtype, dev)
-    mean = torch.empty(rows, dtype=torch.float32, device=dev) if stats else None
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if stats else None
+    mean = _empty((rows,), torch.float32, dev, stream) if stats else None
+    rstd = _empty((rows,), torch.float32, dev, stream) if stats else None
     flags = _io_flag(x) | (SS_SYNC_CHECK if sync_check else 0)
     dims = ss_norm_dims(rows, cols)
     launch = ss_launch(_stream_handle(stream, dev), None, 0, 0, 0)
@@ -821,11 +830,11 @@ def ss_norm_bwd(dy, x, mean, rstd, weight=None, *, dx=None, dweight=None, dbias=
     _check(mean, "mean", (rows,), torch.float32, dev)
     _check(rstd, "rstd", (rows,), torch.float32, dev)
     _check(weight, "weight", (cols,), torch.float32, dev)
-    g = {"dx": torch.empty_like(x) if dx is None else dx}
+    g = {"dx": _empty(x.shape, x.dtype, dev, stream) if dx is None else dx}
     _check(g["dx"], "dx", x.shape, x.dtype, dev)
     if sums:
         for name, t in (("dweight", dweight), ("dbias", dbias)):
-            g[name] = torch.empty(cols, dtype=torch.float32, device=dev) if t is None else t
+            g[name] = _empty((cols,), torch.float32, dev, stream) if t is None else t
             _check(g[name], name, (cols,), torch.float32, dev)
     flags = _io_flag(x) | (SS_SYNC_CHECK if sync_check else 0)
     dims = ss_norm_dims(rows, cols)
@@ -856,7 +865,7 @@ def ss_block_fwd_prenorm(hidden, weights, norm_weight=None, norm_bias=None, *, e
     _check(norm_weight, "norm_weight", (d_model,), torch.float32, dev)
     _check(norm_bias, "norm_bias", (d_model,), torch.float32, dev)
     if out is None:
-        out = torch.empty_like(hidden)
+        out = _empty(hidden.shape, hidden.dtype, dev, stream)
     _check(out, "out", (batch, L, d_model), torch.bfloat16, dev)
     need = int(lib().ss_block_prenorm_scratch_bytes(ctypes.byref(st), batch, L))
     if need == 0:

@@ -1,5 +1,6 @@
 """The binding's workspaces, without a GPU: CPU tensors stand for the device's and a recorder for the library, called
 behind the check for CUDA tensors."""
+import contextlib
 import gc
 import threading
 import time
@@ -123,3 +124,47 @@ def test_streams_do_not_wait_for_one_another(fake, monkeypatch):
     for t in threads:
         t.join(10)
     assert not both.broken
+
+
+class FakeStream:
+    cuda_stream = 7
+
+
+OUTPUTS = {
+    "ss_gdr_fwd": (lambda **kw: bd.ss_gdr_fwd.__wrapped__(*gdr_args(), seqlens=torch.zeros(1, dtype=torch.int32), **kw), 2),
+    "ss_gdr_bwd": (lambda **kw: bd.ss_gdr_bwd.__wrapped__(*gdr_args(), torch.zeros(1, 20, 2, 64), **kw), 6),
+    "ss_gdr_step": (lambda **kw: bd.ss_gdr_step.__wrapped__(torch.zeros(1, 2, 64, 64), *(t[:, 0].contiguous() if t.dim() > 1 else t
+                                                                                      for t in gdr_args()), **kw), 1),
+    "ss_norm_fwd": (lambda **kw: bd.ss_norm_fwd.__wrapped__(torch.zeros(4, 8), **kw), 3),
+    "ss_norm_bwd": (lambda **kw: bd.ss_norm_bwd.__wrapped__(*norm_args(), **kw), 3)}
+
+
+@pytest.mark.parametrize("name", sorted(OUTPUTS))
+def test_outputs_are_made_on_the_calls_stream(name, fake, monkeypatch):
+    """The allocator's blocks belong to a stream: every tensor that a call makes comes from the stream it launches on."""
+    call, count = OUTPUTS[name]
+    on, made = [], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        on.append(s)
+        try:
+            yield
+        finally:
+            on.pop()
+
+    def tracked(fn):
+        def make(*a, **kw):
+            made.append(on[-1] if on else None)
+            return fn(*a, **kw)
+        return make
+
+    fake(4096, lambda called, args: None)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    for n in ("empty", "empty_like", "zeros", "zeros_like"):
+        monkeypatch.setattr(torch, n, tracked(getattr(torch, n)))
+    st = FakeStream()
+    call(stream=st)   # (the inputs' own torch.zeros come first, on no stream)
+    ours = made[len([m for m in made if m is None]):]
+    assert made == [None] * (len(made) - len(ours)) + ours and set(ours) == {st}
+    assert len(ours) >= count   # (and the workspace)

@@ -61,3 +61,24 @@ def test_two_threads_on_one_stream():
     for i in range(2):
         for again in got[i]:
             assert all(torch.equal(a, b) for g, w in zip(again, want[i]) for a, b in zip(g, w))
+
+
+@pytest.mark.parametrize("call", [gdr_call(200, 3), norm_call(500, 640, 4)], ids=["delta rule", "norm"])
+def test_outputs_on_another_stream_leave_pending_work_alone(call):
+    """Blocks freed while work queued on the current stream still reads them are not what a call on another stream
+    writes to."""
+    want = call()
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    call(stream=st)   # (the inputs' copies are done; the stream's own workspace exists)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        old = [torch.full_like(t, 7) for t in want]
+        torch.cuda._sleep(20_000_000)                       # some 10 ms: the copies below wait behind it
+        copies = [t.clone() for t in old]
+        del old
+        got = call(stream=st)
+        st.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        torch.cuda.synchronize()
+        assert all(bool((c == 7).all()) for c in copies)
