@@ -63,10 +63,11 @@ def test_two_threads_on_one_stream():
             assert all(torch.equal(a, b) for g, w in zip(again, want[i]) for a, b in zip(g, w))
 
 
-@pytest.mark.parametrize("call", [gdr_call(200, 3), norm_call(500, 640, 4)], ids=["delta rule", "norm"])
-def test_outputs_on_another_stream_leave_pending_work_alone(call):
+@pytest.mark.parametrize("make", [lambda: gdr_call(200, 3), lambda: norm_call(500, 640, 4)], ids=["delta rule", "norm"])
+def test_outputs_on_another_stream_leave_pending_work_alone(make):
     """Blocks freed while work queued on the current stream still reads them are not what a call on another stream
     writes to."""
+    call = make()
     want = call()
     torch.cuda.synchronize()
     st = torch.cuda.Stream()
