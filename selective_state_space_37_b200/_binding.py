@@ -335,24 +335,20 @@ def ss_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, y=None, last_s
     _check(D, "D", (d,), torch.float32, dev)
     _check(delta_bias, "delta_bias", (d,), torch.float32, dev)
     if y is None:
-        y = torch.empty((batch, L, d), dtype=io, device=dev)
+        y = _empty((batch, L, d), io, dev, stream)
     _check(y, "y", (batch, L, d), io, dev)
     if last_state is None and return_last_state:
-        last_state = torch.empty((batch, d, D_STATE), dtype=torch.float32, device=dev)
+        last_state = _empty((batch, d, D_STATE), torch.float32, dev, stream)
     _check(last_state, "last_state", (batch, d, D_STATE), torch.float32, dev)
     flags = _io_flag(u) | (SS_DELTA_SOFTPLUS if softplus else 0) | int(extra_flags)
     if force_general_A:
         flags |= SS_FORCE_GENERAL_A
     if sync_check:
         flags |= SS_SYNC_CHECK
-    sh = _stream_handle(stream, dev)
     dims = ss_dims(batch, L, d, D_STATE)
     need = int(lib().ss_fwd_workspace_bytes(ctypes.byref(dims), flags, int(chunk_len)))
     with _in_turn(dev, stream):
-        if workspace is None:
-            workspace = workspace_for(need, dev, sh)
-        launch = ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                           int(timeout_iters), int(chunk_len))
+        launch, workspace = _launch_for(need, dev, stream, workspace, timeout_iters, chunk_len)
         if initial_state is not None:
             _check(initial_state, "initial_state", (batch, d, D_STATE), torch.float32, dev)
             rc = lib().ss_fwd_with_state(_ptr(u), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
@@ -402,13 +398,10 @@ def ss_fwd_host(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, y=None, l
         last_state = torch.empty((batch, d, D_STATE), dtype=torch.float32, pin_memory=pin)
     _check(last_state, "last_state", (batch, d, D_STATE), torch.float32, host)
     flags = _io_flag(u) | (SS_DELTA_SOFTPLUS if softplus else 0) | (SS_SYNC_CHECK if sync_check else 0)
-    sh = _stream_handle(stream, dev)
     dims = ss_dims(batch, L, d, D_STATE)
     need = int(lib().ss_fwd_host_workspace_bytes(ctypes.byref(dims), flags, int(rows_per_slice)))
     with _in_turn(dev, stream):
-        if workspace is None:
-            workspace = workspace_for(need, dev, sh)
-        launch = ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(), 0, 0)
+        launch, workspace = _launch_for(need, dev, stream, workspace)
         rc = lib().ss_fwd_host(_ptr(u), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                                _ptr(z), _ptr(y), _ptr(last_state), flags, ctypes.byref(dims),
                                ctypes.byref(launch), int(rows_per_slice))
@@ -464,16 +457,13 @@ def ss_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, dlast_state=N
         shapes["ddelta_bias"] = ((d,), torch.float32)
     for k, (shp, dt) in shapes.items():
         if k not in g:
-            g[k] = torch.empty(shp, dtype=dt, device=dev)
+            g[k] = _empty(shp, dt, dev, stream)
         _check(g[k], k, shp, dt, dev)
     flags = _io_flag(u) | (SS_DELTA_SOFTPLUS if softplus else 0) | (SS_SYNC_CHECK if sync_check else 0)
-    sh = _stream_handle(stream, dev)
     dims = ss_dims(batch, L, d, D_STATE)
     need = int(lib().ss_bwd_workspace_bytes(ctypes.byref(dims), flags))
     with _in_turn(dev, stream):
-        if workspace is None:
-            workspace = workspace_for(need, dev, sh)
-        launch = ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(), 0, int(chunk_len))
+        launch, workspace = _launch_for(need, dev, stream, workspace, 0, chunk_len)
         rc = lib().ss_bwd(_ptr(u), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
                           _ptr(dy), _ptr(dlast_state), _ptr(g["du"]), _ptr(g["ddelta"]), _ptr(g["dA"]),
                           _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g.get("dD")), _ptr(g.get("dz")),
@@ -506,20 +496,16 @@ def ss_fwd_conv(x, conv_w, delta, A, B, C, D=None, z=None, delta_bias=None, conv
     _check(delta_bias, "delta_bias", (d,), torch.float32, dev)
     _check(conv_state, "conv_state", (batch, d, 3), torch.float32, dev)
     if y is None:
-        y = torch.empty((batch, L, d), dtype=io, device=dev)
+        y = _empty((batch, L, d), io, dev, stream)
     _check(y, "y", (batch, L, d), io, dev)
     if last_state is None and return_last_state:
-        last_state = torch.empty((batch, d, D_STATE), dtype=torch.float32, device=dev)
+        last_state = _empty((batch, d, D_STATE), torch.float32, dev, stream)
     _check(last_state, "last_state", (batch, d, D_STATE), torch.float32, dev)
     flags = _io_flag(x) | (SS_DELTA_SOFTPLUS if softplus else 0) | (SS_SYNC_CHECK if sync_check else 0)
-    sh = _stream_handle(stream, dev)
     dims = ss_dims(batch, L, d, D_STATE)
     need = int(lib().ss_fwd_workspace_bytes(ctypes.byref(dims), flags, int(chunk_len)))
     with _in_turn(dev, stream):
-        if workspace is None:
-            workspace = workspace_for(need, dev, sh)
-        launch = ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                           int(timeout_iters), int(chunk_len))
+        launch, workspace = _launch_for(need, dev, stream, workspace, timeout_iters, chunk_len)
         rc = lib().ss_fwd_conv(_ptr(x), _ptr(conv_w), _ptr(conv_b), _ptr(delta), _ptr(delta_bias), _ptr(A),
                                _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(y), _ptr(last_state), _ptr(conv_state),
                                flags, ctypes.byref(dims), ctypes.byref(launch))
@@ -546,7 +532,7 @@ def ss_step_conv(state, conv_state, x, conv_w, delta, A, B, C, D=None, z=None, d
     _check(D, "D", (d,), torch.float32, dev)
     _check(delta_bias, "delta_bias", (d,), torch.float32, dev)
     if y is None:
-        y = torch.empty((batch, d), dtype=io, device=dev)
+        y = _empty((batch, d), io, dev, stream)
     flags = _io_flag(x) | (SS_DELTA_SOFTPLUS if softplus else 0) | (SS_SYNC_CHECK if sync_check else 0)
     sh = _stream_handle(stream, dev)
     dims = ss_dims(batch, 1, d, D_STATE)
@@ -591,17 +577,15 @@ def ss_block_fwd(hidden, weights, *, out=None, scratch=None, stream=None):
         raise ValueError("hidden's last dimension must equal d_model")
     _check(hidden, "hidden", (batch, L, d_model), torch.bfloat16, dev)
     if out is None:
-        out = torch.empty_like(hidden)
+        out = _empty(hidden.shape, hidden.dtype, dev, stream)
     _check(out, "out", (batch, L, d_model), torch.bfloat16, dev)
-    sh = _stream_handle(stream, dev)
     need = int(lib().ss_block_scratch_bytes(ctypes.byref(st), batch, L))
     if need == 0:
         raise SelscanError(SS_ERR_INVALID_ARG, "ss_block_fwd")
     with _in_turn(dev, stream):
-        if scratch is None:
-            scratch = workspace_for(need, dev, sh)
-        rc = lib().ss_block_fwd(_ptr(hidden), _ptr(out), ctypes.byref(st), batch, L, scratch.data_ptr(),
-                                scratch.numel() * scratch.element_size(), sh)
+        launch, scratch = _launch_for(need, dev, stream, scratch)
+        rc = lib().ss_block_fwd(_ptr(hidden), _ptr(out), ctypes.byref(st), batch, L, launch.workspace,
+                                launch.workspace_bytes, launch.stream)
     if rc != SS_OK:
         raise SelscanError(rc, "ss_block_fwd")
     return out
@@ -630,20 +614,18 @@ def ss_ssd_fwd(x, dt, A, B, C, D=None, dt_bias=None, *, softplus=True, y=None, f
     _check(D, "D", (H,), torch.float32, dev)
     _check(dt_bias, "dt_bias", (H,), torch.float32, dev)
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, x.dtype, dev, stream)
     _check(y, "y", (batch, L, H, P), bf, dev)
     if final_state is None and return_final_state:
-        final_state = torch.empty((batch, H, P, N), dtype=torch.float32, device=dev)
+        final_state = _empty((batch, H, P, N), torch.float32, dev, stream)
     _check(final_state, "final_state", (batch, H, P, N), torch.float32, dev)
     flags = (SS_DELTA_SOFTPLUS if softplus else 0) | (SS_SYNC_CHECK if sync_check else 0) | int(extra_flags)
     dims = ss_ssd_dims(batch, L, H, P, N)
     sh = _stream_handle(stream, dev)
     with _in_turn(dev, stream):
         if split:
-            if workspace is None:
-                workspace = workspace_for(int(lib().ss_ssd_fwd_workspace_bytes(ctypes.byref(dims), flags)), dev, sh)
-            launch = ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                               int(timeout_iters), int(chunk_len))
+            need = int(lib().ss_ssd_fwd_workspace_bytes(ctypes.byref(dims), flags))
+            launch, workspace = _launch_for(need, dev, stream, workspace, timeout_iters, chunk_len)
         else:
             launch = ss_launch(sh, None, 0, int(timeout_iters), int(chunk_len))
         rc = lib().ss_ssd_fwd(_ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(y),
@@ -911,7 +893,7 @@ def ss_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, y=None
     _check(D, "D", (d,), torch.float32, dev)
     _check(delta_bias, "delta_bias", (d,), torch.float32, dev)
     if y is None:
-        y = torch.empty((batch, d), dtype=io, device=dev)
+        y = _empty((batch, d), io, dev, stream)
     _check(y, "y", (batch, d), io, dev)
     flags = _io_flag(u) | (SS_DELTA_SOFTPLUS if softplus else 0) | (SS_SYNC_CHECK if sync_check else 0)
     sh = _stream_handle(stream, dev)

@@ -80,14 +80,14 @@ def test_workspace_lives_until_the_library_returns(name, fake, monkeypatch):
     assert alive == [True]
 
 
-def conv_call():
+def conv_call(**kw):
     x, g, s = torch.zeros(1, 8, 64), torch.zeros(1, 8, 16), torch.zeros(64)
-    return bd.ss_fwd_conv(x, torch.zeros(64, 4), x, torch.zeros(64, 16), g, g, D=s, z=x, delta_bias=s)
+    return bd.ss_fwd_conv(x, torch.zeros(64, 4), x, torch.zeros(64, 16), g, g, D=s, z=x, delta_bias=s, **kw)
 
 
-def ssd_call():
+def ssd_call(**kw):
     x, h, b = (torch.zeros(1, 8, *s, dtype=torch.bfloat16) for s in ((2, 64), (2,), (64,)))
-    return bd.ss_ssd_fwd(x, h, torch.zeros(2), b, b)
+    return bd.ss_ssd_fwd(x, h, torch.zeros(2), b, b, **kw)
 
 
 SHARED = {**CALLS, "ss_fwd_conv": conv_call, "ss_ssd_fwd": ssd_call}
@@ -135,6 +135,7 @@ OUTPUTS = {
     "ss_gdr_bwd": (lambda **kw: bd.ss_gdr_bwd.__wrapped__(*gdr_args(), torch.zeros(1, 20, 2, 64), **kw), 6),
     "ss_gdr_step": (lambda **kw: bd.ss_gdr_step.__wrapped__(torch.zeros(1, 2, 64, 64), *(t[:, 0].contiguous() if t.dim() > 1 else t
                                                                                       for t in gdr_args()), **kw), 1),
+    "ss_fwd_conv": (conv_call, 2), "ss_ssd_fwd": (ssd_call, 2),
     "ss_norm_fwd": (lambda **kw: bd.ss_norm_fwd.__wrapped__(torch.zeros(4, 8), **kw), 3),
     "ss_norm_bwd": (lambda **kw: bd.ss_norm_bwd.__wrapped__(*norm_args(), **kw), 3)}
 
@@ -168,3 +169,12 @@ def test_outputs_are_made_on_the_calls_stream(name, fake, monkeypatch):
     ours = made[len([m for m in made if m is None]):]
     assert made == [None] * (len(made) - len(ours)) + ours and set(ours) == {st}
     assert len(ours) >= count   # (and the workspace)
+
+
+@pytest.mark.parametrize("name", sorted(SHARED))
+def test_captured_calls_have_workspaces_of_their_own(name, fake, monkeypatch):
+    """Graphs may be replayed at once, and the cached buffer may be replaced: a capture leaves the cache alone."""
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    fake(4096, lambda called, args: None)
+    SHARED[name]()
+    assert not bd._ws_cache
