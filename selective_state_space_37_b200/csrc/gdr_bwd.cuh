@@ -12,12 +12,14 @@
 //   M^P_ij = (dO_i·E_j) e^{G_i - G_j} β_j (j <= i),   M^A_ij = -(dV_i·E_j) e^{G_i - G_j} β_j (j < i)
 //   dQ̂ = [diag(e^G) dO S + M^P K̂]
 //   dK̂ = [-diag(e^G) dV S + M^A K̂] + [diag(β e^{G_end - G}) E dS + M^Pᵀ Q̂ + M^Aᵀ K̂]
-// For the gates: a token's decay stands in every path that crosses it, so the gradient of log α changes from a token
-// to the next by what ends and what begins there.  With R_t = q̂_t·dq̂_t + k̂_t·(the first bracket of dk̂_t), where
-// paths end, and C_t = k̂_t·(the second), where they begin, and S, dS at the chunk's start:
-//   dlog α_0 = <S, dS>,   dlog α_t+1 = dlog α_t - R_t + C_t,        dβ_j = dV_j·E_j / β_j
-// Every term carries its decay, so a head that forgets fast has small terms and not the difference of large ones (as
-// Σ (dO·Y - dV·V), which is the same sum, would be); and each chunk starts from its own <S, dS>.
+// For the gates: a token's decay stands in every path that crosses it, and log α's gradient is the sum of those paths:
+//   dlog α_t = e^{G_end} <S, dS> + Σ_{i>=t} r_i + Σ_{j<t} c_j + Σ_{i>=t>j} W_ij,        dβ_j = dV_j·E_j / β_j
+//   r_i = q̂_i·(diag(e^G) dO S)_i - k̂_i·(diag(e^G) dV S)_i           from the entering state to token i
+//   c_j = k̂_j·(diag(β e^{G_end - G}) E dS)_j                       from token j to the leaving state
+//   W_ij = M^P_ij (q̂_i·k̂_j) + M^A_ij (k̂_i·k̂_j)                   from token j to token i
+// Every term holds the factor α_t, so that a head that forgets fast sums small terms.  A running sum of what ends less
+// what begins at each token is the same number, but there the paths that do not cross a token (M^P's diagonal above
+// all) come in and cancel only up to rounding: at Δ A = -29 what was left was ten times the gradient.
 //
 // Precision: fp32 operands enter every product as two bf16 terms, as in the forward, and those that go straight into
 // the adjoint as three; the gates' gradients are sums
@@ -389,18 +391,20 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
 // fp32 registers.  Per value head (M = 128 lanes, two 64-row operands on top of one another; every operand but dO, K
 // and Q in two terms):
 //   D2 [dO; dV] Eᵀ             -> columns 384 .. 447 (K: d_v), read into M^P, M^A (two bf16 terms, shared memory)
+//   D0 [Q; K] Kᵀ               ->         448 .. 511 (K: d_k), for W
 //   D1 [dO; dV] S              ->           0 .. 127 (K: d_v)
 //   D4 [M^P; M^A] K            ->         256 .. 383 (K: 64 tokens)
 //   D5 [M^P; M^A]ᵀ [Q; K]      ->         384 .. 511 (K: 128; lanes 64.. repeat the rows 0..63)
 //   D3 E dS                    ->         128 .. 255 (K: d_v; likewise)
 //   dq~ = qe D1 + D4 (lanes 0..63),   dk~ = ek D1 + D4 (lanes 64..127) + wk D3 + D5 (lanes 0..63)
-// (ek carries the minus of -e^G), and of each token the products of these brackets with its own q and k.  dV comes
+// (ek carries the minus of -e^G), and of each token r, c and the sum of W that crosses it: a row's prefix sums over its
+// columns, added over the rows by shuffles.  dV comes
 // from the chain transposed and is turned in shared memory; dO has no lo terms, so the products with dV's write the
 // lanes from 64 on alone; S and dS pass through one buffer.  Bound by the latency of its stages, one block per SM
 // (218 KB): 8 x 2048 tokens, 12 heads of 128 (3072 blocks) 342 us, 16.5 us a block, 2.7 TB/s, tensor pipe 19 % (512
 // threads: 351 against 346 us).
 constexpr int kGradThreads = 256;
-constexpr uint32_t kGK = 0;                       // [K 0][Q 0][K 1][Q 1]
+constexpr uint32_t kGK = 0;                       // [Q 0][K 0][Q 1][K 1]
 constexpr uint32_t kG1 = 4 * kTile;               // [dO 0][dV hi 0][dO 1][dV hi 1]
 constexpr uint32_t kG2 = 8 * kTile;               // [dV lo 0][dV lo 1]; then [M^P lo][M^A lo]
 constexpr uint32_t kGE = 10 * kTile;              // Eᵀ hi, lo: 128 rows each
@@ -409,7 +413,8 @@ constexpr uint32_t kGS = 14 * kTile;              // S hi, lo; then dS hi, lo (t
 constexpr uint32_t kGM = 22 * kTile;              // dVᵀ hi, lo (128 rows each); then [M^P hi][M^A hi] over hi
 constexpr uint32_t kGScal = 26 * kTile;           // Scal, Local (one copy from the record)
 constexpr uint32_t kGRed = kGScal + 1024 + sizeof(Local);   // row products of the two halves, [3][2][64]
-constexpr uint32_t kGBar = kGRed + 3 * 2 * kC * 4;
+constexpr uint32_t kGCross = kGRed + 3 * 2 * kC * 4;        // W's sums across each token, of [P, A][diagonal, left blocks]
+constexpr uint32_t kGBar = kGCross + 4 * kC * 4;
 constexpr uint32_t kGradSmem = kGBar + 128 + 1024;
 constexpr int kGPitch = 132;
 static_assert(kGradSmem <= 227 * 1024, "shared memory");
@@ -516,8 +521,8 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
     if (tid == 0) {
         mbar_arrive_expect_tx(&bar->qk, 2 * KB * kTile);
         for (int kb = 0; kb < KB; ++kb) {
-            tma_load_4d(base + kGK + (2 * kb) * kTile, &tm_k, 64 * kb, hk, t, b, &bar->qk);
-            tma_load_4d(base + kGK + (2 * kb + 1) * kTile, &tm_q, 64 * kb, hk, t, b, &bar->qk);
+            tma_load_4d(base + kGK + (2 * kb) * kTile, &tm_q, 64 * kb, hk, t, b, &bar->qk);
+            tma_load_4d(base + kGK + (2 * kb + 1) * kTile, &tm_k, 64 * kb, hk, t, b, &bar->qk);
         }
     }
     // Σ over this thread's columns of its row of Q or K (own) times d
@@ -541,7 +546,8 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
     for (int e = 0; e < CN; ++e) acc[e] = 0.0f;
     float* const xch = reinterpret_cast<float*>(gbase + kGS);
     float* const red = reinterpret_cast<float*>(gbase + kGRed);
-    const uint32_t own = base + kGK + (is_k ? 0 : kTile);   // this row of K or Q
+    float* const cross = reinterpret_cast<float*>(gbase + kGCross);
+    const uint32_t own = base + kGK + (is_k ? kTile : 0);   // this row of K or Q
     bool bad = false;
     int stage = 0;   // what thread 0 has in flight, for the wind-down
     for (int j = 0; j < rep; ++j) {
@@ -579,6 +585,11 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
         auto a_hi = [&](int ks) { return sdesc(base + kG1 + (ks >> 2) * 2 * kTile + (ks & 3) * 32u, 16, 1024); };
         auto a_lo = [&](int ks) { return sdesc(base + kG2 - kTile + (ks >> 2) * kTile + (ks & 3) * 32u, 16, 1024); };
         if (tid == 0) {
+#pragma unroll
+            for (int ks = 0; ks < DK / 16; ++ks) {
+                const uint32_t off = base + kGK + (ks >> 2) * 2 * kTile + (ks & 3) * 32u;
+                umma(tmem + 448, sdesc(off, 16, 1024), sdesc(off + kTile, 16, 1024), idesc(kC, false), ks > 0);
+            }
             for (int ks = 0; ks < vs; ++ks) {
                 const uint64_t e = sdesc(base + kGE + 2048u * ks, 0, 1024), el = sdesc(base + kGE + 2 * kTile + 2048u * ks, 0, 1024);
                 umma(tmem + 384, a_hi(ks), e, idesc(kC, true), ks > 0);
@@ -593,11 +604,11 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
             *reinterpret_cast<uint4*>(gp.dv + ((static_cast<int64_t>(b) * g.L + t0 + row) * g.H + h) * p.dv + 8 * q) =
                 lds128(chunk_addr(base + kG1 + (2 * (q >> 3) + 1) * kTile, row, q & 7));
         }
-        // <S, dS> of the entering state: dS's terms from memory, quad by quad in the order of S's image, fetched ahead
-        // in two batches
+        // <S, dS> of the entering state and the leaving one's adjoint: dS's terms from memory, quad by quad in the order
+        // of S's image, fetched ahead in two batches
         uint4 dh[2 * KB], dl[2 * KB];
         auto fetch_ds = [&](int w0) {
-            const unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
+            const unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c + 1) * kKeepBytes;
 #pragma unroll
             for (int w = 0; w < 2 * KB; ++w) {
                 const uint32_t o = 16u * (tid + kGradThreads * (w0 + w));
@@ -619,6 +630,36 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
                     decay_diagonal(v, lo, 32 * rb, lo.gh[i], lo.gl[i], row, i & 31, !is_k);
                 } else {
                     decay_left(v, lo, lo.gh[i], lo.gl[i], row);
+                }
+                // W's sums across the tokens of these columns: each row's prefix sums, in the diagonal block up to its
+                // own token, added over the warp's rows; lane t ends with column t
+                float u[32];
+                tmem_ld32(tl + 448 + 32 * half, u);
+                float s = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const float w = v[e] * u[e];
+                    u[e] = diag && e > lane ? 0.0f : s;
+                    s += w;
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const bool up = lane & o;
+#pragma unroll
+                    for (int e = 0; e < o; ++e) {
+                        const float give = up ? u[e] : u[e + o], keep = up ? u[e + o] : u[e];
+                        u[e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                    }
+                }
+                float* x = cross + (2 * is_k + (diag ? 0 : 1)) * kC;
+                x[32 * half + lane] = u[0];
+                if (!diag) {   // whole rows of the left block, across the tokens 32 .. their own
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const float w = __shfl_down_sync(0xffffffffu, s, o);
+                        if (lane + o < 32) s += w;
+                    }
+                    x[32 + lane] = s;
                 }
             } else {
 #pragma unroll
@@ -664,7 +705,7 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
         if (tid == 0) {
             float s = 0.0f;
             for (int w = 0; w < 8; ++w) s += red[w];
-            p.dots[4 * plane + item * (p.nchunks + 1) + c] = s;
+            p.dots[4 * plane + item * (p.nchunks + 1) + c] = s * sc.end[0];
         }
         if (tid == 0) {
             load_states(item, kKeepBytes + kKeepD, kKeepBytes + kKeepDlo, &bar->d);   // the leaving state's
@@ -689,13 +730,12 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
                 const uint32_t mt = base + (w ? kG2 : kGM);
 #pragma unroll
                 for (int ks = 0; ks < kC / 16; ++ks)
-                    umma(tmem + 256, sdesc(mt + 32u * ks, 16, 1024), sdesc(base + kGK + 2048u * ks, 2 * kTile, 1024),
+                    umma(tmem + 256, sdesc(mt + 32u * ks, 16, 1024), sdesc(base + kGK + kTile + 2048u * ks, 2 * kTile, 1024),
                          idesc(DK, true), w + ks > 0);
 #pragma unroll
-                for (int ks = 0; ks < 2 * kC / 16; ++ks) {   // rows r of [M^P; M^A] with rows r of [Q; K]
-                    const uint32_t qk = base + kGK + (ks < 4 ? kTile : 0) + 2048u * (ks & 3);
-                    umma(tmem + 384, sdesc(mt + 2048u * ks, 0, 1024), sdesc(qk, 2 * kTile, 1024), idesc(DK, true, true), w + ks > 0);
-                }
+                for (int ks = 0; ks < 2 * kC / 16; ++ks)   // rows r of [M^P; M^A] with rows r of [Q; K]
+                    umma(tmem + 384, sdesc(mt + 2048u * ks, 0, 1024), sdesc(base + kGK + 2048u * ks, 2 * kTile, 1024),
+                         idesc(DK, true, true), w + ks > 0);
             }
             umma_commit(&bar->m5);
         }
@@ -723,8 +763,8 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
                 tmem_ld32(tl + 256 + CN * half + e, w);
 #pragma unroll
                 for (int x = 0; x < 32; ++x) {
-                    d[e + x] = fmaf(f1, v[x], w[x]);
-                    acc[e + x] += d[e + x];
+                    d[e + x] = f1 * v[x];
+                    acc[e + x] += d[e + x] + w[x];
                 }
             }
             red[(is_k ? 2 : 0) * kC + half * kC + i] = row_product(own, d);
@@ -739,13 +779,13 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
                 tmem_ld32(tl + 128 + CN * half + e, v);
                 tmem_ld32(tl + 384 + CN * half + e, w);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) d[e + x] = fmaf(f3, v[x], w[x]);
+                for (int x = 0; x < 32; ++x) d[e + x] = f3 * v[x];
 #pragma unroll
                 for (int x = 0; x < 32; x += 4)
                     *reinterpret_cast<float4*>(xch + i * kGPitch + CN * half + e + x) =
-                        make_float4(d[e + x], d[e + x + 1], d[e + x + 2], d[e + x + 3]);
+                        make_float4(d[e + x] + w[x], d[e + x + 1] + w[x + 1], d[e + x + 2] + w[x + 2], d[e + x + 3] + w[x + 3]);
             }
-            red[4 * kC + half * kC + i] = row_product(base + kGK, d);
+            red[4 * kC + half * kC + i] = row_product(base + kGK + kTile, d);
         }
         tc_fence_before();
         __syncthreads();
@@ -758,9 +798,10 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
                 acc[x + 2] += q.z;
                 acc[x + 3] += q.w;
             }
-        } else if (half == 0) {   // q's row product, k's two
-#pragma unroll
-            for (int w = 0; w < 3; ++w) p.dots[w * plane + tok] = red[2 * w * kC + i] + red[(2 * w + 1) * kC + i];
+        } else if (half == 0) {   // r, c, W's sum across the token
+            p.dots[tok] = (red[i] + red[kC + i]) + (red[2 * kC + i] + red[3 * kC + i]);
+            p.dots[plane + tok] = red[4 * kC + i] + red[5 * kC + i];
+            p.dots[2 * plane + tok] = (cross[i] + cross[kC + i]) + (cross[2 * kC + i] + cross[3 * kC + i]);
         }
         fence_proxy_async_smem();   // the exchange was written and read before the next head's loads land there
         __syncthreads();
@@ -834,7 +875,7 @@ struct GateParams {
     float* part;              // [items][2]: this item's share of dA and ddt_bias
 };
 
-// One block per (b, h); a warp per chunk, two tokens per lane, the prefix sum by shuffles.  96 items of 2048 tokens:
+// One block per (b, h); a warp per chunk, two tokens per lane, the sums over tokens by shuffles.  96 items of 2048 tokens:
 // 16 us.
 __global__ void __launch_bounds__(256) ss_gdr_gate_kernel(const __grid_constant__ GateParams gt) {
     const Params& p = gt.p;
@@ -848,24 +889,28 @@ __global__ void __launch_bounds__(256) ss_gdr_gate_kernel(const __grid_constant_
     double sa = 0.0, sb = 0.0;
     for (int64_t c = warp; c < p.nchunks; c += 8) {
         const int64_t t = c * kC + 2 * lane;
-        float r[2], ve[2];
+        float r[2], cb[2], w[2], ve[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {   // what begins at a token less what ends there
+        for (int e = 0; e < 2; ++e) {
             const bool in = t + e < len;
             const float* d = p.dots + item * toks + t + e;
-            r[e] = in ? d[2 * plane] - d[0] - d[plane] : 0.0f;
+            r[e] = in ? d[0] : 0.0f;
+            cb[e] = in ? d[plane] : 0.0f;
+            w[e] = in ? d[2 * plane] : 0.0f;
             ve[e] = in ? d[3 * plane] : 0.0f;
         }
-        float s = r[0] + r[1];   // prefix sums over the lanes
+        float ends = r[0] + r[1], begun = cb[0] + cb[1];   // sums from this lane on, and up to it
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float v = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += v;
+            const float x = __shfl_down_sync(0xffffffffu, ends, o), y = __shfl_up_sync(0xffffffffu, begun, o);
+            if (lane + o < 32) ends += x;
+            if (lane >= o) begun += y;
         }
-        const float before = __shfl_up_sync(0xffffffffu, s, 1);
-        const float start = c * kC < len ? p.dots[4 * plane + item * (p.nchunks + 1) + c] : 0.0f;
-        const float first = start + (lane ? before : 0.0f);
-        float dla[2] = {first, first + r[0]};
+        float after = __shfl_down_sync(0xffffffffu, ends, 1), before = __shfl_up_sync(0xffffffffu, begun, 1);
+        if (lane == 31) after = 0.0f;
+        if (lane == 0) before = 0.0f;
+        const float whole = c * kC < len ? p.dots[4 * plane + item * (p.nchunks + 1) + c] : 0.0f;
+        float dla[2] = {whole + (r[0] + (r[1] + after)) + before + w[0], whole + (r[1] + after) + (before + cb[0]) + w[1]};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             if (t + e >= g.L) continue;
@@ -874,7 +919,7 @@ __global__ void __launch_bounds__(256) ss_gdr_gate_kernel(const __grid_constant_
             if (t + e < len) {
                 const float pre = to_f32(static_cast<const __nv_bfloat16*>(g.dt)[o]) + bias;
                 const float delta = g.softplus ? softplus_accurate(pre) : pre;
-                // where α is zero in fp32 so is its gradient; the sums' rounding would be multiplied by a large Δ
+                // where α is zero in fp32 so is its gradient, which an infinite Δ would make NaN below
                 if (delta * A < -104.0f) dla[e] = 0.0f;
                 ddt = dla[e] * A * (g.softplus ? 1.0f / (1.0f + expf(-pre)) : 1.0f);
                 sa += static_cast<double>(dla[e]) * static_cast<double>(delta);

@@ -95,8 +95,8 @@ struct Params {
     float* seg_map;          // [cut items][nseg - 1][d_k][d_k]: its end from the unit matrix, without values
     // backward pass
     unsigned char* keep;     // [items][nchunks + 1]
-    float* dots;             // [4][items][nchunks * 64] of each token, then [items][nchunks + 1]: <S, dS> of the
-                             // states between the chunks
+    float* dots;             // [4][items][nchunks * 64] of each token, then [items][nchunks + 1]: e^{G_end} <S, dS> of a
+                             // chunk's entering state and its leaving one's adjoint
     const float* dfinal;     // [batch, H, d_v, d_k] or null
     float* dinit;            // [batch, H, d_v, d_k] or null
     uint32_t* status;
