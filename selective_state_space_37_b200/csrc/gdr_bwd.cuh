@@ -163,7 +163,9 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 if (!wait1(&bar->full[s], (n >> 1) & 1)) break;
                 const uint32_t ot = base + kRevOffO;
                 if (!wait1(&bar->o_full, par)) break;
-                if (n == 0 && !wait1(&bar->s_ready[0], 0)) break;   // the tiles' rows behind the end are zero by then
+                // the tiles' rows behind the end are zero by then; R's columns hold the third term of the last step's dO
+                // until its update is done (the state warps take the update up meanwhile)
+                if (n == 0 ? !wait1(&bar->s_ready[0], 0) : !wait1(&bar->ds, par ^ 1)) break;
                 tc_fence_after();
                 // R = dOᵀ P, P's terms side by side (their columns were read before dE's terms were handed over)
 #pragma unroll
@@ -585,6 +587,7 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
         auto a_hi = [&](int ks) { return sdesc(base + kG1 + (ks >> 2) * 2 * kTile + (ks & 3) * 32u, 16, 1024); };
         auto a_lo = [&](int ks) { return sdesc(base + kG2 - kTile + (ks >> 2) * kTile + (ks & 3) * 32u, 16, 1024); };
         if (tid == 0) {
+            tc_fence_after();   // (behind the last head's reads of these columns)
 #pragma unroll
             for (int ks = 0; ks < DK / 16; ++ks) {
                 const uint32_t off = base + kGK + (ks >> 2) * 2 * kTile + (ks & 3) * 32u;
