@@ -359,7 +359,16 @@ int ss_gdr_bwd(const void* q, const void* k, const void* v, const void* dt, cons
     int rc = check_gdr(dims, flags);
     if (rc != SS_OK) return rc;
     const int64_t L = dims->seqlen, items = dims->batch * dims->nheads;
-    if (dims->nheads == 0) return SS_OK;
+    if (dims->nheads == 0) {   // no value head reads the key heads: their gradients are zero
+        const double n = double(dims->batch) * double(L) * double(dims->nheads_k) * double(dims->d_k);
+        if (n == 0.0) return SS_OK;
+        if (n > 2.0e18 || !dq || !dk || !aligned16(dq) || !aligned16(dk)) return SS_ERR_INVALID_ARG;
+        const size_t bytes = static_cast<size_t>(dims->batch * L * dims->nheads_k * dims->d_k) * ((flags & SS_BF16) ? 2 : 4);
+        cudaStream_t stream = static_cast<cudaStream_t>(launch->stream);
+        if (cudaMemsetAsync(dq, 0, bytes, stream) != cudaSuccess || cudaMemsetAsync(dk, 0, bytes, stream) != cudaSuccess)
+            return SS_ERR_CUDA;
+        return ((flags & SS_SYNC_CHECK) && cudaStreamSynchronize(stream) != cudaSuccess) ? SS_ERR_CUDA : SS_OK;
+    }
     if (!A || !dA || (ddt_bias && !dt_bias)) return SS_ERR_INVALID_ARG;
     if (dims->batch > 0 && L > 0 &&
         (!q || !k || !v || !dt || !beta || !dy || !dq || !dk || !dv || !ddt || !dbeta))

@@ -67,3 +67,11 @@ def test_resets_between_slow_tokens():
     x["dt_bias"].fill_(-4.0)
     x["dt"][:, ::9] = 34.0
     check(x, 3)
+
+
+def test_key_heads_that_no_value_head_reads():
+    """No value head: q's and k's gradients are written all the same."""
+    x = gdr_inputs(2, 20, 0, 3, 64, 64, seed=1)
+    g = {n: torch.full_like(x[n[1:]], 7.0) for n in ("dq", "dk")}
+    ss.ss_gdr_bwd(*call_args(x), x["v"], grads=g, sync_check=True)
+    assert not g["dq"].any() and not g["dk"].any()

@@ -204,3 +204,18 @@ def test_binding_checks():
         ss.ss_gdr_fwd(q=x, k=x, v=x, dt=g, A=A, beta=g)
     with pytest.raises(ValueError, match="CUDA"):
         ss.ss_norm_fwd(x=torch.zeros(2, 8))
+
+
+def test_gdr_bwd_without_value_heads(L):
+    """dq and dk are written, so they are asked for; nothing else is."""
+    la = ss.ss_launch(None, None, 0, 0, 0)
+
+    def bwd(hk, dq=None, dk=None, batch=2):
+        a = [None] * 11 + [dq, dk] + [None] * 6
+        return L.ss_gdr_bwd(*(P(v) if v else None for v in a), 1.0, ss.SS_BF16,
+                            ctypes.byref(ss.ss_gdr_dims(batch, 64, 0, hk, 128, 64)), ctypes.byref(la))
+
+    bad = ss.SS_ERR_INVALID_ARG
+    assert bwd(2) == bad and bwd(2, 0x10000) == bad and bwd(2, 0x10000, 0x20004) == bad
+    assert bwd(1 << 60, 0x10000, 0x20000) == bad
+    assert bwd(0) == ss.SS_OK and bwd(2, batch=0) == ss.SS_OK
