@@ -18,11 +18,10 @@
 // state's warps, set the pace: 8 700 cycles a chunk.
 //
 // Precision: q, k, v are bf16 values as given and unit lengths are factors of rows and columns, so they enter
-// exactly.  fp32 operands -- S, X, T, P, E -- enter as two bf16 terms, hi + lo, of 16 bits, and W as three: what the
-// terms of W miss goes straight into the state (2.4e-6 of it on average with two), while S, X and T reach it through
-// products that the decay and the corrections make small (3e-7 together).  One term for P and E would do for y's own
-// rounding, but not where keys repeat: the corrections are then differences of values, and P E cancels most of them.
-// Accumulation is fp32, the state is kept in fp32 registers.
+// exactly.  fp32 operands enter as bf16 terms of 8 bits each: S, X and W as three, hi to third, 24 bits; T, P and E as
+// two.  With two for S and X the state is 1.2e-6 off on average, with three 6e-7 (all of it T's; W with two alone: 2.4e-6).
+// One term for P and E would do for y's own rounding, but not where keys repeat: the corrections are then differences
+// of values, and P E cancels most of them.  Accumulation is fp32, the state is kept in fp32 registers.
 #pragma once
 
 #include "../../include/selscan.h"
@@ -619,9 +618,10 @@ constexpr int kThreads = 32 * (kStoreWarp + 1);
 constexpr int kTok = kC / kParts;      // tokens of a state thread
 constexpr int kStages = 2;             // chunks in flight
 
-// TMEM columns.  A: KS, then X's terms over it, then W's (W's third over QS); B: E in two halves, then its terms over the first; S: the
-// state's terms (of each 16 keys, hi then lo), then dS over them; Y: in two halves.
-constexpr uint32_t kColS = 0, kColA = 128, kColQS = 192, kColB = 256, kColY = 384;
+// TMEM columns.  A: KS, then X's terms over it, then W's (W's third over QS); B: E in two halves, then its terms over the
+// first, and the next state's third terms over the second; S: the state's terms (of each 16 keys, hi then lo), then X's
+// third over them, then dS; Y: in two halves.
+constexpr uint32_t kColS = 0, kColA = 128, kColQS = 192, kColB = 256, kColS3 = kColB + kC, kColY = 384;
 constexpr uint32_t kTmemCols = 512;
 
 // Shared memory: byte offsets from a 1024-aligned base.  A stage: [K 0][Q 0][K 1][Q 1][V 0][V 1][record]; then y
@@ -832,6 +832,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                     const uint64_t bd = sdesc(st + (ks >> 2) * M::kPair + (ks & 3) * 32, 16, 1024);
                     umma_ts(tmem + kColA, tmem + kColS + 16 * ks, bd, idesc(Y ? 2 * kC : kC, false), ks > 0);
                     umma_ts(tmem + kColA, tmem + kColS + 16 * ks + 8, bd, idesc(Y ? 2 * kC : kC, false), 1);
+                    umma_ts(tmem + kColA, tmem + kColS3 + 8 * ks, bd, idesc(Y ? 2 * kC : kC, false), 1);
                 };
                 constexpr int kStep = KH / 16;   // (the rows behind a sequence's end are zeroed before s_ready)
                 if (!wait1(&bar->s_ready[0], par)) break;
@@ -845,7 +846,9 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                     for (int ks = 1; ks < DK / 16; ks += 2) ks_step(ks);
                 }
                 if (!(p.test_drop && blockIdx.x == 0 && c == 0)) umma_commit(&bar->ks);
-                // E = Vᵀ Tᵀ, T's terms side by side, once the last chunk's E is read
+                // E = Vᵀ Tᵀ, T's terms side by side, once the last chunk's E and the state's third terms are read (X is
+                // made meanwhile)
+                if (!wait1(&bar->ks, par)) break;
                 if (Y && c > 0 && !wait1(&bar->pv, (c - 1) & 1)) break;
                 tc_fence_after();
 #pragma unroll
@@ -860,6 +863,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                     const uint64_t bd = sdesc(pr + kRecT + 32u * j, 16, 1024);
                     umma_ts(tmem + kColB, tmem + kColA + 16 * j, bd, idesc(2 * kC, false), unit && j == 0 ? 0 : 1);
                     umma_ts(tmem + kColB, tmem + kColA + 16 * j + 8, bd, idesc(2 * kC, false), 1);
+                    umma_ts(tmem + kColB, tmem + kColS + 8 * j, bd, idesc(2 * kC, false), 1);
                 }
                 umma_commit(&bar->e);
                 if (!wait1(&bar->w_ready, par)) break;
@@ -915,7 +919,8 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             S[k / 2 + 1] = pk2(q.z, q.w);
         }
 #pragma unroll
-        for (int k = 0; k < KH; k += 16) store_terms(tl + kColS + part * KH + k, S + k / 2);
+        for (int k = 0; k < KH; k += 16)
+            store_terms3(tl + kColS + part * KH + k, tl + kColS3 + (part * KH + k) / 2, S + k / 2);
         tmem_wait_st();
         tc_fence_before();
         // the terms of the state that enters chunk c, and those of its E (without y); the stores are one behind another
@@ -981,7 +986,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             f32x2 x[8];
             tmem_ld16(tl + kColA + kTok * part, x);   // X, the factors' sign with it
             scale16(x, sc.ek + kTok * part);
-            store_terms(tl + kColA + kTok * part, x);
+            store_terms3(tl + kColA + kTok * part, tl + kColS + 8 * part, x);
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(&bar->x_ready);
@@ -1033,7 +1038,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 tmem_ld16(tl + kColS + part * KH + k, x);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) S[k / 2 + e] = fma2(pk2(end, end), S[k / 2 + e], x[e]);
-                store_terms(tl + kColS + part * KH + k, S + k / 2);
+                store_terms3(tl + kColS + part * KH + k, tl + kColS3 + (part * KH + k) / 2, S + k / 2);
                 if (c + 1 != ragged && c + 1 < nchunk) {
                     tmem_wait_st();
                     tc_fence_before();
