@@ -21,9 +21,9 @@
 // what begins at each token is the same number, but there the paths that do not cross a token (M^P's diagonal above
 // all) come in and cancel only up to rounding: at Δ A = -29 what was left was ten times the gradient.
 //
-// Precision: fp32 operands enter every product as two bf16 terms, as in the forward, and those that go straight into
-// the adjoint as three; the gates' gradients are sums
-// over all tokens and come out in fp32.
+// Precision: as in the forward, P and T enter as two bf16 terms and what the adjoint's chain carries -- dS, dE, dV, dO's
+// scaled rows -- as three (dS and dE as two: the first state's gradient 1.4e-6 off on average instead of 6e-7).  The
+// gradient kernel's operands enter as two; the gates' gradients are sums over all tokens and come out in fp32.
 #pragma once
 
 #include "gdr_tc.cuh"
@@ -32,9 +32,10 @@ namespace selscan {
 namespace gdr {
 
 // ---------------------------------------------------------------------------------------- the adjoint's chain
-// TMEM columns.  S: dS's terms, then its update; A: K dSᵀ, then dE's terms over it; R: Pᵀ dO in two halves (P's terms);
-// V: Tᵀ dE in two halves, then the terms of -e^G dV over the first and its third over the second; O: the terms of
-// scale e^G dO, its third over R.
+// TMEM columns.  S: dS's terms, then its update; A: K dSᵀ, then dE's terms over it; R: Pᵀ dO in two halves (P's terms),
+// then the third terms of scale e^G dO over the first half and dE's over the second; V: Tᵀ dE in two halves, then the
+// terms of -e^G dV over the first and its third over the second, then the next dS's third terms over the first; O: the
+// terms of scale e^G dO.
 constexpr uint32_t kRevS = 0, kRevA = 128, kRevR = 192, kRevV = 320, kRevO = 448;
 // Shared memory: two stages of [K 0][Q 0][K 1][Q 1][record]; dO (swizzled blocks); two images on their way out, dS's
 // terms and then dVᵀ's.
@@ -176,6 +177,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                     const uint64_t bd = sdesc(st + (ks >> 2) * 2 * kTile + (ks & 3) * 32, 16, 1024);
                     umma_ts(tmem + kRevA, tmem + kRevS + 16 * ks, bd, idesc(kC, false), ks > 0);
                     umma_ts(tmem + kRevA, tmem + kRevS + 16 * ks + 8, bd, idesc(kC, false), 1);
+                    umma_ts(tmem + kRevA, tmem + kRevV + 8 * ks, bd, idesc(kC, false), 1);
                 };
                 constexpr int kStep = KH / 16;
                 if (!wait1(&bar->s_ready[0], par)) break;
@@ -197,6 +199,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                     const uint64_t bd = sdesc(pr + kRecT + 2048u * j, kTile, 1024);
                     umma_ts(tmem + kRevV, tmem + kRevA + 16 * j, bd, idesc(2 * kC, true), j > 0);
                     umma_ts(tmem + kRevV, tmem + kRevA + 16 * j + 8, bd, idesc(2 * kC, true), 1);
+                    umma_ts(tmem + kRevV, tmem + kRevR + kC + 16 * j, bd, idesc(2 * kC, true), 1);
                 }
                 umma_commit(&bar->e);
                 // dS's update: (scale e^G dO)ᵀ Q, then (-e^G dV)ᵀ K, over the columns of dS's terms
@@ -233,7 +236,8 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             S[k / 2 + 1] = pk2(q.z, q.w);
         }
 #pragma unroll
-        for (int k = 0; k < KH; k += 16) store_terms(tl + kRevS + part * KH + k, S + k / 2);
+        for (int k = 0; k < KH; k += 16)
+            store_terms3(tl + kRevS + part * KH + k, tl + kRevV + (part * KH + k) / 2, S + k / 2);
         tmem_wait_st();
         tc_fence_before();
         // a bf16 value of token kTok · part + e, row v, of a swizzled [64][d_v] tile
@@ -311,7 +315,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 for (int e = 0; e < 8; ++e) x[e] = add2(x[e], w[e]);
             }
             tmem_st8(tl + kRevR + kTok * part, third);
-            store_terms(tl + kRevA + kTok * part, x);
+            store_terms3(tl + kRevA + kTok * part, tl + kRevR + kC + kTok * part, x);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -350,7 +354,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 tmem_ld16(tl + kRevS + part * KH + k, x);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) S[k / 2 + e] = fma2(pk2(end, end), S[k / 2 + e], x[e]);
-                store_terms(tl + kRevS + part * KH + k, S + k / 2);
+                store_terms3(tl + kRevS + part * KH + k, tl + kRevV + (part * KH + k) / 2, S + k / 2);
                 if (n + 1 < nchunk) {
                     tmem_wait_st();
                     tc_fence_before();
