@@ -22,8 +22,9 @@
 // all) come in and cancel only up to rounding: at Δ A = -29 what was left was ten times the gradient.
 //
 // Precision: as in the forward, P and T enter as two bf16 terms and what the adjoint's chain carries -- dS, dE, dV, dO's
-// scaled rows -- as three (dS and dE as two: the first state's gradient 1.4e-6 off on average instead of 6e-7).  The
-// gradient kernel's operands enter as two; the gates' gradients are sums over all tokens and come out in fp32.
+// scaled rows -- as three (dS and dE as two: the first state's gradient 1.4e-6 off on average instead of 6e-7).  In the
+// gradient kernel dV and M enter as two, E, S and dS as three, and <S, dS> is a sum of fp32 products: dA and ddt_bias are
+// sums over all tokens of both signs, and come out in fp32 (all of them as two terms: 2e-6 to 3e-5 off).
 #pragma once
 
 #include "gdr_tc.cuh"
@@ -37,8 +38,8 @@ namespace gdr {
 // terms of -e^G dV over the first and its third over the second, then the next dS's third terms over the first; O: the
 // terms of scale e^G dO.
 constexpr uint32_t kRevS = 0, kRevA = 128, kRevR = 192, kRevV = 320, kRevO = 448;
-// Shared memory: two stages of [K 0][Q 0][K 1][Q 1][record]; dO (swizzled blocks); two images on their way out, dS's
-// terms and then dVᵀ's.
+// Shared memory: two stages of [K 0][Q 0][K 1][Q 1][record]; dO (swizzled blocks); an image on its way out, dS in fp32
+// and then dVᵀ's terms.
 constexpr uint32_t kRevStage = 4 * kTile + kRecBytes, kRevOffRec = 4 * kTile;
 constexpr uint32_t kRevOffO = 2 * kRevStage, kRevOffImg = kRevOffO + 2 * kTile, kRevOffBar = kRevOffImg + 8 * kTile;
 constexpr uint32_t kRevSmem = kRevOffBar + 256 + 1024;
@@ -145,8 +146,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 if (n & 1) {
                     bulk_store(kp + kKeepV, base + kRevOffImg, 4 * kTile);
                 } else {
-                    bulk_store(kp + kKeepD, base + kRevOffImg, 2 * KB * kTile);
-                    bulk_store(kp + kKeepDlo, base + kRevOffImg + 4 * kTile, 2 * KB * kTile);
+                    bulk_store(kp + kKeepD, base + kRevOffImg, 4 * KB * kTile);
                 }
                 tc::bulk_commit();
                 tc::bulk_wait_read0();
@@ -250,7 +250,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             if (n > 0 && !wait_warp(&bar->img_free, 1)) return false;
 #pragma unroll
             for (int k = 0; k < KH; k += 16)
-                stage_terms(base + kRevOffImg, base + kRevOffImg + 4 * kTile, v, part * KH + k, S + k / 2);
+                stage_f32(base + kRevOffImg, v, part * KH + k, S + k / 2);
             fence_proxy_async_smem();
             arrive_warp(&bar->img_full);
             return true;
@@ -343,7 +343,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             arrive_warp(&bar->w_ready);
             ok = wait_warp(&bar->img_free, 0);   // dV's terms, store 2 n + 1, while dS is multiplied
             if (!ok) break;
-            stage_terms(base + kRevOffImg, base + kRevOffImg + 2 * kTile, v, kTok * part, x);
+            stage_terms<false>(base + kRevOffImg, v, kTok * part, x);
             fence_proxy_async_smem();
             arrive_warp(&bar->img_full);
             ok = wait_warp(&bar->ds, par);
@@ -395,7 +395,7 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
 // ------------------------------------------------------------------------------------ gradients of q and k
 // One block per (b, key head, chunk); the value heads that share the key head one after the other, their sums in
 // fp32 registers.  Per value head (M = 128 lanes, two 64-row operands on top of one another; every operand but dO, K
-// and Q in two terms):
+// and Q in terms, S and dS made so here):
 //   D2 [dO; dV] Eᵀ             -> columns 384 .. 447 (K: d_v), read into M^P, M^A (two bf16 terms, shared memory)
 //   D0 [Q; K] Kᵀ               ->         448 .. 511 (K: d_k), for W
 //   D1 [dO; dV] S              ->           0 .. 127 (K: d_v)
@@ -411,12 +411,13 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
 // threads: 351 against 346 us).
 constexpr int kGradThreads = 256;
 constexpr uint32_t kGK = 0;                       // [Q 0][K 0][Q 1][K 1]
-constexpr uint32_t kG1 = 4 * kTile;               // [dO 0][dV hi 0][dO 1][dV hi 1]
+constexpr uint32_t kG1 = 4 * kTile;               // [dO 0][dV hi 0][dO 1][dV hi 1]; then dS's third terms
 constexpr uint32_t kG2 = 8 * kTile;               // [dV lo 0][dV lo 1]; then [M^P lo][M^A lo]
 constexpr uint32_t kGE = 10 * kTile;              // Eᵀ hi, lo: 128 rows each
-constexpr uint32_t kGS = 14 * kTile;              // S hi, lo; then dS hi, lo (two blocks of 128 rows each); then dk~'s
-                                                  // other bracket, fp32 [64][132]
-constexpr uint32_t kGM = 22 * kTile;              // dVᵀ hi, lo (128 rows each); then [M^P hi][M^A hi] over hi
+constexpr uint32_t kGS = 14 * kTile;              // S, then dS: fp32 (four 32-wide blocks of 128 rows), then the terms in
+                                                  // place, [hi 0][lo 0][hi 1][lo 1]; then dk~'s other bracket, fp32 [64][132]
+constexpr uint32_t kGM = 22 * kTile;              // dVᵀ hi, lo (128 rows each); E's third terms over lo; S's third terms;
+                                                  // then [M^P hi][M^A hi], and E's third terms again
 constexpr uint32_t kGScal = 26 * kTile;           // Scal, Local (one copy from the record)
 constexpr uint32_t kGRed = kGScal + 1024 + sizeof(Local);   // row products of the two halves, [3][2][64]
 constexpr uint32_t kGCross = kGRed + 3 * 2 * kC * 4;        // W's sums across each token, of [P, A][diagonal, left blocks]
@@ -426,7 +427,7 @@ constexpr int kGPitch = 132;
 static_assert(kGradSmem <= 227 * 1024, "shared memory");
 
 struct GradBars {
-    uint64_t qk, in, s, d, m2, m1, m5, m3, fin;
+    uint64_t qk, in, e3, s, d, m2, m1, m5, m3, fin;
     uint32_t tmem;
 };
 
@@ -456,6 +457,28 @@ __device__ __forceinline__ void umma_upper(uint32_t d, uint64_t a, uint64_t b, u
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%4, %4, %5, %5}, p;\n\t}"
         ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(off), "r"(on)
         : "memory");
+}
+
+// 64 keys of a row of an fp32 image (two 32-wide blocks), and their terms: hi in the first block's place, lo in the
+// second's -- a thread rewrites what it alone has read -- and the third in an image of its own.
+__device__ __forceinline__ void read_row(uint32_t img, int r, f32x2 (&s)[32]) {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+        const uint4 w = lds128(chunk_addr(img + (q >> 3) * 2 * kTile, r, q & 7));
+        s[2 * q] = pk2(__uint_as_float(w.x), __uint_as_float(w.y));
+        s[2 * q + 1] = pk2(__uint_as_float(w.z), __uint_as_float(w.w));
+    }
+}
+__device__ __forceinline__ void write_terms(uint32_t img, uint32_t third, int r, const f32x2 (&s)[32]) {
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        uint32_t a[4], b[4], c[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split3(s[4 * w + e], a[e], b[e], c[e]);
+        sts128(chunk_addr(img, r, w), make_uint4(a[0], a[1], a[2], a[3]));
+        sts128(chunk_addr(img + 2 * kTile, r, w), make_uint4(b[0], b[1], b[2], b[3]));
+        sts128(chunk_addr(third, r, w), make_uint4(c[0], c[1], c[2], c[3]));
+    }
 }
 
 template <int DK>
@@ -492,7 +515,7 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
         return;
     }
     if (tid == 0) {
-        uint64_t* all[] = {&bar->qk, &bar->in, &bar->s, &bar->d, &bar->m2, &bar->m1, &bar->m5, &bar->m3, &bar->fin};
+        uint64_t* all[] = {&bar->qk, &bar->in, &bar->e3, &bar->s, &bar->d, &bar->m2, &bar->m1, &bar->m5, &bar->m3, &bar->fin};
         for (uint64_t* x : all) mbar_init(x, 1);
         fence_mbar_init();
     }
@@ -518,11 +541,9 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
         for (int w = 0; w < vb; ++w) tma_load_4d(base + kG1 + 2 * w * kTile, &tm_o, 64 * w, h, t, b, &bar->in);
         bulk_load(base + kGScal, p.rec + (item * p.nchunks + c) * p.rec_bytes + kRecScal, 1024 + sizeof(Local), &bar->in);
     };
-    auto load_states = [&](int64_t item, uint32_t hi, uint32_t lo_off, uint64_t* f) {
-        const unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes;
-        mbar_arrive_expect_tx(f, 4 * KB * kTile);
-        bulk_load(base + kGS, kp + hi, 2 * KB * kTile, f);
-        bulk_load(base + kGS + 4 * kTile, kp + lo_off, 2 * KB * kTile, f);
+    auto load_e3 = [&](int64_t item, uint64_t* f, uint32_t with) {   // and `with` bytes that the caller loads
+        mbar_arrive_expect_tx(f, 2 * kTile + with);
+        bulk_load(base + kGM + 2 * kTile, p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes + kKeepE3, 2 * kTile, f);
     };
     if (tid == 0) {
         mbar_arrive_expect_tx(&bar->qk, 2 * KB * kTile);
@@ -555,7 +576,7 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
     float* const cross = reinterpret_cast<float*>(gbase + kGCross);
     const uint32_t own = base + kGK + (is_k ? kTile : 0);   // this row of K or Q
     bool bad = false;
-    int stage = 0;   // what thread 0 has in flight, for the wind-down
+    int stage = 0, e3s = 0;   // what thread 0 has in flight, for the wind-down
     for (int j = 0; j < rep; ++j) {
         const int h = hk * rep + j;
         const int64_t item = static_cast<int64_t>(b) * g.H + h;
@@ -567,7 +588,8 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
         };
         if (tid == 0) {
             load_in(item, h);
-            load_states(item, kKeepS, kKeepSlo, &bar->s);
+            mbar_arrive_expect_tx(&bar->s, 4 * KB * kTile);
+            bulk_load(base + kGS, p.keep + (item * (p.nchunks + 1) + c) * kKeepBytes + kKeepS, 4 * KB * kTile, &bar->s);
             stage = 4 * j + 2;
         }
         if (j == 0 && !wait_all(&bar->qk, 0)) break;
@@ -592,6 +614,8 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
         auto a_lo = [&](int ks) { return sdesc(base + kG2 - kTile + (ks >> 2) * kTile + (ks & 3) * 32u, 16, 1024); };
         if (tid == 0) {
             tc_fence_after();   // (behind the last head's reads of these columns)
+            load_e3(item, &bar->e3, 0);
+            e3s = j + 1;
 #pragma unroll
             for (int ks = 0; ks < DK / 16; ++ks) {
                 const uint32_t off = base + kGK + (ks >> 2) * 2 * kTile + (ks & 3) * 32u;
@@ -603,7 +627,6 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
                 umma(tmem + 384, a_hi(ks), el, idesc(kC, true), 1);
                 umma_upper(tmem + 384, a_lo(ks), e, idesc(kC, true));
             }
-            umma_commit(&bar->m2);
         }
         // v's gradient: dV's hi terms are its values rounded to bf16
         for (int w = tid; w < rows * vb * 8; w += kGradThreads) {
@@ -611,19 +634,22 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
             *reinterpret_cast<uint4*>(gp.dv + ((static_cast<int64_t>(b) * g.L + t0 + row) * g.H + h) * p.dv + 8 * q) =
                 lds128(chunk_addr(base + kG1 + (2 * (q >> 3) + 1) * kTile, row, q & 7));
         }
-        // <S, dS> of the entering state and the leaving one's adjoint: dS's terms from memory, quad by quad in the order
-        // of S's image, fetched ahead in two batches
-        uint4 dh[2 * KB], dl[2 * KB];
+        // <S, dS> of the entering state and the leaving one's adjoint: dS from memory, quad by quad in the order of S's
+        // image, fetched ahead in two batches
+        float4 ds[4 * KB];
         auto fetch_ds = [&](int w0) {
-            const unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c + 1) * kKeepBytes;
+            const unsigned char* kp = p.keep + (item * (p.nchunks + 1) + c + 1) * kKeepBytes + kKeepD;
 #pragma unroll
-            for (int w = 0; w < 2 * KB; ++w) {
-                const uint32_t o = 16u * (tid + kGradThreads * (w0 + w));
-                dh[w] = __ldg(reinterpret_cast<const uint4*>(kp + kKeepD + o));
-                dl[w] = __ldg(reinterpret_cast<const uint4*>(kp + kKeepDlo + o));
-            }
+            for (int w = 0; w < 4 * KB; ++w)
+                ds[w] = __ldg(reinterpret_cast<const float4*>(kp + 16u * (tid + kGradThreads * (w0 + w))));
         };
         fetch_ds(0);
+        if (tid == 0 && mbar_wait_bounded(&bar->e3, par, p.wait_ns)) {   // (else the next wait runs out)
+            for (int ks = 0; ks < vs; ++ks)
+                umma(tmem + 384, a_hi(ks), sdesc(base + kGM + 2 * kTile + 2048u * ks, 0, 1024), idesc(kC, true), 1);
+            umma_commit(&bar->m2);
+        }
+        __syncwarp();
         if (!wait_all(&bar->m2, par)) break;
         tc_fence_after();
         float v[32];   // M^P (rows 0..63), M^A (64..127): one 32-column block per thread
@@ -674,39 +700,47 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
             }
         }
         if (!wait_all(&bar->s, par)) break;
-        if (tid == 0) {
-            tc_fence_after();
-            for (int ks = 0; ks < vs; ++ks) {
-                const uint64_t sh = sdesc(base + kGS + 2048u * ks, 2 * kTile, 1024);
-                umma(tmem, a_hi(ks), sh, idesc(DK, true), ks > 0);
-                umma(tmem, a_hi(ks), sdesc(base + kGS + 4 * kTile + 2048u * ks, 2 * kTile, 1024), idesc(DK, true), 1);
-                umma_upper(tmem, a_lo(ks), sh, idesc(DK, true));
-            }
-            umma_commit(&bar->m1);
-        }
         {
             float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
             for (int batch = 0; batch < 2; ++batch) {
 #pragma unroll
-                for (int w = 0; w < 2 * KB; ++w) {
-                    const uint32_t o = 16u * (tid + kGradThreads * (2 * KB * batch + w));
-                    const uint4 sh = lds128(base + kGS + o), sl = lds128(base + kGS + 4 * kTile + o);
-                    const bool in = static_cast<int>((o >> 7) & 127) < p.dv;
-                    const uint32_t a[4] = {dh[w].x, dh[w].y, dh[w].z, dh[w].w}, b2[4] = {dl[w].x, dl[w].y, dl[w].z, dl[w].w};
-                    const uint32_t e2[4] = {sh.x, sh.y, sh.z, sh.w}, f[4] = {sl.x, sl.y, sl.z, sl.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (in) s0 = fmaf(lo_f(a[e]) + lo_f(b2[e]), lo_f(e2[e]) + lo_f(f[e]), s0);
-                        if (in) s1 = fmaf(hi_f(a[e]) + hi_f(b2[e]), hi_f(e2[e]) + hi_f(f[e]), s1);
+                for (int w = 0; w < 4 * KB; ++w) {
+                    const uint32_t o = 16u * (tid + kGradThreads * (4 * KB * batch + w));
+                    const uint4 x = lds128(base + kGS + o);
+                    if (static_cast<int>((o >> 7) & 127) < p.dv) {
+                        s0 = fmaf(__uint_as_float(x.x), ds[w].x, fmaf(__uint_as_float(x.y), ds[w].y, s0));
+                        s1 = fmaf(__uint_as_float(x.z), ds[w].z, fmaf(__uint_as_float(x.w), ds[w].w, s1));
                     }
                 }
-                if (batch == 0) fetch_ds(2 * KB);
+                if (batch == 0) fetch_ds(4 * KB);
             }
             s0 += s1;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
             if (lane == 0) red[warp] = s0;
+        }
+        // S's terms in its place; the third over dVᵀ and E's third, which D2 has read
+        const int half64 = tid >> 7;   // 64 keys of row tid & 127
+        const uint32_t sblk = base + kGS + half64 * 4 * kTile;
+        {
+            f32x2 s[32];
+            if (half64 < KB) read_row(sblk, tid & 127, s);
+            __syncthreads();   // (the products above read other rows)
+            if (half64 < KB) write_terms(sblk, base + kGM + half64 * 2 * kTile, tid & 127, s);
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0) {
+            tc_fence_after();
+            for (int ks = 0; ks < vs; ++ks) {
+                const uint64_t sh = sdesc(base + kGS + 2048u * ks, 4 * kTile, 1024);
+                umma(tmem, a_hi(ks), sh, idesc(DK, true), ks > 0);
+                umma(tmem, a_hi(ks), sdesc(base + kGS + 2 * kTile + 2048u * ks, 4 * kTile, 1024), idesc(DK, true), 1);
+                umma(tmem, a_hi(ks), sdesc(base + kGM + 2048u * ks, 2 * kTile, 1024), idesc(DK, true), 1);
+                umma_upper(tmem, a_lo(ks), sh, idesc(DK, true));
+            }
+            umma_commit(&bar->m1);
         }
         if (!wait_all(&bar->m1, par)) break;   // S and dV's lo terms are read
         if (tid == 0) {
@@ -715,7 +749,8 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
             p.dots[4 * plane + item * (p.nchunks + 1) + c] = s * sc.end[0];
         }
         if (tid == 0) {
-            load_states(item, kKeepBytes + kKeepD, kKeepBytes + kKeepDlo, &bar->d);   // the leaving state's
+            load_e3(item, &bar->d, 4 * KB * kTile);   // and the leaving state's dS
+            bulk_load(base + kGS, p.keep + (item * (p.nchunks + 1) + c + 1) * kKeepBytes + kKeepD, 4 * KB * kTile, &bar->d);
             stage = 4 * j + 3;
         }
 #pragma unroll
@@ -747,13 +782,24 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
             umma_commit(&bar->m5);
         }
         if (!wait_all(&bar->d, par)) break;
+        if (half64 < KB) {   // dS's terms, as S's
+            f32x2 s[32];
+            read_row(sblk, tid & 127, s);
+            write_terms(sblk, base + kG1 + half64 * 2 * kTile, tid & 127, s);
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
         if (tid == 0) {
-            for (int ks = 0; ks < vs; ++ks) {
-                const uint64_t dh = sdesc(base + kGS + 2048u * ks, 2 * kTile, 1024);
+            for (int ks = 0; ks < vs; ++ks) {   // every pair of terms down to 2^-24
+                const uint64_t dh = sdesc(base + kGS + 2048u * ks, 4 * kTile, 1024);
+                const uint64_t dl = sdesc(base + kGS + 2 * kTile + 2048u * ks, 4 * kTile, 1024);
                 const uint64_t e = sdesc(base + kGE + 2048u * ks, 0, 1024), el = sdesc(base + kGE + 2 * kTile + 2048u * ks, 0, 1024);
                 umma(tmem + 128, e, dh, idesc(DK, true, true), ks > 0);
-                umma(tmem + 128, e, sdesc(base + kGS + 4 * kTile + 2048u * ks, 2 * kTile, 1024), idesc(DK, true, true), 1);
+                umma(tmem + 128, e, dl, idesc(DK, true, true), 1);
+                umma(tmem + 128, e, sdesc(base + kG1 + 2048u * ks, 2 * kTile, 1024), idesc(DK, true, true), 1);
                 umma(tmem + 128, el, dh, idesc(DK, true, true), 1);
+                umma(tmem + 128, el, dl, idesc(DK, true, true), 1);
+                umma(tmem + 128, sdesc(base + kGM + 2 * kTile + 2048u * ks, 0, 1024), dh, idesc(DK, true, true), 1);
             }
             umma_commit(&bar->m3);
         }
@@ -862,6 +908,7 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
         const uint32_t ph = static_cast<uint32_t>((stage - 1) >> 2) & 1;
         mbar_wait_bounded(&bar->qk, 0, p.drain_ns);
         mbar_wait_bounded(&bar->in, ph, p.drain_ns);
+        if (e3s) mbar_wait_bounded(&bar->e3, (e3s - 1) & 1, p.drain_ns);
         if ((stage & 3) >= 2) mbar_wait_bounded(&bar->s, ph, p.drain_ns);
         if ((stage & 3) == 3) mbar_wait_bounded(&bar->d, ph, p.drain_ns);
         umma_commit(&bar->fin);

@@ -73,12 +73,11 @@ struct alignas(16) Local {  // what a chunk's decay factors are made of (the bac
 constexpr uint32_t kRecLocal = kRecBytes, kRecBwdBytes = kRecBytes + 2048;
 static_assert(sizeof(Local) <= 2048, "record");
 
-// What the backward pass keeps of a chunk, beside its record: images of tiles in the swizzled layout of the MMAs, each
-// value as two bf16 terms.  Eᵀ, dVᵀ: [128 rows v][64 tokens]; S, the state that enters the chunk, and dS, its adjoint:
-// [128 rows v][d_k keys].  (The state that leaves the last chunk has a place behind it.)
-constexpr uint32_t kKeepE = 0, kKeepElo = 2 * kTile, kKeepV = 4 * kTile, kKeepVlo = 6 * kTile;
-constexpr uint32_t kKeepS = 8 * kTile, kKeepSlo = 12 * kTile, kKeepD = 16 * kTile, kKeepDlo = 20 * kTile;
-constexpr uint32_t kKeepBytes = 24 * kTile;
+// What the backward pass keeps of a chunk, beside its record, as images of tiles with the swizzle of the MMAs.  Eᵀ as
+// three bf16 terms, dVᵀ as two: [128 rows v][64 tokens] each; S, the state that enters the chunk, and dS, its adjoint, in
+// fp32: [128 rows v][32 keys], d_k / 32 times.  (The state that leaves the last chunk has a place behind it.)
+constexpr uint32_t kKeepE = 0, kKeepE3 = 4 * kTile, kKeepV = 6 * kTile, kKeepS = 10 * kTile, kKeepD = 18 * kTile;
+constexpr uint32_t kKeepBytes = 26 * kTile;
 
 struct Params {
     GdrParams g;
@@ -626,7 +625,7 @@ constexpr uint32_t kTmemCols = 512;
 
 // Shared memory: byte offsets from a 1024-aligned base.  A stage: [K 0][Q 0][K 1][Q 1][V 0][V 1][record]; then y
 // [64][d_v] for its store.  Without y there is no Q and of the record only T and the factors, and what is kept is
-// staged for its store: E's two images, then S's.
+// staged for its store: E's three images, then S's.
 template <bool Y>
 struct Smem {
     static constexpr uint32_t kPair = Y ? 2 * kTile : kTile;   // from K's first block of keys to its second
@@ -634,24 +633,41 @@ struct Smem {
     static constexpr uint32_t kFactors = kRec + (Y ? kRecScal : 2 * kTile);
     static constexpr uint32_t kStage = kFactors + sizeof(Scal);
     static constexpr uint32_t kOut = kStages * kStage;
-    static constexpr uint32_t kBar = kOut + (Y ? 2 : 12) * kTile;
+    static constexpr uint32_t kBar = kOut + (Y ? 2 : 14) * kTile;
     static constexpr uint32_t kBytes = kBar + 256 + 1024;
     static_assert(kStage % 1024 == 0 && kBytes <= 227 * 1024, "shared memory");
 };
 
-// 16 values' terms to two images in shared memory (rows of 128 bytes in 64-wide blocks of 128 rows): the 16 columns
-// from `col` on of row r.
-__device__ __forceinline__ void stage_terms(uint32_t hi_img, uint32_t lo_img, int r, int col, const f32x2* v) {
-    uint32_t hi[8], lo[8];
+// A pair as three words of bf16 values.
+__device__ __forceinline__ void split3(f32x2 v, uint32_t& hi, uint32_t& lo, uint32_t& third) {
+    hi = pk(v.x, v.y);
+    split2(fma2(pk2(lo_f(hi), hi_f(hi)), pk2(-1.0f, -1.0f), v), lo, third);
+}
+// 16 values' terms, two or three, to images in shared memory one behind another (128 rows of 128 bytes): the 16 columns
+// from `col` < 64 on of row r.
+template <bool THREE>
+__device__ __forceinline__ void stage_terms(uint32_t img, int r, int col, const f32x2* v) {
+    uint32_t t[3][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) split2(v[e], hi[e], lo[e]);
-    const uint32_t blk = static_cast<uint32_t>(col >> 6) * 2 * kTile;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t o = chunk_addr(blk, r, ((col & 63) >> 3) + h);
-        sts128(hi_img + o, make_uint4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]));
-        sts128(lo_img + o, make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]));
+    for (int e = 0; e < 8; ++e) {
+        if (THREE) split3(v[e], t[0][e], t[1][e], t[2][e]);
+        else split2(v[e], t[0][e], t[1][e]);
     }
+#pragma unroll
+    for (int w = 0; w < (THREE ? 3 : 2); ++w)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            sts128(chunk_addr(img + w * 2 * kTile, r, (col >> 3) + h),
+                   make_uint4(t[w][4 * h], t[w][4 * h + 1], t[w][4 * h + 2], t[w][4 * h + 3]));
+}
+// 16 values in fp32 to an image of 32-wide blocks of 128 rows.
+__device__ __forceinline__ void stage_f32(uint32_t img, int r, int col, const f32x2* v) {
+    const uint32_t blk = img + static_cast<uint32_t>(col >> 5) * 2 * kTile;
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+        sts128(chunk_addr(blk, r, ((col & 31) >> 2) + h),
+               make_uint4(__float_as_uint(v[2 * h].x), __float_as_uint(v[2 * h].y), __float_as_uint(v[2 * h + 1].x),
+                          __float_as_uint(v[2 * h + 1].y)));
 }
 
 struct Bars {
@@ -668,7 +684,7 @@ static_assert(sizeof(Bars) <= 256, "barrier region");
 
 // Y: CTAs 0 .. n_whole - 1 run the items 0 .. n_whole - 1 whole, the others a segment each, from the state that
 // enters it.  Y false: there is no y, and with it no QS and no product with P.  With p.keep it is the backward pass's
-// forward half, one CTA per item, and E and the entering state's terms of every chunk are kept; else it is the state
+// forward half, one CTA per item, and E and the entering state of every chunk are kept; else it is the state
 // pass over the cut items' segments but the last.  A segment's end is S_in M + S_loc, row by row: S_loc is its end from
 // a zero state, and M its end from the unit matrix without values, a run of its own (the segment 0 needs none).
 template <int DK, bool Y>
@@ -787,11 +803,8 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             if (!wait_warp(&bar->y_full, n & 1)) break;
             if (lane == 0) {
                 unsigned char* kp = p.keep + (item * (p.nchunks + 1) + (n >> 1)) * kKeepBytes;
-                if (n & 1) bulk_store(kp + kKeepE, base + M::kOut, 4 * kTile);
-                else {
-                    bulk_store(kp + kKeepS, base + M::kOut + 4 * kTile, 2 * KB * kTile);
-                    bulk_store(kp + kKeepSlo, base + M::kOut + 8 * kTile, 2 * KB * kTile);
-                }
+                if (n & 1) bulk_store(kp + kKeepE, base + M::kOut, 6 * kTile);
+                else bulk_store(kp + kKeepS, base + M::kOut + 6 * kTile, 4 * KB * kTile);
                 tc::bulk_commit();
                 tc::bulk_wait_read0();
             }
@@ -923,12 +936,12 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             store_terms3(tl + kColS + part * KH + k, tl + kColS3 + (part * KH + k) / 2, S + k / 2);
         tmem_wait_st();
         tc_fence_before();
-        // the terms of the state that enters chunk c, and those of its E (without y); the stores are one behind another
+        // the state that enters chunk c, and its E's terms (without y); the stores are one behind another
         auto keep_state = [&](int c) {
             if (c > 0 && !wait_warp(&bar->y_free, 1)) return false;   // chunk c - 1's E, store 2 c - 1
 #pragma unroll
             for (int k = 0; k < KH; k += 16)
-                stage_terms(base + M::kOut + 4 * kTile, base + M::kOut + 8 * kTile, v, part * KH + k, S + k / 2);
+                stage_f32(base + M::kOut + 6 * kTile, v, part * KH + k, S + k / 2);
             fence_proxy_async_smem();
             arrive_warp(&bar->y_full);
             return true;
@@ -1026,7 +1039,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             } else if (p.keep) {
                 ok = wait_warp(&bar->y_free, 0);   // its S, store 2 c
                 if (!ok) break;
-                stage_terms(base + M::kOut, base + M::kOut + 2 * kTile, v, kTok * part, x);
+                stage_terms<true>(base + M::kOut, v, kTok * part, x);
                 fence_proxy_async_smem();
                 arrive_warp(&bar->y_full);
             }
