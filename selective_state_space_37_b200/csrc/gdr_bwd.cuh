@@ -21,8 +21,8 @@
 // what begins at each token is the same number, but there the paths that do not cross a token (M^P's diagonal above
 // all) come in and cancel only up to rounding: at Δ A = -29 what was left was ten times the gradient.
 //
-// Precision: as in the forward, P and T enter as two bf16 terms and what the adjoint's chain carries -- dS, dE, dV, dO's
-// scaled rows -- as three (dS and dE as two: the first state's gradient 1.4e-6 off on average instead of 6e-7).  In the
+// Precision: what the adjoint's chain carries -- dS, dE, dV, dO's scaled rows -- and P enter as three bf16 terms, T as two
+// (the first state's gradient is 2e-7 off on average; dS and dE as two and P as two: 1e-6 and 6e-7 more).  In the
 // gradient kernel dV and M enter as two, E, S and dS as three, and <S, dS> is a sum of fp32 products: dA and ddt_bias are
 // sums over all tokens of both signs, and come out in fp32 (all of them as two terms: 2e-6 to 3e-5 off).
 #pragma once
@@ -38,16 +38,16 @@ namespace gdr {
 // terms of -e^G dV over the first and its third over the second, then the next dS's third terms over the first; O: the
 // terms of scale e^G dO.
 constexpr uint32_t kRevS = 0, kRevA = 128, kRevR = 192, kRevV = 320, kRevO = 448;
-// Shared memory: two stages of [K 0][Q 0][K 1][Q 1][record]; dO (swizzled blocks); an image on its way out, dS in fp32
-// and then dVᵀ's terms.
+// Shared memory: two stages of [K 0][Q 0][K 1][Q 1][record]; dO (swizzled blocks) and P's third term; an image on its way
+// out, dS in fp32 and then dVᵀ's terms.
 constexpr uint32_t kRevStage = 4 * kTile + kRecBytes, kRevOffRec = 4 * kTile;
-constexpr uint32_t kRevOffO = 2 * kRevStage, kRevOffImg = kRevOffO + 2 * kTile, kRevOffBar = kRevOffImg + 8 * kTile;
+constexpr uint32_t kRevOffO = 2 * kRevStage, kRevOffP3 = kRevOffO + 2 * kTile, kRevOffImg = kRevOffP3 + kTile, kRevOffBar = kRevOffImg + 8 * kTile;
 constexpr uint32_t kRevSmem = kRevOffBar + 256 + 1024;
 static_assert(kRevStage % 1024 == 0 && kRevSmem <= 227 * 1024, "shared memory");
 
 struct RevBars {
     uint64_t full[2], empty[2];      // K, Q and the record of a stage
-    uint64_t o_full, o_free;         // dO landed; read (state warps, behind its product)
+    uint64_t o_full, o_free;         // dO and P's third term landed; read (state warps, behind their product)
     uint64_t img_full, img_free;     // dS's terms staged, then dV's (state warps); stored (1)
     uint64_t ks, e, ds;              // products done
     uint64_t s_ready[2], x_ready, w_ready;
@@ -131,7 +131,8 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 bulk_load(st + kRevOffRec, p.rec + (item * p.nchunks + c) * p.rec_bytes, kRecBytes, f);
                 issued = n + 1;
                 if (n >= 1 && !wait1(&bar->o_free, (n - 1) & 1)) break;
-                mbar_arrive_expect_tx(&bar->o_full, kC * p.dv * 2);
+                mbar_arrive_expect_tx(&bar->o_full, kC * p.dv * 2 + kTile);
+                bulk_load(base + kRevOffP3, p.rec + (item * p.nchunks + c) * p.rec_bytes + kRecP3, kTile, &bar->o_full);
                 for (int vb = 0; vb < p.dv / 64; ++vb)
                     tma_load_4d(base + kRevOffO + vb * kTile, &tm_o, 64 * vb, h, c * kC, b, &bar->o_full);
                 o_issued = n + 1;
@@ -173,6 +174,10 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 for (int j = 0; j < kC / 16; ++j)
                     umma(tmem + kRevR, sdesc(ot + 2048u * j, lbo, 1024), sdesc(pr + kRecP + 2048u * j, kTile, 1024),
                          idesc(2 * kC, true, true), j > 0);
+#pragma unroll
+                for (int j = 0; j < kC / 16; ++j)
+                    umma(tmem + kRevR, sdesc(ot + 2048u * j, lbo, 1024), sdesc(base + kRevOffP3 + 2048u * j, kTile, 1024),
+                         idesc(kC, true, true), 1);
                 auto ks_step = [&](int ks) {
                     const uint64_t bd = sdesc(st + (ks >> 2) * 2 * kTile + (ks & 3) * 32, 16, 1024);
                     umma_ts(tmem + kRevA, tmem + kRevS + 16 * ks, bd, idesc(kC, false), ks > 0);

@@ -20,6 +20,7 @@
 // Precision: q, k, v are bf16 values as given and unit lengths are factors of rows and columns, so they enter
 // exactly.  fp32 operands enter as bf16 terms of 8 bits each: S, X and W as three, hi to third, 24 bits; T, P and E as
 // two.  With two for S and X the state is 1.2e-6 off on average, with three 6e-7 (all of it T's; W with two alone: 2.4e-6).
+// The backward pass's fp32 outputs are sums of both signs: its forward half takes T, and its adjoint P, as three.
 // One term for P and E would do for y's own rounding, but not where keys repeat: the corrections are then differences
 // of values, and P E cancels most of them.  Accumulation is fp32, the state is kept in fp32 registers.
 #pragma once
@@ -70,7 +71,8 @@ struct alignas(16) Local {  // what a chunk's decay factors are made of (the bac
     float cf[kC];           // β_j / |k_j| e^{G_31 - G_j}, j < 32
     float rk[kC], rq[kC];   // 1 / |k_i|, scale / |q_i|
 };
-constexpr uint32_t kRecLocal = kRecBytes, kRecBwdBytes = kRecBytes + 2048;
+// For the backward pass also the third terms of T and P.
+constexpr uint32_t kRecLocal = kRecBytes, kRecT3 = kRecLocal + 2048, kRecP3 = kRecT3 + kTile, kRecBwdBytes = kRecP3 + kTile;
 static_assert(sizeof(Local) <= 2048, "record");
 
 // What the backward pass keeps of a chunk, beside its record, as images of tiles with the swizzle of the MMAs.  Eᵀ as
@@ -162,6 +164,11 @@ __device__ __forceinline__ void split2(f32x2 v, uint32_t& hi, uint32_t& lo) {
     const f32x2 r = fma2(pk2(lo_f(hi), hi_f(hi)), pk2(-1.0f, -1.0f), v);
     lo = pk(r.x, r.y);
 }
+// A pair as three words of bf16 values.
+__device__ __forceinline__ void split3(f32x2 v, uint32_t& hi, uint32_t& lo, uint32_t& third) {
+    hi = pk(v.x, v.y);
+    split2(fma2(pk2(lo_f(hi), hi_f(hi)), pk2(-1.0f, -1.0f), v), lo, third);
+}
 // 16 values' terms into 16 columns: hi in the first 8, lo in the others.
 __device__ __forceinline__ void store_terms(uint32_t taddr, const f32x2* v) {
     uint32_t hi[8], lo[8];
@@ -174,11 +181,7 @@ __device__ __forceinline__ void store_terms(uint32_t taddr, const f32x2* v) {
 __device__ __forceinline__ void store_terms3(uint32_t taddr, uint32_t third, const f32x2* v) {
     uint32_t hi[8], lo[8], th[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        hi[e] = pk(v[e].x, v[e].y);
-        const f32x2 r = fma2(pk2(lo_f(hi[e]), hi_f(hi[e])), pk2(-1.0f, -1.0f), v[e]);
-        split2(r, lo[e], th[e]);
-    }
+    for (int e = 0; e < 8; ++e) split3(v[e], hi[e], lo[e], th[e]);
     tmem_st8(taddr, hi);
     tmem_st8(taddr + 8, lo);
     tmem_st8(third, th);
@@ -506,6 +509,11 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
         __syncthreads();
         const float gh = lo.gh[i], gl = lo.gl[i];
         const float row = is_q ? rn * g.scale : rn;
+        unsigned char* const rec = p.rec + (item * p.nchunks + c) * p.rec_bytes;
+        // a third term's 8 values of row i, straight to the record (the backward pass's alone)
+        auto put3 = [&](uint32_t image, int w, const uint32_t (&t)[4]) {
+            *reinterpret_cast<uint4*>(rec + chunk_addr(image, i, w)) = make_uint4(t[0], t[1], t[2], t[3]);
+        };
         if (is_q) {
             sc.qe[i] = exp2f(gh) * row;
             lo.rq[i] = row;
@@ -520,6 +528,7 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
                         for (int w = 0; w < 4; ++w) {
                             sts128(chunk_addr(base, i, 4 + w), make_uint4(0, 0, 0, 0));
                             sts128(chunk_addr(base + kTile, i, 4 + w), make_uint4(0, 0, 0, 0));
+                            if (p.keep) put3(kRecP3, 4 + w, {0, 0, 0, 0});
                         }
                     break;
                 }
@@ -531,9 +540,10 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
             if (is_q) {   // (K and Q have been read: by the MMAs, and by the lengths before the barriers above)
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    uint32_t hw[4], lw[4];
+                    uint32_t hw[4], lw[4], tw[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) split2(pk2(v[8 * w + 2 * e], v[8 * w + 2 * e + 1]), hw[e], lw[e]);
+                    for (int e = 0; e < 4; ++e) split3(pk2(v[8 * w + 2 * e], v[8 * w + 2 * e + 1]), hw[e], lw[e], tw[e]);
+                    if (p.keep) put3(kRecP3, j0 / 8 + w, tw);
                     sts128(chunk_addr(base, i, j0 / 8 + w), make_uint4(hw[0], hw[1], hw[2], hw[3]));
                     sts128(chunk_addr(base + kTile, i, j0 / 8 + w), make_uint4(lw[0], lw[1], lw[2], lw[3]));
                 }
@@ -555,11 +565,12 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
             __syncthreads();
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                uint32_t hw[4], lw[4];
-                split2(pk2(u[2 * w].x, u[2 * w].y), hw[0], lw[0]);
-                split2(pk2(u[2 * w].z, u[2 * w].w), hw[1], lw[1]);
-                split2(pk2(u[2 * w + 1].x, u[2 * w + 1].y), hw[2], lw[2]);
-                split2(pk2(u[2 * w + 1].z, u[2 * w + 1].w), hw[3], lw[3]);
+                uint32_t hw[4], lw[4], tw[4];
+                split3(pk2(u[2 * w].x, u[2 * w].y), hw[0], lw[0], tw[0]);
+                split3(pk2(u[2 * w].z, u[2 * w].w), hw[1], lw[1], tw[1]);
+                split3(pk2(u[2 * w + 1].x, u[2 * w + 1].y), hw[2], lw[2], tw[2]);
+                split3(pk2(u[2 * w + 1].z, u[2 * w + 1].w), hw[3], lw[3], tw[3]);
+                if (p.keep) put3(kRecT3, 4 * hf + w, tw);
                 sts128(chunk_addr(base + kPrepT, i, 4 * hf + w), make_uint4(hw[0], hw[1], hw[2], hw[3]));
                 sts128(chunk_addr(base + kPrepT + kTile, i, 4 * hf + w), make_uint4(lw[0], lw[1], lw[2], lw[3]));
             }
@@ -624,25 +635,20 @@ constexpr uint32_t kColS = 0, kColA = 128, kColQS = 192, kColB = 256, kColS3 = k
 constexpr uint32_t kTmemCols = 512;
 
 // Shared memory: byte offsets from a 1024-aligned base.  A stage: [K 0][Q 0][K 1][Q 1][V 0][V 1][record]; then y
-// [64][d_v] for its store.  Without y there is no Q and of the record only T and the factors, and what is kept is
-// staged for its store: E's three images, then S's.
+// [64][d_v] for its store.  Without y there is no Q and of the record only T (three terms, where it has them) and the
+// factors, and what is kept is staged for its store: S's image, then E's three over it.
 template <bool Y>
 struct Smem {
     static constexpr uint32_t kPair = Y ? 2 * kTile : kTile;   // from K's first block of keys to its second
     static constexpr uint32_t kV = 2 * kPair, kRec = kV + 2 * kTile;
-    static constexpr uint32_t kFactors = kRec + (Y ? kRecScal : 2 * kTile);
+    static constexpr uint32_t kFactors = kRec + (Y ? kRecScal : 3 * kTile);
     static constexpr uint32_t kStage = kFactors + sizeof(Scal);
     static constexpr uint32_t kOut = kStages * kStage;
-    static constexpr uint32_t kBar = kOut + (Y ? 2 : 14) * kTile;
+    static constexpr uint32_t kBar = kOut + (Y ? 2 : 8) * kTile;
     static constexpr uint32_t kBytes = kBar + 256 + 1024;
     static_assert(kStage % 1024 == 0 && kBytes <= 227 * 1024, "shared memory");
 };
 
-// A pair as three words of bf16 values.
-__device__ __forceinline__ void split3(f32x2 v, uint32_t& hi, uint32_t& lo, uint32_t& third) {
-    hi = pk(v.x, v.y);
-    split2(fma2(pk2(lo_f(hi), hi_f(hi)), pk2(-1.0f, -1.0f), v), lo, third);
-}
 // 16 values' terms, two or three, to images in shared memory one behind another (128 rows of 128 bytes): the 16 columns
 // from `col` < 64 on of row r.
 template <bool THREE>
@@ -778,7 +784,8 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 if (c >= kStages && !wait1(&bar->empty[s], ((c / kStages) - 1) & 1)) break;
                 const uint32_t st = base + s * M::kStage;
                 uint64_t* f = &bar->full[s];
-                mbar_arrive_expect_tx(f, (Y ? 2 : 1) * KB * kTile + (unit ? 0 : kC * p.dv * 2) + (M::kStage - M::kRec));
+                mbar_arrive_expect_tx(f, (Y ? 2 : 1) * KB * kTile + (unit ? 0 : kC * p.dv * 2) + (M::kStage - M::kRec) -
+                                             (Y || p.keep ? 0 : kTile));
                 const int t0 = (cbase + c) * kC;
                 for (int kb = 0; kb < KB; ++kb) {
                     tma_load_4d(st + kb * M::kPair, &tm_k, 64 * kb, hk, t0, b, f);
@@ -791,6 +798,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                     bulk_load(st + M::kRec, r, kRecBytes, f);
                 } else {
                     bulk_load(st + M::kRec, r + kRecT, 2 * kTile, f);
+                    if (p.keep) bulk_load(st + M::kRec + 2 * kTile, r + kRecT3, kTile, f);
                     bulk_load(st + M::kFactors, r + kRecScal, sizeof(Scal), f);
                 }
                 issued = c + 1;
@@ -804,7 +812,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             if (lane == 0) {
                 unsigned char* kp = p.keep + (item * (p.nchunks + 1) + (n >> 1)) * kKeepBytes;
                 if (n & 1) bulk_store(kp + kKeepE, base + M::kOut, 6 * kTile);
-                else bulk_store(kp + kKeepS, base + M::kOut + 6 * kTile, 4 * KB * kTile);
+                else bulk_store(kp + kKeepS, base + M::kOut, 4 * KB * kTile);
                 tc::bulk_commit();
                 tc::bulk_wait_read0();
             }
@@ -868,6 +876,13 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 for (int j = 0; j < (unit ? 0 : kC / 16); ++j)
                     umma(tmem + kColB, sdesc(st + M::kV + 2048u * j, vlbo, 1024), sdesc(pr + kRecT + 32u * j, 16, 1024),
                          idesc(2 * kC, false, true), j > 0);
+                const bool t3 = !Y && p.keep;   // T's third term, into E's first half
+                if (t3) {
+#pragma unroll
+                    for (int j = 0; j < kC / 16; ++j)
+                        umma(tmem + kColB, sdesc(st + M::kV + 2048u * j, vlbo, 1024), sdesc(pr + 2 * kTile + 32u * j, 16, 1024),
+                             idesc(kC, false, true), 1);
+                }
                 if (!wait1(&bar->x_ready, par)) break;
                 tc_fence_after();
                 // E += X Tᵀ
@@ -877,6 +892,11 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                     umma_ts(tmem + kColB, tmem + kColA + 16 * j, bd, idesc(2 * kC, false), unit && j == 0 ? 0 : 1);
                     umma_ts(tmem + kColB, tmem + kColA + 16 * j + 8, bd, idesc(2 * kC, false), 1);
                     umma_ts(tmem + kColB, tmem + kColS + 8 * j, bd, idesc(2 * kC, false), 1);
+                }
+                if (t3) {
+#pragma unroll
+                    for (int j = 0; j < kC / 16; ++j)
+                        umma_ts(tmem + kColB, tmem + kColA + 16 * j, sdesc(pr + 2 * kTile + 32u * j, 16, 1024), idesc(kC, false), 1);
                 }
                 umma_commit(&bar->e);
                 if (!wait1(&bar->w_ready, par)) break;
@@ -941,7 +961,7 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
             if (c > 0 && !wait_warp(&bar->y_free, 1)) return false;   // chunk c - 1's E, store 2 c - 1
 #pragma unroll
             for (int k = 0; k < KH; k += 16)
-                stage_f32(base + M::kOut + 6 * kTile, v, part * KH + k, S + k / 2);
+                stage_f32(base + M::kOut, v, part * KH + k, S + k / 2);
             fence_proxy_async_smem();
             arrive_warp(&bar->y_full);
             return true;
