@@ -626,12 +626,11 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
                 const uint32_t off = base + kGK + (ks >> 2) * 2 * kTile + (ks & 3) * 32u;
                 umma(tmem + 448, sdesc(off, 16, 1024), sdesc(off + kTile, 16, 1024), idesc(kC, false), ks > 0);
             }
-            for (int ks = 0; ks < vs; ++ks) {
-                const uint64_t e = sdesc(base + kGE + 2048u * ks, 0, 1024), el = sdesc(base + kGE + 2 * kTile + 2048u * ks, 0, 1024);
-                umma(tmem + 384, a_hi(ks), e, idesc(kC, true), ks > 0);
-                umma(tmem + 384, a_hi(ks), el, idesc(kC, true), 1);
-                umma_upper(tmem + 384, a_lo(ks), e, idesc(kC, true));
-            }
+            // (the accumulator is cut off, not rounded, after every product: here and below the small terms come first)
+            for (int ks = 0; ks < vs; ++ks)
+                umma(tmem + 384, a_hi(ks), sdesc(base + kGE + 2 * kTile + 2048u * ks, 0, 1024), idesc(kC, true), ks > 0);
+            for (int ks = 0; ks < vs; ++ks)
+                umma_upper(tmem + 384, a_lo(ks), sdesc(base + kGE + 2048u * ks, 0, 1024), idesc(kC, true));
         }
         // v's gradient: dV's hi terms are its values rounded to bf16
         for (int w = tid; w < rows * vb * 8; w += kGradThreads) {
@@ -652,6 +651,8 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
         if (tid == 0 && mbar_wait_bounded(&bar->e3, par, p.wait_ns)) {   // (else the next wait runs out)
             for (int ks = 0; ks < vs; ++ks)
                 umma(tmem + 384, a_hi(ks), sdesc(base + kGM + 2 * kTile + 2048u * ks, 0, 1024), idesc(kC, true), 1);
+            for (int ks = 0; ks < vs; ++ks)
+                umma(tmem + 384, a_hi(ks), sdesc(base + kGE + 2048u * ks, 0, 1024), idesc(kC, true), 1);
             umma_commit(&bar->m2);
         }
         __syncwarp();
@@ -739,12 +740,12 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
         if (tid == 0) {
             tc_fence_after();
             for (int ks = 0; ks < vs; ++ks) {
-                const uint64_t sh = sdesc(base + kGS + 2048u * ks, 4 * kTile, 1024);
-                umma(tmem, a_hi(ks), sh, idesc(DK, true), ks > 0);
+                umma(tmem, a_hi(ks), sdesc(base + kGM + 2048u * ks, 2 * kTile, 1024), idesc(DK, true), ks > 0);
                 umma(tmem, a_hi(ks), sdesc(base + kGS + 2 * kTile + 2048u * ks, 4 * kTile, 1024), idesc(DK, true), 1);
-                umma(tmem, a_hi(ks), sdesc(base + kGM + 2048u * ks, 2 * kTile, 1024), idesc(DK, true), 1);
-                umma_upper(tmem, a_lo(ks), sh, idesc(DK, true));
+                umma_upper(tmem, a_lo(ks), sdesc(base + kGS + 2048u * ks, 4 * kTile, 1024), idesc(DK, true));
             }
+            for (int ks = 0; ks < vs; ++ks)
+                umma(tmem, a_hi(ks), sdesc(base + kGS + 2048u * ks, 4 * kTile, 1024), idesc(DK, true), 1);
             umma_commit(&bar->m1);
         }
         if (!wait_all(&bar->m1, par)) break;   // S and dV's lo terms are read
@@ -799,13 +800,15 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
                 const uint64_t dh = sdesc(base + kGS + 2048u * ks, 4 * kTile, 1024);
                 const uint64_t dl = sdesc(base + kGS + 2 * kTile + 2048u * ks, 4 * kTile, 1024);
                 const uint64_t e = sdesc(base + kGE + 2048u * ks, 0, 1024), el = sdesc(base + kGE + 2 * kTile + 2048u * ks, 0, 1024);
-                umma(tmem + 128, e, dh, idesc(DK, true, true), ks > 0);
-                umma(tmem + 128, e, dl, idesc(DK, true, true), 1);
-                umma(tmem + 128, e, sdesc(base + kG1 + 2048u * ks, 2 * kTile, 1024), idesc(DK, true, true), 1);
-                umma(tmem + 128, el, dh, idesc(DK, true, true), 1);
+                umma(tmem + 128, e, sdesc(base + kG1 + 2048u * ks, 2 * kTile, 1024), idesc(DK, true, true), ks > 0);
                 umma(tmem + 128, el, dl, idesc(DK, true, true), 1);
                 umma(tmem + 128, sdesc(base + kGM + 2 * kTile + 2048u * ks, 0, 1024), dh, idesc(DK, true, true), 1);
+                umma(tmem + 128, e, dl, idesc(DK, true, true), 1);
+                umma(tmem + 128, el, dh, idesc(DK, true, true), 1);
             }
+            for (int ks = 0; ks < vs; ++ks)
+                umma(tmem + 128, sdesc(base + kGE + 2048u * ks, 0, 1024), sdesc(base + kGS + 2048u * ks, 4 * kTile, 1024),
+                     idesc(DK, true, true), 1);
             umma_commit(&bar->m3);
         }
         if (!wait_all(&bar->m5, par)) break;
