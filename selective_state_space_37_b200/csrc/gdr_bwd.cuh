@@ -178,34 +178,31 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 for (int j = 0; j < kC / 16; ++j)
                     umma(tmem + kRevR, sdesc(ot + 2048u * j, lbo, 1024), sdesc(base + kRevOffP3 + 2048u * j, kTile, 1024),
                          idesc(kC, true, true), 1);
-                auto ks_step = [&](int ks) {
-                    const uint64_t bd = sdesc(st + (ks >> 2) * 2 * kTile + (ks & 3) * 32, 16, 1024);
-                    umma_ts(tmem + kRevA, tmem + kRevS + 16 * ks, bd, idesc(kC, false), ks > 0);
-                    umma_ts(tmem + kRevA, tmem + kRevS + 16 * ks + 8, bd, idesc(kC, false), 1);
-                    umma_ts(tmem + kRevA, tmem + kRevV + 8 * ks, bd, idesc(kC, false), 1);
-                };
                 constexpr int kStep = KH / 16;
+                auto ks_steps = [&](int first) {   // small terms first, as in the forward
+#pragma unroll
+                    for (int w = 0; w < 3; ++w)
+#pragma unroll
+                        for (int ks = first; ks < DK / 16; ks += kStep)
+                            umma_ts(tmem + kRevA, tmem + (w == 0 ? kRevV + 8 * ks : w == 1 ? kRevS + 16 * ks + 8 : kRevS + 16 * ks),
+                                    sdesc(st + (ks >> 2) * 2 * kTile + (ks & 3) * 32, 16, 1024), idesc(kC, false), first + w + ks > 0);
+                };
                 if (!wait1(&bar->s_ready[0], par)) break;
                 tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < DK / 16; ks += kStep) ks_step(ks);
+                ks_steps(0);
                 if (!wait1(&bar->s_ready[1], par)) break;
                 tc_fence_after();
-                if (kStep == 2) {
-#pragma unroll
-                    for (int ks = 1; ks < DK / 16; ks += 2) ks_step(ks);
-                }
+                if (kStep == 2) ks_steps(1);
                 if (!(p.test_drop && blockIdx.x == 0 && n == 0)) umma_commit(&bar->ks);
                 if (!wait1(&bar->x_ready, par)) break;
                 tc_fence_after();
                 // Vᵀ = dEᵀ T
 #pragma unroll
-                for (int j = 0; j < kC / 16; ++j) {
-                    const uint64_t bd = sdesc(pr + kRecT + 2048u * j, kTile, 1024);
-                    umma_ts(tmem + kRevV, tmem + kRevA + 16 * j, bd, idesc(2 * kC, true), j > 0);
-                    umma_ts(tmem + kRevV, tmem + kRevA + 16 * j + 8, bd, idesc(2 * kC, true), 1);
-                    umma_ts(tmem + kRevV, tmem + kRevR + kC + 16 * j, bd, idesc(2 * kC, true), 1);
-                }
+                for (int w = 0; w < 3; ++w)
+#pragma unroll
+                    for (int j = 0; j < kC / 16; ++j)
+                        umma_ts(tmem + kRevV, tmem + (w == 0 ? kRevR + kC : w == 1 ? kRevA + 8 : kRevA) + 16 * j,
+                                sdesc(pr + kRecT + 2048u * j, kTile, 1024), idesc(2 * kC, true), w + j > 0);
                 umma_commit(&bar->e);
                 // dS's update: (scale e^G dO)ᵀ Q, then (-e^G dV)ᵀ K, over the columns of dS's terms
 #pragma unroll

@@ -848,24 +848,24 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 const int s = c % kStages;
                 const uint32_t par = c & 1, st = base + s * M::kStage, pr = st + M::kRec;
                 if (!wait1(&bar->full[s], (c / kStages) & 1)) break;
-                // KS and QS: S's terms of 16 keys in 16 columns, K and Q of a 64-key block side by side
-                auto ks_step = [&](int ks) {
-                    const uint64_t bd = sdesc(st + (ks >> 2) * M::kPair + (ks & 3) * 32, 16, 1024);
-                    umma_ts(tmem + kColA, tmem + kColS + 16 * ks, bd, idesc(Y ? 2 * kC : kC, false), ks > 0);
-                    umma_ts(tmem + kColA, tmem + kColS + 16 * ks + 8, bd, idesc(Y ? 2 * kC : kC, false), 1);
-                    umma_ts(tmem + kColA, tmem + kColS3 + 8 * ks, bd, idesc(Y ? 2 * kC : kC, false), 1);
-                };
+                // KS and QS: S's terms of 16 keys in 16 columns, K and Q of a 64-key block side by side.  (The accumulator
+                // is cut off, not rounded, after every product: of the keys at hand the small terms come first.)
                 constexpr int kStep = KH / 16;   // (the rows behind a sequence's end are zeroed before s_ready)
+                auto ks_steps = [&](int first) {
+#pragma unroll
+                    for (int w = 0; w < 3; ++w)
+#pragma unroll
+                        for (int ks = first; ks < DK / 16; ks += kStep)
+                            umma_ts(tmem + kColA, tmem + (w == 0 ? kColS3 + 8 * ks : w == 1 ? kColS + 16 * ks + 8 : kColS + 16 * ks),
+                                    sdesc(st + (ks >> 2) * M::kPair + (ks & 3) * 32, 16, 1024),
+                                    idesc(Y ? 2 * kC : kC, false), first + w + ks > 0);
+                };
                 if (!wait1(&bar->s_ready[0], par)) break;
                 tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < DK / 16; ks += kStep) ks_step(ks);
+                ks_steps(0);
                 if (!wait1(&bar->s_ready[1], par)) break;
                 tc_fence_after();
-                if (kStep == 2) {
-#pragma unroll
-                    for (int ks = 1; ks < DK / 16; ks += 2) ks_step(ks);
-                }
+                if (kStep == 2) ks_steps(1);
                 if (!(p.test_drop && blockIdx.x == 0 && c == 0)) umma_commit(&bar->ks);
                 // E = Vᵀ Tᵀ, T's terms side by side, once the last chunk's E and the state's third terms are read (X is
                 // made meanwhile)
@@ -886,18 +886,17 @@ ss_gdr_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUten
                 if (!wait1(&bar->x_ready, par)) break;
                 tc_fence_after();
                 // E += X Tᵀ
-#pragma unroll
-                for (int j = 0; j < kC / 16; ++j) {
-                    const uint64_t bd = sdesc(pr + kRecT + 32u * j, 16, 1024);
-                    umma_ts(tmem + kColB, tmem + kColA + 16 * j, bd, idesc(2 * kC, false), unit && j == 0 ? 0 : 1);
-                    umma_ts(tmem + kColB, tmem + kColA + 16 * j + 8, bd, idesc(2 * kC, false), 1);
-                    umma_ts(tmem + kColB, tmem + kColS + 8 * j, bd, idesc(2 * kC, false), 1);
-                }
                 if (t3) {
 #pragma unroll
                     for (int j = 0; j < kC / 16; ++j)
                         umma_ts(tmem + kColB, tmem + kColA + 16 * j, sdesc(pr + 2 * kTile + 32u * j, 16, 1024), idesc(kC, false), 1);
                 }
+#pragma unroll
+                for (int w = 0; w < 3; ++w)
+#pragma unroll
+                    for (int j = 0; j < kC / 16; ++j)
+                        umma_ts(tmem + kColB, tmem + (w == 0 ? kColS + 8 * j : w == 1 ? kColA + 16 * j + 8 : kColA + 16 * j),
+                                sdesc(pr + kRecT + 32u * j, 16, 1024), idesc(2 * kC, false), unit && w + j == 0 ? 0 : 1);
                 umma_commit(&bar->e);
                 if (!wait1(&bar->w_ready, par)) break;
                 tc_fence_after();
