@@ -15,6 +15,10 @@ DEV = "cuda:0"
 # A rounding to bf16 is off by at most 2^-8 of the value; evenly spread, by 2^-8 / sqrt(3) on average where all values
 # stand just above a power of two, and by less elsewhere.  Operands in two terms add 2^-16 at most, four in a row here.
 ROUNDED = 2.0 ** -8 / 3 ** 0.5 + 4 * 2.0 ** -16
+# What is rounded is off by under 2^-16 of itself, so that it falls to the other side of a rounding in at most 2 · 2^-16
+# / step of all cases, a step being at most 2^-7, and is one step off there: sqrt(2 · 2^-16 · 2^-7) on average.  A
+# product with one term (2^-9 off on average) is off by more than that everywhere.
+OTHER_SIDE = 2.0 ** -11
 # An operand in two terms is off by at most 2^-16 (both rounded to nearest: 2^-8 of 2^-8), on average by a third of it
 # twice over; what a chain carries has three, and one operand beside it (T) two.
 STATE = 2.0 ** -16 / 9
@@ -45,6 +49,9 @@ def test_outputs_and_gradients(B, L, H, Hk, dk, dv, seed):
     assert rms_err(y, yr) <= ROUNDED
     for n in ("dq", "dk", "dv", "ddt", "dbeta"):
         assert rms_err(got[n], want[n]) <= ROUNDED, n
+    for n, t, r in (("y", y, yr), *((n, got[n], want[n]) for n in ("dq", "dk", "dv"))):
+        off = to_f64(t) - to_f64(torch.tensor(r).to(BF))
+        assert np.linalg.norm(off) <= OTHER_SIDE * np.linalg.norm(r), n
     assert rms_err(S, Sr) <= STATE
     assert rms_err(got["dinitial_state"], want["dinitial_state"]) <= STATE
     for n in ("dA", "ddt_bias"):
