@@ -5,9 +5,9 @@ kernels.  PyTorch supplies device memory (tensors, the cached workspace) and
 the current stream.  There is no CPU fallback: if the library is missing or a
 call fails, an exception is raised.
 """
-import contextlib
 import ctypes
 import functools
+import inspect
 import os
 import threading
 
@@ -235,10 +235,10 @@ def workspace_for(nbytes, device, stream_handle):
 _ws_locks = {}
 
 
-def _in_turn(device, stream):
+def _in_turn(device, stream_handle):
     """The lock of a (device, stream), held from a call's look-up of the cached workspace to its last launch: a call
     is several launches on one workspace, and ctypes lets other threads run between them."""
-    key = (device.index, int(_stream_handle(stream, device)))
+    key = (device.index, stream_handle)
     return _ws_locks.get(key) or _ws_locks.setdefault(key, threading.RLock())
 
 
@@ -255,9 +255,23 @@ def _stream_handle(stream, device):
     return stream.cuda_stream
 
 
+def _on_stream(fn):
+    """Runs a function with the stream that it is given as the current one: what it makes -- outputs, the cached
+    workspace -- is that stream's then.  (The allocator may hand out a block of the current stream's that work queued there
+    still uses, and hands a freed one out again behind the work of its own stream.)"""
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
 def _on_device(fn):
     """Runs a function with its first tensor's device current (the library launches on the current device)."""
-    name = fn.__code__.co_varnames[0]
+    name = inspect.unwrap(fn).__code__.co_varnames[0]
 
     @functools.wraps(fn)
     def call(*args, **kw):
@@ -271,27 +285,14 @@ def _on_device(fn):
     return call
 
 
-def _empty(shape, dtype, dev, stream):
-    """An output of the call, on the call's stream: the allocator may hand out a block of the current stream's that work
-    queued there still uses."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
-
-
-def _launch_for(need, dev, stream, workspace, timeout_iters=0, chunk_len=0):
+def _launch_for(need, dev, sh, workspace, timeout_iters=0, chunk_len=0):
     """(the call's ss_launch, its workspace): the tensor is the caller's to hold until the library has returned, since
     the cache may let go of it before (another thread's larger request on the same stream)."""
-    sh = _stream_handle(stream, dev)
     if workspace is None:
         # a captured graph gets a workspace of its own, from its memory pool: graphs may be replayed at once,
-        # and the cached buffer may have been replaced by a larger one by then.  On the call's stream, so that the
-        # allocator hands a replaced buffer out again behind the calls that used it
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
-            capturing = torch.cuda.is_current_stream_capturing()
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev) if capturing else \
-                workspace_for(need, dev, sh)
+        # and the cached buffer may have been replaced by a larger one by then
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev) if \
+            torch.cuda.is_current_stream_capturing() else workspace_for(need, dev, sh)
     elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     return ss_launch(sh, workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(timeout_iters),
@@ -308,6 +309,7 @@ def fwd_chunk_len(batch, seqlen, d_inner, bf16=True, d_state=D_STATE):
     return int(lib().ss_fwd_chunk_len(ctypes.byref(dims), SS_BF16 if bf16 else 0))
 
 
+@_on_stream
 def ss_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, y=None, last_state=None,
            return_last_state=True, softplus=True, force_general_A=False, chunk_len=0,
            timeout_iters=0, workspace=None, stream=None, sync_check=False, extra_flags=0,
@@ -335,10 +337,10 @@ def ss_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, y=None, last_s
     _check(D, "D", (d,), torch.float32, dev)
     _check(delta_bias, "delta_bias", (d,), torch.float32, dev)
     if y is None:
-        y = _empty((batch, L, d), io, dev, stream)
+        y = torch.empty((batch, L, d), dtype=io, device=dev)
     _check(y, "y", (batch, L, d), io, dev)
     if last_state is None and return_last_state:
-        last_state = _empty((batch, d, D_STATE), torch.float32, dev, stream)
+        last_state = torch.empty((batch, d, D_STATE), dtype=torch.float32, device=dev)
     _check(last_state, "last_state", (batch, d, D_STATE), torch.float32, dev)
     flags = _io_flag(u) | (SS_DELTA_SOFTPLUS if softplus else 0) | int(extra_flags)
     if force_general_A:
@@ -347,8 +349,9 @@ def ss_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, y=None, last_s
         flags |= SS_SYNC_CHECK
     dims = ss_dims(batch, L, d, D_STATE)
     need = int(lib().ss_fwd_workspace_bytes(ctypes.byref(dims), flags, int(chunk_len)))
-    with _in_turn(dev, stream):
-        launch, workspace = _launch_for(need, dev, stream, workspace, timeout_iters, chunk_len)
+    sh = _stream_handle(stream, dev)
+    with _in_turn(dev, sh):
+        launch, workspace = _launch_for(need, dev, sh, workspace, timeout_iters, chunk_len)
         if initial_state is not None:
             _check(initial_state, "initial_state", (batch, d, D_STATE), torch.float32, dev)
             rc = lib().ss_fwd_with_state(_ptr(u), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
@@ -363,6 +366,7 @@ def ss_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, y=None, last_s
     return y, last_state
 
 
+@_on_stream
 def ss_fwd_host(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, y=None, last_state=None,
                 return_last_state=True, softplus=True, rows_per_slice=1, workspace=None, stream=None,
                 sync_check=False):
@@ -400,8 +404,9 @@ def ss_fwd_host(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, y=None, l
     flags = _io_flag(u) | (SS_DELTA_SOFTPLUS if softplus else 0) | (SS_SYNC_CHECK if sync_check else 0)
     dims = ss_dims(batch, L, d, D_STATE)
     need = int(lib().ss_fwd_host_workspace_bytes(ctypes.byref(dims), flags, int(rows_per_slice)))
-    with _in_turn(dev, stream):
-        launch, workspace = _launch_for(need, dev, stream, workspace)
+    sh = _stream_handle(stream, dev)
+    with _in_turn(dev, sh):
+        launch, workspace = _launch_for(need, dev, sh, workspace)
         rc = lib().ss_fwd_host(_ptr(u), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                                _ptr(z), _ptr(y), _ptr(last_state), flags, ctypes.byref(dims),
                                ctypes.byref(launch), int(rows_per_slice))
@@ -420,6 +425,7 @@ def bwd_workspace_bytes(batch, seqlen, d_inner, bf16=True, d_state=D_STATE):
     return int(lib().ss_bwd_workspace_bytes(ctypes.byref(dims), SS_BF16 if bf16 else 0))
 
 
+@_on_stream
 def ss_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, dlast_state=None, *,
            softplus=True, grads=None, chunk_len=0, workspace=None, stream=None, sync_check=False):
     """Backward of ss_fwd through libselscan's ss_bwd.
@@ -457,13 +463,14 @@ def ss_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, dlast_state=N
         shapes["ddelta_bias"] = ((d,), torch.float32)
     for k, (shp, dt) in shapes.items():
         if k not in g:
-            g[k] = _empty(shp, dt, dev, stream)
+            g[k] = torch.empty(shp, dtype=dt, device=dev)
         _check(g[k], k, shp, dt, dev)
     flags = _io_flag(u) | (SS_DELTA_SOFTPLUS if softplus else 0) | (SS_SYNC_CHECK if sync_check else 0)
     dims = ss_dims(batch, L, d, D_STATE)
     need = int(lib().ss_bwd_workspace_bytes(ctypes.byref(dims), flags))
-    with _in_turn(dev, stream):
-        launch, workspace = _launch_for(need, dev, stream, workspace, 0, chunk_len)
+    sh = _stream_handle(stream, dev)
+    with _in_turn(dev, sh):
+        launch, workspace = _launch_for(need, dev, sh, workspace, 0, chunk_len)
         rc = lib().ss_bwd(_ptr(u), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
                           _ptr(dy), _ptr(dlast_state), _ptr(g["du"]), _ptr(g["ddelta"]), _ptr(g["dA"]),
                           _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g.get("dD")), _ptr(g.get("dz")),
@@ -473,6 +480,7 @@ def ss_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, dlast_state=N
     return {k: g[k] for k in shapes}
 
 
+@_on_stream
 def ss_fwd_conv(x, conv_w, delta, A, B, C, D=None, z=None, delta_bias=None, conv_b=None, *, y=None,
                 last_state=None, return_last_state=True, conv_state=None, softplus=True, chunk_len=0,
                 timeout_iters=0, workspace=None, stream=None, sync_check=False):
@@ -496,16 +504,17 @@ def ss_fwd_conv(x, conv_w, delta, A, B, C, D=None, z=None, delta_bias=None, conv
     _check(delta_bias, "delta_bias", (d,), torch.float32, dev)
     _check(conv_state, "conv_state", (batch, d, 3), torch.float32, dev)
     if y is None:
-        y = _empty((batch, L, d), io, dev, stream)
+        y = torch.empty((batch, L, d), dtype=io, device=dev)
     _check(y, "y", (batch, L, d), io, dev)
     if last_state is None and return_last_state:
-        last_state = _empty((batch, d, D_STATE), torch.float32, dev, stream)
+        last_state = torch.empty((batch, d, D_STATE), dtype=torch.float32, device=dev)
     _check(last_state, "last_state", (batch, d, D_STATE), torch.float32, dev)
     flags = _io_flag(x) | (SS_DELTA_SOFTPLUS if softplus else 0) | (SS_SYNC_CHECK if sync_check else 0)
     dims = ss_dims(batch, L, d, D_STATE)
     need = int(lib().ss_fwd_workspace_bytes(ctypes.byref(dims), flags, int(chunk_len)))
-    with _in_turn(dev, stream):
-        launch, workspace = _launch_for(need, dev, stream, workspace, timeout_iters, chunk_len)
+    sh = _stream_handle(stream, dev)
+    with _in_turn(dev, sh):
+        launch, workspace = _launch_for(need, dev, sh, workspace, timeout_iters, chunk_len)
         rc = lib().ss_fwd_conv(_ptr(x), _ptr(conv_w), _ptr(conv_b), _ptr(delta), _ptr(delta_bias), _ptr(A),
                                _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(y), _ptr(last_state), _ptr(conv_state),
                                flags, ctypes.byref(dims), ctypes.byref(launch))
@@ -514,6 +523,7 @@ def ss_fwd_conv(x, conv_w, delta, A, B, C, D=None, z=None, delta_bias=None, conv
     return y, last_state
 
 
+@_on_stream
 def ss_step_conv(state, conv_state, x, conv_w, delta, A, B, C, D=None, z=None, delta_bias=None, conv_b=None,
                  *, y=None, softplus=True, stream=None, sync_check=False):
     """One decode step with the conv prologue; state [batch, d_inner, 16] and
@@ -532,7 +542,7 @@ def ss_step_conv(state, conv_state, x, conv_w, delta, A, B, C, D=None, z=None, d
     _check(D, "D", (d,), torch.float32, dev)
     _check(delta_bias, "delta_bias", (d,), torch.float32, dev)
     if y is None:
-        y = _empty((batch, d), io, dev, stream)
+        y = torch.empty((batch, d), dtype=io, device=dev)
     flags = _io_flag(x) | (SS_DELTA_SOFTPLUS if softplus else 0) | (SS_SYNC_CHECK if sync_check else 0)
     sh = _stream_handle(stream, dev)
     dims = ss_dims(batch, 1, d, D_STATE)
@@ -565,6 +575,7 @@ def block_scratch_bytes(weights, batch, seqlen):
     return int(lib().ss_block_scratch_bytes(ctypes.byref(st), batch, seqlen))
 
 
+@_on_stream
 def ss_block_fwd(hidden, weights, *, out=None, scratch=None, stream=None):
     """Forward of one Mamba block's inner path through libselscan's
     ss_block_fwd.  hidden [batch, L, d_model] bf16; weights: a dict of
@@ -577,13 +588,14 @@ def ss_block_fwd(hidden, weights, *, out=None, scratch=None, stream=None):
         raise ValueError("hidden's last dimension must equal d_model")
     _check(hidden, "hidden", (batch, L, d_model), torch.bfloat16, dev)
     if out is None:
-        out = _empty(hidden.shape, hidden.dtype, dev, stream)
+        out = torch.empty_like(hidden)
     _check(out, "out", (batch, L, d_model), torch.bfloat16, dev)
     need = int(lib().ss_block_scratch_bytes(ctypes.byref(st), batch, L))
     if need == 0:
         raise SelscanError(SS_ERR_INVALID_ARG, "ss_block_fwd")
-    with _in_turn(dev, stream):
-        launch, scratch = _launch_for(need, dev, stream, scratch)
+    sh = _stream_handle(stream, dev)
+    with _in_turn(dev, sh):
+        launch, scratch = _launch_for(need, dev, sh, scratch)
         rc = lib().ss_block_fwd(_ptr(hidden), _ptr(out), ctypes.byref(st), batch, L, launch.workspace,
                                 launch.workspace_bytes, launch.stream)
     if rc != SS_OK:
@@ -591,6 +603,7 @@ def ss_block_fwd(hidden, weights, *, out=None, scratch=None, stream=None):
     return out
 
 
+@_on_stream
 def ss_ssd_fwd(x, dt, A, B, C, D=None, dt_bias=None, *, softplus=True, y=None, final_state=None,
                return_final_state=True, chunk_len=0, split=True, workspace=None, stream=None, sync_check=False,
                timeout_iters=0, extra_flags=0):
@@ -614,18 +627,18 @@ def ss_ssd_fwd(x, dt, A, B, C, D=None, dt_bias=None, *, softplus=True, y=None, f
     _check(D, "D", (H,), torch.float32, dev)
     _check(dt_bias, "dt_bias", (H,), torch.float32, dev)
     if y is None:
-        y = _empty(x.shape, x.dtype, dev, stream)
+        y = torch.empty_like(x)
     _check(y, "y", (batch, L, H, P), bf, dev)
     if final_state is None and return_final_state:
-        final_state = _empty((batch, H, P, N), torch.float32, dev, stream)
+        final_state = torch.empty((batch, H, P, N), dtype=torch.float32, device=dev)
     _check(final_state, "final_state", (batch, H, P, N), torch.float32, dev)
     flags = (SS_DELTA_SOFTPLUS if softplus else 0) | (SS_SYNC_CHECK if sync_check else 0) | int(extra_flags)
     dims = ss_ssd_dims(batch, L, H, P, N)
     sh = _stream_handle(stream, dev)
-    with _in_turn(dev, stream):
+    with _in_turn(dev, sh):
         if split:
             need = int(lib().ss_ssd_fwd_workspace_bytes(ctypes.byref(dims), flags))
-            launch, workspace = _launch_for(need, dev, stream, workspace, timeout_iters, chunk_len)
+            launch, workspace = _launch_for(need, dev, sh, workspace, timeout_iters, chunk_len)
         else:
             launch = ss_launch(sh, None, 0, int(timeout_iters), int(chunk_len))
         rc = lib().ss_ssd_fwd(_ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(y),
@@ -656,6 +669,7 @@ def _gdr_setup(q, k, v, dt, A, beta, dt_bias, io, softplus, beta_sigmoid, qk_l2n
 
 
 @_on_device
+@_on_stream
 def ss_gdr_fwd(q, k, v, dt, A, beta, dt_bias=None, initial_state=None, seqlens=None, *, scale=None, softplus=True,
                beta_sigmoid=True, qk_l2norm=True, y=None, final_state=None, return_final_state=True, chunk_len=0,
                workspace=None, stream=None, sync_check=False, timeout_iters=0, extra_flags=0):
@@ -664,8 +678,8 @@ def ss_gdr_fwd(q, k, v, dt, A, beta, dt_bias=None, initial_state=None, seqlens=N
     all the same; d_k, d_v 64 or 128; nheads a multiple of nheads_k); A, dt_bias [nheads] fp32;
     initial_state [batch, nheads, d_v, d_k] fp32 or None; seqlens [batch] int32 on the device or None:
     the tokens of each sequence, the rows of y behind them staying as they were (zero when y is made
-    here).  With stream=, outputs that the call makes are that stream's.  scale defaults to d_k ** -0.5.  Returns (y, final_state or None); final_state may be
-    initial_state."""
+    here).  With stream=, outputs that the call makes are that stream's.  scale defaults to d_k ** -0.5.
+    Returns (y, final_state or None); final_state may be initial_state."""
     if q.dim() != 4:
         raise ValueError("q must be [batch, L, nheads_k, d_k]")
     batch, L = q.shape[:2]
@@ -675,18 +689,18 @@ def ss_gdr_fwd(q, k, v, dt, A, beta, dt_bias=None, initial_state=None, seqlens=N
     _check(initial_state, "initial_state", states, torch.float32, dev)
     _check(seqlens, "seqlens", (batch,), torch.int32, dev)
     if y is None:
-        y = _empty(v.shape, v.dtype, dev, stream)
+        y = torch.empty_like(v)
         if seqlens is not None:
-            with torch.cuda.stream(stream):   # (None: the current one)
-                y.zero_()
+            y.zero_()
     _check(y, "y", v.shape, v.dtype, dev)
     if final_state is None and return_final_state:
-        final_state = _empty(states, torch.float32, dev, stream)
+        final_state = torch.empty(states, dtype=torch.float32, device=dev)
     _check(final_state, "final_state", states, torch.float32, dev)
     flags |= (SS_SYNC_CHECK if sync_check else 0) | int(extra_flags)
     need = int(lib().ss_gdr_fwd_workspace_bytes(ctypes.byref(dims), flags, int(chunk_len)))
-    with _in_turn(dev, stream):
-        launch, workspace = _launch_for(need, dev, stream, workspace, timeout_iters, chunk_len)
+    sh = _stream_handle(stream, dev)
+    with _in_turn(dev, sh):
+        launch, workspace = _launch_for(need, dev, sh, workspace, timeout_iters, chunk_len)
         rc = lib().ss_gdr_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(beta),
                               _ptr(initial_state), _ptr(seqlens), _ptr(y), _ptr(final_state),
                               dims.d_k ** -0.5 if scale is None else float(scale), flags, ctypes.byref(dims),
@@ -697,6 +711,7 @@ def ss_gdr_fwd(q, k, v, dt, A, beta, dt_bias=None, initial_state=None, seqlens=N
 
 
 @_on_device
+@_on_stream
 def ss_gdr_step(state, q, k, v, dt, A, beta, dt_bias=None, *, scale=None, softplus=True, beta_sigmoid=True,
                 qk_l2norm=True, y=None, stream=None, sync_check=False):
     """One token of the gated delta rule through libselscan's ss_gdr_step; `state`
@@ -711,7 +726,7 @@ def ss_gdr_step(state, q, k, v, dt, A, beta, dt_bias=None, *, scale=None, softpl
                              (state.shape[0],))
     _check(state, "state", (dims.batch, dims.nheads, dims.d_v, dims.d_k), torch.float32, dev)
     if y is None:
-        y = _empty(v.shape, v.dtype, dev, stream)
+        y = torch.empty_like(v)
     _check(y, "y", v.shape, v.dtype, dev)
     flags |= SS_SYNC_CHECK if sync_check else 0
     launch = ss_launch(_stream_handle(stream, dev), None, 0, 0, 0)
@@ -724,6 +739,7 @@ def ss_gdr_step(state, q, k, v, dt, A, beta, dt_bias=None, *, scale=None, softpl
 
 
 @_on_device
+@_on_stream
 def ss_gdr_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, initial_state=None, dfinal_state=None, seqlens=None, *,
                scale=None, softplus=True, beta_sigmoid=True, qk_l2norm=True, grads=None, workspace=None, stream=None,
                sync_check=False, timeout_iters=0, extra_flags=0):
@@ -751,12 +767,13 @@ def ss_gdr_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, initial_state=None, dfina
     g = {}
     for name, t in like.items():
         given = (grads or {}).get(name)
-        g[name] = _empty(t.shape, t.dtype, dev, stream) if given is None else given
+        g[name] = torch.empty_like(t) if given is None else given
         _check(g[name], name, t.shape, t.dtype, dev)
     flags |= (SS_SYNC_CHECK if sync_check else 0) | int(extra_flags)
     need = int(lib().ss_gdr_bwd_workspace_bytes(ctypes.byref(dims), flags))
-    with _in_turn(dev, stream):
-        launch, workspace = _launch_for(need, dev, stream, workspace, timeout_iters)
+    sh = _stream_handle(stream, dev)
+    with _in_turn(dev, sh):
+        launch, workspace = _launch_for(need, dev, sh, workspace, timeout_iters)
         rc = lib().ss_gdr_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(beta),
                               _ptr(initial_state), _ptr(seqlens), _ptr(dy), _ptr(dfinal_state), _ptr(g["dq"]),
                               _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["ddt"]), _ptr(g["dbeta"]), _ptr(g["dA"]),
@@ -769,6 +786,7 @@ def ss_gdr_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, initial_state=None, dfina
 
 
 @_on_device
+@_on_stream
 def ss_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, y=None, stats=True, stream=None, sync_check=False):
     """Layer norm over the last dimension of x (bf16 or fp32, contiguous) through libselscan's
     ss_norm_fwd; weight, bias [cols] fp32 or None; y may be x.  Returns (y, mean, rstd), the statistics
@@ -782,10 +800,10 @@ def ss_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, y=None, stats=True, stre
     _check(weight, "weight", (cols,), torch.float32, dev)
     _check(bias, "bias", (cols,), torch.float32, dev)
     if y is None:
-        y = _empty(x.shape, x.dtype, dev, stream)
+        y = torch.empty_like(x)
     _check(y, "y", x.shape, x.dtype, dev)
-    mean = _empty((rows,), torch.float32, dev, stream) if stats else None
-    rstd = _empty((rows,), torch.float32, dev, stream) if stats else None
+    mean = torch.empty(rows, dtype=torch.float32, device=dev) if stats else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if stats else None
     flags = _io_flag(x) | (SS_SYNC_CHECK if sync_check else 0)
     dims = ss_norm_dims(rows, cols)
     launch = ss_launch(_stream_handle(stream, dev), None, 0, 0, 0)
@@ -797,6 +815,7 @@ def ss_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, y=None, stats=True, stre
 
 
 @_on_device
+@_on_stream
 def ss_norm_bwd(dy, x, mean, rstd, weight=None, *, dx=None, dweight=None, dbias=None, sums=True, workspace=None,
                 stream=None, sync_check=False):
     """Backward of ss_norm_fwd through libselscan's ss_norm_bwd: dy and x of one shape and type, mean and
@@ -812,17 +831,18 @@ def ss_norm_bwd(dy, x, mean, rstd, weight=None, *, dx=None, dweight=None, dbias=
     _check(mean, "mean", (rows,), torch.float32, dev)
     _check(rstd, "rstd", (rows,), torch.float32, dev)
     _check(weight, "weight", (cols,), torch.float32, dev)
-    g = {"dx": _empty(x.shape, x.dtype, dev, stream) if dx is None else dx}
+    g = {"dx": torch.empty_like(x) if dx is None else dx}
     _check(g["dx"], "dx", x.shape, x.dtype, dev)
     if sums:
         for name, t in (("dweight", dweight), ("dbias", dbias)):
-            g[name] = _empty((cols,), torch.float32, dev, stream) if t is None else t
+            g[name] = torch.empty(cols, dtype=torch.float32, device=dev) if t is None else t
             _check(g[name], name, (cols,), torch.float32, dev)
     flags = _io_flag(x) | (SS_SYNC_CHECK if sync_check else 0)
     dims = ss_norm_dims(rows, cols)
     need = int(lib().ss_norm_bwd_workspace_bytes(ctypes.byref(dims), flags))
-    with _in_turn(dev, stream):
-        launch, workspace = _launch_for(need, dev, stream, workspace)
+    sh = _stream_handle(stream, dev)
+    with _in_turn(dev, sh):
+        launch, workspace = _launch_for(need, dev, sh, workspace)
         rc = lib().ss_norm_bwd(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(g["dx"]),
                                _ptr(g.get("dweight")), _ptr(g.get("dbias")), flags, ctypes.byref(dims),
                                ctypes.byref(launch))
@@ -832,6 +852,7 @@ def ss_norm_bwd(dy, x, mean, rstd, weight=None, *, dx=None, dweight=None, dbias=
 
 
 @_on_device
+@_on_stream
 def ss_block_fwd_prenorm(hidden, weights, norm_weight=None, norm_bias=None, *, eps=1e-5, out=None, scratch=None,
                          stream=None):
     """hidden + block(layer_norm(hidden)) through libselscan's ss_block_fwd_prenorm: ss_block_fwd's arguments,
@@ -847,13 +868,14 @@ def ss_block_fwd_prenorm(hidden, weights, norm_weight=None, norm_bias=None, *, e
     _check(norm_weight, "norm_weight", (d_model,), torch.float32, dev)
     _check(norm_bias, "norm_bias", (d_model,), torch.float32, dev)
     if out is None:
-        out = _empty(hidden.shape, hidden.dtype, dev, stream)
+        out = torch.empty_like(hidden)
     _check(out, "out", (batch, L, d_model), torch.bfloat16, dev)
     need = int(lib().ss_block_prenorm_scratch_bytes(ctypes.byref(st), batch, L))
     if need == 0:
         raise SelscanError(SS_ERR_INVALID_ARG, "ss_block_fwd_prenorm")
-    with _in_turn(dev, stream):
-        launch, scratch = _launch_for(need, dev, stream, scratch)
+    sh = _stream_handle(stream, dev)
+    with _in_turn(dev, sh):
+        launch, scratch = _launch_for(need, dev, sh, scratch)
         rc = lib().ss_block_fwd_prenorm(_ptr(hidden), _ptr(norm_weight), _ptr(norm_bias), float(eps), _ptr(out),
                                         ctypes.byref(st), batch, L, launch.workspace, launch.workspace_bytes,
                                         launch.stream)
@@ -870,6 +892,7 @@ def ss_check(workspace, stream=None, device=None):
     return int(lib().ss_check(ctypes.byref(launch)))
 
 
+@_on_stream
 def ss_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, y=None, softplus=True,
             stream=None, sync_check=False):
     """One decode step through libselscan's ss_step; `state` is updated in place.
@@ -893,7 +916,7 @@ def ss_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, y=None
     _check(D, "D", (d,), torch.float32, dev)
     _check(delta_bias, "delta_bias", (d,), torch.float32, dev)
     if y is None:
-        y = _empty((batch, d), io, dev, stream)
+        y = torch.empty((batch, d), dtype=io, device=dev)
     _check(y, "y", (batch, d), io, dev)
     flags = _io_flag(u) | (SS_DELTA_SOFTPLUS if softplus else 0) | (SS_SYNC_CHECK if sync_check else 0)
     sh = _stream_handle(stream, dev)
