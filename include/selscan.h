@@ -345,9 +345,12 @@ typedef struct ss_gdr_dims {
  *                idle, segments run in parallel, from entering states that a first
  *                pass over them and a fold make exact up to rounding.
  * The state is fp32 throughout.  bf16 runs chunk by chunk (64 steps) as dense products
- * on the tensor cores, in which the fp32 operands (the state, the chunk's inverse and
- * its corrections) enter as two bf16 terms each; fp32, and short bf16 sequences, run
- * token by token in fp32.  Errors: SS_ERR_INVALID_ARG for NULL or misaligned pointers
+ * on the tensor cores, in which the fp32 operands enter as three bf16 terms (the state
+ * and what goes into it) or two (the chunk's inverse, and what y alone takes): the final
+ * state is under 1e-6 of itself off; fp32, and short bf16 sequences, run token by token
+ * in fp32.  In chunks an infinity or NaN in a token's k, v, dt or beta may reach every
+ * token of its 64, the earlier ones too (their y, and all their gradients); token by
+ * token it reaches itself and later ones.  Errors: SS_ERR_INVALID_ARG for NULL or misaligned pointers
  * or sizes, SS_ERR_UNSUPPORTED for d_k or d_v other than 64 and 128, SS_ERR_WORKSPACE,
  * SS_ERR_CUDA.  batch or nheads 0 is a no-op; seqlen 0 copies h_init (or zero) to
  * final_state. */
@@ -384,11 +387,13 @@ SS_API int ss_gdr_step(float* state, const void* q, const void* k, const void* v
  * sums are added in a fixed order: the same call gives the same bits.  Outputs overlap
  * neither the inputs nor one another (dh_init may be dfinal_state).
  * bf16 runs chunk by chunk on the tensor cores, fp32 and short bf16 sequences token by
- * token in fp32.  In chunks dA and ddt_bias, sums of terms of both signs, are off by a
- * few 1e-6 of themselves, more where they nearly cancel (2^-15 of the terms' absolute
- * sum at most); token by token as any fp32 sum.  Workspace: launch->workspace of at least ss_gdr_bwd_workspace_bytes()
- * bytes (about 230 KB per 64 tokens of a head: the chunks' states and their adjoints;
- * token by token up to 17 KB per token of a head), 16-byte aligned; its first word is the status word, as in ss_gdr_fwd.  Errors: as ss_gdr_fwd. */
+ * token in fp32.  In chunks dh_init is under 1e-6 of itself off, dA and ddt_bias, sums of
+ * terms of both signs, about 1e-6, more where they nearly cancel; token by token as any
+ * fp32 sum.  Workspace: launch->workspace of at least ss_gdr_bwd_workspace_bytes() bytes
+ * (about 260 KB per 64 tokens of a head: the chunks' states and their adjoints; token by
+ * token up to 17 KB per token of a head), 16-byte aligned; its first word is the status
+ * word, as in ss_gdr_fwd.  Errors: as ss_gdr_fwd; without value heads dq and dk are
+ * written (zero) and must be given. */
 SS_API int ss_gdr_bwd(const void* q, const void* k, const void* v, const void* dt, const float* dt_bias,
                       const float* A, const void* beta, const float* h_init, const int32_t* seqlens,
                       const void* dy, const float* dfinal_state, void* dq, void* dk, void* dv, void* ddt,

@@ -66,8 +66,8 @@ int run_rec(const GdrParams& p, const ss_gdr_dims* d, uint32_t flags, cudaStream
 }
 
 // bf16 sequences of at least this many tokens run in chunks (token by token against in chunks, d_k = d_v = 128: at 8
-// tokens 10 / 21 us with 12 items, 16 / 23 with 96, 82 / 128 with 1280; at 16 tokens 15 / 22, 26 / 23 and 154 / 127; at
-// 24 tokens 21 / 21, 36 / 23 and 225 / 127).
+// tokens 10 / 22 us with 12 items, 16 / 23 with 96, 84 / 134 with 1280; at 16 tokens 16 / 23, 27 / 23 and 154 / 133; at
+// 24 tokens 22 / 22, 37 / 23 and 225 / 133: the two are even near 24, 13 and 14 tokens, and one border serves all).
 constexpr int64_t kChunkedFrom = 16;
 
 // 4-D map of a [batch, L, heads, d] bf16 tensor, boxes of `cols` x 64 tokens of one head.
@@ -89,9 +89,9 @@ struct GdrPlan {
 };
 // The plan with the least chunk-times on the busiest SM (one CTA per SM).  A chunk of the state pass takes 0.8 of one
 // with y; the extra launches are charged 3 chunks and the fold one per segment.  Whole call, items whole / in segments:
-// 16 items of 16 chunks 72 / 62 us in 4 (75 in 8), of 32 chunks 127 / 84 in 6 (90 in 4), of 512 chunks 1795 / 695 in 9;
-// 12 items of 8 chunks 43 / 47 in 4 (runs whole); 160 items of 128 chunks 1210 / 934, the last wave's 12 items in segments (all
-// of them in 4: 1541).
+// 16 items of 16 chunks 82 / 68 us in 4 (80 in 8), of 32 chunks 148 / 92 in 6 (102 in 4), of 512 chunks 2118 / 822 in 9;
+// 12 items of 8 chunks 49 / 50 in 4 (runs whole); 160 items of 128 chunks 1392 / 1058, the last wave's 12 items in segments
+// (all of them in 4: 1794).
 GdrPlan gdr_plan(int64_t items, int64_t nchunks, int32_t chunk_len) {
     GdrPlan best{items, 1, nchunks};
     if (items == 0 || nchunks < 2 || items * 2 * kGdrMaxSeg >= (int64_t(1) << 31)) return best;   // (a launch's blocks)
@@ -206,8 +206,9 @@ int run_tc(const GdrParams& g, const ss_gdr_dims* d, uint32_t flags, const ss_la
 }
 
 // bf16 sequences of at least this many tokens run their backward pass in chunks (token by token against in chunks, d_k =
-// d_v = 128: at 4 tokens 24 / 52 us with 2 items, 39 / 54 with 96, 352 / 388 with 1280; at 8 tokens 33 / 53, 62 / 54 and
-// 646 / 389; at 16 tokens 51 / 53, 104 / 54 and 1238 / 393).
+// d_v = 128: at 4 tokens 24 / 59 us with 2 items, 40 / 61 with 96, 354 / 447 with 1280; at 8 tokens 33 / 58, 62 / 61 and
+// 648 / 448; at 16 tokens 50 / 58, 106 / 61 and 1245 / 451: the two are even near 19, 8 and 5 tokens, and one border
+// serves all).
 constexpr int64_t kBwdChunkedFrom = 8;
 
 // The backward pass's workspace: header, records, what the chains keep, the tokens' sums, the items' shares.

@@ -58,7 +58,7 @@ static_assert(sizeof(RevBars) <= 256, "barrier region");
 
 // Grid: one CTA per (b, h).  dV of every chunk and the adjoints of the states between the chunks are kept, and leave by
 // bulk copies from shared memory (16-byte stores from the threads' registers: 279 against 236 us).  8 x 2048 tokens, 12
-// heads of 128 (96 CTAs of 32 chunks): 171 us, 5.3 us a chunk, tensor pipe 31 %: its hand-overs bound it, beside
+// heads of 128 (96 CTAs of 32 chunks): 159 us, 5.0 us a chunk, tensor pipe 42 %: its hand-overs bound it, beside
 // the 96 KB that a chunk keeps.
 template <int DK>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -408,9 +408,10 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
 // (ek carries the minus of -e^G), and of each token r, c and the sum of W that crosses it: a row's prefix sums over its
 // columns, added over the rows by shuffles.  dV comes
 // from the chain transposed and is turned in shared memory; dO has no lo terms, so the products with dV's write the
-// lanes from 64 on alone; S and dS pass through one buffer.  Bound by the latency of its stages, one block per SM
-// (218 KB): 8 x 2048 tokens, 12 heads of 128 (3072 blocks) 342 us, 16.5 us a block, 2.7 TB/s, tensor pipe 19 % (512
-// threads: 351 against 346 us).
+// lanes from 64 on alone; S and dS pass through one buffer, in fp32 and then as terms.  Bound by the latency of its
+// stages, one block per SM (219 KB): 8 x 2048 tokens, 12 heads of 128 (a block per head and chunk) 442 us, 21 us a block,
+// 2.2 TB/s, tensor pipe 22 %.  (S, dS and E as two terms, made by the chains: 342 us, and dA 5 times further off; 512
+// threads then 351 against 346 us.)
 constexpr int kGradThreads = 256;
 constexpr uint32_t kGK = 0;                       // [Q 0][K 0][Q 1][K 1]
 constexpr uint32_t kG1 = 4 * kTile;               // [dO 0][dV hi 0][dO 1][dV hi 1]; then dS's third terms

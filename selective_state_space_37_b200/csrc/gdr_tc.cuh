@@ -386,8 +386,9 @@ static_assert(kPrepXs % 16 == 0 && 5 * (kPrepSmem + 1024) <= 228 * 1024, "five r
 
 // Grid: one block per (item, chunk), a sequence's chunks together.  Bound by the latency of the triangular inverse
 // (fp32, about 75 000 multiply-adds in a dozen dependent steps), which the five resident blocks hide for one another.
-// 20480 chunks (4 x 8192 tokens, 40 heads of 128): 344 us, 2.5 us a chunk and SM, issue slots 40 % busy (four resident
-// blocks: 366 us; the inverse's products on tf32 mma.sync: 395 against 366 us).
+// 20480 chunks (4 x 8192 tokens, 40 heads of 128): 344-356 us, 2.5 us a chunk and SM, issue slots 40 % busy (four
+// resident blocks: 366 us; the inverse's products on tf32 mma.sync: 395 against 366 us).  The third terms of T and P, for
+// the backward pass alone, go from the registers to the record (3000 chunks: 68 against 51 us).
 template <int DK>
 __global__ void __launch_bounds__(kPrepThreads)
 ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_q,
@@ -618,9 +619,10 @@ ss_gdr_prep_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
 // Warps: 0..15 state (above); 16 issues the MMAs; 17 the loads (two chunks in flight); 18 stores y.  They hand over
 // through mbarriers.  Every wait is bounded: one that runs out records SS_ERR_TIMEOUT and the CTA winds down.
 //
-// Bound by that chain: 8 x 2048 tokens, 12 heads of 128 (96 CTAs of 32 chunks) 121 us, 3.5 us a chunk of which 1.2 us
-// are products' time; 160 items of 128 chunks with their segments 520 us, tensor pipe 50 %.  Half the state warps:
-// 1738 us for what 1378 us then took.
+// Bound by that chain: 8 x 2048 tokens, 12 heads of 128 (96 CTAs of 32 chunks) 147 us, 4.5 us a chunk of which 1.8 us
+// are products' time (tensor pipe 47 %); 160 items of 128 chunks with their segments 606 us.  (With S and X as two terms
+// 121 and 520 us; 28 bytes of each thread's registers spill at the 96 that 19 warps leave.)  Half the state warps: 1738 us
+// for what 1378 us then took.
 constexpr int kParts = 4;              // threads to a row of the state
 constexpr int kStateWarps = 4 * kParts;
 constexpr int kMmaWarp = kStateWarps, kLoadWarp = kMmaWarp + 1, kStoreWarp = kMmaWarp + 2;

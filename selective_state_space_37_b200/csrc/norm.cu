@@ -300,7 +300,9 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads) ss_norm_f
 // Forward, rows of whole 16-byte vectors that a warp holds: NV vectors per lane, all loaded before the first is used,
 // no barrier; the parameters lie in shared memory (their vectors' quads in planes, so that a warp's reads are
 // consecutive), loaded once by a block that walks rows.  32768 x 2560 bf16: 60 us, 5.6 TB/s, bound by HBM's
-// latency at 24 resident warps per SM.
+// latency at 16 resident warps per SM (two blocks from NV = 9 on, three below).  In bf16 NV = 16 spills 372 bytes of
+// registers and NV = 8 136 (32768 x 4096 111 us, 4.9 TB/s); rows of few vectors leave lanes idle (65536 x 256 17.6 us,
+// x 64 14 us).
 constexpr int kRowWarps = 8;
 template <typename IO, int NV>
 __global__ void __launch_bounds__(32 * kRowWarps, NV <= 8 ? 3 : 2) ss_norm_fwd_rows_kernel(const NormParams p) {
@@ -587,9 +589,10 @@ NormPlan norm_plan(int64_t rows, int64_t cols, bool bf16, bool bwd) {
     const int threads = pl.warp ? 32 * kWarpRows : pl.T;
     const int64_t sms = sm_count_of_current_device();
     // forward: a block per row while there are few, else blocks that walk rows with the parameters in registers;
-    // backward: as many blocks as are resident together (at 128 registers a thread; 32768 x 2560 bf16: 128 us with twice
+    // backward: as many blocks as are resident together at 128 registers a thread (32768 x 2560 bf16: 128 us with twice
     // as many, 120 us so; rows through a ring of bulk copies in shared memory instead of the next row in registers:
-    // 117 us, not kept), and their partial rows are written and read once
+    // 117 us, not kept), and their partial rows are written and read once.  (Where a warp takes a row, fp32 and unaligned
+    // rows take 146 and 168 registers: three of the four blocks per SM run first, then the fourth.)
     const int64_t resident = sms * std::max(1, (bwd ? 512 : 2048) / threads);
     pl.blocks = std::max<int64_t>(1, std::min(items, resident));
     if (bwd && !pl.held) {
