@@ -409,8 +409,8 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
 // columns, added over the rows by shuffles.  dV comes
 // from the chain transposed and is turned in shared memory; dO has no lo terms, so the products with dV's write the
 // lanes from 64 on alone; S and dS pass through one buffer, in fp32 and then as terms.  Bound by the latency of its
-// stages, one block per SM (219 KB): 8 x 2048 tokens, 12 heads of 128 (a block per head and chunk) 442 us, 21 us a block,
-// 2.2 TB/s, tensor pipe 22 %.  (S, dS and E as two terms, made by the chains: 342 us, and dA 5 times further off; 512
+// stages, one block per SM (219 KB): 8 x 2048 tokens, 12 heads of 128 (a block per head and chunk) 450 us, 22 us a block,
+// 2.1 TB/s, tensor pipe 22 %.  (S, dS and E as two terms, made by the chains: 342 us, and dA 5 times further off; 512
 // threads then 351 against 346 us.)
 constexpr int kGradThreads = 256;
 constexpr uint32_t kGK = 0;                       // [Q 0][K 0][Q 1][K 1]
@@ -627,8 +627,10 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
             // (the accumulator is cut off, not rounded, after every product: here and below the small terms come first)
             for (int ks = 0; ks < vs; ++ks)
                 umma(tmem + 384, a_hi(ks), sdesc(base + kGE + 2 * kTile + 2048u * ks, 0, 1024), idesc(kC, true), ks > 0);
-            for (int ks = 0; ks < vs; ++ks)
+            for (int ks = 0; ks < vs; ++ks) {
+                umma_upper(tmem + 384, a_lo(ks), sdesc(base + kGE + 2 * kTile + 2048u * ks, 0, 1024), idesc(kC, true));
                 umma_upper(tmem + 384, a_lo(ks), sdesc(base + kGE + 2048u * ks, 0, 1024), idesc(kC, true));
+            }
         }
         // v's gradient: dV's hi terms are its values rounded to bf16
         for (int w = tid; w < rows * vb * 8; w += kGradThreads) {
@@ -740,6 +742,7 @@ ss_gdr_grad_kernel(const __grid_constant__ GradParams gp, const __grid_constant_
             for (int ks = 0; ks < vs; ++ks) {
                 umma(tmem, a_hi(ks), sdesc(base + kGM + 2048u * ks, 2 * kTile, 1024), idesc(DK, true), ks > 0);
                 umma(tmem, a_hi(ks), sdesc(base + kGS + 2 * kTile + 2048u * ks, 4 * kTile, 1024), idesc(DK, true), 1);
+                umma_upper(tmem, a_lo(ks), sdesc(base + kGS + 2 * kTile + 2048u * ks, 4 * kTile, 1024), idesc(DK, true));
                 umma_upper(tmem, a_lo(ks), sdesc(base + kGS + 2048u * ks, 4 * kTile, 1024), idesc(DK, true));
             }
             for (int ks = 0; ks < vs; ++ks)
