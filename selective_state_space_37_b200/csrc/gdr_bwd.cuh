@@ -41,7 +41,8 @@ constexpr uint32_t kRevS = 0, kRevA = 128, kRevR = 192, kRevV = 320, kRevO = 448
 // Shared memory: two stages of [K 0][Q 0][K 1][Q 1][record]; dO (swizzled blocks) and P's third term; an image on its way
 // out, dS in fp32 and then dVᵀ's terms.
 constexpr uint32_t kRevStage = 4 * kTile + kRecBytes, kRevOffRec = 4 * kTile;
-constexpr uint32_t kRevOffO = 2 * kRevStage, kRevOffP3 = kRevOffO + 2 * kTile, kRevOffImg = kRevOffP3 + kTile, kRevOffBar = kRevOffImg + 8 * kTile;
+constexpr uint32_t kRevOffO = 2 * kRevStage, kRevOffP3 = kRevOffO + 2 * kTile, kRevOffImg = kRevOffP3 + kTile;
+constexpr uint32_t kRevOffBar = kRevOffImg + 8 * kTile;
 constexpr uint32_t kRevSmem = kRevOffBar + 256 + 1024;
 static_assert(kRevStage % 1024 == 0 && kRevSmem <= 227 * 1024, "shared memory");
 
@@ -406,12 +407,11 @@ ss_gdr_rev_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
 //   D3 E dS                    ->         128 .. 255 (K: d_v; likewise)
 //   dq~ = qe D1 + D4 (lanes 0..63),   dk~ = ek D1 + D4 (lanes 64..127) + wk D3 + D5 (lanes 0..63)
 // (ek carries the minus of -e^G), and of each token r, c and the sum of W that crosses it: a row's prefix sums over its
-// columns, added over the rows by shuffles.  dV comes
-// from the chain transposed and is turned in shared memory; dO has no lo terms, so the products with dV's write the
-// lanes from 64 on alone; S and dS pass through one buffer, in fp32 and then as terms.  Bound by the latency of its
-// stages, one block per SM (219 KB): 8 x 2048 tokens, 12 heads of 128 (a block per head and chunk) 450 us, 22 us a block,
-// 2.1 TB/s, tensor pipe 22 %.  (S, dS and E as two terms, made by the chains: 342 us, and dA 5 times further off; 512
-// threads then 351 against 346 us.)
+// columns, added over the rows by shuffles.  dV comes from the chain transposed and is turned in shared memory; dO has
+// no lo terms, so the products with dV's write the lanes from 64 on alone; S and dS pass through one buffer, in fp32 and
+// then as terms.  Bound by the latency of its stages, one block per SM (219 KB): 8 x 2048 tokens, 12 heads of 128 (a
+// block per head and chunk) 450 us, 22 us a block, 2.1 TB/s, tensor pipe 22 %.  (S, dS and E as two terms, made by the
+// chains: 342 us, and dA 5 times further off; 512 threads then 351 against 346 us.)
 constexpr int kGradThreads = 256;
 constexpr uint32_t kGK = 0;                       // [Q 0][K 0][Q 1][K 1]
 constexpr uint32_t kG1 = 4 * kTile;               // [dO 0][dV hi 0][dO 1][dV hi 1]; then dS's third terms
